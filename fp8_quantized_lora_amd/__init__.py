@@ -34,7 +34,10 @@ __all__ = ["load", "FalqError", "fp8_quantize", "fp8_quantize_workspace_bytes",
            "melded_linear_fwd_xa_workspace_bytes", "melded_linear_bwd_xa_workspace_bytes",
            "lora_separate_fp8_saved_bytes", "lora_separate_fp8_workspace_bytes",
            "lora_separate_fp8_fwd", "lora_separate_fp8_bwd", "lora_bf16_saved_bytes",
-           "lora_bf16_workspace_bytes", "lora_bf16_fwd", "lora_bf16_bwd"]
+           "lora_bf16_workspace_bytes", "lora_bf16_fwd", "lora_bf16_bwd", "layer_norm_fwd",
+           "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "ACTIVATIONS",
+           "melded_linear_fwd_act", "linear_act_bwd", "linear_act_bwd_workspace_bytes",
+           "grad_norm", "grad_clip", "grad_norm_workspace_bytes", "GRAD_MAX_TENSORS"]
 
 #: bytes of the per-device scratch array behind fp8_quantize_noalloc
 QUANTIZE_SCRATCH_BYTES = 16384
@@ -114,6 +117,19 @@ _SIGS = {
                              _c_p, _c_p, _sz, _c_p, _sz, _c_p]),
     "lora_bf16_bwd": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _sz, _i64,
                              _i64, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _sz, _c_p]),
+    "layer_norm_fwd": (_i32, [_c_p, _i32, _c_p, _c_p, _i64, _i64, _f32, _c_p, _i32, _c_p, _c_p,
+                              _c_p]),
+    "layer_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "layer_norm_bwd": (_i32, [_c_p, _i32, _c_p, _i32, _c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p,
+                              _c_p, _c_p, _sz, _c_p]),
+    "melded_linear_fwd_act": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _i32, _c_p, _i64, _i64, _i64,
+                                     _i32, _c_p, _c_p, _c_p]),
+    "linear_act_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "linear_act_bwd": (_i32, [_c_p, _i32, _c_p, _i32, _i32, _i64, _i64, _c_p, _c_p, _c_p, _sz,
+                              _c_p]),
+    "grad_norm_workspace_bytes": (_sz, [_i64]),
+    "grad_norm": (_i32, [_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _sz, _c_p]),
+    "grad_clip": (_i32, [_i64, _c_p, _c_p, _c_p, _f32, _f32, _c_p, _c_p, _c_p, _sz, _c_p]),
 }
 
 
@@ -697,6 +713,199 @@ def lora_bf16_bwd(dy, gq, s_g, x, wq, s_w, A, B, saved, dx, dA, dB, ws=None,
                                 saved.numel() * saved.element_size(), T, d_in, d_out, r,
                                 _ptr(dx), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(),
                                 _stream(stream)), "lora_bf16_bwd")
+
+
+# ---------------------------------------------------------------------------
+# Around the linear: layer norm, the product with an epilogue, clipping.
+# These calls run on the device of their tensors, whichever is current.
+
+#: activations of melded_linear_fwd_act and linear_act_bwd (falq_activation)
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+#: tensors that one grad_norm or grad_clip call takes at most
+GRAD_MAX_TENSORS = 65536
+
+_ELEM = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _elem(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _ELEM:
+        raise FalqError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return _ELEM[t.dtype]
+
+
+def _act(act) -> int:
+    if act not in ACTIVATIONS:
+        raise FalqError(f"act must be one of {sorted(ACTIVATIONS)}, not {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _call(what: str, tensors, ws, ws_bytes: int, stream, f) -> None:
+    """f(workspace pointer, its bytes, stream) on the tensors' device.  A
+    workspace that the caller did not give is allocated for the stream of the
+    call, so that its memory is not handed to other work while the call runs."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise FalqError(f"{what}: tensors on {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise FalqError("tensor arguments must live on the GPU")
+    if ws is not None and (ws.device != dev or ws.dtype != torch.uint8):
+        raise FalqError(f"{what}: ws must be uint8 on {dev}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(what, tensors, ws, ws_bytes, stream, f)
+    st = _stream(stream)
+    if ws is None and ws_bytes:
+        if stream is None or st == torch.cuda.current_stream().cuda_stream:
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(st, device=dev)):
+                ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    _check(f(_ptr(ws), 0 if ws is None else ws.numel(), st), what)
+
+
+def _optional(t: Optional[torch.Tensor], dtype, shape, name) -> None:
+    if t is not None:
+        _req(t, dtype, shape, name)
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor],
+                   y: torch.Tensor, mean: Optional[torch.Tensor] = None,
+                   rstd: Optional[torch.Tensor] = None, eps: float = 1e-5, stream=None) -> None:
+    """y = (x - mean) * rstd * weight + bias per row of x [T x d], rstd =
+    1 / sqrt(var + eps); x and y float32 or bfloat16 each, weight and bias
+    float32 or None; mean and rstd [T] are what layer_norm_bwd takes."""
+    T, d = x.shape
+    xt, yt = _elem(x, "x"), _elem(y, "y")
+    _req(y, y.dtype, (T, d), "y")
+    _optional(weight, torch.float32, (d,), "weight")
+    _optional(bias, torch.float32, (d,), "bias")
+    _optional(mean, torch.float32, (T,), "mean")
+    _optional(rstd, torch.float32, (T,), "rstd")
+    _call("layer_norm_fwd", (x, weight, bias, y, mean, rstd), None, 0, stream,
+          lambda ws, n, st: load().layer_norm_fwd(_ptr(x), xt, _ptr(weight), _ptr(bias), T, d, eps,
+                                                  _ptr(y), yt, _ptr(mean), _ptr(rstd), st))
+
+
+def layer_norm_bwd_workspace_bytes(T: int, d: int) -> int:
+    return int(load().layer_norm_bwd_workspace_bytes(T, d))
+
+
+def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                   mean: torch.Tensor, rstd: torch.Tensor, dx: Optional[torch.Tensor],
+                   dweight: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The gradients of layer_norm_fwd: dx (dy's type; may be dy, or None), and
+    the sums over rows dweight and dbias (float32, each may be None)."""
+    T, d = x.shape
+    gt, xt = _elem(dy, "dy"), _elem(x, "x")
+    _req(dy, dy.dtype, (T, d), "dy")
+    _optional(weight, torch.float32, (d,), "weight")
+    _req(mean, torch.float32, (T,), "mean")
+    _req(rstd, torch.float32, (T,), "rstd")
+    _optional(dx, dy.dtype, (T, d), "dx")
+    _optional(dweight, torch.float32, (d,), "dweight")
+    _optional(dbias, torch.float32, (d,), "dbias")
+    need = 0 if dweight is None and dbias is None else layer_norm_bwd_workspace_bytes(T, d)
+    _call("layer_norm_bwd", (dy, x, weight, mean, rstd, dx, dweight, dbias), ws, need, stream,
+          lambda w, n, st: load().layer_norm_bwd(_ptr(dy), gt, _ptr(x), xt, _ptr(weight),
+                                                 _ptr(mean), _ptr(rstd), T, d, _ptr(dx),
+                                                 _ptr(dweight), _ptr(dbias), w, n, st))
+
+
+def melded_linear_fwd_act(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tensor,
+                          s_w: torch.Tensor, y: torch.Tensor,
+                          bias: Optional[torch.Tensor] = None, act: str = "none",
+                          residual: Optional[torch.Tensor] = None,
+                          z: Optional[torch.Tensor] = None, stream=None) -> None:
+    """z = dec(xq) dec(wq)^T / (s_x s_w) + bias and y = act(z) + residual in one
+    call; y, z and residual share one type (float32 or bfloat16), bias is
+    float32; residual may be y; z (None: not kept) is what linear_act_bwd takes."""
+    T, d_in = xq.shape
+    d_out = wq.shape[0]
+    t, a = _elem(y, "y"), _act(act)
+    _req(xq, torch.uint8, (T, d_in), "xq")
+    _req(wq, torch.uint8, (d_out, d_in), "wq")
+    _req(s_x, torch.float32, (1,), "s_x")
+    _req(s_w, torch.float32, (1,), "s_w")
+    _req(y, y.dtype, (T, d_out), "y")
+    _optional(bias, torch.float32, (d_out,), "bias")
+    _optional(residual, y.dtype, (T, d_out), "residual")
+    _optional(z, y.dtype, (T, d_out), "z")
+    _call("melded_linear_fwd_act", (xq, s_x, wq, s_w, y, bias, residual, z), None, 0, stream,
+          lambda ws, n, st: load().melded_linear_fwd_act(
+              _ptr(xq), _ptr(s_x), _ptr(wq), _ptr(s_w), _ptr(bias), a, _ptr(residual), T, d_in,
+              d_out, t, _ptr(y), _ptr(z), st))
+
+
+def linear_act_bwd_workspace_bytes(T: int, d_out: int) -> int:
+    return int(load().linear_act_bwd_workspace_bytes(T, d_out))
+
+
+def linear_act_bwd(dy: torch.Tensor, z: Optional[torch.Tensor], dz: torch.Tensor,
+                   dbias: Optional[torch.Tensor] = None, act: str = "none",
+                   ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dz = dy * act'(z) (dy's type; dz may be dy) and dbias = the sum of dz over
+    the rows (float32, or None); z float32 or bfloat16, None for act "none"."""
+    T, d_out = dy.shape
+    gt, a = _elem(dy, "dy"), _act(act)
+    if z is None and a != 0:
+        raise FalqError(f"linear_act_bwd: z is needed for act {act!r}")
+    zt = 0 if z is None else _elem(z, "z")
+    if z is not None:
+        _req(z, z.dtype, (T, d_out), "z")
+    _req(dz, dy.dtype, (T, d_out), "dz")
+    _optional(dbias, torch.float32, (d_out,), "dbias")
+    need = 0 if dbias is None else linear_act_bwd_workspace_bytes(T, d_out)
+    _call("linear_act_bwd", (dy, z, dz, dbias), ws, need, stream,
+          lambda w, n, st: load().linear_act_bwd(_ptr(dy), gt, _ptr(z), zt, a, T, d_out, _ptr(dz),
+                                                 _ptr(dbias), w, n, st))
+
+
+def grad_norm_workspace_bytes(count: int) -> int:
+    return int(load().grad_norm_workspace_bytes(count))
+
+
+def _tensor_list(what: str, tensors):
+    """Host arrays of addresses, element counts and types."""
+    n = len(tensors)
+    if not all(t.is_cuda and t.is_contiguous() and t.dtype in _ELEM for t in tensors):
+        raise FalqError(f"{what}: tensors must be contiguous float32 or bfloat16 on the GPU")
+    return ((_c_p * n)(*[t.data_ptr() for t in tensors]),
+            (_i64 * n)(*[t.numel() for t in tensors]),
+            (ctypes.c_int32 * n)(*[_ELEM[t.dtype] for t in tensors]))
+
+
+def grad_norm(grads, norm: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """norm = sqrt of the sum of squares over all elements of all tensors
+    (float32 and bfloat16, any shapes), summed in float64 on the device."""
+    grads = list(grads)
+    _req(norm, torch.float32, (1,), "norm")
+    p, n, t = _tensor_list("grad_norm", grads)
+    _call("grad_norm", (norm, *grads), ws, grad_norm_workspace_bytes(len(grads)), stream,
+          lambda w, nb, st: load().grad_norm(len(grads), p, n, t, _ptr(norm), w, nb, st))
+
+
+def grad_clip(grads, max_norm: float, norm: torch.Tensor, out=None, eps: float = 1e-6,
+              ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Multiply every tensor by min(1, max_norm / (norm + eps)), norm being the
+    global norm over all of them (written to `norm` as grad_norm does): in
+    place, or into the tensors `out`.  No tensor may be listed twice."""
+    grads = list(grads)
+    _req(norm, torch.float32, (1,), "norm")
+    p, n, t = _tensor_list("grad_clip", grads)
+    q, outs = None, ()
+    if out is not None:
+        outs = list(out)
+        if len(outs) != len(grads):
+            raise FalqError(f"grad_clip: {len(outs)} outputs for {len(grads)} tensors")
+        for g, o in zip(grads, outs):
+            if o.dtype != g.dtype or o.shape != g.shape:
+                raise FalqError("grad_clip: out must have the tensors' types and shapes")
+        q = _tensor_list("grad_clip", outs)[0]
+    _call("grad_clip", (norm, *grads, *outs), ws, grad_norm_workspace_bytes(len(grads)), stream,
+          lambda w, nb, st: load().grad_clip(len(grads), p, n, t, max_norm, eps, q, _ptr(norm), w,
+                                             nb, st))
 
 
 from .step import MeldedLinear  # noqa: E402  (buffers + the step's call sequence)

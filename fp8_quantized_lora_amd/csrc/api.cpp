@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <vector>
 
 namespace {
 
@@ -705,6 +706,165 @@ falq_status fp8_transpose(const uint8_t* q, int64_t rows, int64_t cols, uint8_t*
   if (!need(q) || !need(qT) || q == qT) return FALQ_EINVAL;
   return hip_status(
       falq::launch_transpose_u8(q, rows, cols, qT, reinterpret_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+inline bool dtype_ok(int t) { return t == FALQ_F32 || t == FALQ_BF16; }
+
+// rows and columns of the row-wise operators: a column count is exact in
+// float32 and every launch fits a 32-bit grid
+inline bool rows_ok(int64_t T, int64_t d) {
+  return T >= 0 && T <= (int64_t)1 << 30 && d >= 1 && d <= (int64_t)1 << 24;
+}
+
+// Whether the outputs are disjoint from each other and from every input but
+// their own, which an output may be (in place) or miss, never overlap partly.
+bool disjoint(int64_t count, const void* const* g, const int64_t* n, const int32_t* dtype,
+              void* const* out) {
+  struct Span {
+    uintptr_t lo, hi;
+    int64_t i;
+  };
+  const auto span = [&](const void* p, int64_t i) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return Span{lo, lo + (uintptr_t)n[i] * (dtype[i] == FALQ_BF16 ? 2 : 4), i};
+  };
+  std::vector<Span> o;
+  o.reserve((size_t)count);
+  for (int64_t i = 0; i < count; ++i)
+    if (n[i] > 0) o.push_back(span(out[i], i));
+  std::sort(o.begin(), o.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  for (size_t k = 1; k < o.size(); ++k)
+    if (o[k].lo < o[k - 1].hi) return false;
+  for (int64_t i = 0; i < count; ++i) {
+    if (n[i] == 0) continue;
+    const Span a = span(g[i], i);
+    // the disjoint outputs that end behind the input's start, in order
+    auto it = std::upper_bound(o.begin(), o.end(), a.lo,
+                               [](uintptr_t v, const Span& b) { return v < b.hi; });
+    for (; it != o.end() && it->lo < a.hi; ++it)
+      if (it->i != i || it->lo != a.lo) return false;
+  }
+  return true;
+}
+
+falq_status grad_norm_impl(int64_t count, const void* const* g, const int64_t* n,
+                           const int32_t* dtype, float max_norm, float eps,
+                           void* const* out, float* norm, void* ws, size_t ws_bytes,
+                           falq_stream stream) {
+  if (count < 0 || count > FALQ_GRAD_MAX_TENSORS || !scalar(norm)) return FALQ_EINVAL;
+  if (count > 0 && (!g || !n || !dtype)) return FALQ_EINVAL;
+  if (!(max_norm >= 0.0f) || !(eps >= 0.0f) || std::isinf(eps)) return FALQ_EINVAL;
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (n[i] < 0 || n[i] > (int64_t)1 << 40 || !dtype_ok(dtype[i])) return FALQ_EINVAL;
+    total += n[i];
+    if (total > (int64_t)1 << 40) return FALQ_EINVAL;
+    const size_t size = dtype[i] == FALQ_BF16 ? 2 : 4;
+    if (n[i] > 0 && (!g[i] || !aligned(g[i], size))) return FALQ_EINVAL;
+    if (n[i] > 0 && out && (!out[i] || !aligned(out[i], size))) return FALQ_EINVAL;
+  }
+  if (!ws_ok(ws, ws_bytes, falq::grad_norm_ws_bytes(count))) return FALQ_EINVAL;
+  if (out) {
+    try {
+      if (!disjoint(count, g, n, dtype, out)) return FALQ_EINVAL;
+    } catch (...) {                            // no host memory for the check
+      return FALQ_EUNSUPPORTED;
+    }
+  }
+  return hip_status(falq::launch_grad_norm(count, g, n, dtype, max_norm, eps, out, norm, ws,
+                                           reinterpret_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+falq_status layer_norm_fwd(const void* x, int x_dtype, const float* weight, const float* bias,
+                           int64_t T, int64_t d, float eps, void* y, int y_dtype, float* mean,
+                           float* rstd, falq_stream stream) {
+  if (!rows_ok(T, d) || !dtype_ok(x_dtype) || !dtype_ok(y_dtype)) return FALQ_EINVAL;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return FALQ_EINVAL;
+  if (!opt(weight) || !opt(bias) || !opt(mean) || !opt(rstd)) return FALQ_EINVAL;
+  if (T > 0 && (!need(x) || !need(y) || x == y)) return FALQ_EINVAL;
+  return hip_status(falq::launch_layer_norm_fwd(x, x_dtype, weight, bias, T, d, eps, y, y_dtype,
+                                                mean, rstd,
+                                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t layer_norm_bwd_workspace_bytes(int64_t T, int64_t d) {
+  return rows_ok(T, d) ? falq::layer_norm_bwd_ws_bytes(T, d) : 0;
+}
+
+falq_status layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x_dtype,
+                           const float* weight, const float* mean, const float* rstd, int64_t T,
+                           int64_t d, void* dx, float* dweight, float* dbias, void* ws,
+                           size_t ws_bytes, falq_stream stream) {
+  if (!rows_ok(T, d) || !dtype_ok(x_dtype) || !dtype_ok(dy_dtype)) return FALQ_EINVAL;
+  if (!opt(weight) || !opt(dx) || !opt(dweight) || !opt(dbias)) return FALQ_EINVAL;
+  if (dweight && dweight == dbias) return FALQ_EINVAL;
+  if (T > 0 && (!need(dy) || !need(x) || !need(mean) || !need(rstd))) return FALQ_EINVAL;
+  if (T > 0 && dx == x) return FALQ_EINVAL;
+  if ((dweight || dbias) && !ws_ok(ws, ws_bytes, falq::layer_norm_bwd_ws_bytes(T, d)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_layer_norm_bwd(dy, dy_dtype, x, x_dtype, weight, mean, rstd, T,
+                                                d, dx, dweight, dbias, ws,
+                                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+falq_status melded_linear_fwd_act(const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                  const float* s_w, const float* bias, int act,
+                                  const void* residual, int64_t T, int64_t d_in, int64_t d_out,
+                                  int dtype, void* y, void* z, falq_stream stream) {
+  if (!gemm_dims_ok(T, d_in, d_out) || !dtype_ok(dtype)) return FALQ_EINVAL;
+  if (act < FALQ_ACT_NONE || act > FALQ_ACT_SILU) return FALQ_EINVAL;
+  if (!scalar(s_x) || !scalar(s_w) || !opt(bias)) return FALQ_EINVAL;
+  if (T * d_in > 0 && !need(xq)) return FALQ_EINVAL;
+  if (d_out * d_in > 0 && !need(wq)) return FALQ_EINVAL;
+  if (T * d_out > 0 && (!need(y) || !opt(z) || !opt(residual))) return FALQ_EINVAL;
+  if (T * d_out > 0 && z && (z == y || z == residual)) return FALQ_EINVAL;
+  return hip_status(falq::launch_linear_act(xq, s_x, wq, s_w, bias, residual, T, d_in, d_out, act,
+                                            dtype, y, z, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t linear_act_bwd_workspace_bytes(int64_t T, int64_t d_out) {
+  return rows_ok(T, std::max<int64_t>(d_out, 1)) && d_out > 0
+             ? falq::linear_act_bwd_ws_bytes(T, d_out)
+             : 0;
+}
+
+falq_status linear_act_bwd(const void* dy, int dy_dtype, const void* z, int z_dtype, int act,
+                           int64_t T, int64_t d_out, void* dz, float* dbias, void* ws,
+                           size_t ws_bytes, falq_stream stream) {
+  if (!dtype_ok(dy_dtype) || !dtype_ok(z_dtype)) return FALQ_EINVAL;
+  if (act < FALQ_ACT_NONE || act > FALQ_ACT_SILU) return FALQ_EINVAL;
+  if (d_out < 0 || !rows_ok(T, std::max<int64_t>(d_out, 1)) || !opt(dbias)) return FALQ_EINVAL;
+  if (d_out == 0) return FALQ_OK;
+  if (T > 0 && (!need(dy) || !need(dz) || dz == z)) return FALQ_EINVAL;
+  if (T > 0 && act != FALQ_ACT_NONE && !need(z)) return FALQ_EINVAL;
+  if (dbias && !ws_ok(ws, ws_bytes, falq::linear_act_bwd_ws_bytes(T, d_out))) return FALQ_EINVAL;
+  return hip_status(falq::launch_linear_act_bwd(dy, dy_dtype, z, z_dtype, T, d_out, act, dz,
+                                                dbias, ws,
+                                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t grad_norm_workspace_bytes(int64_t count) {
+  return count >= 0 && count <= FALQ_GRAD_MAX_TENSORS ? falq::grad_norm_ws_bytes(count) : 0;
+}
+
+falq_status grad_norm(int64_t count, const void* const* g, const int64_t* n, const int32_t* dtype,
+                      float* norm, void* ws, size_t ws_bytes, falq_stream stream) {
+  return grad_norm_impl(count, g, n, dtype, 1.0f, 0.0f, nullptr, norm, ws, ws_bytes, stream);
+}
+
+falq_status grad_clip(int64_t count, void* const* g, const int64_t* n, const int32_t* dtype,
+                      float max_norm, float eps, void* const* out, float* norm, void* ws,
+                      size_t ws_bytes, falq_stream stream) {
+  return grad_norm_impl(count, g, n, dtype, max_norm, eps, out ? out : g, norm, ws,
+                        ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -227,7 +227,40 @@ hipError_t launch_proxy_update_topk_rank(uint8_t* wq, const float* s_w, const fl
                                          int32_t* n_sel, float* rho, int32_t* comp_idx,
                                          void* ws, hipStream_t s);
 
+// ---- layer norm ------------------------------------------------------------
+// dtype arguments: 0 float32, 1 bfloat16
+size_t layer_norm_bwd_ws_bytes(int64_t T, int64_t d);
+hipError_t launch_layer_norm_fwd(const void* x, int xt, const float* w, const float* b, int64_t T,
+                                 int64_t d, float eps, void* y, int yt, float* mean, float* rstd,
+                                 hipStream_t s);
+// dx, dw and db may each be null; dx may be dy
+hipError_t launch_layer_norm_bwd(const void* dy, int gt, const void* x, int xt, const float* w,
+                                 const float* mean, const float* rstd, int64_t T, int64_t d,
+                                 void* dx, float* dw, float* db, void* ws, hipStream_t s);
+
+// ---- linear layer with an epilogue, and the epilogue's backward -------------
+hipError_t launch_linear_act(const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                             const float* s_w, const float* bias, const void* residual, int64_t T,
+                             int64_t d_in, int64_t d_out, int act, int dtype, void* y, void* z,
+                             hipStream_t s);
+size_t linear_act_bwd_ws_bytes(int64_t T, int64_t d);
+// dbias may be null (then ws is not used); dz may be dy
+hipError_t launch_linear_act_bwd(const void* dy, int gt, const void* z, int zt, int64_t T,
+                                 int64_t d, int act, void* dz, float* dbias, void* ws,
+                                 hipStream_t s);
+
+// ---- gradient norm and clipping ---------------------------------------------
+size_t grad_norm_ws_bytes(int64_t count);
+// out == null: the norm only
+hipError_t launch_grad_norm(int64_t count, const void* const* g, const int64_t* n,
+                            const int32_t* dtype, float max_norm, float eps, void* const* out,
+                            float* norm, void* ws, hipStream_t s);
+
 // ---- misc -----------------------------------------------------------------
+// out0[c], out1[c] = sum over p < P of part[p][c], part[p][d + c] (rows of
+// nout * d floats, nout 1 or 2; a null output is skipped), in a fixed order
+hipError_t launch_column_sum(const float* part, int64_t P, int64_t d, int nout, float* out0,
+                             float* out1, hipStream_t s);
 hipError_t launch_fill_f32(float* p, int64_t n, float v, hipStream_t s);
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

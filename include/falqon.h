@@ -599,6 +599,122 @@ falq_status lora_bf16_bwd(const float *dy, const uint8_t *gq, const float *s_g, 
                           int64_t d_out, int64_t r, float *dx, float *dA, float *dB, void *ws,
                           size_t ws_bytes, falq_stream stream);
 
+/*
+ * ---- Around the linear: layer norm, the product with an epilogue, clipping --
+ * The operators that stand between two melded linears of a block and around
+ * its step: the norm in front of a projection, the bias, activation and
+ * residual of a product, the backward of both, and the clipping of every
+ * layer's dA and dB by their global norm before the adapter step.  Elements
+ * are float32 or bfloat16 (falq_dtype); sums, statistics and norms are
+ * float32 or wider and their order is fixed by the sizes, so results repeat
+ * bit for bit.  Two calls that may run at the same time need a workspace each.
+ */
+
+/*
+ * layer_norm_fwd — per row of x [T x d], with
+ *     mu = sum(x) / d,  var = sum((x - mu)^2) / d,  rstd = 1 / sqrt(var + eps):
+ *     y = (x - mu) * rstd * weight + bias
+ * rounded once to y's type.  A row with a NaN or an infinity is NaN.
+ *
+ *   x, y          [T x d] float32 or bfloat16 each, not the same memory;
+ *                 1 <= d <= 2^24
+ *   weight, bias  [d] float32, device, or NULL (1 and 0)
+ *   mean, rstd    [T] float32, device (output), or NULL; the backward's inputs
+ *   eps           >= 0, finite
+ */
+falq_status layer_norm_fwd(const void *x, int x_dtype, const float *weight, const float *bias,
+                           int64_t T, int64_t d, float eps, void *y, int y_dtype, float *mean,
+                           float *rstd, falq_stream stream);
+
+/*
+ * layer_norm_bwd — with xh = (x - mean) * rstd and g = dy * weight, per row
+ *     dx = rstd * (g - sum(g) / d - xh * sum(g * xh) / d)
+ * and over the rows
+ *     dweight = sum dy * xh,   dbias = sum dy.
+ *
+ *   dy, dx          [T x d], one type; dx may be dy (in place) or NULL
+ *   x               [T x d] float32 or bfloat16: the forward's input
+ *   weight          [d] float32, or NULL (1)
+ *   mean, rstd      [T] float32: the forward's
+ *   dweight, dbias  [d] float32 (output), each may be NULL; zero for T = 0
+ *   ws              layer_norm_bwd_workspace_bytes(T, d); not used (may be
+ *                   NULL) when dweight and dbias are both NULL
+ */
+size_t layer_norm_bwd_workspace_bytes(int64_t T, int64_t d);
+falq_status layer_norm_bwd(const void *dy, int dy_dtype, const void *x, int x_dtype,
+                           const float *weight, const float *mean, const float *rstd, int64_t T,
+                           int64_t d, void *dx, float *dweight, float *dbias, void *ws,
+                           size_t ws_bytes, falq_stream stream);
+
+typedef enum {
+    FALQ_ACT_NONE = 0,      /* z */
+    FALQ_ACT_RELU = 1,      /* max(z, 0) */
+    FALQ_ACT_GELU = 2,      /* z * Phi(z), Phi the normal distribution function */
+    FALQ_ACT_GELU_TANH = 3, /* z * (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    FALQ_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} falq_activation;
+
+/*
+ * melded_linear_fwd_act — the forward product with its epilogue in one call:
+ *     z = dec(xq) dec(wq)^T / (s_x s_w) + bias,   y = act(z) + residual
+ * accumulated and evaluated in float32, y and z rounded once each.
+ *
+ *   xq, s_x, wq, s_w  as melded_linear_fwd
+ *   bias              [d_out] float32, device, or NULL
+ *   act               falq_activation
+ *   residual          [T x d_out] of type dtype, or NULL; may be y (added in place)
+ *   y                 [T x d_out] of type dtype (output)
+ *   z                 [T x d_out] of type dtype (output), or NULL; not y or residual
+ */
+falq_status melded_linear_fwd_act(const uint8_t *xq, const float *s_x, const uint8_t *wq,
+                                  const float *s_w, const float *bias, int act,
+                                  const void *residual, int64_t T, int64_t d_in, int64_t d_out,
+                                  int dtype, void *y, void *z, falq_stream stream);
+
+/*
+ * linear_act_bwd — the backward of that epilogue:
+ *     dz = dy * act'(z),   dbias = sum over rows of dz  (before dz's rounding)
+ * (relu'(z) = 1 for z > 0, else 0).  dz is what fp8_quantize and the product's
+ * backward take as the upstream gradient; the residual's gradient is dy.
+ *
+ *   dy, dz   [T x d_out], one type; dz may be dy (in place), not z
+ *   z        [T x d_out] float32 or bfloat16: the forward's z; NULL allowed
+ *            for FALQ_ACT_NONE; any d_out from 0 to 2^24
+ *   dbias    [d_out] float32 (output), or NULL; zero for T = 0
+ *   ws       linear_act_bwd_workspace_bytes(T, d_out); not used without dbias
+ */
+size_t linear_act_bwd_workspace_bytes(int64_t T, int64_t d_out);
+falq_status linear_act_bwd(const void *dy, int dy_dtype, const void *z, int z_dtype, int act,
+                           int64_t T, int64_t d_out, void *dz, float *dbias, void *ws,
+                           size_t ws_bytes, falq_stream stream);
+
+/*
+ * grad_norm — norm = sqrt(sum of squares over every element of every tensor),
+ * summed in float64.  grad_clip — the same, then with
+ *     coef = min(1, max_norm / (norm + eps)):   out[i] = g[i] * coef
+ * rounded once to the tensor's type.  A NaN anywhere makes norm and every
+ * output NaN; an infinity makes norm infinite and coef 0.
+ *
+ *   count    number of tensors, 0 <= count <= FALQ_GRAD_MAX_TENSORS
+ *   g, out   HOST arrays of device pointers, read before the call returns;
+ *            each tensor contiguous and aligned to its element size (views
+ *            into a larger buffer qualify).  out NULL: in place.  An output
+ *            may be its own input or lie apart from every tensor; calls whose
+ *            outputs overlap each other or another input are refused.
+ *   n        HOST array: elements of each tensor, >= 0, 2^40 in all at most
+ *   dtype    HOST array: FALQ_F32 or FALQ_BF16 of each tensor
+ *   max_norm >= 0 (may be infinite);   eps >= 0, finite
+ *   norm     device float (output): the norm before clipping
+ *   ws       grad_norm_workspace_bytes(count)
+ */
+#define FALQ_GRAD_MAX_TENSORS 65536
+size_t grad_norm_workspace_bytes(int64_t count);
+falq_status grad_norm(int64_t count, const void *const *g, const int64_t *n, const int32_t *dtype,
+                      float *norm, void *ws, size_t ws_bytes, falq_stream stream);
+falq_status grad_clip(int64_t count, void *const *g, const int64_t *n, const int32_t *dtype,
+                      float max_norm, float eps, void *const *out, float *norm, void *ws,
+                      size_t ws_bytes, falq_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
