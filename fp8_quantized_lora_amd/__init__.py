@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Optional
 
 import torch
@@ -725,12 +726,14 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 GRAD_MAX_TENSORS = 65536
 
 _ELEM = {torch.float32: 0, torch.bfloat16: 1}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _elem(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _ELEM:
+    e = _ELEM.get(t.dtype)
+    if e is None:
         raise FalqError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
-    return _ELEM[t.dtype]
+    return e
 
 
 def _act(act) -> int:
@@ -739,34 +742,54 @@ def _act(act) -> int:
     return ACTIVATIONS[act]
 
 
-def _call(what: str, tensors, ws, ws_bytes: int, stream, f) -> None:
-    """f(workspace pointer, its bytes, stream) on the tensors' device.  A
-    workspace that the caller did not give is allocated for the stream of the
-    call, so that its memory is not handed to other work while the call runs."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise FalqError(f"{what}: tensors on {dev} and {t.device}")
-    if dev.type != "cuda":
-        raise FalqError("tensor arguments must live on the GPU")
-    if ws is not None and (ws.device != dev or ws.dtype != torch.uint8):
-        raise FalqError(f"{what}: ws must be uint8 on {dev}")
-    if dev.index != torch.cuda.current_device():
+def _arg(t: Optional[torch.Tensor], dtype, shape, dev: int, name: str) -> Optional[int]:
+    """The address of t (None: not given), a contiguous tensor of that type and
+    shape on device dev.  The small calls are bound by the host, so the checks
+    take the short way where all hold."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _req(t, dtype, shape, name)
+    _ptr(t)
+    raise FalqError(f"{name}: expected device cuda:{dev}, got {t.device}")
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise FalqError(f"{name}: tensor arguments must live on the GPU")
+    return dev
+
+
+def _stream_of(dev: int, stream) -> int:
+    return _raw_stream(dev) if stream is None else _stream(stream)
+
+
+def _scratch(ws: Optional[torch.Tensor], need: int, dev: int, stream, st: int):
+    """The caller's workspace, or one allocated for the stream of the call, so
+    that its memory is not handed to other work while the call runs."""
+    if ws is not None:
+        if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+            raise FalqError(f"ws must be contiguous uint8 on cuda:{dev}")
+        return ws
+    if not need:
+        return None
+    where = torch.device("cuda", dev)
+    if stream is None or st == _raw_stream(dev):
+        return torch.empty(need, dtype=torch.uint8, device=where)
+    with torch.cuda.stream(torch.cuda.ExternalStream(st, device=where)):
+        return torch.empty(need, dtype=torch.uint8, device=where)
+
+
+def _run(fn, what: str, dev: int, *args) -> None:
+    if dev == torch.cuda.current_device():
+        status = fn(*args)
+    else:
         with torch.cuda.device(dev):
-            return _call(what, tensors, ws, ws_bytes, stream, f)
-    st = _stream(stream)
-    if ws is None and ws_bytes:
-        if stream is None or st == torch.cuda.current_stream().cuda_stream:
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(st, device=dev)):
-                ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    _check(f(_ptr(ws), 0 if ws is None else ws.numel(), st), what)
-
-
-def _optional(t: Optional[torch.Tensor], dtype, shape, name) -> None:
-    if t is not None:
-        _req(t, dtype, shape, name)
+            status = fn(*args)
+    if status:
+        _check(status, what)
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor],
@@ -776,15 +799,12 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Option
     1 / sqrt(var + eps); x and y float32 or bfloat16 each, weight and bias
     float32 or None; mean and rstd [T] are what layer_norm_bwd takes."""
     T, d = x.shape
-    xt, yt = _elem(x, "x"), _elem(y, "y")
-    _req(y, y.dtype, (T, d), "y")
-    _optional(weight, torch.float32, (d,), "weight")
-    _optional(bias, torch.float32, (d,), "bias")
-    _optional(mean, torch.float32, (T,), "mean")
-    _optional(rstd, torch.float32, (T,), "rstd")
-    _call("layer_norm_fwd", (x, weight, bias, y, mean, rstd), None, 0, stream,
-          lambda ws, n, st: load().layer_norm_fwd(_ptr(x), xt, _ptr(weight), _ptr(bias), T, d, eps,
-                                                  _ptr(y), yt, _ptr(mean), _ptr(rstd), st))
+    xt, yt, dev = _elem(x, "x"), _elem(y, "y"), _device(x, "x")
+    f32 = torch.float32
+    _run(load().layer_norm_fwd, "layer_norm_fwd", dev, _arg(x, x.dtype, (T, d), dev, "x"), xt,
+         _arg(weight, f32, (d,), dev, "weight"), _arg(bias, f32, (d,), dev, "bias"), T, d, eps,
+         _arg(y, y.dtype, (T, d), dev, "y"), yt, _arg(mean, f32, (T,), dev, "mean"),
+         _arg(rstd, f32, (T,), dev, "rstd"), _stream_of(dev, stream))
 
 
 def layer_norm_bwd_workspace_bytes(T: int, d: int) -> int:
@@ -798,19 +818,20 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Ten
     """The gradients of layer_norm_fwd: dx (dy's type; may be dy, or None), and
     the sums over rows dweight and dbias (float32, each may be None)."""
     T, d = x.shape
-    gt, xt = _elem(dy, "dy"), _elem(x, "x")
-    _req(dy, dy.dtype, (T, d), "dy")
-    _optional(weight, torch.float32, (d,), "weight")
-    _req(mean, torch.float32, (T,), "mean")
-    _req(rstd, torch.float32, (T,), "rstd")
-    _optional(dx, dy.dtype, (T, d), "dx")
-    _optional(dweight, torch.float32, (d,), "dweight")
-    _optional(dbias, torch.float32, (d,), "dbias")
-    need = 0 if dweight is None and dbias is None else layer_norm_bwd_workspace_bytes(T, d)
-    _call("layer_norm_bwd", (dy, x, weight, mean, rstd, dx, dweight, dbias), ws, need, stream,
-          lambda w, n, st: load().layer_norm_bwd(_ptr(dy), gt, _ptr(x), xt, _ptr(weight),
-                                                 _ptr(mean), _ptr(rstd), T, d, _ptr(dx),
-                                                 _ptr(dweight), _ptr(dbias), w, n, st))
+    gt, xt, dev = _elem(dy, "dy"), _elem(x, "x"), _device(x, "x")
+    f32, lib, st = torch.float32, load(), _stream_of(dev, stream)
+    args = (_arg(dy, dy.dtype, (T, d), dev, "dy"), gt, _arg(x, x.dtype, (T, d), dev, "x"), xt,
+            _arg(weight, f32, (d,), dev, "weight"), _arg(mean, f32, (T,), dev, "mean"),
+            _arg(rstd, f32, (T,), dev, "rstd"), T, d, _arg(dx, dy.dtype, (T, d), dev, "dx"),
+            _arg(dweight, f32, (d,), dev, "dweight"), _arg(dbias, f32, (d,), dev, "dbias"))
+    need = (0 if dweight is None and dbias is None
+            else lib.layer_norm_bwd_workspace_bytes(T, d))
+    w = _scratch(ws, need, dev, stream, st)
+    _run(lib.layer_norm_bwd, "layer_norm_bwd", dev, *args, *_span(w), st)
+
+
+def _span(ws: Optional[torch.Tensor]):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
 
 
 def melded_linear_fwd_act(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tensor,
@@ -823,19 +844,14 @@ def melded_linear_fwd_act(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tensor,
     float32; residual may be y; z (None: not kept) is what linear_act_bwd takes."""
     T, d_in = xq.shape
     d_out = wq.shape[0]
-    t, a = _elem(y, "y"), _act(act)
-    _req(xq, torch.uint8, (T, d_in), "xq")
-    _req(wq, torch.uint8, (d_out, d_in), "wq")
-    _req(s_x, torch.float32, (1,), "s_x")
-    _req(s_w, torch.float32, (1,), "s_w")
-    _req(y, y.dtype, (T, d_out), "y")
-    _optional(bias, torch.float32, (d_out,), "bias")
-    _optional(residual, y.dtype, (T, d_out), "residual")
-    _optional(z, y.dtype, (T, d_out), "z")
-    _call("melded_linear_fwd_act", (xq, s_x, wq, s_w, y, bias, residual, z), None, 0, stream,
-          lambda ws, n, st: load().melded_linear_fwd_act(
-              _ptr(xq), _ptr(s_x), _ptr(wq), _ptr(s_w), _ptr(bias), a, _ptr(residual), T, d_in,
-              d_out, t, _ptr(y), _ptr(z), st))
+    t, a, dev = _elem(y, "y"), _act(act), _device(xq, "xq")
+    u8, f32, out = torch.uint8, torch.float32, (T, d_out)
+    _run(load().melded_linear_fwd_act, "melded_linear_fwd_act", dev,
+         _arg(xq, u8, (T, d_in), dev, "xq"), _arg(s_x, f32, (1,), dev, "s_x"),
+         _arg(wq, u8, (d_out, d_in), dev, "wq"), _arg(s_w, f32, (1,), dev, "s_w"),
+         _arg(bias, f32, (d_out,), dev, "bias"), a, _arg(residual, y.dtype, out, dev, "residual"),
+         T, d_in, d_out, t, _arg(y, y.dtype, out, dev, "y"), _arg(z, y.dtype, out, dev, "z"),
+         _stream_of(dev, stream))
 
 
 def linear_act_bwd_workspace_bytes(T: int, d_out: int) -> int:
@@ -852,38 +868,50 @@ def linear_act_bwd(dy: torch.Tensor, z: Optional[torch.Tensor], dz: torch.Tensor
     if z is None and a != 0:
         raise FalqError(f"linear_act_bwd: z is needed for act {act!r}")
     zt = 0 if z is None else _elem(z, "z")
-    if z is not None:
-        _req(z, z.dtype, (T, d_out), "z")
-    _req(dz, dy.dtype, (T, d_out), "dz")
-    _optional(dbias, torch.float32, (d_out,), "dbias")
-    need = 0 if dbias is None else linear_act_bwd_workspace_bytes(T, d_out)
-    _call("linear_act_bwd", (dy, z, dz, dbias), ws, need, stream,
-          lambda w, n, st: load().linear_act_bwd(_ptr(dy), gt, _ptr(z), zt, a, T, d_out, _ptr(dz),
-                                                 _ptr(dbias), w, n, st))
+    dev, lib = _device(dy, "dy"), load()
+    st = _stream_of(dev, stream)
+    args = (_arg(dy, dy.dtype, (T, d_out), dev, "dy"), gt,
+            None if z is None else _arg(z, z.dtype, (T, d_out), dev, "z"), zt, a, T, d_out,
+            _arg(dz, dy.dtype, (T, d_out), dev, "dz"),
+            _arg(dbias, torch.float32, (d_out,), dev, "dbias"))
+    need = 0 if dbias is None else lib.linear_act_bwd_workspace_bytes(T, d_out)
+    w = _scratch(ws, need, dev, stream, st)
+    _run(lib.linear_act_bwd, "linear_act_bwd", dev, *args, *_span(w), st)
 
 
 def grad_norm_workspace_bytes(count: int) -> int:
     return int(load().grad_norm_workspace_bytes(count))
 
 
-def _tensor_list(what: str, tensors):
-    """Host arrays of addresses, element counts and types."""
-    n = len(tensors)
-    if not all(t.is_cuda and t.is_contiguous() and t.dtype in _ELEM for t in tensors):
-        raise FalqError(f"{what}: tensors must be contiguous float32 or bfloat16 on the GPU")
-    return ((_c_p * n)(*[t.data_ptr() for t in tensors]),
-            (_i64 * n)(*[t.numel() for t in tensors]),
-            (ctypes.c_int32 * n)(*[_ELEM[t.dtype] for t in tensors]))
+def _addresses(what: str, tensors, dev: int) -> array:
+    """Host array of the tensors' addresses, all contiguous on device dev."""
+    for t in tensors:
+        if t.get_device() != dev or not t.is_contiguous():
+            raise FalqError(f"{what}: every tensor must be contiguous and on cuda:{dev}")
+    return array("q", [t.data_ptr() for t in tensors])
+
+
+def _sizes_types(what: str, tensors):
+    try:
+        kinds = array("i", [_ELEM[t.dtype] for t in tensors])
+    except KeyError as e:
+        raise FalqError(f"{what}: expected float32 or bfloat16, got {e.args[0]}") from None
+    return array("q", [t.numel() for t in tensors]), kinds
+
+
+def _at(a: array) -> int:
+    return a.buffer_info()[0]
 
 
 def grad_norm(grads, norm: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """norm = sqrt of the sum of squares over all elements of all tensors
     (float32 and bfloat16, any shapes), summed in float64 on the device."""
-    grads = list(grads)
-    _req(norm, torch.float32, (1,), "norm")
-    p, n, t = _tensor_list("grad_norm", grads)
-    _call("grad_norm", (norm, *grads), ws, grad_norm_workspace_bytes(len(grads)), stream,
-          lambda w, nb, st: load().grad_norm(len(grads), p, n, t, _ptr(norm), w, nb, st))
+    grads, dev, lib = list(grads), _device(norm, "norm"), load()
+    st, count = _stream_of(dev, stream), len(grads)
+    p, (n, t) = _addresses("grad_norm", grads, dev), _sizes_types("grad_norm", grads)
+    out = _arg(norm, torch.float32, (1,), dev, "norm")
+    w = _scratch(ws, lib.grad_norm_workspace_bytes(count), dev, stream, st)
+    _run(lib.grad_norm, "grad_norm", dev, count, _at(p), _at(n), _at(t), out, *_span(w), st)
 
 
 def grad_clip(grads, max_norm: float, norm: torch.Tensor, out=None, eps: float = 1e-6,
@@ -891,21 +919,21 @@ def grad_clip(grads, max_norm: float, norm: torch.Tensor, out=None, eps: float =
     """Multiply every tensor by min(1, max_norm / (norm + eps)), norm being the
     global norm over all of them (written to `norm` as grad_norm does): in
     place, or into the tensors `out`.  No tensor may be listed twice."""
-    grads = list(grads)
-    _req(norm, torch.float32, (1,), "norm")
-    p, n, t = _tensor_list("grad_clip", grads)
-    q, outs = None, ()
+    grads, dev, lib = list(grads), _device(norm, "norm"), load()
+    st, count = _stream_of(dev, stream), len(grads)
+    p, (n, t) = _addresses("grad_clip", grads, dev), _sizes_types("grad_clip", grads)
+    q = None
     if out is not None:
-        outs = list(out)
-        if len(outs) != len(grads):
-            raise FalqError(f"grad_clip: {len(outs)} outputs for {len(grads)} tensors")
-        for g, o in zip(grads, outs):
-            if o.dtype != g.dtype or o.shape != g.shape:
-                raise FalqError("grad_clip: out must have the tensors' types and shapes")
-        q = _tensor_list("grad_clip", outs)[0]
-    _call("grad_clip", (norm, *grads, *outs), ws, grad_norm_workspace_bytes(len(grads)), stream,
-          lambda w, nb, st: load().grad_clip(len(grads), p, n, t, max_norm, eps, q, _ptr(norm), w,
-                                             nb, st))
+        out = list(out)
+        if len(out) != count:
+            raise FalqError(f"grad_clip: {len(out)} outputs for {count} tensors")
+        q = _addresses("grad_clip", out, dev)
+        if _sizes_types("grad_clip", out) != (n, t):
+            raise FalqError("grad_clip: out must have the tensors' types and sizes")
+    norm_at = _arg(norm, torch.float32, (1,), dev, "norm")
+    w = _scratch(ws, lib.grad_norm_workspace_bytes(count), dev, stream, st)
+    _run(lib.grad_clip, "grad_clip", dev, count, _at(p), _at(n), _at(t), max_norm, eps,
+         None if q is None else _at(q), norm_at, *_span(w), st)
 
 
 from .step import MeldedLinear  # noqa: E402  (buffers + the step's call sequence)

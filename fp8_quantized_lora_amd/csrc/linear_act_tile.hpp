@@ -1,0 +1,214 @@
+// The FP8 product with an epilogue in tiles: see linear_act.hip.
+#pragma once
+
+#include "linear_act_few.hpp"
+
+namespace falq {
+namespace {
+
+template <int BM_, int BN_, int WGM_, int WGN_, int S_ = 2>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, BK = 128, S = S_;
+  static constexpr int NW = WGM * WGN, kThreads = NW * 64;
+  static constexpr int WTM = BM / WGM, WTN = BN / WGN, MB = WTM / 16, NB = WTN / 16;
+  static constexpr int STAGE = (BM + BN) * BK;
+  static constexpr int AI = BM / 8 / NW, BI = BN / 8 / NW;   // 1 KB loads per wave and stage
+  static constexpr int LPS = AI + BI;
+  // the epilogue: rows of a wave's sub-tile per pass through its LDS
+  static constexpr int pass_of(int p) { return p * WTN * 4 * NW <= S * STAGE ? p : pass_of(p / 2); }
+  static constexpr int PASS = pass_of(WTM);
+  static_assert(AI * 8 * NW == BM && BI * 8 * NW == BN, "whole loads");
+  static_assert(S * STAGE <= 160 * 1024, "LDS");
+  static_assert(PASS % 16 == 0 && WTM % PASS == 0, "whole blocks per pass");
+};
+
+// waits until at most N vector-memory instructions of the wave are in flight
+template <int N>
+__device__ __forceinline__ void wait_vmem_at_most() {
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+// at most ahead * LPS, ahead <= A
+template <int A, int LPS>
+__device__ __forceinline__ void wait_stages(int ahead) {
+  if constexpr (A == 0) {
+    wait_vmem_at_most<0>();
+  } else {
+    if (ahead >= A)
+      wait_vmem_at_most<A * LPS>();
+    else
+      wait_stages<A - 1, LPS>(ahead);
+  }
+}
+
+template <class C, class OT>
+__global__ __launch_bounds__(C::kThreads) void linear_act_tile(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int n_first,
+    int tilesM, int tilesN, Epilogue ep) {
+  constexpr int BK = C::BK, MB = C::MB, NB = C::NB;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::S * C::STAGE];
+  int tm, tn;
+  gemm::tile_of(gemm::xcd_remap(blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
+  const int m0 = tm * C::BM, n0 = n_first + tn * C::BN;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w / C::WGN, wn = w % C::WGN;
+  // the step at nk, if any, is the one of rem bytes
+  const int nk = K / BK, rem = K % BK, steps = nk + (rem > 0);
+
+  v4f acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.0f;
+
+  // per-lane source of each direct load: a row (clamped into the matrix) and
+  // the swizzled chunk
+  const int lrow = lane >> 3, lslot = lane & 7;
+  const uint8_t* gA[C::AI];
+  const uint8_t* gB[C::BI];
+#pragma unroll
+  for (int j = 0; j < C::AI; ++j) {
+    const int row = (w * C::AI + j) * 8 + lrow;
+    gA[j] = A + (int64_t)min(m0 + row, M - 1) * K + ((lslot ^ gemm::dma::swz(row)) * 16);
+  }
+#pragma unroll
+  for (int j = 0; j < C::BI; ++j) {
+    const int row = (w * C::BI + j) * 8 + lrow;
+    gB[j] = B + (int64_t)min(n0 + row, N - 1) * K + ((lslot ^ gemm::dma::swz(row)) * 16);
+  }
+  auto issue = [&](int stage, int k0) {
+    const uint32_t base = lds_offset(smem + stage * C::STAGE);
+    const uint32_t la = __builtin_amdgcn_readfirstlane(base + w * C::AI * 1024);
+    const uint32_t lb = __builtin_amdgcn_readfirstlane(base + C::BM * BK + w * C::BI * 1024);
+#pragma unroll
+    for (int j = 0; j < C::AI; ++j) load16_to_lds(gA[j] + k0, la + j * 1024);
+#pragma unroll
+    for (int j = 0; j < C::BI; ++j) load16_to_lds(gB[j] + k0, lb + j * 1024);
+  };
+  // the step of fewer than BK bytes: chunks past K load the row's last chunk
+  auto issue_rem = [&](int stage) {
+    const uint32_t base = lds_offset(smem + stage * C::STAGE);
+    const uint32_t la = __builtin_amdgcn_readfirstlane(base + w * C::AI * 1024);
+    const uint32_t lb = __builtin_amdgcn_readfirstlane(base + C::BM * BK + w * C::BI * 1024);
+#pragma unroll
+    for (int j = 0; j < C::AI; ++j) {
+      const int co = (lslot ^ gemm::dma::swz((w * C::AI + j) * 8 + lrow)) * 16;
+      load16_to_lds(gA[j] + nk * BK - max(0, co - (rem - 16)), la + j * 1024);
+    }
+#pragma unroll
+    for (int j = 0; j < C::BI; ++j) {
+      const int co = (lslot ^ gemm::dma::swz((w * C::BI + j) * 8 + lrow)) * 16;
+      load16_to_lds(gB[j] + nk * BK - max(0, co - (rem - 16)), lb + j * 1024);
+    }
+  };
+  auto fetch = [&](int kt) {
+    const int stage = kt % C::S;
+    if (kt < nk)
+      issue(stage, kt * BK);
+    else
+      issue_rem(stage);
+  };
+#pragma unroll
+  for (int s = 0; s < C::S - 1; ++s)
+    if (s < steps) fetch(s);
+
+  const int r16 = lane & 15, g = lane >> 4;
+  const int sw = gemm::dma::swz(r16);
+  const int o0 = ((2 * g) ^ sw) * 16, o1 = ((2 * g + 1) ^ sw) * 16;
+  const int offA = (wm * C::WTM + r16) * BK, offB = C::BM * BK + (wn * C::WTN + r16) * BK;
+  auto frag = [&](const uint8_t* p) {
+    return gemm::join(*reinterpret_cast<const uint4*>(p + o0),
+                      *reinterpret_cast<const uint4*>(p + o1));
+  };
+  const float scale = 1.0f / (ep.sa[0] * ep.sb[0]);
+  // fragment reads in the order the MFMAs consume them; next(): the loads of
+  // the following stage, sent once the first fragments are in registers
+  auto step = [&](const uint8_t* st, auto&& next) {
+    v8i bf[NB], af[2];
+    af[0] = frag(st + offA);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      bf[j] = frag(st + offB + j * 16 * BK);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      if (i + 1 < MB) af[(i + 1) & 1] = frag(st + offA + (i + 1) * 16 * BK);
+      __builtin_amdgcn_sched_barrier(0);
+      // D = B A^T per block: a lane ends with four columns of one row
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 1], acc[i][j],
+                                                                     0, 0, 0, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i == 0) next();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  __builtin_amdgcn_s_waitcnt(0xC07F);                        // lgkmcnt(0)
+  for (int kt = 0; kt < nk; ++kt) {
+    wait_stages<C::S - 2, C::LPS>(steps - 1 - kt);
+    barrier_no_drain();
+    step(smem + kt % C::S * C::STAGE, [&] {
+      if (kt + C::S - 1 < steps) fetch(kt + C::S - 1);
+    });
+  }
+  if (rem) {
+    uint8_t* st = smem + nk % C::S * C::STAGE;
+    wait_vmem(0);
+    barrier_no_drain();
+    const int valid = rem / 16;                              // chunks of K in the step
+    for (int i = tid; i < (C::BM + C::BN) * 8; i += C::kThreads) {
+      const int row = i >> 3, c = i & 7;                     // BM is a multiple of 16
+      if (c >= valid)
+        *reinterpret_cast<uint4*>(st + row * BK + ((c ^ gemm::dma::swz(row & 15)) * 16)) =
+            make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    step(st, [] {});
+  }
+  __syncthreads();                                           // the stages are free
+
+  constexpr int CH = C::WTN / 4, LPR = C::WTN / 8, RPI = 64 / LPR;
+  v4f* mine = reinterpret_cast<v4f*>(smem + w * (C::S * C::STAGE / C::NW));
+  const int cl = lane % LPR, rl = lane / LPR;
+  const int col = n0 + wn * C::WTN + cl * 8;
+  const bool col_ok = col < N;                               // N is a multiple of 16
+  float bias[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
+  if (ep.bias && col_ok) load_elems<8>(ep.bias + col, bias);
+  auto rows = [&](auto act, int first) {
+    for (int r = rl; r < C::PASS; r += RPI) {
+      const int row = m0 + wm * C::WTM + first + r;
+      const v4f a = mine[r * CH + ((2 * cl) ^ (r & (CH - 1)))];
+      const v4f b = mine[r * CH + ((2 * cl + 1) ^ (r & (CH - 1)))];
+      if (!col_ok || row >= M) continue;
+      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      finish8<decltype(act)::value, OT>(v, scale, bias, ep, (int64_t)row * N + col);
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < C::WTM / C::PASS; ++p) {
+    // the wave's own LDS: its accesses are executed in order
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < C::PASS / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        mine[(i * 16 + r16) * CH + ((4 * j + g) ^ ((i * 16 + r16) & (CH - 1)))] =
+            acc[p * (C::PASS / 16) + i][j];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int first = p * C::PASS;
+    switch (ep.act) {
+      case kRelu: rows(std::integral_constant<int, kRelu>{}, first); break;
+      case kGelu: rows(std::integral_constant<int, kGelu>{}, first); break;
+      case kGeluTanh: rows(std::integral_constant<int, kGeluTanh>{}, first); break;
+      case kSilu: rows(std::integral_constant<int, kSilu>{}, first); break;
+      default: rows(std::integral_constant<int, kNone>{}, first); break;
+    }
+  }
+}
+
+}  // namespace
+}  // namespace falq

@@ -56,7 +56,7 @@ def test_linear_act_fwd():
     # more 256 x 256 tiles than a 32-bit grid holds
     assert f(P, P, Q, P, None, 0, None, 1 << 30, 32, 1 << 30, 1, R, None, None) == EINVAL
     assert f(None, P, Q, P, None, 0, None, 0, 32, 48, 1, None, None, None) == OK     # T = 0
-    assert f(None, P, None, P, None, 0, None, 4, 32, 0, 1, None, None, None) == OK   # d_out = 0
+    assert f(P, P, None, P, None, 0, None, 4, 32, 0, 1, None, None, None) == OK      # d_out = 0
 
 
 def test_linear_act_bwd():
