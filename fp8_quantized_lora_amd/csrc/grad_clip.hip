@@ -6,12 +6,18 @@
 // sums; the conversion and the fused multiply-add are far below the memory
 // time), in an order that the sizes fix.
 //
-// The tensors' addresses travel in the kernel arguments, kTable of them per
-// launch, so a captured graph holds them and nothing is copied to the device.
-// Work is dealt in chunks of kChunk elements, counted from each tensor's
-// address rounded down to 16 bytes: the 16-byte accesses then fit a tensor
-// that starts at any element, and only its first and last vectors are done
-// element by element.
+// The tensors' addresses travel in kernel arguments, so a captured graph holds
+// them and nothing is copied from the host: up to kTable tensors directly, more
+// of them through the workspace, written there by one small launch for each
+// kTable tensors, so that the passes over the gradients stay single launches.
+//
+// Work is counted in chunks of 256 threads x 16 bytes from each tensor's
+// address rounded down to 16 bytes: the 16-byte accesses then fit a tensor that
+// starts at any element, and only vectors across its ends are done element by
+// element.  A workgroup takes one run of consecutive chunks (the tensor is
+// looked up once) and has eight chunks' loads in flight.  Both passes take the
+// same runs, the second from the end back: what the first one read last is the
+// likeliest to be in the last-level cache still.
 #include "elem.hpp"
 #include "kernels.hpp"
 
@@ -20,63 +26,107 @@
 namespace falq {
 namespace {
 
-constexpr int kTable = 112;                    // 112 * 32 + 8 bytes of kernel arguments
-constexpr int kChunk = 8192, kThreads = 256, kMaxBlocks = 1024;
+constexpr int kTable = 112, kThreads = 256, kAhead = 8;
+// elements of a vector and of a chunk
+template <class GT>
+constexpr int kVec = 16 / sizeof(GT);
+template <class GT>
+constexpr int kChunk = kThreads * kVec<GT>;
+constexpr int kMaxBlocks = 2048;               // eight workgroups per CU
 
-struct Table {
-  const void* g[kTable];
-  void* out[kTable];
-  int64_t n[kTable];
-  uint32_t first[kTable];                      // the tensor's first chunk
-  uint32_t bf16[(kTable + 31) / 32];           // its type
+struct Entry {
+  const void* g;
+  void* out;
+  int64_t n;
+  uint32_t first;                              // the tensor's first chunk
+  int32_t bf16;
+};
+struct Table {                                 // in the kernel arguments
+  Entry e[kTable];
   int count;
   uint32_t chunks;
 };
-static_assert(sizeof(Table) <= 3800, "kernel arguments");
+static_assert(sizeof(Table) <= 3600, "kernel arguments");
+struct TableInMemory {
+  const Entry* e;
+  int count;
+  uint32_t chunks;
+};
+
+__global__ __launch_bounds__(128) void write_table_kernel(Table t, Entry* __restrict__ to) {
+  if ((int)threadIdx.x < t.count) to[threadIdx.x] = t.e[threadIdx.x];
+}
 
 template <class GT>
 __device__ __forceinline__ int lead_of(const GT* g) {
   return (int)((reinterpret_cast<uintptr_t>(g) % 16) / sizeof(GT));
 }
 
-// f(i, v): vectors of 8 elements from element i on (all inside); f1(i): one element
-template <class GT, class F, class F1>
-__device__ __forceinline__ void each(const GT* g, int64_t n, uint32_t chunk, F&& f, F1&& f1) {
-  const int lead = lead_of(g);
-  const int64_t base = (int64_t)chunk * kChunk - lead;
-#pragma unroll 4
-  for (int k = 0; k < kChunk / (kThreads * 8); ++k) {
-    const int64_t i = base + (k * kThreads + (int)threadIdx.x) * 8;
-    if (i >= 0 && i + 8 <= n) {
-      f(i);
-    } else if (i + 8 > 0 && i < n) {
-      for (int64_t j = i < 0 ? 0 : i; j < (i + 8 < n ? i + 8 : n); ++j) f1(j);
+// The thread's vectors of chunks [a, b) of a tensor, last to first: many(i) has
+// kAhead whole vectors at elements i, i + kChunk, ...; one(i) a whole vector;
+// each(i) one element of a vector across an end.
+template <class GT, class Many, class One, class Each>
+__device__ __forceinline__ void run_of(const GT* g, int64_t n, int64_t a, int64_t b, Many&& many,
+                                       One&& one, Each&& each) {
+  const int64_t lead = lead_of(g), mine = (int64_t)threadIdx.x * kVec<GT> - lead;
+  while (b > a) {
+    if (b - a >= kAhead && (b - kAhead) * kChunk<GT> >= lead && b * kChunk<GT> - lead <= n) {
+      b -= kAhead;
+      many(b * kChunk<GT> + mine);
+      continue;
+    }
+    --b;
+    const int64_t i = b * kChunk<GT> + mine;
+    if (i >= 0 && i + kVec<GT> <= n) {
+      one(i);
+    } else if (i + kVec<GT> > 0 && i < n) {
+      for (int64_t j = i < 0 ? 0 : i; j < (i + kVec<GT> < n ? i + kVec<GT> : n); ++j) each(j);
     }
   }
 }
 
-__device__ __forceinline__ int tensor_of(const Table& t, uint32_t chunk) {
-  int lo = 0, hi = t.count - 1;                // the last tensor whose first chunk is <= chunk
+// f(entry, a, b) for the workgroup's run of chunks, tensor by tensor, last to
+// first
+template <class Tab, class F>
+__device__ __forceinline__ void walk(const Tab& t, F&& f) {
+  const uint32_t c0 = (uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x);
+  uint32_t c1 = (uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x);
+  if (c0 == c1) return;
+  int lo = 0, hi = t.count - 1;                // the tensor of chunk c1 - 1
   while (lo < hi) {
     const int m = (lo + hi + 1) / 2;
-    if (t.first[m] <= chunk)
+    if (t.e[m].first < c1)
       lo = m;
     else
       hi = m - 1;
   }
-  return lo;
+  for (; c1 > c0; --lo) {
+    const uint32_t first = t.e[lo].first, from = first > c0 ? first : c0;
+    f(t.e[lo], (int64_t)(from - first), (int64_t)(c1 - first));
+    c1 = from;
+  }
 }
 
 template <class GT>
-__device__ __forceinline__ double chunk_squares(const GT* g, int64_t n, uint32_t chunk) {
+__device__ __forceinline__ double squares(const GT* g, int64_t n, int64_t a, int64_t b) {
   double s = 0.0;
-  each(
-      g, n, chunk,
-      [&](int64_t i) {
-        float v[8];
-        load_elems<8>(g + i, v);
+  auto add = [&](const Raw<GT, kVec<GT>>& v) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fma((double)v[e], (double)v[e], s);
+    for (int e = 0; e < kVec<GT>; ++e) s = fma((double)v[e], (double)v[e], s);
+  };
+  run_of(
+      g, n, a, b,
+      [&](int64_t i) {
+        Raw<GT, kVec<GT>> v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) v[k].load(g + i + k * kChunk<GT>);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) add(v[k]);
+      },
+      [&](int64_t i) {
+        Raw<GT, kVec<GT>> v;
+        v.load(g + i);
+        add(v);
       },
       [&](int64_t i) { s = fma((double)(float)g[i], (double)(float)g[i], s); });
   return s;
@@ -89,143 +139,147 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 }
 
 // sum over the workgroup, in every thread
-template <int NT>
 __device__ __forceinline__ double block_sum_f64(double v) {
-  __shared__ double red[NT / 64];
+  __shared__ double red[kThreads / 64];
   v = wave_sum_f64(v);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   v = 0.0;
 #pragma unroll
-  for (int i = 0; i < NT / 64; ++i) v += red[i];
+  for (int i = 0; i < kThreads / 64; ++i) v += red[i];
   return v;
 }
 
-__global__ __launch_bounds__(kThreads) void squares_kernel(Table t, double* __restrict__ part) {
+template <class Tab>
+__global__ __launch_bounds__(kThreads) void squares_kernel(Tab t, double* __restrict__ part) {
   double s = 0.0;
-  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const int k = tensor_of(t, c);
-    const uint32_t in = c - t.first[k];
-    if ((t.bf16[k / 32] >> (k % 32)) & 1)
-      s += chunk_squares((const __bf16*)t.g[k], t.n[k], in);
-    else
-      s += chunk_squares((const float*)t.g[k], t.n[k], in);
-  }
-  s = block_sum_f64<kThreads>(s);
+  walk(t, [&](const Entry& e, int64_t a, int64_t b) {
+    s += e.bf16 ? squares((const __bf16*)e.g, e.n, a, b) : squares((const float*)e.g, e.n, a, b);
+  });
+  s = block_sum_f64(s);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-// norm (and the coefficient) from the partial sums, in one workgroup
-__global__ __launch_bounds__(kThreads) void norm_kernel(const double* __restrict__ part, int P,
-                                                        float max_norm, float eps,
-                                                        float* __restrict__ norm,
-                                                        float* __restrict__ coef) {
+// the norm from the partial sums, the same in every thread of every workgroup
+__device__ __forceinline__ double norm_of(const double* __restrict__ part, int P) {
   double s = 0.0;
   for (int i = threadIdx.x; i < P; i += kThreads) s += part[i];
-  const double r = sqrt(block_sum_f64<kThreads>(s));
-  if (threadIdx.x == 0) {
-    if (norm) *norm = (float)r;
-    if (coef) {
-      const float c = (float)((double)max_norm / (r + (double)eps));
-      *coef = c > 1.0f ? 1.0f : c;             // NaN stays NaN
-    }
-  }
+  return sqrt(block_sum_f64(s));
 }
 
-template <class GT>
-__device__ __forceinline__ void chunk_scale(const GT* g, GT* o, int64_t n, uint32_t chunk,
-                                            float c) {
+__global__ __launch_bounds__(kThreads) void norm_kernel(const double* __restrict__ part, int P,
+                                                        float* __restrict__ norm) {
+  const double r = norm_of(part, P);
+  if (threadIdx.x == 0) *norm = (float)r;
+}
+
+template <bool STREAM, class GT>
+__device__ __forceinline__ void scale(const GT* g, GT* o, int64_t n, int64_t a, int64_t b,
+                                      float c) {
   // the vector form needs the output at the input's place within 16 bytes
   const bool same = lead_of(g) == lead_of(o);
-  each(
-      g, n, chunk,
+  auto put = [&](int64_t i, const Raw<GT, kVec<GT>>& r) {
+    float v[kVec<GT>];
+#pragma unroll
+    for (int e = 0; e < kVec<GT>; ++e) v[e] = r[e] * c;
+    if (same) {
+      store_elems<kVec<GT>, STREAM>(o + i, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec<GT>; ++e) o[i + e] = (GT)v[e];
+    }
+  };
+  run_of(
+      g, n, a, b,
       [&](int64_t i) {
-        float v[8];
-        load_elems<8>(g + i, v);
+        Raw<GT, kVec<GT>> v[kAhead];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= c;
-        if (same) {
-          store_elems<8>(o + i, v);
-        } else {
+        for (int k = 0; k < kAhead; ++k) v[k].template load<STREAM>(g + i + k * kChunk<GT>);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[i + e] = (GT)v[e];
-        }
+        for (int k = 0; k < kAhead; ++k) put(i + k * kChunk<GT>, v[k]);
+      },
+      [&](int64_t i) {
+        Raw<GT, kVec<GT>> v;
+        v.template load<STREAM>(g + i);
+        put(i, v);
       },
       [&](int64_t i) { o[i] = (GT)((float)g[i] * c); });
 }
 
-__global__ __launch_bounds__(kThreads) void scale_kernel(Table t, const float* __restrict__ coef) {
-  const float c = *coef;
-  for (uint32_t b = blockIdx.x; b < t.chunks; b += gridDim.x) {
-    const int k = tensor_of(t, b);
-    if (c == 1.0f && t.g[k] == t.out[k]) continue;           // in place and not clipped
-    const uint32_t in = b - t.first[k];
-    if ((t.bf16[k / 32] >> (k % 32)) & 1)
-      chunk_scale((const __bf16*)t.g[k], (__bf16*)t.out[k], t.n[k], in, c);
+// Every workgroup forms the coefficient from the P partial sums (at most 16 KB
+// from the caches; a launch between the passes would cost more), and workgroup
+// 0 writes the norm.
+template <class Tab, bool STREAM>
+__global__ __launch_bounds__(kThreads) void scale_kernel(Tab t, const double* __restrict__ part,
+                                                         int P, float max_norm, float eps,
+                                                         float* __restrict__ norm) {
+  const double r = norm_of(part, P);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)r;
+  float c = (float)((double)max_norm / (r + (double)eps));
+  c = c > 1.0f ? 1.0f : c;                     // NaN stays NaN
+  walk(t, [&](const Entry& e, int64_t a, int64_t b) {
+    if (c == 1.0f && e.g == e.out) return;     // in place and not clipped
+    if (e.bf16)
+      scale<STREAM>((const __bf16*)e.g, (__bf16*)e.out, e.n, a, b, c);
     else
-      chunk_scale((const float*)t.g[k], (float*)t.out[k], t.n[k], in, c);
-  }
+      scale<STREAM>((const float*)e.g, (float*)e.out, e.n, a, b, c);
+  });
 }
 
-// calls f(table, blocks) for each table of tensors; empty tensors are left out
-// (the entry bounds the elements of all tensors, so the chunks fit 32 bits)
-template <class F>
-hipError_t each_table(int64_t count, const void* const* g, const int64_t* n, const int32_t* dtype,
-                      void* const* out, F&& f) {
-  int64_t i = 0;
-  while (i < count) {
-    Table t;
-    t.count = 0;
-    for (uint32_t& w : t.bf16) w = 0;
-    uint64_t chunks = 0;
-    for (; i < count && t.count < kTable; ++i) {
-      if (n[i] == 0) continue;
-      const int k = t.count;
-      const int size = dtype[i] ? 2 : 4;
-      const int64_t lead = (int64_t)(reinterpret_cast<uintptr_t>(g[i]) % 16) / size;
-      const uint64_t c = (uint64_t)((n[i] + lead + kChunk - 1) / kChunk);
-      t.g[k] = g[i];
-      t.out[k] = out ? out[i] : nullptr;
-      t.n[k] = n[i];
-      t.first[k] = (uint32_t)chunks;
-      if (dtype[i]) t.bf16[k / 32] |= 1u << (k % 32);
-      chunks += c;
-      ++t.count;
-    }
-    if (t.count == 0) break;
-    t.chunks = (uint32_t)chunks;
-    const hipError_t e = f(t, (int)std::min<uint64_t>(chunks, kMaxBlocks));
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+template <class Tab>
+hipError_t passes(const Tab& t, int64_t bytes, float max_norm, float eps, bool clip, float* norm,
+                  double* part, hipStream_t s) {
+  const int blocks = (int)std::min<uint32_t>(t.chunks, kMaxBlocks);
+  if (blocks) squares_kernel<Tab><<<blocks, kThreads, 0, s>>>(t, part);
+  if (blocks && clip && 2 * bytes > kStreamBytes)
+    scale_kernel<Tab, true><<<blocks, kThreads, 0, s>>>(t, part, blocks, max_norm, eps, norm);
+  else if (blocks && clip)
+    scale_kernel<Tab, false><<<blocks, kThreads, 0, s>>>(t, part, blocks, max_norm, eps, norm);
+  else
+    norm_kernel<<<1, kThreads, 0, s>>>(part, blocks, norm);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-// the coefficient, then kMaxBlocks partial sums per table
+// the partial sums, then the tensors' table where the kernel arguments do not hold it
 size_t grad_norm_ws_bytes(int64_t count) {
-  return 64 + (size_t)((count + kTable - 1) / kTable) * kMaxBlocks * 8;
+  return kMaxBlocks * 8 + (count > kTable ? (size_t)count * sizeof(Entry) : 0);
 }
 
 hipError_t launch_grad_norm(int64_t count, const void* const* g, const int64_t* n,
                             const int32_t* dtype, float max_norm, float eps, void* const* out,
                             float* norm, void* ws, hipStream_t s) {
-  float* coef = (float*)ws;
-  double* part = (double*)((uint8_t*)ws + 64);
-  int P = 0;
-  hipError_t e = each_table(count, g, n, dtype, out, [&](const Table& t, int blocks) {
-    squares_kernel<<<blocks, kThreads, 0, s>>>(t, part + P);
-    P += blocks;
+  double* part = (double*)ws;
+  Entry* table = (Entry*)((uint8_t*)ws + kMaxBlocks * 8);
+  Table t;
+  t.count = 0;
+  t.chunks = 0;
+  int64_t bytes = 0;
+  int written = 0;
+  auto flush = [&] {
+    write_table_kernel<<<1, 128, 0, s>>>(t, table + written);
+    written += t.count;
+    t.count = 0;
     return hipGetLastError();
-  });
+  };
+  for (int64_t i = 0; i < count; ++i) {
+    if (n[i] == 0) continue;                   // the entry bounds all elements: chunks fit 32 bits
+    if (t.count == kTable) {
+      const hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    const int64_t size = dtype[i] ? 2 : 4, chunk = kThreads * 16 / size;
+    const int64_t lead = (int64_t)(reinterpret_cast<uintptr_t>(g[i]) % 16) / size;
+    t.e[t.count++] = {g[i], out ? out[i] : nullptr, n[i], t.chunks, dtype[i]};
+    bytes += n[i] * size;
+    t.chunks += (uint32_t)((n[i] + lead + chunk - 1) / chunk);
+  }
+  if (!written) return passes(t, bytes, max_norm, eps, out != nullptr, norm, part, s);
+  const hipError_t e = flush();
   if (e != hipSuccess) return e;
-  norm_kernel<<<1, kThreads, 0, s>>>(part, P, max_norm, eps, norm, out ? coef : nullptr);
-  e = hipGetLastError();
-  if (e != hipSuccess || !out) return e;
-  return each_table(count, g, n, dtype, out, [&](const Table& t, int blocks) {
-    scale_kernel<<<std::min<int>(t.chunks, 4 * blocks), kThreads, 0, s>>>(t, coef);
-    return hipGetLastError();
-  });
+  return passes(TableInMemory{table, written, t.chunks}, bytes, max_norm, eps, out != nullptr,
+                norm, part, s);
 }
 
 }  // namespace falq

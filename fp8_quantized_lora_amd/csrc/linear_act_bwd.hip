@@ -13,10 +13,11 @@
 namespace falq {
 namespace {
 
-constexpr int kRows = 8, kLanes = 32;
+constexpr int kLanes = 32;
 
-template <class GT, class ZT, int E, int ACT>
-__global__ __launch_bounds__(256) void act_bwd_kernel(const GT* dy, const ZT* __restrict__ z,
+// part: the strips' sums, one row of d floats each (dbias itself with one strip)
+template <class GT, class ZT, int E, int ACT, int kRows, bool STREAM>
+__global__ __launch_bounds__(kRows * kLanes) void act_bwd_kernel(const GT* dy, const ZT* __restrict__ z,
                                                       GT* dz, float* __restrict__ part, int64_t T,
                                                       int64_t d, int64_t rows_per_strip) {
   __shared__ float sb[kRows][kLanes * E];
@@ -29,23 +30,26 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const GT* dy, const ZT* __
   if (col < d) {
 #pragma unroll 2
     for (int64_t r = r0 + rl; r < r1; r += kRows) {
-      float g[E], v[E];
-      load_elems<E>(dy + r * d + col, g);
-      if constexpr (ACT != kNone) {
-        load_elems<E>(z + r * d + col, v);
+      Raw<GT, E> gr;
+      Raw<ZT, E> v;
+      gr.template load<STREAM>(dy + r * d + col);
+      if constexpr (ACT != kNone) v.template load<STREAM>(z + r * d + col);
+      float g[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) g[e] *= act_slope<ACT>(v[e]);
+      for (int e = 0; e < E; ++e) {
+        g[e] = gr[e];
+        if constexpr (ACT != kNone) g[e] *= act_slope<ACT>(v[e]);
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) ab[e] += g[e];
-      store_elems<E>(dz + r * d + col, g);
+      store_elems<E, STREAM>(dz + r * d + col, g);
     }
   }
   if (!part) return;
 #pragma unroll
   for (int e = 0; e < E; ++e) sb[rl][cl * E + e] = ab[e];
   __syncthreads();
-  for (int i = threadIdx.x; i < kLanes * E; i += 256) {
+  for (int i = threadIdx.x; i < kLanes * E; i += kRows * kLanes) {
     const int64_t c = (int64_t)blockIdx.x * kLanes * E + i;
     if (c >= d) continue;
     float b = 0.0f;
@@ -58,23 +62,27 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const GT* dy, const ZT* __
 struct Strips {
   int64_t n, rows;
 };
+// Up to kShort rows one strip of 32 row lanes writes dbias itself: no second
+// launch and no workspace.
+constexpr int kShort = 256;
 Strips strips_of(int64_t T, int64_t d) {
-  const int64_t per = d % 8 == 0 ? kLanes * 8 : kLanes;
+  if (T <= kShort) return {1, T};
+  const int64_t per = d % 8 == 0 ? kLanes * 4 : kLanes;
   const int64_t cols = std::max<int64_t>(1, (d + per - 1) / per);
-  int64_t n = std::min<int64_t>((T + 2 * kRows - 1) / (2 * kRows), (4096 + cols - 1) / cols);
-  n = std::max<int64_t>(1, std::min<int64_t>(n, 1024));
+  const int64_t n = std::min<int64_t>({(T + 15) / 16, (4096 + cols - 1) / cols, 1024});
   const int64_t rows = (T + n - 1) / n;
-  return {rows ? (T + rows - 1) / rows : 0, rows};
+  return {(T + rows - 1) / rows, rows};
 }
 
-template <class GT, class ZT, int E>
+template <class GT, class ZT, int E, int kRows, bool STREAM>
 hipError_t by_act(const GT* dy, const ZT* z, int act, int64_t T, int64_t d, GT* dz, float* part,
                   hipStream_t s) {
   const Strips st = strips_of(T, d);
   const dim3 grid((unsigned)((d + kLanes * E - 1) / (kLanes * E)), (unsigned)st.n);
-#define FALQ_ACT(A)                                                                      \
-  case A:                                                                                \
-    act_bwd_kernel<GT, ZT, E, A><<<grid, 256, 0, s>>>(dy, z, dz, part, T, d, st.rows);   \
+#define FALQ_ACT(A)                                                                         \
+  case A:                                                                                   \
+    act_bwd_kernel<GT, ZT, E, A, kRows, STREAM>                                             \
+        <<<grid, kRows * kLanes, 0, s>>>(dy, z, dz, part, T, d, st.rows);                   \
     break;
   switch (act) {
     FALQ_ACT(kNone) FALQ_ACT(kRelu) FALQ_ACT(kGelu) FALQ_ACT(kGeluTanh) FALQ_ACT(kSilu)
@@ -84,17 +92,29 @@ hipError_t by_act(const GT* dy, const ZT* z, int act, int64_t T, int64_t d, GT* 
   return hipGetLastError();
 }
 
+template <class GT, class ZT, int E>
+hipError_t by_rows(const GT* dy, const ZT* z, int act, int64_t T, int64_t d, GT* dz, float* part,
+                   hipStream_t s) {
+  if (T <= kShort) return by_act<GT, ZT, E, 32, false>(dy, z, act, T, d, dz, part, s);
+  if constexpr (E > 1)
+    if (T * d * (int64_t)(2 * sizeof(GT) + sizeof(ZT)) > kStreamBytes)
+      return by_act<GT, ZT, E, 8, true>(dy, z, act, T, d, dz, part, s);
+  return by_act<GT, ZT, E, 8, false>(dy, z, act, T, d, dz, part, s);
+}
+
 template <class GT, class ZT>
 hipError_t by_width(const void* dy, const void* z, int act, int64_t T, int64_t d, void* dz,
                     float* part, hipStream_t s) {
-  return d % 8 == 0 ? by_act<GT, ZT, 8>((const GT*)dy, (const ZT*)z, act, T, d, (GT*)dz, part, s)
-                    : by_act<GT, ZT, 1>((const GT*)dy, (const ZT*)z, act, T, d, (GT*)dz, part, s);
+  constexpr int E = sizeof(GT) + sizeof(ZT) == 4 ? 8 : 4;
+  return d % 8 == 0 ? by_rows<GT, ZT, E>((const GT*)dy, (const ZT*)z, act, T, d, (GT*)dz, part, s)
+                    : by_rows<GT, ZT, 1>((const GT*)dy, (const ZT*)z, act, T, d, (GT*)dz, part, s);
 }
 
 }  // namespace
 
 size_t linear_act_bwd_ws_bytes(int64_t T, int64_t d) {
-  return (size_t)strips_of(T, d).n * (size_t)d * 4;
+  const int64_t n = strips_of(T, d).n;
+  return n == 1 ? 0 : (size_t)n * (size_t)d * 4;
 }
 
 hipError_t launch_linear_act_bwd(const void* dy, int gt, const void* z, int zt, int64_t T,
@@ -102,7 +122,8 @@ hipError_t launch_linear_act_bwd(const void* dy, int gt, const void* z, int zt, 
                                  hipStream_t s) {
   if (d == 0) return hipSuccess;
   if (T == 0) return dbias ? launch_fill_f32(dbias, d, 0.0f, s) : hipSuccess;
-  float* part = dbias ? (float*)ws : nullptr;
+  const int64_t n = strips_of(T, d).n;
+  float* part = n > 1 && dbias ? (float*)ws : dbias;
   hipError_t e;
   if (gt == 0)
     e = zt == 0 ? by_width<float, float>(dy, z, act, T, d, dz, part, s)
@@ -110,8 +131,8 @@ hipError_t launch_linear_act_bwd(const void* dy, int gt, const void* z, int zt, 
   else
     e = zt == 0 ? by_width<__bf16, float>(dy, z, act, T, d, dz, part, s)
                 : by_width<__bf16, __bf16>(dy, z, act, T, d, dz, part, s);
-  if (e != hipSuccess || !dbias) return e;
-  return launch_column_sum(part, strips_of(T, d).n, d, 1, dbias, nullptr, s);
+  if (e != hipSuccess || !dbias || n == 1) return e;
+  return launch_column_sum(part, n, d, 1, dbias, nullptr, s);
 }
 
 }  // namespace falq

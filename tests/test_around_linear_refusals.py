@@ -61,10 +61,11 @@ def test_linear_act_fwd():
 
 def test_linear_act_bwd():
     f = fq.load().linear_act_bwd
-    ws = fq.linear_act_bwd_workspace_bytes(8, 48)
+    ws = fq.linear_act_bwd_workspace_bytes(1000, 48)
     assert ws >= 48 * 4 and fq.linear_act_bwd_workspace_bytes(8, -1) == 0
-    #     dy gt z  zt act T  d   dz db ws n   stream
-    ok = [P, 0, Q, 1, 2, 8, 48, R, S, P, ws, None]
+    assert fq.linear_act_bwd_workspace_bytes(8, 48) == 0        # few rows need none
+    #     dy gt z  zt act T    d   dz db ws n   stream
+    ok = [P, 0, Q, 1, 2, 1000, 48, R, S, P, ws, None]
     refused(f, ok, [(0, None), (0, MIS), (2, None), (2, MIS), (7, None), (7, MIS), (7, Q),
                     (1, 2), (3, 2), (4, -1), (4, 5), (5, -1), (6, -1), (6, (1 << 24) + 1),
                     (8, MIS), (9, None), (9, P + 16), (10, ws - 1)])
