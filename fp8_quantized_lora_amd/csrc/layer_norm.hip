@@ -363,6 +363,80 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
   }
 }
 
+// Few rows (kShortRows): dx, dw and db in one launch and without a workspace.
+// The first `row_blocks` workgroups form dx, a row per group; the others take
+// 32 columns each and all rows, and write dw and db themselves: dw and db need
+// only the forward's statistics, and the second read of dy and x comes from
+// the caches.
+constexpr int kShortCols = 32;
+template <class XT, class GT, int E, int C>
+__global__ __launch_bounds__(1024) void ln_bwd_short(
+    const GT* dy, const XT* __restrict__ x, const float* __restrict__ w,
+    const float* __restrict__ mean, const float* __restrict__ rstd, GT* dx,
+    float* __restrict__ dw, float* __restrict__ db, int T, int d, int nt, int row_blocks) {
+  if ((int)blockIdx.x < row_blocks) {
+    __shared__ float red[16][2];
+    const Group gr(nt);
+    const int64_t at = (int64_t)blockIdx.x * ((int)blockDim.x / nt) + gr.index();
+    const int64_t row = __builtin_amdgcn_readfirstlane((int)at);
+    const bool live = row < T;
+    const int64_t from = (live ? row : T - 1) * d;
+    const float mu = mean[live ? row : T - 1], rs = rstd[live ? row : T - 1];
+    float gw[C][E], xh[C][E], s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t i = gr.at<E>(c);
+      if (i >= (uint32_t)d) continue;
+      float f[E];
+      load_elems<E>(dy + from + i, gw[c]);
+      load_elems<E>(x + from + i, xh[c]);
+      if (w) load_elems<E>(w + i, f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (w) gw[c][e] *= f[e];
+        xh[c][e] = (xh[c][e] - mu) * rs;
+        s[0] += gw[c][e];
+        s[1] = fmaf(gw[c][e], xh[c][e], s[1]);
+      }
+    }
+    gr.sum(s, red);
+    if (!live) return;
+    const float inv = 1.0f / (float)d, c1 = s[0] * inv, c2 = s[1] * inv;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t i = gr.at<E>(c);
+      if (i >= (uint32_t)d) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) gw[c][e] = rs * (gw[c][e] - c1 - xh[c][e] * c2);
+      store_elems<E>(dx + from + i, gw[c]);
+    }
+    return;
+  }
+  __shared__ float sums[2][32][kShortCols];
+  const int cl = threadIdx.x % kShortCols, rl = threadIdx.x / kShortCols;
+  const int lanes = (int)blockDim.x / kShortCols;            // at most 32
+  const int col = ((int)blockIdx.x - row_blocks) * kShortCols + cl;
+  float a = 0.0f, b = 0.0f;
+  if (col < d) {
+#pragma unroll 8
+    for (int r = rl; r < T; r += lanes) {
+      const float g = (float)dy[(int64_t)r * d + col];
+      a = fmaf(g, ((float)x[(int64_t)r * d + col] - mean[r]) * rstd[r], a);
+      b += g;
+    }
+  }
+  sums[0][rl][cl] = a;
+  sums[1][rl][cl] = b;
+  __syncthreads();
+  if (rl < 2 && col < d) {
+    float* o = rl ? db : dw;
+    if (!o) return;
+    float v = sums[rl][0][cl];
+    for (int r = 1; r < lanes; ++r) v += sums[rl][r][cl];
+    o[col] = v;
+  }
+}
+
 // Columns of dw and db: a workgroup takes kColW columns and the rows of one
 // strip, and writes its sums to row `strip` of the partials ([2 d] floats:
 // dw, then db).
@@ -462,9 +536,37 @@ hipError_t bwd_rows(const BwdPlan& p, const GT* dy, const XT* x, const float* w,
   return hipGetLastError();
 }
 
+constexpr int64_t kShortRows = 1024;
+bool bwd_short_fits(int64_t T, int64_t d) {
+  return T <= kShortRows && row_threads(d, 8, 1024) > 0;
+}
+
+template <class XT, class GT, int E>
+hipError_t bwd_short(const GT* dy, const XT* x, const float* w, const float* mean,
+                     const float* rstd, int64_t T, int64_t d, GT* dx, float* dw, float* db,
+                     hipStream_t s) {
+  const int nt = row_threads(d, 8, 1024), G = 1024 / nt;
+  const int rows = dx ? (int)((T + G - 1) / G) : 0;
+  const int cols = dw || db ? (int)((d + kShortCols - 1) / kShortCols) : 0;
+  auto launch = [&](int row_blocks, int col_blocks) {
+    if (row_blocks + col_blocks > 0)
+      ln_bwd_short<XT, GT, E, 8 / E><<<row_blocks + col_blocks, nt * G, 0, s>>>(
+          dy, x, w, mean, rstd, dx, dw, db, (int)T, (int)d, nt, row_blocks);
+  };
+  if ((const GT*)dx == dy) {                   // in place: the columns are read first
+    launch(0, cols);
+    launch(rows, 0);
+  } else {
+    launch(rows, cols);
+  }
+  return hipGetLastError();
+}
+
 template <class XT, class GT, int E>
 hipError_t bwd(const GT* dy, const XT* x, const float* w, const float* mean, const float* rstd,
                int64_t T, int64_t d, GT* dx, float* dw, float* db, float* part, hipStream_t s) {
+  if (bwd_short_fits(T, d))
+    return bwd_short<XT, GT, E>(dy, x, w, mean, rstd, T, d, dx, dw, db, s);
   if (!dw && !db) part = nullptr;
   const BwdPlan p = bwd_plan(T, d);
   hipError_t e = hipSuccess;
@@ -597,6 +699,7 @@ hipError_t launch_column_sum(const float* part, int64_t P, int64_t d, int nout, 
 }
 
 size_t layer_norm_bwd_ws_bytes(int64_t T, int64_t d) {
+  if (bwd_short_fits(T, d)) return 0;
   const BwdPlan p = bwd_plan(T, d);
   return (size_t)(p.n ? p.blocks : strips_of(T, d).n) * 2 * (size_t)d * 4;
 }

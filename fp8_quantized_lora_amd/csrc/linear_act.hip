@@ -33,8 +33,14 @@ hipError_t launch_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N
                         int64_t n_first, int64_t n_end, const Epilogue& ep, hipStream_t s) {
   const int tM = (int)((M + C::BM - 1) / C::BM);
   const int tN = (int)((n_end - n_first + C::BN - 1) / C::BN);
-  linear_act_tile<C, OT><<<tM * tN, C::kThreads, 0, s>>>(A, B, (int)M, (int)N, (int)K,
-                                                         (int)n_first, tM, tN, ep);
+  const int64_t out = M * N * (int64_t)sizeof(OT) * (1 + (ep.z != nullptr) + (ep.residual != nullptr));
+  // the streaming hint needs whole lines: 16-byte stores, so bfloat16
+  if (sizeof(OT) == 2 && out + M * K + N * K > kStreamBytes)
+    linear_act_tile<C, OT, sizeof(OT) == 2><<<tM * tN, C::kThreads, 0, s>>>(
+        A, B, (int)M, (int)N, (int)K, (int)n_first, tM, tN, ep);
+  else
+    linear_act_tile<C, OT, false><<<tM * tN, C::kThreads, 0, s>>>(
+        A, B, (int)M, (int)N, (int)K, (int)n_first, tM, tN, ep);
   return hipGetLastError();
 }
 

@@ -19,12 +19,12 @@ struct Epilogue {
 };
 
 // eight columns of one row
-template <int ACT, class OT>
+template <int ACT, class OT, bool STREAM>
 __device__ __forceinline__ void finish8(float (&v)[8], float scale, const float (&bias)[8],
                                         const Epilogue& e, int64_t at) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], scale, bias[i]);
-  if (e.z) store_elems<8>((OT*)e.z + at, v);
+  if (e.z) store_elems<8, STREAM>((OT*)e.z + at, v);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = act_value<ACT>(v[i]);
   if (e.residual) {
@@ -33,7 +33,7 @@ __device__ __forceinline__ void finish8(float (&v)[8], float scale, const float 
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += r[i];
   }
-  store_elems<8>((OT*)e.y + at, v);
+  store_elems<8, STREAM>((OT*)e.y + at, v);
 }
 
 // one column of one row

@@ -35,12 +35,13 @@ def test_layer_norm_fwd():
 
 def test_layer_norm_bwd():
     f = fq.load().layer_norm_bwd
-    ws = fq.layer_norm_bwd_workspace_bytes(4, 64)
+    ws = fq.layer_norm_bwd_workspace_bytes(2000, 64)
     assert ws >= 2 * 64 * 4
     assert fq.layer_norm_bwd_workspace_bytes(-1, 64) == 0
     assert fq.layer_norm_bwd_workspace_bytes(4, 0) == 0
-    #     dy gt x  xt w  mu rs T  d   dx dw db ws n   stream
-    ok = [P, 0, Q, 1, R, S, S, 4, 64, P, Q, R, S, ws, None]
+    assert fq.layer_norm_bwd_workspace_bytes(4, 64) == 0       # few rows need none
+    #     dy gt x  xt w  mu rs T     d   dx dw db ws n   stream
+    ok = [P, 0, Q, 1, R, S, S, 2000, 64, P, Q, R, S, ws, None]
     refused(f, ok, [(0, None), (0, MIS), (2, None), (2, MIS), (5, None), (6, None), (4, MIS),
                     (9, MIS), (9, Q), (10, MIS), (10, R), (11, MIS), (1, 5), (3, 2), (7, -1),
                     (8, 0), (8, (1 << 24) + 1), (12, None), (12, P + 16), (13, ws - 1)])

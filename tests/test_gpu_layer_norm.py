@@ -156,7 +156,7 @@ def stats_of(x, eps=1e-5):
 
 
 @pytest.mark.parametrize("xt,gt", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
-@pytest.mark.parametrize("T,d", SHAPES + [(1500, 96), (700, 1027), (2100, 264)])
+@pytest.mark.parametrize("T,d", SHAPES + [(1500, 96), (700, 1027), (2100, 264), (1025, 1029), (1500, 4096), (1100, 9000)])
 def test_backward(gpu_lib, T, d, xt, gt):
     announce(f"layer_norm_bwd T={T} d={d} {xt} {gt}")
     x, dy, w, _ = problem(T * 5 + d, T, d, xt, gt)
@@ -170,7 +170,7 @@ def test_backward(gpu_lib, T, d, xt, gt):
     check(db, rb, tb, "dbias")
 
 
-@pytest.mark.parametrize("T,d", [(50, 515), (50, 768)])
+@pytest.mark.parametrize("T,d", [(50, 515), (50, 768), (1300, 515), (1300, 768), (1050, 8200)])
 def test_backward_parts_and_in_place(gpu_lib, T, d):
     """dx alone, dweight or dbias alone, no weight, dx onto dy: the same bits."""
     x, dy, w, _ = problem(8, T, d)
