@@ -14,10 +14,11 @@
 // Work is counted in chunks of 256 threads x 16 bytes from each tensor's
 // address rounded down to 16 bytes: the 16-byte accesses then fit a tensor that
 // starts at any element, and only vectors across its ends are done element by
-// element.  A workgroup takes one run of consecutive chunks (the tensor is
-// looked up once) and has eight chunks' loads in flight.  Both passes take the
-// same runs, the second from the end back: what the first one read last is the
-// likeliest to be in the last-level cache still.
+// element.  Runs of kAhead chunks are dealt round the workgroups (one long run
+// for each would put them all on the same memory channels where sizes are powers
+// of two: 160 M floats 375 us), a run's loads all in flight.  The second pass
+// goes from the end back: what the first one read last is the likeliest to be
+// in the last-level cache still.
 #include "elem.hpp"
 #include "kernels.hpp"
 
@@ -62,21 +63,23 @@ __device__ __forceinline__ int lead_of(const GT* g) {
   return (int)((reinterpret_cast<uintptr_t>(g) % 16) / sizeof(GT));
 }
 
-// The thread's vectors of chunks [a, b) of a tensor, last to first: many(i) has
-// kAhead whole vectors at elements i, i + kChunk, ...; one(i) a whole vector;
-// each(i) one element of a vector across an end.
-template <class GT, class Many, class One, class Each>
+// The thread's vectors of chunks [a, b) of a tensor, in order or (BACK) from the
+// last to the first: many(i) has kAhead whole vectors at elements i,
+// i + kChunk, ...; one(i) a whole vector; each(i) one element of a vector
+// across an end.
+template <bool BACK, class GT, class Many, class One, class Each>
 __device__ __forceinline__ void run_of(const GT* g, int64_t n, int64_t a, int64_t b, Many&& many,
                                        One&& one, Each&& each) {
   const int64_t lead = lead_of(g), mine = (int64_t)threadIdx.x * kVec<GT> - lead;
-  while (b > a) {
-    if (b - a >= kAhead && (b - kAhead) * kChunk<GT> >= lead && b * kChunk<GT> - lead <= n) {
-      b -= kAhead;
-      many(b * kChunk<GT> + mine);
+  while (a < b) {
+    const int64_t first = BACK ? b - kAhead : a;
+    if (b - a >= kAhead && first * kChunk<GT> >= lead &&
+        (first + kAhead) * kChunk<GT> - lead <= n) {
+      many(first * kChunk<GT> + mine);
+      (BACK ? b : a) += BACK ? -kAhead : kAhead;
       continue;
     }
-    --b;
-    const int64_t i = b * kChunk<GT> + mine;
+    const int64_t i = (BACK ? --b : a++) * kChunk<GT> + mine;
     if (i >= 0 && i + kVec<GT> <= n) {
       one(i);
     } else if (i + kVec<GT> > 0 && i < n) {
@@ -85,25 +88,34 @@ __device__ __forceinline__ void run_of(const GT* g, int64_t n, int64_t a, int64_
   }
 }
 
-// f(entry, a, b) for the workgroup's run of chunks, tensor by tensor, last to
-// first
-template <class Tab, class F>
+// f(entry, a, b) for the workgroup's runs of chunks, tensor by tensor
+template <bool BACK, class Tab, class F>
 __device__ __forceinline__ void walk(const Tab& t, F&& f) {
-  const uint32_t c0 = (uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x);
-  uint32_t c1 = (uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x);
-  if (c0 == c1) return;
-  int lo = 0, hi = t.count - 1;                // the tensor of chunk c1 - 1
-  while (lo < hi) {
-    const int m = (lo + hi + 1) / 2;
-    if (t.e[m].first < c1)
-      lo = m;
-    else
-      hi = m - 1;
-  }
-  for (; c1 > c0; --lo) {
-    const uint32_t first = t.e[lo].first, from = first > c0 ? first : c0;
-    f(t.e[lo], (int64_t)(from - first), (int64_t)(c1 - first));
-    c1 = from;
+  const uint32_t runs = (t.chunks + kAhead - 1) / kAhead;
+  for (uint32_t r = blockIdx.x; r < runs; r += gridDim.x) {
+    uint32_t c0 = (BACK ? runs - 1 - r : r) * kAhead;
+    uint32_t c1 = c0 + kAhead < t.chunks ? c0 + kAhead : t.chunks;
+    const uint32_t begin = BACK ? c1 - 1 : c0;
+    int k = 0, hi = t.count - 1;               // the tensor of that chunk
+    while (k < hi) {
+      const int m = (k + hi + 1) / 2;
+      if (t.e[m].first <= begin)
+        k = m;
+      else
+        hi = m - 1;
+    }
+    while (c0 < c1) {
+      const uint32_t first = t.e[k].first;
+      if (BACK) {
+        const uint32_t from = first > c0 ? first : c0;
+        f(t.e[k--], (int64_t)(from - first), (int64_t)(c1 - first));
+        c1 = from;
+      } else {
+        const uint32_t end = k + 1 < t.count && t.e[k + 1].first < c1 ? t.e[k + 1].first : c1;
+        f(t.e[k++], (int64_t)(c0 - first), (int64_t)(end - first));
+        c0 = end;
+      }
+    }
   }
 }
 
@@ -114,7 +126,7 @@ __device__ __forceinline__ double squares(const GT* g, int64_t n, int64_t a, int
 #pragma unroll
     for (int e = 0; e < kVec<GT>; ++e) s = fma((double)v[e], (double)v[e], s);
   };
-  run_of(
+  run_of<false>(
       g, n, a, b,
       [&](int64_t i) {
         Raw<GT, kVec<GT>> v[kAhead];
@@ -153,7 +165,7 @@ __device__ __forceinline__ double block_sum_f64(double v) {
 template <class Tab>
 __global__ __launch_bounds__(kThreads) void squares_kernel(Tab t, double* __restrict__ part) {
   double s = 0.0;
-  walk(t, [&](const Entry& e, int64_t a, int64_t b) {
+  walk<false>(t, [&](const Entry& e, int64_t a, int64_t b) {
     s += e.bf16 ? squares((const __bf16*)e.g, e.n, a, b) : squares((const float*)e.g, e.n, a, b);
   });
   s = block_sum_f64(s);
@@ -189,7 +201,7 @@ __device__ __forceinline__ void scale(const GT* g, GT* o, int64_t n, int64_t a, 
       for (int e = 0; e < kVec<GT>; ++e) o[i + e] = (GT)v[e];
     }
   };
-  run_of(
+  run_of<true>(
       g, n, a, b,
       [&](int64_t i) {
         Raw<GT, kVec<GT>> v[kAhead];
@@ -217,7 +229,7 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(Tab t, const double* __
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)r;
   float c = (float)((double)max_norm / (r + (double)eps));
   c = c > 1.0f ? 1.0f : c;                     // NaN stays NaN
-  walk(t, [&](const Entry& e, int64_t a, int64_t b) {
+  walk<true>(t, [&](const Entry& e, int64_t a, int64_t b) {
     if (c == 1.0f && e.g == e.out) return;     // in place and not clipped
     if (e.bf16)
       scale<STREAM>((const __bf16*)e.g, (__bf16*)e.out, e.n, a, b, c);

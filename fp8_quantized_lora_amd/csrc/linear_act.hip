@@ -55,16 +55,16 @@ hipError_t launch_few(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, 
 // Which tile: the one whose rounds of the 256 CUs take least.  A round of
 // tiles costs, at 4096 K-bytes (us, measured at 256, 512, 768 and 1024 tiles;
 // 5 more for the first loads and the last stores, whatever the tile):
-//     256 x 256   58     128 x 128   20     64 x 128   11
-//      64 x  64    7      32 x  64  5.6
+//     256 x 320   75     256 x 256   58     128 x 128   20
+//      64 x 128   11      64 x  64    7      32 x  64    5.6
 // so a larger tile moves fewer bytes per product but leaves more of its last
 // round empty.  512 x 4096 outputs: 15.3 in tiles of 64 x 128 (one round), 18.9
 // in 128 x 128 (half a round), 17.5 in 32 x 128; 128 x 4096: 10.0 in 32 x 64,
 // 10.9 in 64 x 64, 14 in 64 x 128.
-enum TileKind { k256, k128, k64x128, k64, k32x64, kTileKinds };
-constexpr int kTileM[kTileKinds] = {256, 128, 64, 64, 32};
-constexpr int kTileN[kTileKinds] = {256, 128, 128, 64, 64};
-constexpr float kRound[kTileKinds] = {58.0f, 20.0f, 11.0f, 7.0f, 5.6f};
+enum TileKind { k256, k256x320, k128, k64x128, k64, k32x64, kTileKinds };
+constexpr int kTileM[kTileKinds] = {256, 256, 128, 64, 64, 32};
+constexpr int kTileN[kTileKinds] = {256, 320, 128, 128, 64, 64};
+constexpr float kRound[kTileKinds] = {58.0f, 75.0f, 20.0f, 11.0f, 7.0f, 5.6f};
 constexpr int kCUs = 256;
 
 float tile_cost(TileKind k, int64_t M, int64_t n) {
@@ -85,6 +85,8 @@ hipError_t launch_kind(TileKind k, const uint8_t* A, const uint8_t* B, int64_t M
                        hipStream_t s) {
   switch (k) {
     case k256: return launch_tiles<Tile<256, 256, 2, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
+    case k256x320:
+      return launch_tiles<Tile<256, 320, 2, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
     case k128:
       return launch_tiles<Tile<128, 128, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
     case k64x128:

@@ -173,19 +173,23 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
   __syncthreads();                                           // the stages are free
 
   constexpr int CH = C::WTN / 4, LPR = C::WTN / 8, RPI = 64 / LPR;
+  // 16-byte chunk c of row r: swizzled where the rows' stride is a power of two
+  // (else the stride itself spreads the rows over the banks)
+  constexpr int SWZ = (CH & (CH - 1)) == 0 ? CH - 1 : 0;
+  auto slot = [](int r, int c) { return r * CH + (c ^ (r & SWZ)); };
   v4f* mine = reinterpret_cast<v4f*>(smem + w * (C::S * C::STAGE / C::NW));
   const int cl = lane % LPR, rl = lane / LPR;
   const int col = n0 + wn * C::WTN + cl * 8;
-  const bool col_ok = col < N;                               // N is a multiple of 16
+  const bool col_ok = rl < RPI && col < N;                   // N is a multiple of 16
   float bias[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
   if (ep.bias && col_ok) load_elems<8>(ep.bias + col, bias);
   auto rows = [&](auto act, int first) {
-    for (int r = rl; r < C::PASS; r += RPI) {
+    for (int r = rl; r < C::PASS; r += RPI) {                // lanes past RPI rows: idle
       const int row = m0 + wm * C::WTM + first + r;
-      const v4f a = mine[r * CH + ((2 * cl) ^ (r & (CH - 1)))];
-      const v4f b = mine[r * CH + ((2 * cl + 1) ^ (r & (CH - 1)))];
+      const v4f a = mine[slot(r, 2 * cl)];
+      const v4f b = mine[slot(r, 2 * cl + 1)];
       if (!col_ok || row >= M) continue;
       float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
       finish8<decltype(act)::value, OT, STREAM>(v, scale, bias, ep, (int64_t)row * N + col);
@@ -199,8 +203,7 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
     for (int i = 0; i < C::PASS / 16; ++i)
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-        mine[(i * 16 + r16) * CH + ((4 * j + g) ^ ((i * 16 + r16) & (CH - 1)))] =
-            acc[p * (C::PASS / 16) + i][j];
+        mine[slot(i * 16 + r16, 4 * j + g)] = acc[p * (C::PASS / 16) + i][j];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int first = p * C::PASS;
     switch (ep.act) {

@@ -108,6 +108,7 @@ SHAPES = [  # (T, d_in, d_out): one token, a few, every tile size, ragged in eac
     (1, 16, 16), (1, 512, 256), (1, 400, 1040), (2, 4096, 48), (5, 144, 272), (16, 256, 512),
     (17, 1040, 80), (37, 528, 1008), (64, 384, 128), (65, 2048, 320), (130, 400, 272),
     (200, 112, 1552), (257, 640, 784), (513, 1152, 1280), (1100, 240, 2576), (3000, 128, 2832),
+    (3900, 272, 5120), (2304, 160, 8208), (4096, 96, 6416),
 ]
 
 
