@@ -727,6 +727,7 @@ GRAD_MAX_TENSORS = 65536
 
 _ELEM = {torch.float32: 0, torch.bfloat16: 1}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _elem(t: torch.Tensor, name: str) -> int:
@@ -755,6 +756,12 @@ def _arg(t: Optional[torch.Tensor], dtype, shape, dev: int, name: str) -> Option
     raise FalqError(f"{name}: expected device cuda:{dev}, got {t.device}")
 
 
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise FalqError(f"{name}: expected two dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
 def _device(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
@@ -778,12 +785,14 @@ def _scratch(ws: Optional[torch.Tensor], need: int, dev: int, stream, st: int):
     where = torch.device("cuda", dev)
     if stream is None or st == _raw_stream(dev):
         return torch.empty(need, dtype=torch.uint8, device=where)
-    with torch.cuda.stream(torch.cuda.ExternalStream(st, device=where)):
+    own = (torch.cuda.ExternalStream(st, device=where) if st
+           else torch.cuda.default_stream(where))
+    with torch.cuda.stream(own):
         return torch.empty(need, dtype=torch.uint8, device=where)
 
 
 def _run(fn, what: str, dev: int, *args) -> None:
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -798,7 +807,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Option
     """y = (x - mean) * rstd * weight + bias per row of x [T x d], rstd =
     1 / sqrt(var + eps); x and y float32 or bfloat16 each, weight and bias
     float32 or None; mean and rstd [T] are what layer_norm_bwd takes."""
-    T, d = x.shape
+    T, d = _matrix(x, "x")
     xt, yt, dev = _elem(x, "x"), _elem(y, "y"), _device(x, "x")
     f32 = torch.float32
     _run(load().layer_norm_fwd, "layer_norm_fwd", dev, _arg(x, x.dtype, (T, d), dev, "x"), xt,
@@ -817,7 +826,7 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Ten
                    ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """The gradients of layer_norm_fwd: dx (dy's type; may be dy, or None), and
     the sums over rows dweight and dbias (float32, each may be None)."""
-    T, d = x.shape
+    T, d = _matrix(x, "x")
     gt, xt, dev = _elem(dy, "dy"), _elem(x, "x"), _device(x, "x")
     f32, lib, st = torch.float32, load(), _stream_of(dev, stream)
     args = (_arg(dy, dy.dtype, (T, d), dev, "dy"), gt, _arg(x, x.dtype, (T, d), dev, "x"), xt,
@@ -842,8 +851,8 @@ def melded_linear_fwd_act(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tensor,
     """z = dec(xq) dec(wq)^T / (s_x s_w) + bias and y = act(z) + residual in one
     call; y, z and residual share one type (float32 or bfloat16), bias is
     float32; residual may be y; z (None: not kept) is what linear_act_bwd takes."""
-    T, d_in = xq.shape
-    d_out = wq.shape[0]
+    T, d_in = _matrix(xq, "xq")
+    d_out = _matrix(wq, "wq")[0]
     t, a, dev = _elem(y, "y"), _act(act), _device(xq, "xq")
     u8, f32, out = torch.uint8, torch.float32, (T, d_out)
     _run(load().melded_linear_fwd_act, "melded_linear_fwd_act", dev,
@@ -858,12 +867,13 @@ def linear_act_bwd_workspace_bytes(T: int, d_out: int) -> int:
     return int(load().linear_act_bwd_workspace_bytes(T, d_out))
 
 
-def linear_act_bwd(dy: torch.Tensor, z: Optional[torch.Tensor], dz: torch.Tensor,
+def linear_act_bwd(dy: torch.Tensor, z: Optional[torch.Tensor], dz: Optional[torch.Tensor],
                    dbias: Optional[torch.Tensor] = None, act: str = "none",
                    ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """dz = dy * act'(z) (dy's type; dz may be dy) and dbias = the sum of dz over
-    the rows (float32, or None); z float32 or bfloat16, None for act "none"."""
-    T, d_out = dy.shape
+    the rows (float32); either may be None.  z float32 or bfloat16, None for act
+    "none"."""
+    T, d_out = _matrix(dy, "dy")
     gt, a = _elem(dy, "dy"), _act(act)
     if z is None and a != 0:
         raise FalqError(f"linear_act_bwd: z is needed for act {act!r}")
@@ -936,5 +946,5 @@ def grad_clip(grads, max_norm: float, norm: torch.Tensor, out=None, eps: float =
          None if q is None else _at(q), norm_at, *_span(w), st)
 
 
-from .step import MeldedLinear  # noqa: E402  (buffers + the step's call sequence)
-__all__.append("MeldedLinear")
+from .step import MeldedLinear, clip_gradients  # noqa: E402  (buffers + the call sequence)
+__all__ += ["MeldedLinear", "clip_gradients"]

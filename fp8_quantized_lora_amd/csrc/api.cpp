@@ -843,7 +843,8 @@ falq_status linear_act_bwd(const void* dy, int dy_dtype, const void* z, int z_dt
   if (act < FALQ_ACT_NONE || act > FALQ_ACT_SILU) return FALQ_EINVAL;
   if (d_out < 0 || !rows_ok(T, std::max<int64_t>(d_out, 1)) || !opt(dbias)) return FALQ_EINVAL;
   if (d_out == 0) return FALQ_OK;
-  if (T > 0 && (!need(dy) || !need(dz) || dz == z)) return FALQ_EINVAL;
+  if (!dz && !dbias) return FALQ_EINVAL;
+  if (T > 0 && (!need(dy) || !opt(dz) || (dz && dz == z))) return FALQ_EINVAL;
   if (T > 0 && act != FALQ_ACT_NONE && !need(z)) return FALQ_EINVAL;
   if (dbias && !ws_ok(ws, ws_bytes, falq::linear_act_bwd_ws_bytes(T, d_out))) return FALQ_EINVAL;
   return hip_status(falq::launch_linear_act_bwd(dy, dy_dtype, z, z_dtype, T, d_out, act, dz,

@@ -244,7 +244,7 @@ hipError_t launch_linear_act(const uint8_t* xq, const float* s_x, const uint8_t*
                              int64_t d_in, int64_t d_out, int act, int dtype, void* y, void* z,
                              hipStream_t s);
 size_t linear_act_bwd_ws_bytes(int64_t T, int64_t d);
-// dbias may be null (then ws is not used); dz may be dy
+// dz or dbias may be null (without dbias ws is not used); dz may be dy
 hipError_t launch_linear_act_bwd(const void* dy, int gt, const void* z, int zt, int64_t T,
                                  int64_t d, int act, void* dz, float* dbias, void* ws,
                                  hipStream_t s);

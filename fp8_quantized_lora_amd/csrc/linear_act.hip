@@ -23,6 +23,7 @@
 #include "linear_act_tile.hpp"
 
 #include <algorithm>
+#include <cmath>
 
 namespace falq {
 namespace {
@@ -69,6 +70,8 @@ constexpr int kCUs = 256;
 
 float tile_cost(TileKind k, int64_t M, int64_t n) {
   const int64_t nt = ((M + kTileM[k] - 1) / kTileM[k]) * ((n + kTileN[k] - 1) / kTileN[k]);
+  // a grid holds fewer than 2^32 threads: very long outputs take large tiles
+  if (k != k256 && nt >= 1 << 23) return HUGE_VALF;
   return kRound[k] * (float)((nt + kCUs - 1) / kCUs);
 }
 

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kRows * kLanes) void act_bwd_kernel(const GT* dy, c
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) ab[e] += g[e];
-      store_elems<E, STREAM>(dz + r * d + col, g);
+      if (dz) store_elems<E, STREAM>(dz + r * d + col, g);
     }
   }
   if (!part) return;

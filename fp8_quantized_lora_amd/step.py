@@ -27,6 +27,15 @@ quantized once to A~ at init, the forward is melded_linear_fwd_frozen_a (Y and
 U = X~ A~^T), the backward melded_linear_bwd_frozen_a (dX and dB from U), and
 the proxy update's A is DQ(A~).
 
+With bias=True, act other than "none" or y_dtype bfloat16 the layer has an
+epilogue: the forward is melded_linear_fwd_act (bias, activation and, where
+forward is given one, a residual in the product's launch; z kept for the
+backward), the backward linear_act_bwd in front of fp8_quantize, then
+melded_linear_bwd, which forms X^ A^T itself.
+
+clip_gradients clips the adapter (and bias) gradients of many layers by their
+global norm, between their backward calls and their adapter updates.
+
 Every buffer and workspace is allocated once up front, so a step makes no
 allocation and no host synchronisation.  This module only sequences calls
 into the HIP library; it computes nothing itself.
@@ -47,23 +56,45 @@ from . import (fp8_quantize, fp8_quantize_workspace_bytes, fp8_dequantize, melde
                adamw_state, rowwise_proxy_update, rowwise_proxy_update_workspace_bytes,
                rowwise_proxy_update_topk_rank, rowwise_proxy_update_topk_rank_workspace_bytes,
                adapter_pieces_bytes, adapter_pieces, adapter_step_pieces,
-               melded_linear_fwd_xa_pieces)
+               melded_linear_fwd_xa_pieces, melded_linear_fwd_act, linear_act_bwd,
+               linear_act_bwd_workspace_bytes, grad_clip, ACTIVATIONS)
+
+
+def clip_gradients(layers, max_norm: float, norm: torch.Tensor, extra=(), eps: float = 1e-6,
+                   ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Clip dA, dB and dbias of all `layers`, and the tensors `extra`, in place
+    by the global norm over them (grad_clip; the norm goes to `norm`)."""
+    grads = [g for m in layers for g in (m.dA, m.dB, m.dbias) if g is not None]
+    grad_clip([*grads, *extra], max_norm, norm, eps=eps, ws=ws, stream=stream)
 
 
 class MeldedLinear:
     def __init__(self, d_out: int, d_in: int, rank: int, tokens: int, device="cuda",
                  x_dtype=torch.float32, train_a: bool = True, optimizer: str = "sgd",
                  adamw: Optional[dict] = None, fp8_a: bool = False, g_fmt: str = "e4m3",
-                 topk_rank: int = 0, merge_every: int = 1):
+                 topk_rank: int = 0, merge_every: int = 1, bias: bool = False,
+                 act: str = "none", y_dtype=torch.float32, dy_dtype=torch.float32):
         """optimizer "sgd" (adapter_step) or "adamw" (adapter_step_adamw, with
         hyper-parameters `adamw`: beta1, beta2, eps, weight_decay); fp8_a
         freezes A in FP8 (implies train_a=False); g_fmt is the FP8 format of the
         upstream gradient dY ("e4m3" or "e5m2"); topk_rank > 0 merges only the
         top-k rank components of the proxy (rowwise_proxy_update_topk_rank);
         merge_every: how often the caller will merge (update(merge=...)), which
-        decides whether W~^T is kept (worth it from every second step on)."""
+        decides whether W~^T is kept (worth it from every second step on); bias
+        adds a bias (self.bias, zero at the start; its gradient in self.dbias),
+        act an activation of melded_linear_fwd_act, y_dtype is the type of Y
+        (and of a residual), dy_dtype that of the upstream gradient dY."""
         if optimizer not in ("sgd", "adamw"):
             raise ValueError(f"optimizer must be 'sgd' or 'adamw', not {optimizer!r}")
+        if act not in ACTIVATIONS:
+            raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, not {act!r}")
+        if y_dtype not in (torch.float32, torch.bfloat16) or dy_dtype not in (torch.float32,
+                                                                              torch.bfloat16):
+            raise ValueError("y_dtype and dy_dtype must be float32 or bfloat16")
+        self.act = act
+        self.epilogue = bias or act != "none" or y_dtype != torch.float32
+        if fp8_a and self.epilogue:
+            raise ValueError("a layer with A frozen in FP8 has no epilogue")
         if fp8_a:
             train_a = False
         self.fp8_a = fp8_a
@@ -88,10 +119,16 @@ class MeldedLinear:
         self.gq = torch.empty((tokens, d_out), dtype=u8, device=dev)
         self.s_x = torch.empty(1, dtype=f32, device=dev)
         self.s_g = torch.empty(1, dtype=f32, device=dev)
-        self.y = torch.empty((tokens, d_out), dtype=f32, device=dev)
+        self.y = torch.empty((tokens, d_out), dtype=y_dtype, device=dev)
         self.dx = torch.empty((tokens, d_in), dtype=f32, device=dev)
         self.dA = torch.empty((rank, d_in), dtype=f32, device=dev) if train_a else None
         self.dB = torch.empty((d_out, rank), dtype=f32, device=dev)
+        # the epilogue: bias and its gradient, z for the backward, dz
+        self.bias = torch.zeros(d_out, dtype=f32, device=dev) if bias else None
+        self.dbias = torch.empty(d_out, dtype=f32, device=dev) if bias else None
+        kept = act != "none"
+        self.z = torch.empty((tokens, d_out), dtype=y_dtype, device=dev) if kept else None
+        self.dz = torch.empty((tokens, d_out), dtype=dy_dtype, device=dev) if kept else None
         if fp8_a:                         # A~, its scale, and U = X~ A~^T of the forward
             self.aq = torch.empty((rank, d_in), dtype=u8, device=dev)
             self.s_a = torch.empty(1, dtype=f32, device=dev)
@@ -109,7 +146,7 @@ class MeldedLinear:
         nq = max(tokens * max(d_in, d_out), d_out * d_in)
         self.ws_q = torch.empty(fp8_quantize_workspace_bytes(nq), dtype=u8, device=dev)
         # X^ A^T with the forward product, G^ B with the dX product
-        self.use_xa = (not fp8_a and train_a and tokens > 0
+        self.use_xa = (not fp8_a and not self.epilogue and train_a and tokens > 0
                        and melded_linear_xa_fused(tokens, d_in, d_out, rank))
         if fp8_a:
             fw = melded_linear_fwd_frozen_a_workspace_bytes(tokens, d_in, rank)
@@ -144,6 +181,9 @@ class MeldedLinear:
         else:
             px = rowwise_proxy_update_workspace_bytes(d_in, d_out, rank)
         self.ws_px = torch.empty(max(1, px), dtype=u8, device=dev)
+        if bias:
+            nb = linear_act_bwd_workspace_bytes(tokens, d_out) if d_out else 0
+            self.ws_act = torch.empty(max(1, nb), dtype=u8, device=dev)
 
     def init_state(self, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, stream=None):
         """W~ = E4M3(W * s_w), s_w = 448 / max|W| (the initial quantization
@@ -171,15 +211,21 @@ class MeldedLinear:
         if self.keep_pieces:
             adapter_pieces(self.A, self.a_pieces, stream=stream)
 
-    def forward(self, X: torch.Tensor, stream=None):
+    def forward(self, X: torch.Tensor, stream=None, residual: Optional[torch.Tensor] = None):
         fp8_quantize(X, self.xq, self.s_x, ws=self.ws_q, stream=stream)
-        self.forward_product(stream)
+        self.forward_product(stream, residual)
         return self.y
 
-    def forward_product(self, stream=None):
+    def forward_product(self, stream=None, residual: Optional[torch.Tensor] = None):
         """The forward call on the quantized activations (Y, and X^ A^T or
-        X~ A~^T where the route forms it)."""
-        if self.fp8_a:
+        X~ A~^T where the route forms it); a residual (of Y's type) is added by
+        layers with an epilogue."""
+        if residual is not None and not self.epilogue:
+            raise ValueError("a residual needs a layer with an epilogue")
+        if self.epilogue:
+            melded_linear_fwd_act(self.xq, self.s_x, self.wq, self.s_w, self.y, bias=self.bias,
+                                  act=self.act, residual=residual, z=self.z, stream=stream)
+        elif self.fp8_a:
             melded_linear_fwd_frozen_a(self.xq, self.s_x, self.wq, self.s_w, self.aq, self.s_a,
                                        self.y, self.u, ws=self.ws_fwd, stream=stream)
         elif self.keep_pieces:
@@ -192,6 +238,12 @@ class MeldedLinear:
             melded_linear_fwd(self.xq, self.s_x, self.wq, self.s_w, self.y, stream=stream)
 
     def backward(self, dY: torch.Tensor, stream=None):
+        if self.dz is not None or self.dbias is not None:
+            # through the activation, and the bias's gradient
+            linear_act_bwd(dY, self.z, self.dz, dbias=self.dbias, act=self.act,
+                           ws=self.ws_act if self.dbias is not None else None, stream=stream)
+        if self.dz is not None:
+            dY = self.dz
         fp8_quantize(dY, self.gq, self.s_g, ws=self.ws_q, stream=stream, fmt=self.g_fmt)
         self.backward_product(stream)
         return self.dx

@@ -637,8 +637,8 @@ falq_status layer_norm_fwd(const void *x, int x_dtype, const float *weight, cons
  *   weight          [d] float32, or NULL (1)
  *   mean, rstd      [T] float32: the forward's
  *   dweight, dbias  [d] float32 (output), each may be NULL; zero for T = 0
- *   ws              layer_norm_bwd_workspace_bytes(T, d); not used (may be
- *                   NULL) when dweight and dbias are both NULL
+ *   ws              layer_norm_bwd_workspace_bytes(T, d) (0 for few rows); not
+ *                   used (may be NULL) when dweight and dbias are both NULL
  */
 size_t layer_norm_bwd_workspace_bytes(int64_t T, int64_t d);
 falq_status layer_norm_bwd(const void *dy, int dy_dtype, const void *x, int x_dtype,
@@ -677,11 +677,13 @@ falq_status melded_linear_fwd_act(const uint8_t *xq, const float *s_x, const uin
  * (relu'(z) = 1 for z > 0, else 0).  dz is what fp8_quantize and the product's
  * backward take as the upstream gradient; the residual's gradient is dy.
  *
- *   dy, dz   [T x d_out], one type; dz may be dy (in place), not z
+ *   dy, dz   [T x d_out], one type; dz may be dy (in place), not z, or NULL
+ *            where only dbias is wanted
  *   z        [T x d_out] float32 or bfloat16: the forward's z; NULL allowed
  *            for FALQ_ACT_NONE; any d_out from 0 to 2^24
  *   dbias    [d_out] float32 (output), or NULL; zero for T = 0
- *   ws       linear_act_bwd_workspace_bytes(T, d_out); not used without dbias
+ *   ws       linear_act_bwd_workspace_bytes(T, d_out) (0 for few rows); not used
+ *            without dbias
  */
 size_t linear_act_bwd_workspace_bytes(int64_t T, int64_t d_out);
 falq_status linear_act_bwd(const void *dy, int dy_dtype, const void *z, int z_dtype, int act,

@@ -67,10 +67,11 @@ def test_linear_act_bwd():
     assert fq.linear_act_bwd_workspace_bytes(8, 48) == 0        # few rows need none
     #     dy gt z  zt act T    d   dz db ws n   stream
     ok = [P, 0, Q, 1, 2, 1000, 48, R, S, P, ws, None]
-    refused(f, ok, [(0, None), (0, MIS), (2, None), (2, MIS), (7, None), (7, MIS), (7, Q),
+    refused(f, ok, [(0, None), (0, MIS), (2, None), (2, MIS), (7, MIS), (7, Q),
                     (1, 2), (3, 2), (4, -1), (4, 5), (5, -1), (6, -1), (6, (1 << 24) + 1),
                     (8, MIS), (9, None), (9, P + 16), (10, ws - 1)])
     assert f(None, 0, None, 0, 2, 8, 0, None, None, None, 0, None) == OK             # d_out = 0
+    assert f(P, 0, Q, 1, 2, 8, 48, None, None, None, 0, None) == EINVAL              # no output
 
 
 def arrays(ptrs, n, t):
@@ -141,6 +142,8 @@ def test_binding_refuses_before_the_library():
         fq.linear_act_bwd(x, x[:2], x.clone(), act="gelu")
     with bad:
         fq.linear_act_bwd(x, x, x.bfloat16(), act="gelu")
+    with bad:
+        fq.layer_norm_fwd(x[0], w, w, x[0].clone())               # one dimension
     with bad:
         fq.grad_norm([x], one)                                    # not on the GPU
     with bad:

@@ -200,7 +200,10 @@ def test_backward(gpu_lib, T, d, act, zt, gt):
                                + (7.6e-8 if act == "gelu" else 0.0)) + U * ref.abs()
     check(dz, ref, tol + half_step(gt) * (ref.abs() + tol), "dz")
     check(db, ref.sum(0), tol.sum(0) + (T + 8) * U * ref.abs().sum(0), "dbias")
-    # in place, and without dbias: the same bits
+    # dbias alone, in place, and without dbias: the same bits
+    alone = torch.full((d,), float("nan"), device="cuda")
+    gpu_lib.linear_act_bwd(dy.cuda(), z.cuda(), None, dbias=alone, act=act)
+    assert torch.equal(alone, db)
     inp = dy.cuda()
     gpu_lib.linear_act_bwd(inp, z.cuda(), inp, act=act)
     assert torch.equal(inp, dz)
