@@ -37,7 +37,7 @@ __all__ = ["load", "FalqError", "fp8_quantize", "fp8_quantize_workspace_bytes",
            "lora_separate_fp8_fwd", "lora_separate_fp8_bwd", "lora_bf16_saved_bytes",
            "lora_bf16_workspace_bytes", "lora_bf16_fwd", "lora_bf16_bwd", "layer_norm_fwd",
            "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "ACTIVATIONS",
-           "melded_linear_fwd_act", "linear_act_bwd", "linear_act_bwd_workspace_bytes",
+           "melded_linear_fwd_act", "melded_linear_fwd_act_workspace_bytes", "linear_act_bwd", "linear_act_bwd_workspace_bytes",
            "grad_norm", "grad_clip", "grad_norm_workspace_bytes", "GRAD_MAX_TENSORS"]
 
 #: bytes of the per-device scratch array behind fp8_quantize_noalloc
@@ -123,8 +123,9 @@ _SIGS = {
     "layer_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
     "layer_norm_bwd": (_i32, [_c_p, _i32, _c_p, _i32, _c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p,
                               _c_p, _c_p, _sz, _c_p]),
+    "melded_linear_fwd_act_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "melded_linear_fwd_act": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _i32, _c_p, _i64, _i64, _i64,
-                                     _i32, _c_p, _c_p, _c_p]),
+                                     _i32, _c_p, _c_p, _c_p, _sz, _c_p]),
     "linear_act_bwd_workspace_bytes": (_sz, [_i64, _i64]),
     "linear_act_bwd": (_i32, [_c_p, _i32, _c_p, _i32, _i32, _i64, _i64, _c_p, _c_p, _c_p, _sz,
                               _c_p]),
@@ -843,11 +844,16 @@ def _span(ws: Optional[torch.Tensor]):
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
 
 
+def melded_linear_fwd_act_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
+    return int(load().melded_linear_fwd_act_workspace_bytes(T, d_in, d_out))
+
+
 def melded_linear_fwd_act(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tensor,
                           s_w: torch.Tensor, y: torch.Tensor,
                           bias: Optional[torch.Tensor] = None, act: str = "none",
                           residual: Optional[torch.Tensor] = None,
-                          z: Optional[torch.Tensor] = None, stream=None) -> None:
+                          z: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                          stream=None) -> None:
     """z = dec(xq) dec(wq)^T / (s_x s_w) + bias and y = act(z) + residual in one
     call; y, z and residual share one type (float32 or bfloat16), bias is
     float32; residual may be y; z (None: not kept) is what linear_act_bwd takes."""
@@ -855,12 +861,14 @@ def melded_linear_fwd_act(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tensor,
     d_out = _matrix(wq, "wq")[0]
     t, a, dev = _elem(y, "y"), _act(act), _device(xq, "xq")
     u8, f32, out = torch.uint8, torch.float32, (T, d_out)
-    _run(load().melded_linear_fwd_act, "melded_linear_fwd_act", dev,
-         _arg(xq, u8, (T, d_in), dev, "xq"), _arg(s_x, f32, (1,), dev, "s_x"),
-         _arg(wq, u8, (d_out, d_in), dev, "wq"), _arg(s_w, f32, (1,), dev, "s_w"),
-         _arg(bias, f32, (d_out,), dev, "bias"), a, _arg(residual, y.dtype, out, dev, "residual"),
-         T, d_in, d_out, t, _arg(y, y.dtype, out, dev, "y"), _arg(z, y.dtype, out, dev, "z"),
-         _stream_of(dev, stream))
+    lib, st = load(), _stream_of(dev, stream)
+    args = (_arg(xq, u8, (T, d_in), dev, "xq"), _arg(s_x, f32, (1,), dev, "s_x"),
+            _arg(wq, u8, (d_out, d_in), dev, "wq"), _arg(s_w, f32, (1,), dev, "s_w"),
+            _arg(bias, f32, (d_out,), dev, "bias"), a,
+            _arg(residual, y.dtype, out, dev, "residual"), T, d_in, d_out, t,
+            _arg(y, y.dtype, out, dev, "y"), _arg(z, y.dtype, out, dev, "z"))
+    w = _scratch(ws, lib.melded_linear_fwd_act_workspace_bytes(T, d_in, d_out), dev, stream, st)
+    _run(lib.melded_linear_fwd_act, "melded_linear_fwd_act", dev, *args, *_span(w), st)
 
 
 def linear_act_bwd_workspace_bytes(T: int, d_out: int) -> int:

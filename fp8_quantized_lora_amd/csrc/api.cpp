@@ -815,10 +815,15 @@ falq_status layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x_dt
                                                 reinterpret_cast<hipStream_t>(stream)));
 }
 
+size_t melded_linear_fwd_act_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out) {
+  return gemm_dims_ok(T, d_in, d_out) ? falq::linear_act_ws_bytes(T, d_in, d_out) : 0;
+}
+
 falq_status melded_linear_fwd_act(const uint8_t* xq, const float* s_x, const uint8_t* wq,
                                   const float* s_w, const float* bias, int act,
                                   const void* residual, int64_t T, int64_t d_in, int64_t d_out,
-                                  int dtype, void* y, void* z, falq_stream stream) {
+                                  int dtype, void* y, void* z, void* ws, size_t ws_bytes,
+                                  falq_stream stream) {
   if (!gemm_dims_ok(T, d_in, d_out) || !dtype_ok(dtype)) return FALQ_EINVAL;
   if (act < FALQ_ACT_NONE || act > FALQ_ACT_SILU) return FALQ_EINVAL;
   if (!scalar(s_x) || !scalar(s_w) || !opt(bias)) return FALQ_EINVAL;
@@ -826,8 +831,10 @@ falq_status melded_linear_fwd_act(const uint8_t* xq, const float* s_x, const uin
   if (d_out * d_in > 0 && !need(wq)) return FALQ_EINVAL;
   if (T * d_out > 0 && (!need(y) || !opt(z) || !opt(residual))) return FALQ_EINVAL;
   if (T * d_out > 0 && z && (z == y || z == residual)) return FALQ_EINVAL;
+  if (!ws_ok(ws, ws_bytes, falq::linear_act_ws_bytes(T, d_in, d_out))) return FALQ_EINVAL;
   return hip_status(falq::launch_linear_act(xq, s_x, wq, s_w, bias, residual, T, d_in, d_out, act,
-                                            dtype, y, z, reinterpret_cast<hipStream_t>(stream)));
+                                            dtype, y, z, ws,
+                                            reinterpret_cast<hipStream_t>(stream)));
 }
 
 size_t linear_act_bwd_workspace_bytes(int64_t T, int64_t d_out) {

@@ -13,7 +13,7 @@
 //
 // Work is counted in chunks of 256 threads x 16 bytes from each tensor's
 // address rounded down to 16 bytes: the 16-byte accesses then fit a tensor that
-// starts at any element, and only vectors across its ends are done element by
+// starts at any element, and only part vectors at its ends are done element by
 // element.  Runs of kAhead chunks are dealt round the workgroups (one long run
 // for each would put them all on the same memory channels where sizes are powers
 // of two: 160 M floats 375 us), a run's loads all in flight.  The second pass
@@ -65,12 +65,16 @@ __device__ __forceinline__ int lead_of(const GT* g) {
 
 // The thread's vectors of chunks [a, b) of a tensor, in order or (BACK) from the
 // last to the first: many(i) has kAhead whole vectors at elements i,
-// i + kChunk, ...; one(i) a whole vector; each(i) one element of a vector
-// across an end.
+// i + kChunk, ...; one(i) a whole vector; each(i) one element of the part
+// vectors at the tensor's two ends, which a thread each takes.
 template <bool BACK, class GT, class Many, class One, class Each>
 __device__ __forceinline__ void run_of(const GT* g, int64_t n, int64_t a, int64_t b, Many&& many,
                                        One&& one, Each&& each) {
-  const int64_t lead = lead_of(g), mine = (int64_t)threadIdx.x * kVec<GT> - lead;
+  constexpr int V = kVec<GT>;
+  const int tid = (int)threadIdx.x;
+  const int64_t lead = lead_of(g), mine = (int64_t)tid * V - lead;
+  const int64_t head = lead == 0 ? 0 : (V - lead < n ? V - lead : n);
+  const int64_t last = (n + lead) / V * V - lead, tail = last > head ? last : head;
   while (a < b) {
     const int64_t first = BACK ? b - kAhead : a;
     if (b - a >= kAhead && first * kChunk<GT> >= lead &&
@@ -79,22 +83,26 @@ __device__ __forceinline__ void run_of(const GT* g, int64_t n, int64_t a, int64_
       (BACK ? b : a) += BACK ? -kAhead : kAhead;
       continue;
     }
-    const int64_t i = (BACK ? --b : a++) * kChunk<GT> + mine;
-    if (i >= 0 && i + kVec<GT> <= n) {
-      one(i);
-    } else if (i + kVec<GT> > 0 && i < n) {
-      for (int64_t j = i < 0 ? 0 : i; j < (i + kVec<GT> < n ? i + kVec<GT> : n); ++j) each(j);
-    }
+    const int64_t c = BACK ? --b : a++, i = c * kChunk<GT> + mine;
+    if (i >= 0 && i + V <= n) one(i);
+    if (c == 0 && tid < head) each(tid);
+    if (tid >= V && tid - V < n - tail && (tail + lead) / kChunk<GT> == c) each(tail + tid - V);
   }
+}
+
+// chunks in a workgroup's run: kAhead, fewer where there are not enough for all
+__host__ __device__ __forceinline__ uint32_t run_chunks(uint32_t chunks) {
+  const uint32_t r = chunks / kMaxBlocks;
+  return r < 1 ? 1 : r > kAhead ? kAhead : r;
 }
 
 // f(entry, a, b) for the workgroup's runs of chunks, tensor by tensor
 template <bool BACK, class Tab, class F>
 __device__ __forceinline__ void walk(const Tab& t, F&& f) {
-  const uint32_t runs = (t.chunks + kAhead - 1) / kAhead;
+  const uint32_t len = run_chunks(t.chunks), runs = (t.chunks + len - 1) / len;
   for (uint32_t r = blockIdx.x; r < runs; r += gridDim.x) {
-    uint32_t c0 = (BACK ? runs - 1 - r : r) * kAhead;
-    uint32_t c1 = c0 + kAhead < t.chunks ? c0 + kAhead : t.chunks;
+    uint32_t c0 = (BACK ? runs - 1 - r : r) * len;
+    uint32_t c1 = c0 + len < t.chunks ? c0 + len : t.chunks;
     const uint32_t begin = BACK ? c1 - 1 : c0;
     int k = 0, hi = t.count - 1;               // the tensor of that chunk
     while (k < hi) {
@@ -241,7 +249,8 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(Tab t, const double* __
 template <class Tab>
 hipError_t passes(const Tab& t, int64_t bytes, float max_norm, float eps, bool clip, float* norm,
                   double* part, hipStream_t s) {
-  const int blocks = (int)std::min<uint32_t>(t.chunks, kMaxBlocks);
+  const uint32_t len = run_chunks(t.chunks);
+  const int blocks = (int)std::min<uint32_t>((t.chunks + len - 1) / len, kMaxBlocks);
   if (blocks) squares_kernel<Tab><<<blocks, kThreads, 0, s>>>(t, part);
   if (blocks && clip && 2 * bytes > kStreamBytes)
     scale_kernel<Tab, true><<<blocks, kThreads, 0, s>>>(t, part, blocks, max_norm, eps, norm);

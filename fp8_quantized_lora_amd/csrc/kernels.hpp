@@ -239,10 +239,11 @@ hipError_t launch_layer_norm_bwd(const void* dy, int gt, const void* x, int xt, 
                                  void* dx, float* dw, float* db, void* ws, hipStream_t s);
 
 // ---- linear layer with an epilogue, and the epilogue's backward -------------
+size_t linear_act_ws_bytes(int64_t T, int64_t d_in, int64_t d_out);
 hipError_t launch_linear_act(const uint8_t* xq, const float* s_x, const uint8_t* wq,
                              const float* s_w, const float* bias, const void* residual, int64_t T,
                              int64_t d_in, int64_t d_out, int act, int dtype, void* y, void* z,
-                             hipStream_t s);
+                             void* ws, hipStream_t s);
 size_t linear_act_bwd_ws_bytes(int64_t T, int64_t d);
 // dz or dbias may be null (without dbias ws is not used); dz may be dy
 hipError_t launch_linear_act_bwd(const void* dy, int gt, const void* z, int zt, int64_t T,

@@ -53,33 +53,94 @@ hipError_t launch_few(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, 
   return hipGetLastError();
 }
 
-// Which tile: the one whose rounds of the 256 CUs take least.  A round of
-// tiles costs, at 4096 K-bytes (us, measured at 256, 512, 768 and 1024 tiles;
-// 5 more for the first loads and the last stores, whatever the tile):
-//     256 x 320   75     256 x 256   58     128 x 128   20
-//      64 x 128   11      64 x  64    7      32 x  64    5.6
-// so a larger tile moves fewer bytes per product but leaves more of its last
-// round empty.  512 x 4096 outputs: 15.3 in tiles of 64 x 128 (one round), 18.9
-// in 128 x 128 (half a round), 17.5 in 32 x 128; 128 x 4096: 10.0 in 32 x 64,
-// 10.9 in 64 x 64, 14 in 64 x 128.
+// Which tile: the one whose rounds of the 256 CUs take least.  A K step of a
+// round of tiles costs (us, measured at 256 to 1024 tiles and 4096 and 8192
+// K-bytes)
+//     256 x 320  2.1      256 x 256  1.68     128 x 128  0.62
+//      64 x 128  0.55      64 x  64  0.27      32 x  64  0.24
+// and a launch about 4 more for the first loads and the last stores: a larger
+// tile moves fewer bytes per product but leaves more of its last round empty.
+// 512 x 4096 x 4096: 15.3 in tiles of 64 x 128 (one round), 18.9 in 128 x 128
+// (half a round), 17.5 in 32 x 128; 128 x 4096: 10.0 in 32 x 64, 10.9 in 64 x
+// 64, 14 in 64 x 128; 4096 x 5120 x 13824: 230 in 256 x 320 (one round), 252 in
+// a round of 256 x 256 and one of 128 x 128, 345 in 256 x 256.
 enum TileKind { k256, k256x320, k128, k64x128, k64, k32x64, kTileKinds };
 constexpr int kTileM[kTileKinds] = {256, 256, 128, 64, 64, 32};
 constexpr int kTileN[kTileKinds] = {256, 320, 128, 128, 64, 64};
-constexpr float kRound[kTileKinds] = {58.0f, 75.0f, 20.0f, 11.0f, 7.0f, 5.6f};
+constexpr float kStep[kTileKinds] = {1.68f, 2.1f, 0.62f, 0.55f, 0.27f, 0.24f};
+constexpr float kLaunch = 4.0f;
 constexpr int kCUs = 256;
 
-float tile_cost(TileKind k, int64_t M, int64_t n) {
-  const int64_t nt = ((M + kTileM[k] - 1) / kTileM[k]) * ((n + kTileN[k] - 1) / kTileN[k]);
-  // a grid holds fewer than 2^32 threads: very long outputs take large tiles
-  if (k != k256 && nt >= 1 << 23) return HUGE_VALF;
-  return kRound[k] * (float)((nt + kCUs - 1) / kCUs);
+int64_t tiles_of(TileKind k, int64_t M, int64_t n) {
+  return ((M + kTileM[k] - 1) / kTileM[k]) * ((n + kTileN[k] - 1) / kTileN[k]);
 }
 
-TileKind best_tile(int64_t M, int64_t n) {
+float tile_cost(TileKind k, int64_t M, int64_t n, int64_t steps) {
+  const int64_t nt = tiles_of(k, M, n);
+  // a grid holds fewer than 2^32 threads: very long outputs take large tiles
+  if (k != k256 && nt >= 1 << 23) return HUGE_VALF;
+  return kLaunch + kStep[k] * (float)steps * (float)((nt + kCUs - 1) / kCUs);
+}
+
+TileKind best_tile(int64_t M, int64_t n, int64_t steps) {
   int best = 0;
   for (int k = 1; k < kTileKinds; ++k)
-    if (tile_cost((TileKind)k, M, n) < tile_cost((TileKind)best, M, n)) best = k;
+    if (tile_cost((TileKind)k, M, n, steps) < tile_cost((TileKind)best, M, n, steps)) best = k;
   return (TileKind)best;
+}
+
+// How a product runs: by few tokens, by tiles of one kind, by whole rounds of
+// 256 x 256 tiles (cols of their columns) and the remaining columns in tiles of
+// `kind`, or by 128 x 128 tiles split over K (`split` parts, kc steps each).
+struct Plan {
+  int few = 0;
+  TileKind kind = k256;
+  int64_t cols = 0;
+  int split = 1, kc = 0;
+};
+
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  Plan p;
+  const int64_t steps = (K + 127) / 128;
+  // few tokens: 4096 x 4096 5.6 us at 1 token and 6.6 at 16 (tiles of 32 x 64:
+  // 9.5); at 32 tokens 8.3 against 9.6 while one workgroup per CU holds all
+  // columns, 21 against 14.4 at 11008 columns
+  if (K > 0 && M <= 16) p.few = 1;
+  if (K > 0 && M > 16 && M <= 32 && N <= 16 * kCUs) p.few = 2;
+  if (p.few) return p;
+  p.kind = best_tile(M, N, steps);
+  float cost = tile_cost(p.kind, M, N, steps);
+  // whole rounds of large tiles, and the columns of a short last round in
+  // smaller ones by a second launch
+  const int64_t tM = (M + 255) / 256, tN = (N + 255) / 256;
+  const int64_t c = tM * tN / kCUs * kCUs / tM;              // tile columns in whole rounds
+  if (c > 0 && c < tN) {
+    const TileKind k2 = best_tile(M, N - c * 256, steps);
+    const float both = tile_cost(k256, M, c * 256, steps) + tile_cost(k2, M, N - c * 256, steps);
+    if (both < cost) {
+      cost = both;
+      p.kind = k2;
+      p.cols = c * 256;
+    }
+  }
+  // few tiles and a long K: as many splits as give a workgroup to each CU, at
+  // least 8 steps each, and the planes written and read once at 4 TB/s.  64 x
+  // 5120 x 13824: 22.5 us in 6 splits, 32.5 whole; 100 x 4096 x 11008: 19.8 in
+  // 8, 25.8 whole; 512 x 4096 x 4096 21.1 in 2, 15.3 whole.
+  const int64_t nt = tiles_of(k128, M, N);
+  const int64_t s = nt > 0 ? std::min<int64_t>(kCUs / nt, steps / 8) : 0;
+  if (s >= 2) {
+    const int64_t kc = (steps + s - 1) / s, parts = (steps + kc - 1) / kc;
+    const float split = 2 * kLaunch + kStep[k128] * (float)kc +
+                        (float)(parts * M * N) * 8.0f / 4e6f;
+    if (parts >= 2 && split < cost) {
+      p.kind = k128;
+      p.cols = 0;
+      p.split = (int)parts;
+      p.kc = (int)kc;
+    }
+  }
+  return p;
 }
 
 template <class OT>
@@ -100,39 +161,49 @@ hipError_t launch_kind(TileKind k, const uint8_t* A, const uint8_t* B, int64_t M
 }
 
 template <class OT>
-hipError_t by_size(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
-                   const Epilogue& ep, hipStream_t s) {
-  // few tokens: 4096 x 4096 5.6 us at 1 token and 6.6 at 16 (tiles of 32 x 64:
-  // 9.5); at 32 tokens 8.3 against 9.6 while one workgroup per CU holds all
-  // columns, 21 against 14.4 at 11008 columns
-  if (K > 0 && M <= 16) return launch_few<1, 1, 16, 1, OT>(A, B, M, N, K, ep, s);
-  if (K > 0 && M <= 32 && N <= 16 * kCUs) return launch_few<2, 1, 8, 2, OT>(A, B, M, N, K, ep, s);
-  const TileKind k = best_tile(M, N);
-  // whole rounds of large tiles, and the columns of a short last round in
-  // smaller ones (a second launch, about 3 us)
-  const int64_t tM = (M + 255) / 256, tN = (N + 255) / 256;
-  const int64_t c = tM * tN / kCUs * kCUs / tM;              // tile columns in whole rounds
-  if (c > 0 && c < tN) {
-    const TileKind k2 = best_tile(M, N - c * 256);
-    if (tile_cost(k256, M, c * 256) + tile_cost(k2, M, N - c * 256) + 3.0f < tile_cost(k, M, N)) {
-      const hipError_t e = launch_kind<OT>(k256, A, B, M, N, K, 0, c * 256, ep, s);
-      if (e != hipSuccess) return e;
-      return launch_kind<OT>(k2, A, B, M, N, K, c * 256, N, ep, s);
-    }
+hipError_t launch_split(const Plan& p, const uint8_t* A, const uint8_t* B, int64_t M, int64_t N,
+                        int64_t K, const Epilogue& ep, float* part, hipStream_t s) {
+  using C = Tile<128, 128, 2, 4, 3>;
+  const int tM = (int)((M + C::BM - 1) / C::BM), tN = (int)((N + C::BN - 1) / C::BN);
+  linear_act_tile<C, OT, false, true><<<tM * tN * p.split, C::kThreads, 0, s>>>(
+      A, B, (int)M, (int)N, (int)K, 0, tM, tN, ep, part, p.kc);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int blocks = (int)std::min<int64_t>((M * N / 8 + 255) / 256, 2048);
+  linear_act_join<OT><<<blocks, 256, 0, s>>>(part, p.split, M, (int)N, ep);
+  return hipGetLastError();
+}
+
+template <class OT>
+hipError_t by_plan(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
+                   const Epilogue& ep, float* part, hipStream_t s) {
+  const Plan p = plan_of(M, N, K);
+  if (p.few == 1) return launch_few<1, 1, 16, 1, OT>(A, B, M, N, K, ep, s);
+  if (p.few == 2) return launch_few<2, 1, 8, 2, OT>(A, B, M, N, K, ep, s);
+  if (p.split > 1) return launch_split<OT>(p, A, B, M, N, K, ep, part, s);
+  if (p.cols > 0) {
+    const hipError_t e = launch_kind<OT>(k256, A, B, M, N, K, 0, p.cols, ep, s);
+    if (e != hipSuccess) return e;
   }
-  return launch_kind<OT>(k, A, B, M, N, K, 0, N, ep, s);
+  return launch_kind<OT>(p.kind, A, B, M, N, K, p.cols, N, ep, s);
 }
 
 }  // namespace
 
+size_t linear_act_ws_bytes(int64_t T, int64_t d_in, int64_t d_out) {
+  if (T == 0 || d_out == 0) return 0;
+  const Plan p = plan_of(T, d_out, d_in);
+  return p.split > 1 ? (size_t)p.split * (size_t)T * (size_t)d_out * 4 : 0;
+}
+
 hipError_t launch_linear_act(const uint8_t* xq, const float* s_x, const uint8_t* wq,
                              const float* s_w, const float* bias, const void* residual, int64_t T,
                              int64_t d_in, int64_t d_out, int act, int dtype, void* y, void* z,
-                             hipStream_t s) {
+                             void* ws, hipStream_t s) {
   if (T == 0 || d_out == 0) return hipSuccess;
   const Epilogue ep{s_x, s_w, bias, residual, y, z, act};
-  return dtype == 0 ? by_size<float>(xq, wq, T, d_out, d_in, ep, s)
-                    : by_size<__bf16>(xq, wq, T, d_out, d_in, ep, s);
+  return dtype == 0 ? by_plan<float>(xq, wq, T, d_out, d_in, ep, (float*)ws, s)
+                    : by_plan<__bf16>(xq, wq, T, d_out, d_in, ep, (float*)ws, s);
 }
 
 }  // namespace falq

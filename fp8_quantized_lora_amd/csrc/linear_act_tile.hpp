@@ -43,18 +43,23 @@ __device__ __forceinline__ void wait_stages(int ahead) {
 // STREAM: the outputs go past the caches, which keeps the operands in them
 // (kStreamBytes in elem.hpp; 8192 x 11008 x 4096 with two bf16 outputs: 336 us,
 // 386 without, one launch of 256 x 256 tiles)
-template <class C, class OT, bool STREAM>
+// SPLIT (few tiles, long K): workgroup b takes tile b % tiles and the kc K steps
+// of split b / tiles, and writes its sums, unscaled, to that split's plane of
+// `part` ([M x N] floats each); linear_act_join adds the planes in order.
+template <class C, class OT, bool STREAM, bool SPLIT = false>
 __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int n_first,
-    int tilesM, int tilesN, Epilogue ep) {
+    int tilesM, int tilesN, Epilogue ep, float* __restrict__ part = nullptr, int kc = 0) {
   constexpr int BK = C::BK, MB = C::MB, NB = C::NB;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::S * C::STAGE];
   int tm, tn;
-  gemm::tile_of(gemm::xcd_remap(blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
+  const int nt = tilesM * tilesN, sp = SPLIT ? (int)blockIdx.x / nt : 0;
+  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x - sp * nt, nt), tilesM, tilesN, tm, tn);
   const int m0 = tm * C::BM, n0 = n_first + tn * C::BN;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w / C::WGN, wn = w % C::WGN;
   // the step at nk, if any, is the one of rem bytes
-  const int nk = K / BK, rem = K % BK, steps = nk + (rem > 0);
+  const int nk = K / BK, rem = K % BK, all = nk + (rem > 0);
+  const int k_lo = SPLIT ? sp * kc : 0, steps = SPLIT ? min(all, k_lo + kc) : all;
 
   v4f acc[MB][NB];
 #pragma unroll
@@ -105,7 +110,7 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
     }
   };
   auto fetch = [&](int kt) {
-    const int stage = kt % C::S;
+    const int stage = (kt - k_lo) % C::S;
     if (kt < nk)
       issue(stage, kt * BK);
     else
@@ -113,7 +118,7 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
   };
 #pragma unroll
   for (int s = 0; s < C::S - 1; ++s)
-    if (s < steps) fetch(s);
+    if (k_lo + s < steps) fetch(k_lo + s);
 
   const int r16 = lane & 15, g = lane >> 4;
   const int sw = gemm::dma::swz(r16);
@@ -149,15 +154,16 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
     }
   };
   __builtin_amdgcn_s_waitcnt(0xC07F);                        // lgkmcnt(0)
-  for (int kt = 0; kt < nk; ++kt) {
+  const int k_whole = min(steps, nk);
+  for (int kt = k_lo; kt < k_whole; ++kt) {
     wait_stages<C::S - 2, C::LPS>(steps - 1 - kt);
     barrier_no_drain();
-    step(smem + kt % C::S * C::STAGE, [&] {
+    step(smem + (kt - k_lo) % C::S * C::STAGE, [&] {
       if (kt + C::S - 1 < steps) fetch(kt + C::S - 1);
     });
   }
-  if (rem) {
-    uint8_t* st = smem + nk % C::S * C::STAGE;
+  if (rem && steps == all) {
+    uint8_t* st = smem + (nk - k_lo) % C::S * C::STAGE;
     wait_vmem(0);
     barrier_no_drain();
     const int valid = rem / 16;                              // chunks of K in the step
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
   float bias[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
-  if (ep.bias && col_ok) load_elems<8>(ep.bias + col, bias);
+  if (!SPLIT && ep.bias && col_ok) load_elems<8>(ep.bias + col, bias);
   auto rows = [&](auto act, int first) {
     for (int r = rl; r < C::PASS; r += RPI) {                // lanes past RPI rows: idle
       const int row = m0 + wm * C::WTM + first + r;
@@ -192,7 +198,10 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
       const v4f b = mine[slot(r, 2 * cl + 1)];
       if (!col_ok || row >= M) continue;
       float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      finish8<decltype(act)::value, OT, STREAM>(v, scale, bias, ep, (int64_t)row * N + col);
+      if constexpr (SPLIT)
+        store_elems<8>(part + ((int64_t)sp * M + row) * N + col, v);
+      else
+        finish8<decltype(act)::value, OT, STREAM>(v, scale, bias, ep, (int64_t)row * N + col);
     }
   };
 #pragma unroll
@@ -206,12 +215,49 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
         mine[slot(i * 16 + r16, 4 * j + g)] = acc[p * (C::PASS / 16) + i][j];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int first = p * C::PASS;
-    switch (ep.act) {
+    switch (SPLIT ? (int)kNone : ep.act) {
       case kRelu: rows(std::integral_constant<int, kRelu>{}, first); break;
       case kGelu: rows(std::integral_constant<int, kGelu>{}, first); break;
       case kGeluTanh: rows(std::integral_constant<int, kGeluTanh>{}, first); break;
       case kSilu: rows(std::integral_constant<int, kSilu>{}, first); break;
       default: rows(std::integral_constant<int, kNone>{}, first); break;
+    }
+  }
+}
+
+
+// y (and z) from the S planes of partial sums
+template <int ACT, class OT>
+__device__ __forceinline__ void join8(const float* __restrict__ part, int S, int64_t plane,
+                                      int64_t at, int col, float scale, const Epilogue& ep) {
+  float v[8], bias[8];
+  load_elems<8>(part + at, v);
+  for (int s = 1; s < S; ++s) {
+    float t[8];
+    load_elems<8>(part + s * plane + at, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
+  if (ep.bias) load_elems<8>(ep.bias + col, bias);
+  finish8<ACT, OT, false>(v, scale, bias, ep, at);
+}
+template <class OT>
+__global__ __launch_bounds__(256) void linear_act_join(const float* __restrict__ part, int S,
+                                                       int64_t M, int N, Epilogue ep) {
+  const int64_t plane = M * N;
+  const float scale = 1.0f / (ep.sa[0] * ep.sb[0]);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < plane / 8;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t at = i * 8;
+    const int col = (int)(at % N);
+    switch (ep.act) {
+      case kRelu: join8<kRelu, OT>(part, S, plane, at, col, scale, ep); break;
+      case kGelu: join8<kGelu, OT>(part, S, plane, at, col, scale, ep); break;
+      case kGeluTanh: join8<kGeluTanh, OT>(part, S, plane, at, col, scale, ep); break;
+      case kSilu: join8<kSilu, OT>(part, S, plane, at, col, scale, ep); break;
+      default: join8<kNone, OT>(part, S, plane, at, col, scale, ep); break;
     }
   }
 }

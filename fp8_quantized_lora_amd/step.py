@@ -56,7 +56,8 @@ from . import (fp8_quantize, fp8_quantize_workspace_bytes, fp8_dequantize, melde
                adamw_state, rowwise_proxy_update, rowwise_proxy_update_workspace_bytes,
                rowwise_proxy_update_topk_rank, rowwise_proxy_update_topk_rank_workspace_bytes,
                adapter_pieces_bytes, adapter_pieces, adapter_step_pieces,
-               melded_linear_fwd_xa_pieces, melded_linear_fwd_act, linear_act_bwd,
+               melded_linear_fwd_xa_pieces, melded_linear_fwd_act,
+               melded_linear_fwd_act_workspace_bytes, linear_act_bwd,
                linear_act_bwd_workspace_bytes, grad_clip, ACTIVATIONS)
 
 
@@ -152,6 +153,9 @@ class MeldedLinear:
             fw = melded_linear_fwd_frozen_a_workspace_bytes(tokens, d_in, rank)
             bw = melded_linear_bwd_frozen_a_workspace_bytes(tokens, d_in, d_out, rank)
             self.ws_fwd = torch.empty(max(1, fw), dtype=u8, device=dev)
+        elif self.epilogue:
+            nb = melded_linear_fwd_act_workspace_bytes(tokens, d_in, d_out)
+            self.ws_fwd = torch.empty(max(1, nb), dtype=u8, device=dev)
         elif self.use_xa:
             self.xa = torch.empty((tokens, rank), dtype=f32, device=dev)
             fw = melded_linear_fwd_xa_workspace_bytes(tokens, d_in, d_out, rank)
@@ -224,7 +228,8 @@ class MeldedLinear:
             raise ValueError("a residual needs a layer with an epilogue")
         if self.epilogue:
             melded_linear_fwd_act(self.xq, self.s_x, self.wq, self.s_w, self.y, bias=self.bias,
-                                  act=self.act, residual=residual, z=self.z, stream=stream)
+                                  act=self.act, residual=residual, z=self.z, ws=self.ws_fwd,
+                                  stream=stream)
         elif self.fp8_a:
             melded_linear_fwd_frozen_a(self.xq, self.s_x, self.wq, self.s_w, self.aq, self.s_a,
                                        self.y, self.u, ws=self.ws_fwd, stream=stream)

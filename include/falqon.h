@@ -665,11 +665,15 @@ typedef enum {
  *   residual          [T x d_out] of type dtype, or NULL; may be y (added in place)
  *   y                 [T x d_out] of type dtype (output)
  *   z                 [T x d_out] of type dtype (output), or NULL; not y or residual
+ *   ws                melded_linear_fwd_act_workspace_bytes(T, d_in, d_out): 0
+ *                     (ws may be NULL) unless few outputs meet a long d_in
  */
+size_t melded_linear_fwd_act_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
 falq_status melded_linear_fwd_act(const uint8_t *xq, const float *s_x, const uint8_t *wq,
                                   const float *s_w, const float *bias, int act,
                                   const void *residual, int64_t T, int64_t d_in, int64_t d_out,
-                                  int dtype, void *y, void *z, falq_stream stream);
+                                  int dtype, void *y, void *z, void *ws, size_t ws_bytes,
+                                  falq_stream stream);
 
 /*
  * linear_act_bwd — the backward of that epilogue:

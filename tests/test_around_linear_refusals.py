@@ -49,15 +49,22 @@ def test_layer_norm_bwd():
 
 def test_linear_act_fwd():
     f = fq.load().melded_linear_fwd_act
-    #     xq sx wq sw b  act res T  di  do  t  y  z     stream
-    ok = [P, P, Q, P, R, 2, S, 8, 32, 48, 1, P, Q, None]
+    assert fq.melded_linear_fwd_act_workspace_bytes(8, 32, 48) == 0
+    assert fq.melded_linear_fwd_act_workspace_bytes(8, 33, 48) == 0
+    nb = fq.melded_linear_fwd_act_workspace_bytes(64, 13824, 5120)
+    assert nb >= 2 * 64 * 5120 * 4                              # split over d_in
+    #     xq sx wq sw b  act res T  di  do  t  y  z  ws n  stream
+    ok = [P, P, Q, P, R, 2, S, 64, 13824, 5120, 1, P, Q, R, nb, None]
+    refused(f, ok, [(13, None), (13, P + 16), (14, nb - 1)])
+    ok = [P, P, Q, P, R, 2, S, 8, 32, 48, 1, P, Q, None, 0, None]
     refused(f, ok, [(0, None), (0, MIS), (1, None), (1, P + 2), (2, None), (3, None), (4, MIS),
                     (5, -1), (5, 5), (6, MIS), (7, -1), (8, 24), (9, 40), (10, 2), (11, None),
                     (11, MIS), (12, MIS), (12, P), (12, S), (7, 1 << 31)])
     # more 256 x 256 tiles than a 32-bit grid holds
-    assert f(P, P, Q, P, None, 0, None, 1 << 30, 32, 1 << 30, 1, R, None, None) == EINVAL
-    assert f(None, P, Q, P, None, 0, None, 0, 32, 48, 1, None, None, None) == OK     # T = 0
-    assert f(P, P, None, P, None, 0, None, 4, 32, 0, 1, None, None, None) == OK      # d_out = 0
+    assert f(P, P, Q, P, None, 0, None, 1 << 30, 32, 1 << 30, 1, R, None, None, 0,
+             None) == EINVAL
+    assert f(None, P, Q, P, None, 0, None, 0, 32, 48, 1, None, None, None, 0, None) == OK  # T = 0
+    assert f(P, P, None, P, None, 0, None, 4, 32, 0, 1, None, None, None, 0, None) == OK   # d_out
 
 
 def test_linear_act_bwd():

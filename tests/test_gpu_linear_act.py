@@ -109,6 +109,7 @@ SHAPES = [  # (T, d_in, d_out): one token, a few, every tile size, ragged in eac
     (17, 1040, 80), (37, 528, 1008), (64, 384, 128), (65, 2048, 320), (130, 400, 272),
     (200, 112, 1552), (257, 640, 784), (513, 1152, 1280), (1100, 240, 2576), (3000, 128, 2832),
     (3900, 272, 5120), (2304, 160, 8208), (4096, 96, 6416),
+    (64, 8208, 512), (100, 6160, 784), (40, 13824, 272),     # split over d_in, ragged ends
 ]
 
 
@@ -117,6 +118,8 @@ SHAPES = [  # (T, d_in, d_out): one token, a few, every tile size, ragged in eac
 def test_forward(gpu_lib, T, d_in, d_out, dtype):
     act = ACTS[(T + d_in + d_out // 16) % 5]
     announce(f"melded_linear_fwd_act T={T} d_in={d_in} d_out={d_out} {act} {dtype}")
+    if d_in > 4096:
+        assert gpu_lib.melded_linear_fwd_act_workspace_bytes(T, d_in, d_out) > 0
     p = problem(T + d_in, T, d_in, d_out, dtype)
     z, tz, y, ty = reference(p, act, True, True)
     gy, gz = run(gpu_lib, p, act, dtype)
