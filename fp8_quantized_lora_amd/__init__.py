@@ -867,7 +867,9 @@ def melded_linear_fwd_act(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tensor,
             _arg(bias, f32, (d_out,), dev, "bias"), a,
             _arg(residual, y.dtype, out, dev, "residual"), T, d_in, d_out, t,
             _arg(y, y.dtype, out, dev, "y"), _arg(z, y.dtype, out, dev, "z"))
-    w = _scratch(ws, lib.melded_linear_fwd_act_workspace_bytes(T, d_in, d_out), dev, stream, st)
+    # up to 16 tokens need no workspace (and are bound by the host)
+    need = 0 if T <= 16 else lib.melded_linear_fwd_act_workspace_bytes(T, d_in, d_out)
+    w = _scratch(ws, need, dev, stream, st)
     _run(lib.melded_linear_fwd_act, "melded_linear_fwd_act", dev, *args, *_span(w), st)
 
 

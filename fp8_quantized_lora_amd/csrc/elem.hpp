@@ -1,8 +1,7 @@
 // Loads and stores of float32 / bfloat16 elements as floats, and wave sums, for
 // the row-wise operators.
 //
-// E consecutive elements per lane: 4 or 8, or 1 where rows are not aligned for
-// that.  Stores of float32 take 4, 16 bytes a lane, so that a wave's store is
+// E consecutive elements per lane: 4 or 8 (1 for rows shorter than that).  Stores of float32 take 4, 16 bytes a lane, so that a wave's store is
 // one run of whole 128-byte lines: 32 bytes of a lane are two stores of half
 // lines each, which the streaming hint below does not join again (backward of
 // an activation, 8192 x 11008, fp32 gradients: 216 us with 8, 175 with 4).
@@ -22,26 +21,27 @@ typedef float v8f __attribute__((ext_vector_type(8)));
 // calls leave their results in the caches for the next one.
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 
-// the vector of E elements of T in memory
+// the vector of E elements of T in memory, aligned as T is: the 16-byte accesses
+// work at any element, at full speed where the address is a multiple of 16
 template <class T, int E>
 struct VecOf {
   typedef T type;
 };
 template <>
 struct VecOf<float, 4> {
-  typedef v4f type;
+  typedef v4f type __attribute__((aligned(4)));
 };
 template <>
 struct VecOf<float, 8> {
-  typedef v8f type;
+  typedef v8f type __attribute__((aligned(4)));
 };
 template <>
 struct VecOf<__bf16, 4> {
-  typedef v2i type;
+  typedef v2i type __attribute__((aligned(2)));
 };
 template <>
 struct VecOf<__bf16, 8> {
-  typedef v4i type;
+  typedef v4i type __attribute__((aligned(2)));
 };
 
 // E elements as they lie in memory, for a load well ahead of its use
@@ -77,7 +77,7 @@ __device__ __forceinline__ void load_elems(const float* p, float (&v)[E]) {
   } else {
 #pragma unroll
     for (int h = 0; h < E / 4; ++h) {
-      const v4f a = *reinterpret_cast<const v4f*>(p + 4 * h);
+      const VecOf<float, 4>::type a = *reinterpret_cast<const VecOf<float, 4>::type*>(p + 4 * h);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * h + e] = a[e];
     }
@@ -100,9 +100,9 @@ __device__ __forceinline__ void store_elems(float* p, const float (&v)[E]) {
     for (int h = 0; h < E / 4; ++h) {
       const v4f a = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
       if constexpr (STREAM)
-        __builtin_nontemporal_store(a, reinterpret_cast<v4f*>(p + 4 * h));
+        __builtin_nontemporal_store(a, reinterpret_cast<VecOf<float, 4>::type*>(p + 4 * h));
       else
-        *reinterpret_cast<v4f*>(p + 4 * h) = a;
+        *reinterpret_cast<VecOf<float, 4>::type*>(p + 4 * h) = a;
     }
   }
 }
@@ -123,6 +123,33 @@ __device__ __forceinline__ void store_elems(__bf16* p, const float (&v)[E]) {
       *reinterpret_cast<V*>(p) = __builtin_bit_cast(V, a);
   }
 }
+
+// A lane's E elements of a row of d, from element i on.  ODD: d is no multiple of
+// E, and the last piece ends with the row: it begins `over` elements early, and
+// those are its neighbour's, to be left out of sums and stores.
+template <int E, bool ODD>
+struct Piece {
+  uint32_t base;
+  int over;
+  bool any;
+  __device__ __forceinline__ Piece(uint32_t i, uint32_t d) : base(i), over(0), any(i < d) {
+    if (ODD && any && i + E > d) {
+      over = (int)(i + E - d);
+      base = d - E;
+    }
+  }
+  __device__ __forceinline__ bool own(int e) const { return !ODD || e >= over; }
+  template <bool STREAM = false, class T>
+  __device__ __forceinline__ void store(T* row, const float (&v)[E]) const {
+    if (!ODD || over == 0) {
+      store_elems<E, STREAM>(row + base, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e >= over) row[base + e] = (T)v[e];
+    }
+  }
+};
 
 // Sum over the wave's 64 lanes, in every lane.  Within rows of 16 lanes by
 // shifts, then across the rows: cross-lane operands of ordinary additions,

@@ -90,9 +90,10 @@ __device__ __forceinline__ void run_of(const GT* g, int64_t n, int64_t a, int64_
   }
 }
 
-// chunks in a workgroup's run: kAhead, fewer where there are not enough for all
+// chunks in a workgroup's run: kAhead, fewer where there are not enough for two
+// workgroups per CU (4 M floats: 14.9 us, 18.6 with short runs on 2048 workgroups)
 __host__ __device__ __forceinline__ uint32_t run_chunks(uint32_t chunks) {
-  const uint32_t r = chunks / kMaxBlocks;
+  const uint32_t r = chunks / 512;
   return r < 1 ? 1 : r > kAhead ? kAhead : r;
 }
 
@@ -182,8 +183,14 @@ __global__ __launch_bounds__(kThreads) void squares_kernel(Tab t, double* __rest
 
 // the norm from the partial sums, the same in every thread of every workgroup
 __device__ __forceinline__ double norm_of(const double* __restrict__ part, int P) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < P; i += kThreads) s += part[i];
+  double v[kMaxBlocks / kThreads], s = 0.0;
+#pragma unroll
+  for (int k = 0; k < kMaxBlocks / kThreads; ++k) {
+    const int i = k * kThreads + (int)threadIdx.x;
+    v[k] = i < P ? part[i] : 0.0;
+  }
+#pragma unroll
+  for (int k = 0; k < kMaxBlocks / kThreads; ++k) s += v[k];
   return sqrt(block_sum_f64(s));
 }
 

@@ -153,7 +153,7 @@ struct Group {
   }
 };
 
-template <class XT, class YT, int E, int C, bool STREAM>
+template <class XT, class YT, int E, int C, bool STREAM, bool ODD>
 __global__ __launch_bounds__(1024) void ln_fwd_rows(const XT* __restrict__ x,
                                                     const float* __restrict__ w,
                                                     const float* __restrict__ b,
@@ -173,36 +173,43 @@ __global__ __launch_bounds__(1024) void ln_fwd_rows(const XT* __restrict__ x,
     Raw<XT, E> raw[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const uint32_t i = gr.at<E>(c);
-      if (i < (uint32_t)d) raw[c].template load<STREAM>(xr + i);
+      const Piece<E, ODD> p(gr.at<E>(c), d);
+      if (p.any) raw[c].template load<STREAM>(xr + p.base);
     }
     float v[C][E], s[1] = {0.0f};
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (gr.at<E>(c) < (uint32_t)d)
+    for (int c = 0; c < C; ++c) {
+      const Piece<E, ODD> p(gr.at<E>(c), d);
+      if (p.any)
 #pragma unroll
-        for (int e = 0; e < E; ++e) s[0] += v[c][e] = raw[c][e];
+        for (int e = 0; e < E; ++e) {
+          v[c][e] = raw[c][e];
+          if (p.own(e)) s[0] += v[c][e];
+        }
+    }
     gr.sum(s, red[0]);
     const float mu = s[0] * inv;
     s[0] = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (gr.at<E>(c) < (uint32_t)d)
+    for (int c = 0; c < C; ++c) {
+      const Piece<E, ODD> p(gr.at<E>(c), d);
+      if (p.any)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           v[c][e] -= mu;
-          s[0] = fmaf(v[c][e], v[c][e], s[0]);
+          if (p.own(e)) s[0] = fmaf(v[c][e], v[c][e], s[0]);
         }
+    }
     gr.sum(s, red[1]);
     const float rs = 1.0f / sqrtf(s[0] * inv + eps);
     if (live) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const uint32_t i = gr.at<E>(c);
-        if (i >= (uint32_t)d) continue;
+        const Piece<E, ODD> p(gr.at<E>(c), d);
+        if (!p.any) continue;
         float f[E];
         if (w) {
-          load_elems<E>(w + i, f);
+          load_elems<E>(w + p.base, f);
 #pragma unroll
           for (int e = 0; e < E; ++e) v[c][e] = v[c][e] * rs * f[e];
         } else {
@@ -210,11 +217,11 @@ __global__ __launch_bounds__(1024) void ln_fwd_rows(const XT* __restrict__ x,
           for (int e = 0; e < E; ++e) v[c][e] *= rs;
         }
         if (b) {
-          load_elems<E>(b + i, f);
+          load_elems<E>(b + p.base, f);
 #pragma unroll
           for (int e = 0; e < E; ++e) v[c][e] += f[e];
         }
-        store_elems<E, STREAM>(yr + i, v[c]);
+        p.template store<STREAM>(yr, v[c]);
       }
       if (gr.t == 0) {
         if (mean) mean[row] = mu;
@@ -228,7 +235,7 @@ __global__ __launch_bounds__(1024) void ln_fwd_rows(const XT* __restrict__ x,
 // partials, [2 d] floats: dw, then db), in one pass: the next row's loads are
 // sent before the current row's sums are waited for, and the current row stays
 // in registers as it lies in memory.
-template <class XT, class GT, int E, int C, int MOST, bool STREAM>
+template <class XT, class GT, int E, int C, int MOST, bool STREAM, bool ODD>
 __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __restrict__ x,
                                                     const float* __restrict__ w,
                                                     const float* __restrict__ mean,
@@ -250,8 +257,8 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
       wv[c][e] = 1.0f;
       aw[c][e] = ab[c][e] = 0.0f;
     }
-    const uint32_t i = gr.at<E>(c);
-    if (w && i < (uint32_t)d) load_elems<E>(w + i, wv[c]);
+    const Piece<E, ODD> p(gr.at<E>(c), d);
+    if (w && p.any) load_elems<E>(w + p.base, wv[c]);
   }
   // a row, its statistics in scalar registers (a wave is within one row);
   // zeros in the threads past its end
@@ -268,10 +275,10 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
     o.rs = rstd[row];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const uint32_t i = gr.at<E>(c);
-      if (i < (uint32_t)d) {
-        o.g[c].template load<STREAM>(dyr + i);
-        o.v[c].template load<STREAM>(xr + i);
+      const Piece<E, ODD> p(gr.at<E>(c), d);
+      if (p.any) {
+        o.g[c].template load<STREAM>(dyr + p.base);
+        o.v[c].template load<STREAM>(xr + p.base);
       } else {
         o.g[c].clear();
         o.v[c].clear();
@@ -285,10 +292,12 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
     GT* dxr = dx + row * d;
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (gr.at<E>(c) < (uint32_t)d)
+    for (int c = 0; c < C; ++c) {
+      const Piece<E, ODD> p(gr.at<E>(c), d);
+      if (p.any)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
+          if (!p.own(e)) continue;
           const float g = o.g[c][e], xh = (o.v[c][e] - o.mu) * o.rs, gw = g * wv[c][e];
           s[0] += gw;
           s[1] = fmaf(gw, xh, s[1]);
@@ -297,19 +306,20 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
             ab[c][e] += g;
           }
         }
+    }
     if (kAhead && r0 + stride < T) load(next, row + stride);
     gr.sum(s, red[half]);
     if (live && dx) {
       const float c1 = s[0] * inv, c2 = s[1] * inv;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const uint32_t i = gr.at<E>(c);
-        if (i >= (uint32_t)d) continue;
+        const Piece<E, ODD> p(gr.at<E>(c), d);
+        if (!p.any) continue;
         float out[E];
 #pragma unroll
         for (int e = 0; e < E; ++e)
           out[e] = o.rs * (o.g[c][e] * wv[c][e] - c1 - (o.v[c][e] - o.mu) * o.rs * c2);
-        store_elems<E, STREAM>(dxr + i, out);
+        p.template store<STREAM>(dxr, out);
       }
     }
     if (!kAhead && r0 + stride < T) load(next, row + stride);
@@ -349,15 +359,16 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
     n = keep;
   }
   if (gr.index() == 0) {
-    float* p = part + (int64_t)blockIdx.x * 2 * d;
+    float* to = part + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const uint32_t i = gr.at<E>(c);
-      if (i >= (uint32_t)d) continue;
+      const Piece<E, ODD> p(gr.at<E>(c), d);
+      if (!p.any) continue;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        p[i + e] = aw[c][e];
-        p[d + i + e] = ab[c][e];
+        if (!p.own(e)) continue;
+        to[p.base + e] = aw[c][e];
+        to[d + p.base + e] = ab[c][e];
       }
     }
   }
@@ -369,7 +380,7 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
 // only the forward's statistics, and the second read of dy and x comes from
 // the caches.
 constexpr int kShortCols = 32;
-template <class XT, class GT, int E, int C>
+template <class XT, class GT, int E, int C, bool ODD>
 __global__ __launch_bounds__(1024) void ln_bwd_short(
     const GT* dy, const XT* __restrict__ x, const float* __restrict__ w,
     const float* __restrict__ mean, const float* __restrict__ rstd, GT* dx,
@@ -385,16 +396,17 @@ __global__ __launch_bounds__(1024) void ln_bwd_short(
     float gw[C][E], xh[C][E], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const uint32_t i = gr.at<E>(c);
-      if (i >= (uint32_t)d) continue;
+      const Piece<E, ODD> p(gr.at<E>(c), d);
+      if (!p.any) continue;
       float f[E];
-      load_elems<E>(dy + from + i, gw[c]);
-      load_elems<E>(x + from + i, xh[c]);
-      if (w) load_elems<E>(w + i, f);
+      load_elems<E>(dy + from + p.base, gw[c]);
+      load_elems<E>(x + from + p.base, xh[c]);
+      if (w) load_elems<E>(w + p.base, f);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         if (w) gw[c][e] *= f[e];
         xh[c][e] = (xh[c][e] - mu) * rs;
+        if (!p.own(e)) continue;
         s[0] += gw[c][e];
         s[1] = fmaf(gw[c][e], xh[c][e], s[1]);
       }
@@ -404,11 +416,11 @@ __global__ __launch_bounds__(1024) void ln_bwd_short(
     const float inv = 1.0f / (float)d, c1 = s[0] * inv, c2 = s[1] * inv;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const uint32_t i = gr.at<E>(c);
-      if (i >= (uint32_t)d) continue;
+      const Piece<E, ODD> p(gr.at<E>(c), d);
+      if (!p.any) continue;
 #pragma unroll
       for (int e = 0; e < E; ++e) gw[c][e] = rs * (gw[c][e] - c1 - xh[c][e] * c2);
-      store_elems<E>(dx + from + i, gw[c]);
+      p.store(dx + from, gw[c]);
     }
     return;
   }
@@ -512,36 +524,36 @@ int row_threads(int64_t d, int n, int most) {
 constexpr int kBwdBlocks = 256;
 
 struct BwdPlan {
-  int n, nt, G, blocks;                        // n elements a thread; 0: rows too long
+  int n, nt, G, blocks;                        // n elements a thread; 0: rows too long or short
 };
 BwdPlan bwd_plan(int64_t T, int64_t d) {
   int n = 8, nt = row_threads(d, n, 1024);
-  if (!nt && d % 8 == 0) nt = row_threads(d, n = 16, 1024);
-  if (!nt) return {0, 0, 0, 0};
+  if (!nt) nt = row_threads(d, n = 16, 1024);
+  if (!nt || d < 4) return {0, 0, 0, 0};
   const int G = std::max(1, 512 / nt);
   return {n, nt, G, (int)std::min<int64_t>((T + G - 1) / G, kBwdBlocks)};
 }
 
-template <class XT, class GT, int E, int C, bool STREAM>
+template <class XT, class GT, int E, int C, bool STREAM, bool ODD>
 hipError_t bwd_rows(const BwdPlan& p, const GT* dy, const XT* x, const float* w, const float* mean,
                     const float* rstd, int64_t T, int64_t d, GT* dx, float* part, hipStream_t s) {
   const size_t lds = (size_t)C * E * (p.G / 2) * p.nt * 4;
   // a workgroup of at most 512 threads may use twice the registers
   if (p.nt <= 512)
-    ln_bwd_rows<XT, GT, E, C, 512, STREAM><<<p.blocks, p.nt * p.G, lds, s>>>(
+    ln_bwd_rows<XT, GT, E, C, 512, STREAM, ODD><<<p.blocks, p.nt * p.G, lds, s>>>(
         dy, x, w, mean, rstd, dx, part, T, (int)d, p.nt);
   else
-    ln_bwd_rows<XT, GT, E, C, 1024, STREAM><<<p.blocks, p.nt, lds, s>>>(
+    ln_bwd_rows<XT, GT, E, C, 1024, STREAM, ODD><<<p.blocks, p.nt, lds, s>>>(
         dy, x, w, mean, rstd, dx, part, T, (int)d, p.nt);
   return hipGetLastError();
 }
 
 constexpr int64_t kShortRows = 1024;
 bool bwd_short_fits(int64_t T, int64_t d) {
-  return T <= kShortRows && row_threads(d, 8, 1024) > 0;
+  return T <= kShortRows && d >= 4 && row_threads(d, 8, 1024) > 0;
 }
 
-template <class XT, class GT, int E>
+template <class XT, class GT, int E, bool ODD>
 hipError_t bwd_short(const GT* dy, const XT* x, const float* w, const float* mean,
                      const float* rstd, int64_t T, int64_t d, GT* dx, float* dw, float* db,
                      hipStream_t s) {
@@ -550,7 +562,7 @@ hipError_t bwd_short(const GT* dy, const XT* x, const float* w, const float* mea
   const int cols = dw || db ? (int)((d + kShortCols - 1) / kShortCols) : 0;
   auto launch = [&](int row_blocks, int col_blocks) {
     if (row_blocks + col_blocks > 0)
-      ln_bwd_short<XT, GT, E, 8 / E><<<row_blocks + col_blocks, nt * G, 0, s>>>(
+      ln_bwd_short<XT, GT, E, 8 / E, ODD><<<row_blocks + col_blocks, nt * G, 0, s>>>(
           dy, x, w, mean, rstd, dx, dw, db, (int)T, (int)d, nt, row_blocks);
   };
   if ((const GT*)dx == dy) {                   // in place: the columns are read first
@@ -562,39 +574,45 @@ hipError_t bwd_short(const GT* dy, const XT* x, const float* w, const float* mea
   return hipGetLastError();
 }
 
+// rows that no group of threads holds in registers (or shorter than a piece):
+// dx in two passes over the row, dw and db in strips of rows
 template <class XT, class GT, int E>
+hipError_t bwd_long(const GT* dy, const XT* x, const float* w, const float* mean,
+                    const float* rstd, int64_t T, int64_t d, GT* dx, float* part, hipStream_t s) {
+  if (part) {                                  // before dx, which may overwrite dy
+    const Strips st = strips_of(T, d);
+    const dim3 grid((unsigned)((d + kColLanes * E - 1) / (kColLanes * E)), (unsigned)st.n);
+    ln_bwd_cols<XT, GT, E><<<grid, 256, 0, s>>>(dy, x, mean, rstd, part, T, d, st.rows);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (dx) ln_bwd_dx_long<XT, GT, E><<<row_grid(T), 1024, 0, s>>>(dy, x, w, mean, rstd, dx, T, d);
+  return hipGetLastError();
+}
+
+template <class XT, class GT, int E, bool ODD>
 hipError_t bwd(const GT* dy, const XT* x, const float* w, const float* mean, const float* rstd,
                int64_t T, int64_t d, GT* dx, float* dw, float* db, float* part, hipStream_t s) {
   if (bwd_short_fits(T, d))
-    return bwd_short<XT, GT, E>(dy, x, w, mean, rstd, T, d, dx, dw, db, s);
+    return bwd_short<XT, GT, E, ODD>(dy, x, w, mean, rstd, T, d, dx, dw, db, s);
   if (!dw && !db) part = nullptr;
   const BwdPlan p = bwd_plan(T, d);
-  hipError_t e = hipSuccess;
-  int64_t P = p.blocks;
-  const bool stream = T * d * (int64_t)(2 * sizeof(GT) + sizeof(XT)) > kStreamBytes;
-  if (p.n == 16) {
-    if constexpr (E > 1)
-      e = stream ? bwd_rows<XT, GT, E, 16 / E, true>(p, dy, x, w, mean, rstd, T, d, dx, part, s)
-                 : bwd_rows<XT, GT, E, 16 / E, false>(p, dy, x, w, mean, rstd, T, d, dx, part, s);
-  } else if (p.n) {
-    e = E > 1 && stream
-            ? bwd_rows<XT, GT, E, 8 / E, (E > 1)>(p, dy, x, w, mean, rstd, T, d, dx, part, s)
-            : bwd_rows<XT, GT, E, 8 / E, false>(p, dy, x, w, mean, rstd, T, d, dx, part, s);
-  } else {
-    if (part) {                                // before dx, which may overwrite dy
-      const Strips st = strips_of(T, d);
-      P = st.n;
-      const dim3 grid((unsigned)((d + kColLanes * E - 1) / (kColLanes * E)), (unsigned)st.n);
-      ln_bwd_cols<XT, GT, E><<<grid, 256, 0, s>>>(dy, x, mean, rstd, part, T, d, st.rows);
-      e = hipGetLastError();
-    }
-    if (e == hipSuccess && dx) {
-      ln_bwd_dx_long<XT, GT, E><<<row_grid(T), 1024, 0, s>>>(dy, x, w, mean, rstd, dx, T, d);
-      e = hipGetLastError();
-    }
-  }
+  // the streaming hint needs whole lines
+  constexpr bool HINT = !ODD;
+  const bool stream = HINT && T * d * (int64_t)(2 * sizeof(GT) + sizeof(XT)) > kStreamBytes;
+  hipError_t e;
+  if (p.n == 16)
+    e = stream ? bwd_rows<XT, GT, E, 16 / E, HINT, ODD>(p, dy, x, w, mean, rstd, T, d, dx, part, s)
+               : bwd_rows<XT, GT, E, 16 / E, false, ODD>(p, dy, x, w, mean, rstd, T, d, dx, part,
+                                                         s);
+  else if (p.n)
+    e = stream ? bwd_rows<XT, GT, E, 8 / E, HINT, ODD>(p, dy, x, w, mean, rstd, T, d, dx, part, s)
+               : bwd_rows<XT, GT, E, 8 / E, false, ODD>(p, dy, x, w, mean, rstd, T, d, dx, part,
+                                                        s);
+  else
+    e = bwd_long<XT, GT, ODD ? 1 : E>(dy, x, w, mean, rstd, T, d, dx, part, s);
   if (e != hipSuccess || !part) return e;
-  return launch_column_sum(part, P, d, 2, dw, db, s);
+  return launch_column_sum(part, p.n ? p.blocks : strips_of(T, d).n, d, 2, dw, db, s);
 }
 
 template <class XT, class GT>
@@ -604,28 +622,28 @@ hipError_t bwd_by_width(const void* dy, const void* x, const float* w, const flo
   const GT* g = (const GT*)dy;
   const XT* v = (const XT*)x;
   constexpr int E = sizeof(XT) + sizeof(GT) == 4 ? 8 : 4;
-  return d % 8 == 0 ? bwd<XT, GT, E>(g, v, w, mean, rstd, T, d, (GT*)dx, dw, db, part, s)
-                    : bwd<XT, GT, 1>(g, v, w, mean, rstd, T, d, (GT*)dx, dw, db, part, s);
+  return d % 8 == 0 ? bwd<XT, GT, E, false>(g, v, w, mean, rstd, T, d, (GT*)dx, dw, db, part, s)
+                    : bwd<XT, GT, 4, true>(g, v, w, mean, rstd, T, d, (GT*)dx, dw, db, part, s);
 }
 
-template <class XT, class YT, int E, int N, bool STREAM>
+template <class XT, class YT, int E, int N, bool STREAM, bool ODD>
 bool fwd_rows(const XT* x, const float* w, const float* b, int64_t T, int64_t d, float eps, YT* y,
               float* mean, float* rstd, hipStream_t s) {
   const int nt = row_threads(d, N, 1024);
   if (!nt) return false;
   const int G = nt >= 256 ? std::max(1, 512 / nt) : 256 / nt;
   const unsigned grid = (unsigned)std::min<int64_t>((T + G - 1) / G, 1 << 20);
-  ln_fwd_rows<XT, YT, E, N / E, STREAM><<<grid, nt * G, 0, s>>>(x, w, b, y, mean, rstd, T, (int)d,
-                                                                eps, nt);
+  ln_fwd_rows<XT, YT, E, N / E, STREAM, ODD><<<grid, nt * G, 0, s>>>(x, w, b, y, mean, rstd, T,
+                                                                     (int)d, eps, nt);
   return true;
 }
 
 // 16 elements a thread, 32 for longer rows (4096 x 13824 bf16: 66 us, 75 with 16)
-template <class XT, class YT, int E, bool STREAM>
+template <class XT, class YT, int E, bool STREAM, bool ODD>
 bool fwd_vec(const XT* x, const float* w, const float* b, int64_t T, int64_t d, float eps, YT* y,
              float* mean, float* rstd, hipStream_t s) {
-  return d <= 8192 ? fwd_rows<XT, YT, E, 16, STREAM>(x, w, b, T, d, eps, y, mean, rstd, s)
-                   : fwd_rows<XT, YT, E, 32, STREAM>(x, w, b, T, d, eps, y, mean, rstd, s);
+  return d <= 8192 ? fwd_rows<XT, YT, E, 16, STREAM, ODD>(x, w, b, T, d, eps, y, mean, rstd, s)
+                   : fwd_rows<XT, YT, E, 32, STREAM, ODD>(x, w, b, T, d, eps, y, mean, rstd, s);
 }
 
 template <class XT, class YT>
@@ -641,12 +659,12 @@ hipError_t fwd(const void* xv, const float* w, const float* b, int64_t T, int64_
     constexpr bool wide = std::is_same_v<YT, float>;
     constexpr int E = wide && std::is_same_v<XT, __bf16> ? 4 : 8;
     done = T * d * (int64_t)(sizeof(XT) + sizeof(YT)) > kStreamBytes
-               ? fwd_vec<XT, YT, wide ? 4 : 8, true>(x, w, b, T, d, eps, y, mean, rstd, s)
-               : fwd_vec<XT, YT, E, false>(x, w, b, T, d, eps, y, mean, rstd, s);
+               ? fwd_vec<XT, YT, wide ? 4 : 8, true, false>(x, w, b, T, d, eps, y, mean, rstd, s)
+               : fwd_vec<XT, YT, E, false, false>(x, w, b, T, d, eps, y, mean, rstd, s);
     if (!done)
       ln_fwd_long<XT, YT, 4><<<row_grid(T), 1024, 0, s>>>(x, w, b, y, mean, rstd, T, d, eps);
   } else {
-    done = fwd_rows<XT, YT, 1, 8, false>(x, w, b, T, d, eps, y, mean, rstd, s);
+    done = d >= 4 && fwd_vec<XT, YT, 4, false, true>(x, w, b, T, d, eps, y, mean, rstd, s);
     if (!done)
       ln_fwd_long<XT, YT, 1><<<row_grid(T), 1024, 0, s>>>(x, w, b, y, mean, rstd, T, d, eps);
   }

@@ -16,24 +16,24 @@ namespace {
 constexpr int kLanes = 32;
 
 // part: the strips' sums, one row of d floats each (dbias itself with one strip)
-template <class GT, class ZT, int E, int ACT, int kRows, bool STREAM>
+template <class GT, class ZT, int E, int ACT, int kRows, bool STREAM, bool ODD>
 __global__ __launch_bounds__(kRows * kLanes) void act_bwd_kernel(const GT* dy, const ZT* __restrict__ z,
                                                       GT* dz, float* __restrict__ part, int64_t T,
                                                       int64_t d, int64_t rows_per_strip) {
   __shared__ float sb[kRows][kLanes * E];
   const int cl = threadIdx.x % kLanes, rl = threadIdx.x / kLanes;
-  const int64_t col = ((int64_t)blockIdx.x * kLanes + cl) * E;
+  const Piece<E, ODD> p(((uint32_t)blockIdx.x * kLanes + cl) * E, (uint32_t)d);
   const int64_t r0 = blockIdx.y * rows_per_strip, r1 = min(T, r0 + rows_per_strip);
   float ab[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) ab[e] = 0.0f;
-  if (col < d) {
+  if (p.any) {
 #pragma unroll 2
     for (int64_t r = r0 + rl; r < r1; r += kRows) {
       Raw<GT, E> gr;
       Raw<ZT, E> v;
-      gr.template load<STREAM>(dy + r * d + col);
-      if constexpr (ACT != kNone) v.template load<STREAM>(z + r * d + col);
+      gr.template load<STREAM>(dy + r * d + p.base);
+      if constexpr (ACT != kNone) v.template load<STREAM>(z + r * d + p.base);
       float g[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -42,12 +42,13 @@ __global__ __launch_bounds__(kRows * kLanes) void act_bwd_kernel(const GT* dy, c
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) ab[e] += g[e];
-      if (dz) store_elems<E, STREAM>(dz + r * d + col, g);
+      if (dz) p.template store<STREAM>(dz + r * d, g);
     }
   }
   if (!part) return;
 #pragma unroll
-  for (int e = 0; e < E; ++e) sb[rl][cl * E + e] = ab[e];
+  for (int e = 0; e < E; ++e)                  // elements before the piece's own: none's
+    if (p.own(e)) sb[rl][cl * E + e - p.over] = ab[e];
   __syncthreads();
   for (int i = threadIdx.x; i < kLanes * E; i += kRows * kLanes) {
     const int64_t c = (int64_t)blockIdx.x * kLanes * E + i;
@@ -67,21 +68,21 @@ struct Strips {
 constexpr int kShort = 256;
 Strips strips_of(int64_t T, int64_t d) {
   if (T <= kShort) return {1, T};
-  const int64_t per = d % 8 == 0 ? kLanes * 4 : kLanes;
+  const int64_t per = kLanes * 4;
   const int64_t cols = std::max<int64_t>(1, (d + per - 1) / per);
   const int64_t n = std::min<int64_t>({(T + 15) / 16, (4096 + cols - 1) / cols, 1024});
   const int64_t rows = (T + n - 1) / n;
   return {(T + rows - 1) / rows, rows};
 }
 
-template <class GT, class ZT, int E, int kRows, bool STREAM>
+template <class GT, class ZT, int E, int kRows, bool STREAM, bool ODD>
 hipError_t by_act(const GT* dy, const ZT* z, int act, int64_t T, int64_t d, GT* dz, float* part,
                   hipStream_t s) {
   const Strips st = strips_of(T, d);
   const dim3 grid((unsigned)((d + kLanes * E - 1) / (kLanes * E)), (unsigned)st.n);
 #define FALQ_ACT(A)                                                                         \
   case A:                                                                                   \
-    act_bwd_kernel<GT, ZT, E, A, kRows, STREAM>                                             \
+    act_bwd_kernel<GT, ZT, E, A, kRows, STREAM, ODD>                                        \
         <<<grid, kRows * kLanes, 0, s>>>(dy, z, dz, part, T, d, st.rows);                   \
     break;
   switch (act) {
@@ -92,22 +93,26 @@ hipError_t by_act(const GT* dy, const ZT* z, int act, int64_t T, int64_t d, GT* 
   return hipGetLastError();
 }
 
-template <class GT, class ZT, int E>
+template <class GT, class ZT, int E, bool ODD>
 hipError_t by_rows(const GT* dy, const ZT* z, int act, int64_t T, int64_t d, GT* dz, float* part,
                    hipStream_t s) {
-  if (T <= kShort) return by_act<GT, ZT, E, 32, false>(dy, z, act, T, d, dz, part, s);
-  if constexpr (E > 1)
+  if (T <= kShort) return by_act<GT, ZT, E, 32, false, ODD>(dy, z, act, T, d, dz, part, s);
+  // the streaming hint needs whole lines
+  if constexpr (!ODD)
     if (T * d * (int64_t)(2 * sizeof(GT) + sizeof(ZT)) > kStreamBytes)
-      return by_act<GT, ZT, E, 8, true>(dy, z, act, T, d, dz, part, s);
-  return by_act<GT, ZT, E, 8, false>(dy, z, act, T, d, dz, part, s);
+      return by_act<GT, ZT, E, 8, true, false>(dy, z, act, T, d, dz, part, s);
+  return by_act<GT, ZT, E, 8, false, ODD>(dy, z, act, T, d, dz, part, s);
 }
 
 template <class GT, class ZT>
 hipError_t by_width(const void* dy, const void* z, int act, int64_t T, int64_t d, void* dz,
                     float* part, hipStream_t s) {
   constexpr int E = sizeof(GT) + sizeof(ZT) == 4 ? 8 : 4;
-  return d % 8 == 0 ? by_rows<GT, ZT, E>((const GT*)dy, (const ZT*)z, act, T, d, (GT*)dz, part, s)
-                    : by_rows<GT, ZT, 1>((const GT*)dy, (const ZT*)z, act, T, d, (GT*)dz, part, s);
+  const GT* g = (const GT*)dy;
+  const ZT* v = (const ZT*)z;
+  if (d % 8 == 0) return by_rows<GT, ZT, E, false>(g, v, act, T, d, (GT*)dz, part, s);
+  return d >= 4 ? by_rows<GT, ZT, 4, true>(g, v, act, T, d, (GT*)dz, part, s)
+                : by_rows<GT, ZT, 1, true>(g, v, act, T, d, (GT*)dz, part, s);
 }
 
 }  // namespace

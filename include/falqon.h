@@ -666,7 +666,8 @@ typedef enum {
  *   y                 [T x d_out] of type dtype (output)
  *   z                 [T x d_out] of type dtype (output), or NULL; not y or residual
  *   ws                melded_linear_fwd_act_workspace_bytes(T, d_in, d_out): 0
- *                     (ws may be NULL) unless few outputs meet a long d_in
+ *                     (ws may be NULL) unless few outputs meet a long d_in,
+ *                     and always for T <= 16
  */
 size_t melded_linear_fwd_act_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
 falq_status melded_linear_fwd_act(const uint8_t *xq, const float *s_x, const uint8_t *wq,

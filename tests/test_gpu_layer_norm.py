@@ -66,7 +66,7 @@ def fwd_tol(x, w, b, y, mu, rstd, xh, yt):
     return t + half_step(yt) * (y.abs() + t), dmu + U * mu.abs(), rel * rstd
 
 
-SHAPES = [(1, 1), (3, 7), (5, 8), (1, 4096), (2, 64), (130, 400), (67, 1000), (33, 1027),
+SHAPES = [(1, 1), (4, 2), (3, 3), (6, 4), (7, 5), (9, 6), (3, 7), (5, 8), (1, 4096), (2, 64), (130, 400), (67, 1000), (33, 1027),
           (9, 2048), (40, 4096), (17, 5120), (6, 8192), (5, 8200), (3, 13824), (2, 16384),
           (2, 16392), (2, 20001)]
 
@@ -156,7 +156,8 @@ def stats_of(x, eps=1e-5):
 
 
 @pytest.mark.parametrize("xt,gt", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
-@pytest.mark.parametrize("T,d", SHAPES + [(1500, 96), (700, 1027), (2100, 264), (1025, 1029), (1500, 4096), (1100, 9000)])
+@pytest.mark.parametrize("T,d", SHAPES + [(1500, 96), (700, 1027), (2100, 264), (1025, 1029), (1500, 4096), (1100, 9000), (1030, 3), (1040, 6), (1100, 9001),
+                                           (1050, 255)])
 def test_backward(gpu_lib, T, d, xt, gt):
     announce(f"layer_norm_bwd T={T} d={d} {xt} {gt}")
     x, dy, w, _ = problem(T * 5 + d, T, d, xt, gt)
@@ -170,7 +171,8 @@ def test_backward(gpu_lib, T, d, xt, gt):
     check(db, rb, tb, "dbias")
 
 
-@pytest.mark.parametrize("T,d", [(50, 515), (50, 768), (1300, 515), (1300, 768), (1050, 8200)])
+@pytest.mark.parametrize("T,d", [(50, 515), (50, 768), (1300, 515), (1300, 768), (1050, 8200),
+                                 (1030, 8201), (30, 2), (1100, 3)])
 def test_backward_parts_and_in_place(gpu_lib, T, d):
     """dx alone, dweight or dbias alone, no weight, dx onto dy: the same bits."""
     x, dy, w, _ = problem(8, T, d)

@@ -187,7 +187,7 @@ def test_empty(gpu_lib):
 
 @pytest.mark.parametrize("zt,gt", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
 @pytest.mark.parametrize("act", ACTS)
-@pytest.mark.parametrize("T,d", [(1, 1), (3, 17), (130, 400), (1, 4096), (1003, 1027),
+@pytest.mark.parametrize("T,d", [(1, 1), (300, 3), (5, 4), (300, 130), (3, 17), (130, 400), (1, 4096), (1003, 1027),
                                  (2050, 264), (40, 11008)])
 def test_backward(gpu_lib, T, d, act, zt, gt):
     announce(f"linear_act_bwd T={T} d={d} {act} {zt} {gt}")
