@@ -6,8 +6,7 @@
 // |e| <= 1.5e-7.  With x = |z| / sqrt(2) the exponential is exp(-z^2 / 2),
 // which the derivative needs as well, so one exponential and one reciprocal
 // serve both.  Phi(z) is therefore off by at most 7.5e-8 + roundings, about
-// one float32 step of its largest value; the library's erff takes three times
-// the instructions, and the backward of gelu is bound by them.
+// one float32 step of its largest value.
 #pragma once
 
 #include "common.hpp"

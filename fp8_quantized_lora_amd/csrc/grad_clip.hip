@@ -14,11 +14,15 @@
 // Work is counted in chunks of 256 threads x 16 bytes from each tensor's
 // address rounded down to 16 bytes: the 16-byte accesses then fit a tensor that
 // starts at any element, and only part vectors at its ends are done element by
-// element.  Runs of kAhead chunks are dealt round the workgroups (one long run
-// for each would put them all on the same memory channels where sizes are powers
-// of two: 160 M floats 375 us), a run's loads all in flight.  The second pass
-// goes from the end back: what the first one read last is the likeliest to be
-// in the last-level cache still.
+// element.  Runs of kAhead chunks are dealt round the workgroups (448 tensors of
+// 160 M floats 322 us; 338 with one long run for each workgroup), a run's loads
+// all in flight.  The second pass goes from the end back: what the first one
+// read last is the likeliest to be in the last-level cache still.
+//
+// Bound by memory: the gradients are read twice (the norm comes before the
+// scaling) and written once.  160 M floats: 105 us for the first pass, 215 for
+// the second, 6.1 and 6.0 TB/s; a call of a single layer (0.5 M floats) is two
+// launches, 6.8 us.
 #include "elem.hpp"
 #include "kernels.hpp"
 
