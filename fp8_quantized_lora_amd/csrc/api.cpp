@@ -714,6 +714,14 @@ namespace {
 
 inline bool dtype_ok(int t) { return t == FALQ_F32 || t == FALQ_BF16; }
 
+// a required or optional tensor of float32 or bfloat16 elements: aligned to its
+// element, since the kernels' accesses are
+inline bool opt_elems(const void* p, int dtype) {
+  return p == nullptr || aligned(p, dtype == FALQ_BF16 ? 2 : 4);
+}
+inline bool elems(const void* p, int dtype) { return p != nullptr && opt_elems(p, dtype); }
+inline bool opt_f32(const void* p) { return opt_elems(p, FALQ_F32); }
+
 // rows and columns of the row-wise operators: a column count is exact in
 // float32 and every launch fits a 32-bit grid
 inline bool rows_ok(int64_t T, int64_t d) {
@@ -788,8 +796,8 @@ falq_status layer_norm_fwd(const void* x, int x_dtype, const float* weight, cons
                            float* rstd, falq_stream stream) {
   if (!rows_ok(T, d) || !dtype_ok(x_dtype) || !dtype_ok(y_dtype)) return FALQ_EINVAL;
   if (!(eps >= 0.0f) || std::isinf(eps)) return FALQ_EINVAL;
-  if (!opt(weight) || !opt(bias) || !opt(mean) || !opt(rstd)) return FALQ_EINVAL;
-  if (T > 0 && (!need(x) || !need(y) || x == y)) return FALQ_EINVAL;
+  if (!opt_f32(weight) || !opt_f32(bias) || !opt_f32(mean) || !opt_f32(rstd)) return FALQ_EINVAL;
+  if (T > 0 && (!elems(x, x_dtype) || !elems(y, y_dtype) || x == y)) return FALQ_EINVAL;
   return hip_status(falq::launch_layer_norm_fwd(x, x_dtype, weight, bias, T, d, eps, y, y_dtype,
                                                 mean, rstd,
                                                 reinterpret_cast<hipStream_t>(stream)));
@@ -804,9 +812,11 @@ falq_status layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x_dt
                            int64_t d, void* dx, float* dweight, float* dbias, void* ws,
                            size_t ws_bytes, falq_stream stream) {
   if (!rows_ok(T, d) || !dtype_ok(x_dtype) || !dtype_ok(dy_dtype)) return FALQ_EINVAL;
-  if (!opt(weight) || !opt(dx) || !opt(dweight) || !opt(dbias)) return FALQ_EINVAL;
+  if (!opt_f32(weight) || !opt_elems(dx, dy_dtype) || !opt_f32(dweight) || !opt_f32(dbias))
+    return FALQ_EINVAL;
   if (dweight && dweight == dbias) return FALQ_EINVAL;
-  if (T > 0 && (!need(dy) || !need(x) || !need(mean) || !need(rstd))) return FALQ_EINVAL;
+  if (T > 0 && (!elems(dy, dy_dtype) || !elems(x, x_dtype) || !scalar(mean) || !scalar(rstd)))
+    return FALQ_EINVAL;
   if (T > 0 && dx == x) return FALQ_EINVAL;
   if ((dweight || dbias) && !ws_ok(ws, ws_bytes, falq::layer_norm_bwd_ws_bytes(T, d)))
     return FALQ_EINVAL;
@@ -826,10 +836,11 @@ falq_status melded_linear_fwd_act(const uint8_t* xq, const float* s_x, const uin
                                   falq_stream stream) {
   if (!gemm_dims_ok(T, d_in, d_out) || !dtype_ok(dtype)) return FALQ_EINVAL;
   if (act < FALQ_ACT_NONE || act > FALQ_ACT_SILU) return FALQ_EINVAL;
-  if (!scalar(s_x) || !scalar(s_w) || !opt(bias)) return FALQ_EINVAL;
+  if (!scalar(s_x) || !scalar(s_w) || !opt_f32(bias)) return FALQ_EINVAL;
   if (T * d_in > 0 && !need(xq)) return FALQ_EINVAL;
   if (d_out * d_in > 0 && !need(wq)) return FALQ_EINVAL;
-  if (T * d_out > 0 && (!need(y) || !opt(z) || !opt(residual))) return FALQ_EINVAL;
+  if (T * d_out > 0 && (!elems(y, dtype) || !opt_elems(z, dtype) || !opt_elems(residual, dtype)))
+    return FALQ_EINVAL;
   if (T * d_out > 0 && z && (z == y || z == residual)) return FALQ_EINVAL;
   if (!ws_ok(ws, ws_bytes, falq::linear_act_ws_bytes(T, d_in, d_out))) return FALQ_EINVAL;
   return hip_status(falq::launch_linear_act(xq, s_x, wq, s_w, bias, residual, T, d_in, d_out, act,
@@ -848,11 +859,12 @@ falq_status linear_act_bwd(const void* dy, int dy_dtype, const void* z, int z_dt
                            size_t ws_bytes, falq_stream stream) {
   if (!dtype_ok(dy_dtype) || !dtype_ok(z_dtype)) return FALQ_EINVAL;
   if (act < FALQ_ACT_NONE || act > FALQ_ACT_SILU) return FALQ_EINVAL;
-  if (d_out < 0 || !rows_ok(T, std::max<int64_t>(d_out, 1)) || !opt(dbias)) return FALQ_EINVAL;
+  if (d_out < 0 || !rows_ok(T, std::max<int64_t>(d_out, 1)) || !opt_f32(dbias)) return FALQ_EINVAL;
   if (d_out == 0) return FALQ_OK;
   if (!dz && !dbias) return FALQ_EINVAL;
-  if (T > 0 && (!need(dy) || !opt(dz) || (dz && dz == z))) return FALQ_EINVAL;
-  if (T > 0 && act != FALQ_ACT_NONE && !need(z)) return FALQ_EINVAL;
+  if (T > 0 && (!elems(dy, dy_dtype) || !opt_elems(dz, dy_dtype) || (dz && dz == z)))
+    return FALQ_EINVAL;
+  if (T > 0 && act != FALQ_ACT_NONE && !elems(z, z_dtype)) return FALQ_EINVAL;
   if (dbias && !ws_ok(ws, ws_bytes, falq::linear_act_bwd_ws_bytes(T, d_out))) return FALQ_EINVAL;
   return hip_status(falq::launch_linear_act_bwd(dy, dy_dtype, z, z_dtype, T, d_out, act, dz,
                                                 dbias, ws,

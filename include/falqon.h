@@ -607,7 +607,10 @@ falq_status lora_bf16_bwd(const float *dy, const uint8_t *gq, const float *s_g, 
  * layer's dA and dB by their global norm before the adapter step.  Elements
  * are float32 or bfloat16 (falq_dtype); sums, statistics and norms are
  * float32 or wider and their order is fixed by the sizes, so results repeat
- * bit for bit.  Two calls that may run at the same time need a workspace each.
+ * bit for bit.  These tensors need only their element's alignment (the FP8
+ * codes 16 bytes as elsewhere), so rows may begin anywhere in a larger buffer;
+ * 16-byte aligned rows are the fastest.  Two calls that may run at the same
+ * time need a workspace each.
  */
 
 /*

@@ -11,7 +11,7 @@ import fp8_quantized_lora_amd as fq
 EINVAL, OK = 1, 0
 P = 1 << 20          # 16-byte aligned fake addresses, never dereferenced
 Q, R, S = 1 << 21, 1 << 22, 1 << 23
-MIS = P + 4
+MIS = P + 1          # no element's alignment
 BIG = 1 << 40
 NAN, INF = float("nan"), float("inf")
 

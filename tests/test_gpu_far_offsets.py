@@ -1,0 +1,89 @@
+"""Tensors of more than 2^31 elements: rows past a 32-bit offset are read and
+written where they belong.  Rows of these operators do not depend on each other
+(the sums over rows aside), so the last rows are checked against the same rows
+in a call of their own, within half a step of bfloat16 twice (2^-7: two
+roundings of values that differ by float32 roundings at most)."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+T, D, TAIL = 270_000, 8192, 500                      # 2.2e9 elements
+
+
+def close(a, b):
+    a, b = a.float(), b.float()
+    return bool(((a - b).abs() <= 2.0 ** -7 * b.abs() + 1e-3 * b.abs().max()).all())
+
+
+@pytest.fixture(scope="module")
+def big():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.empty((T, D), dtype=BF16, device="cuda")
+    x.normal_(generator=g)
+    assert x.numel() > 2 ** 31
+    yield x
+    del x
+    torch.cuda.empty_cache()
+
+
+def test_layer_norm(gpu_lib, big):
+    w, b = torch.randn(D, device="cuda"), torch.randn(D, device="cuda")
+    y = torch.empty_like(big)
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    gpu_lib.layer_norm_fwd(big, w, b, y, mean, rstd)
+    x = big[-TAIL:].contiguous()
+    y2, m2, r2 = torch.empty_like(x), *(torch.empty(TAIL, device="cuda") for _ in range(2))
+    gpu_lib.layer_norm_fwd(x, w, b, y2, m2, r2)
+    assert close(y[-TAIL:], y2) and close(mean[-TAIL:], m2) and close(rstd[-TAIL:], r2)
+    # backward, dy = x, dx in y's memory
+    dw, db = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    gpu_lib.layer_norm_bwd(big, big, w, mean, rstd, y, dw, db)
+    gpu_lib.layer_norm_bwd(x, x, w, m2, r2, y2)
+    assert close(y[-TAIL:], y2)
+    ref = torch.zeros(D, dtype=torch.float64, device="cuda")
+    for part in big.split(30_000):
+        ref += part.double().sum(0)
+    # 2.7e5 standard normals: a chain of at most T roundings of sums below 5 sqrt(T)
+    assert float((db.double() - ref).abs().max()) <= T * 2.0 ** -24 * 5 * math.sqrt(T)
+
+
+def test_activation_backward(gpu_lib, big):
+    dz, db = torch.empty_like(big), torch.empty(D, device="cuda")
+    gpu_lib.linear_act_bwd(big, big, dz, dbias=db, act="silu")
+    x = big[-TAIL:].contiguous()
+    z2 = torch.empty_like(x)
+    gpu_lib.linear_act_bwd(x, x, z2, act="silu")
+    assert close(dz[-TAIL:], z2)
+
+
+def test_product(gpu_lib):
+    xq = torch.randint(0, 120, (T, 64), dtype=torch.uint8, device="cuda")
+    wq = torch.randint(0, 120, (D, 64), dtype=torch.uint8, device="cuda")
+    one, bias = torch.ones(1, device="cuda"), torch.randn(D, device="cuda")
+    y = torch.empty((T, D), dtype=BF16, device="cuda")
+    gpu_lib.melded_linear_fwd_act(xq, one, wq, one, y, bias=bias, act="relu")
+    x = xq[-TAIL:].contiguous()
+    y2 = torch.empty((TAIL, D), dtype=BF16, device="cuda")
+    gpu_lib.melded_linear_fwd_act(x, one, wq, one, y2, bias=bias, act="relu")
+    assert close(y[-TAIL:], y2)
+
+
+def test_clip(gpu_lib, big):
+    flat = big.view(-1)
+    n = flat.numel()
+    views = [flat[1:n - 7], flat[n - 5:]]
+    out = torch.empty_like(flat)
+    norm = torch.empty(1, device="cuda")
+    gpu_lib.grad_clip(views, 1.0, norm, out=[out[1:n - 7], out[n - 5:]])
+    ref = math.sqrt(sum(float(p.double().square().sum()) for p in flat.split(2 ** 28)))
+    assert abs(float(norm) / ref - 1) <= 1e-6        # three elements are left out
+    want = flat[-1000:].float() / float(norm)
+    got = out[-1000:].float()
+    keep = torch.ones(1000, dtype=torch.bool, device="cuda")
+    keep[-7:-5] = False                              # between the views
+    assert bool(((got - want).abs() <= 2.0 ** -7 * want.abs())[keep].all())

@@ -196,6 +196,35 @@ def test_backward_parts_and_in_place(gpu_lib, T, d):
     assert torch.equal(inp, full[0]) and torch.equal(dw, full[1]) and torch.equal(db, full[2])
 
 
+@pytest.mark.parametrize("T,d", [(40, 129), (40, 640), (1100, 264), (3, 20000)])
+@pytest.mark.parametrize("t", [F32, BF16])
+def test_rows_anywhere_in_a_buffer(gpu_lib, T, d, t):
+    """Rows, parameters and statistics that begin one element into a buffer:
+    the bits of aligned ones, and nothing around the outputs changes."""
+    x, dy, w, b = problem(31, T, d, t, t)
+
+    def at1(v):
+        buf = torch.full((v.numel() + 2,), 7.0, dtype=v.dtype, device="cuda")
+        buf[1:-1] = v.reshape(-1).cuda()
+        return buf, buf[1:-1].view(v.shape)
+
+    def run(place):
+        ins = [place(v) for v in (x, dy, w, b)]
+        outs = [place(torch.zeros(s, dtype=dt)) for s, dt in (((T, d), t), ((T,), F32),
+                                                              ((T,), F32), ((T, d), t),
+                                                              ((d,), F32), ((d,), F32))]
+        (_, xv), (_, gv), (_, wv), (_, bv) = ins
+        y, m, r, dx, dw, db = (v for _, v in outs)
+        gpu_lib.layer_norm_fwd(xv, wv, bv, y, m, r)
+        gpu_lib.layer_norm_bwd(gv, xv, wv, m, r, dx, dw, db)
+        return outs
+
+    shifted, plain = run(at1), run(lambda v: (None, v.cuda()))
+    for (buf, v), (_, p) in zip(shifted, plain):
+        assert torch.equal(v, p)
+        assert float(buf[0]) == 7.0 and float(buf[-1]) == 7.0
+
+
 def test_no_rows(gpu_lib):
     """T = 0: nothing but zero gradients of weight and bias."""
     e = torch.empty((0, 24), device="cuda")

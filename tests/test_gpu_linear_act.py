@@ -215,6 +215,33 @@ def test_backward(gpu_lib, T, d, act, zt, gt):
         assert torch.equal(inp, dz)
 
 
+@pytest.mark.parametrize("T", [2, 60, 300])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_anywhere_in_a_buffer(gpu_lib, T, dtype):
+    """Outputs, residual, bias and z that begin one element into a buffer: the
+    bits of aligned ones, and nothing around the outputs changes."""
+    d_in, d_out = 272, 144
+    p = problem(13, T, d_in, d_out, dtype)
+    xq, s_x, wq, s_w, bias, res = (t.cuda() for t in p)
+
+    def at1(v):
+        buf = torch.full((v.numel() + 2,), 7.0, dtype=v.dtype, device="cuda")
+        buf[1:-1] = v.reshape(-1)
+        return buf, buf[1:-1].view(v.shape)
+
+    def run(place):
+        y, z, dz = (place(torch.zeros((T, d_out), dtype=dtype, device="cuda")) for _ in range(3))
+        db = place(torch.zeros(d_out, device="cuda"))
+        gpu_lib.melded_linear_fwd_act(xq, s_x, wq, s_w, y[1], bias=place(bias)[1], act="silu",
+                                      residual=place(res)[1], z=z[1])
+        gpu_lib.linear_act_bwd(place(res)[1], z[1], dz[1], dbias=db[1], act="silu")
+        return y, z, dz, db
+
+    for (buf, v), (_, q) in zip(run(at1), run(lambda v: (None, v.clone()))):
+        assert torch.equal(v, q)
+        assert float(buf[0]) == 7.0 and float(buf[-1]) == 7.0
+
+
 @pytest.mark.parametrize("act", ACTS[1:])
 def test_slopes_against_differences(gpu_lib, act):
     """dz for dy = 1 against central differences of the activation in float64:
