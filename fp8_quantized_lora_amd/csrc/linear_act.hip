@@ -65,18 +65,24 @@ hipError_t launch_few(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, 
 // Which tile: the one whose rounds of the 256 CUs take least.  A K step of a
 // round of tiles costs (us, measured at 256 to 1024 tiles and 4096 and 8192
 // K-bytes)
-//     256 x 320  2.1      256 x 256  1.68     128 x 128  0.62
-//      64 x 128  0.55      64 x  64  0.27      32 x  64  0.24
+//     256 x 320  2.1      256 x 256  1.68     256 x 128  1.08     128 x 256  1.08
+//     192 x 128  0.82     128 x 192  0.82     128 x 128  0.62
+//      64 x  64  0.27      32 x  64  0.24
 // and a launch about 4 more for the first loads and the last stores: a larger
 // tile moves fewer bytes per product but leaves more of its last round empty.
-// 512 x 4096 x 4096: 15.3 in tiles of 64 x 128 (one round), 18.9 in 128 x 128
-// (half a round), 17.5 in 32 x 128; 128 x 4096: 10.0 in 32 x 64, 10.9 in 64 x
-// 64, 14 in 64 x 128; 4096 x 5120 x 13824: 230 in 256 x 320 (one round), 252 in
-// a round of 256 x 256 and one of 128 x 128, 345 in 256 x 256.
-enum TileKind { k256, k256x320, k128, k64x128, k64, k32x64, kTileKinds };
-constexpr int kTileM[kTileKinds] = {256, 256, 128, 64, 64, 32};
-constexpr int kTileN[kTileKinds] = {256, 320, 128, 128, 64, 64};
-constexpr float kStep[kTileKinds] = {1.68f, 2.1f, 0.62f, 0.55f, 0.27f, 0.24f};
+// 512 x 4096 x 4096: 15.5 in tiles of 64 x 64, 18.9 in 128 x 128 (half a round),
+// 17.5 in 32 x 128; 128 x 4096: 10.0 in 32 x 64, 10.9 in 64 x 64, 14 in 64 x
+// 128; 4096 x 5120 x 13824: 230 in 256 x 320 (one round), 252 in
+// a round of 256 x 256 and one of 128 x 128, 345 in 256 x 256; 512 x 11008 x 4096
+// with gelu and z: 31.5 in 128 x 192 (232 tiles), 36.7 in 128 x 256, 45 in 128 x
+// 128.
+enum TileKind {
+  k256, k256x320, k256x128, k128x256, k192x128, k128x192, k128, k64, k32x64, kTileKinds
+};
+constexpr int kTileM[kTileKinds] = {256, 256, 256, 128, 192, 128, 128, 64, 32};
+constexpr int kTileN[kTileKinds] = {256, 320, 128, 256, 128, 192, 128, 64, 64};
+constexpr float kStep[kTileKinds] = {1.68f, 2.1f,  1.08f, 1.08f, 0.82f,
+                                     0.82f, 0.62f, 0.27f, 0.24f};
 constexpr float kLaunch = 4.0f;
 constexpr int kCUs = 256;
 
@@ -135,7 +141,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   // few tiles and a long K: as many splits as give a workgroup to each CU, at
   // least 8 steps each, and the planes written and read once at 4 TB/s.  64 x
   // 5120 x 13824: 22.5 us in 6 splits, 32.5 whole; 100 x 4096 x 11008: 19.8 in
-  // 8, 25.8 whole; 512 x 4096 x 4096 21.1 in 2, 15.3 whole.
+  // 8, 25.8 whole; 512 x 4096 x 4096 21.1 in 2, 15.5 whole.
   const int64_t nt = tiles_of(k128, M, N);
   const int64_t s = nt > 0 ? std::min<int64_t>(kCUs / nt, steps / 8) : 0;
   if (s >= 2) {
@@ -160,10 +166,16 @@ hipError_t launch_kind(TileKind k, const uint8_t* A, const uint8_t* B, int64_t M
     case k256: return launch_tiles<Tile<256, 256, 2, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
     case k256x320:
       return launch_tiles<Tile<256, 320, 2, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
+    case k256x128:
+      return launch_tiles<Tile<256, 128, 4, 2, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
+    case k192x128:
+      return launch_tiles<Tile<192, 128, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
+    case k128x192:
+      return launch_tiles<Tile<128, 192, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
+    case k128x256:
+      return launch_tiles<Tile<128, 256, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
     case k128:
       return launch_tiles<Tile<128, 128, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
-    case k64x128:
-      return launch_tiles<Tile<64, 128, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
     case k64: return launch_tiles<Tile<64, 64, 2, 2, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
     default: return launch_tiles<Tile<32, 64, 1, 4, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
   }

@@ -109,7 +109,8 @@ SHAPES = [  # (T, d_in, d_out): one token, a few, every tile size, ragged in eac
     (17, 1040, 80), (37, 528, 1008), (64, 384, 128), (65, 2048, 320), (130, 400, 272),
     (200, 112, 1552), (257, 640, 784), (513, 1152, 1280), (1100, 240, 2576), (3000, 128, 2832),
     (3900, 272, 5120), (2304, 160, 8208), (4096, 96, 6416),
-    (64, 8208, 512), (100, 6160, 784), (40, 13824, 272),     # split over d_in, ragged ends
+    (132, 48, 11008), (387, 48, 10992), (515, 48, 11104), (259, 48, 10928), (386, 48, 12368),
+    (35, 112, 8480), (64, 8208, 512), (100, 6160, 784), (40, 13824, 272),     # split over d_in, ragged ends
 ]
 
 
@@ -125,6 +126,20 @@ def test_forward(gpu_lib, T, d_in, d_out, dtype):
     gy, gz = run(gpu_lib, p, act, dtype)
     check(gz, z, tz + half_step(dtype) * (z.abs() + tz), "z")
     check(gy, y, ty + half_step(dtype) * (y.abs() + ty), "y")
+
+
+@pytest.mark.parametrize("T,d_in,d_out", [(1540, 656, 11600), (1287, 656, 14864)])
+def test_forward_in_two_launches(gpu_lib, T, d_in, d_out):
+    """Whole rounds of large tiles, the remaining columns in smaller ones:
+    a sample of the rows, the last ones among them."""
+    p = problem(17, T, d_in, d_out, BF16)
+    gy, gz = run(gpu_lib, p, "gelu_tanh", BF16)
+    rows = torch.tensor([0, 1, 255, 256, T // 2, T - 2, T - 1])
+    xq, s_x, wq, s_w, bias, res = p
+    z, tz, y, ty = reference((xq[rows], s_x, wq, s_w, bias, res[rows]), "gelu_tanh", True, True)
+    check(gz.cpu()[rows], z, tz + half_step(BF16) * (z.abs() + tz), "z")
+    check(gy.cpu()[rows], y, ty + half_step(BF16) * (y.abs() + ty), "y")
+    assert torch.isfinite(gy).all() and torch.isfinite(gz).all()
 
 
 @pytest.mark.parametrize("use_bias,use_res,keep_z", [(False, False, False), (True, False, True),
