@@ -37,7 +37,8 @@ __all__ = ["load", "FalqError", "fp8_quantize", "fp8_quantize_workspace_bytes",
            "lora_separate_fp8_fwd", "lora_separate_fp8_bwd", "lora_bf16_saved_bytes",
            "lora_bf16_workspace_bytes", "lora_bf16_fwd", "lora_bf16_bwd", "layer_norm_fwd",
            "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "ACTIVATIONS",
-           "melded_linear_fwd_act", "melded_linear_fwd_act_workspace_bytes", "linear_act_bwd", "linear_act_bwd_workspace_bytes",
+           "melded_linear_fwd_act", "melded_linear_fwd_act_workspace_bytes",
+           "linear_act_bwd", "linear_act_bwd_workspace_bytes",
            "grad_norm", "grad_clip", "grad_norm_workspace_bytes", "GRAD_MAX_TENSORS"]
 
 #: bytes of the per-device scratch array behind fp8_quantize_noalloc

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <vector>
 
 namespace {
@@ -728,6 +729,35 @@ inline bool rows_ok(int64_t T, int64_t d) {
   return T >= 0 && T <= (int64_t)1 << 30 && d >= 1 && d <= (int64_t)1 << 24;
 }
 
+// memory of a call: count elements of size bytes (NULL: not given)
+struct Mem {
+  uintptr_t lo, hi;
+  Mem(const void* p, int64_t count, int64_t size)
+      : lo(reinterpret_cast<uintptr_t>(p)), hi(p ? lo + (uintptr_t)(count * size) : lo) {}
+  bool meets(const Mem& o) const {
+    return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi;
+  }
+};
+inline Mem elements(const void* p, int64_t count, int dtype) {
+  return Mem(p, count, dtype == FALQ_BF16 ? 2 : 4);
+}
+inline Mem floats(const void* p, int64_t count) { return Mem(p, count, 4); }
+inline Mem bytes(const void* p, size_t count) { return Mem(p, (int64_t)count, 1); }
+
+// Whether the outputs lie apart from each other and from the inputs.  in_place:
+// an input that may also be outs[0] itself, but not overlap it partly.
+bool apart(std::initializer_list<Mem> outs, std::initializer_list<Mem> ins, const Mem& in_place) {
+  const Mem* o = outs.begin();
+  for (size_t i = 0; i < outs.size(); ++i) {
+    for (size_t k = i + 1; k < outs.size(); ++k)
+      if (o[i].meets(o[k])) return false;
+    for (const Mem& m : ins)
+      if (o[i].meets(m)) return false;
+    if (o[i].meets(in_place) && (i != 0 || o[i].lo != in_place.lo)) return false;
+  }
+  return true;
+}
+
 // Whether the outputs are disjoint from each other and from every input but
 // their own, which an output may be (in place) or miss, never overlap partly.
 bool disjoint(int64_t count, const void* const* g, const int64_t* n, const int32_t* dtype,
@@ -766,6 +796,10 @@ falq_status grad_norm_impl(int64_t count, const void* const* g, const int64_t* n
   if (count < 0 || count > FALQ_GRAD_MAX_TENSORS || !scalar(norm)) return FALQ_EINVAL;
   if (count > 0 && (!g || !n || !dtype)) return FALQ_EINVAL;
   if (!(max_norm >= 0.0f) || !(eps >= 0.0f) || std::isinf(eps)) return FALQ_EINVAL;
+  const size_t need_ws = falq::grad_norm_ws_bytes(count);
+  if (!ws_ok(ws, ws_bytes, need_ws)) return FALQ_EINVAL;
+  const Mem result = floats(norm, 1), work = bytes(ws, need_ws);
+  if (result.meets(work)) return FALQ_EINVAL;
   int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (n[i] < 0 || n[i] > (int64_t)1 << 40 || !dtype_ok(dtype[i])) return FALQ_EINVAL;
@@ -774,8 +808,11 @@ falq_status grad_norm_impl(int64_t count, const void* const* g, const int64_t* n
     const size_t size = dtype[i] == FALQ_BF16 ? 2 : 4;
     if (n[i] > 0 && (!g[i] || !aligned(g[i], size))) return FALQ_EINVAL;
     if (n[i] > 0 && out && (!out[i] || !aligned(out[i], size))) return FALQ_EINVAL;
+    const Mem in = elements(g[i], n[i], dtype[i]);
+    const Mem to = elements(out ? out[i] : nullptr, n[i], dtype[i]);
+    if (in.meets(result) || in.meets(work) || to.meets(result) || to.meets(work))
+      return FALQ_EINVAL;
   }
-  if (!ws_ok(ws, ws_bytes, falq::grad_norm_ws_bytes(count))) return FALQ_EINVAL;
   if (out) {
     try {
       if (!disjoint(count, g, n, dtype, out)) return FALQ_EINVAL;
@@ -797,7 +834,10 @@ falq_status layer_norm_fwd(const void* x, int x_dtype, const float* weight, cons
   if (!rows_ok(T, d) || !dtype_ok(x_dtype) || !dtype_ok(y_dtype)) return FALQ_EINVAL;
   if (!(eps >= 0.0f) || std::isinf(eps)) return FALQ_EINVAL;
   if (!opt_f32(weight) || !opt_f32(bias) || !opt_f32(mean) || !opt_f32(rstd)) return FALQ_EINVAL;
-  if (T > 0 && (!elems(x, x_dtype) || !elems(y, y_dtype) || x == y)) return FALQ_EINVAL;
+  if (T > 0 && (!elems(x, x_dtype) || !elems(y, y_dtype))) return FALQ_EINVAL;
+  if (!apart({elements(y, T * d, y_dtype), floats(mean, T), floats(rstd, T)},
+             {elements(x, T * d, x_dtype), floats(weight, d), floats(bias, d)}, floats(nullptr, 0)))
+    return FALQ_EINVAL;
   return hip_status(falq::launch_layer_norm_fwd(x, x_dtype, weight, bias, T, d, eps, y, y_dtype,
                                                 mean, rstd,
                                                 reinterpret_cast<hipStream_t>(stream)));
@@ -814,11 +854,14 @@ falq_status layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x_dt
   if (!rows_ok(T, d) || !dtype_ok(x_dtype) || !dtype_ok(dy_dtype)) return FALQ_EINVAL;
   if (!opt_f32(weight) || !opt_elems(dx, dy_dtype) || !opt_f32(dweight) || !opt_f32(dbias))
     return FALQ_EINVAL;
-  if (dweight && dweight == dbias) return FALQ_EINVAL;
   if (T > 0 && (!elems(dy, dy_dtype) || !elems(x, x_dtype) || !scalar(mean) || !scalar(rstd)))
     return FALQ_EINVAL;
-  if (T > 0 && dx == x) return FALQ_EINVAL;
-  if ((dweight || dbias) && !ws_ok(ws, ws_bytes, falq::layer_norm_bwd_ws_bytes(T, d)))
+  const size_t need_ws = dweight || dbias ? falq::layer_norm_bwd_ws_bytes(T, d) : 0;
+  if (!ws_ok(ws, ws_bytes, need_ws)) return FALQ_EINVAL;
+  if (!apart({elements(dx, T * d, dy_dtype), floats(dweight, d), floats(dbias, d),
+              bytes(ws, need_ws)},
+             {elements(x, T * d, x_dtype), floats(weight, d), floats(mean, T), floats(rstd, T)},
+             elements(dy, T * d, dy_dtype)))
     return FALQ_EINVAL;
   return hip_status(falq::launch_layer_norm_bwd(dy, dy_dtype, x, x_dtype, weight, mean, rstd, T,
                                                 d, dx, dweight, dbias, ws,
@@ -841,8 +884,13 @@ falq_status melded_linear_fwd_act(const uint8_t* xq, const float* s_x, const uin
   if (d_out * d_in > 0 && !need(wq)) return FALQ_EINVAL;
   if (T * d_out > 0 && (!elems(y, dtype) || !opt_elems(z, dtype) || !opt_elems(residual, dtype)))
     return FALQ_EINVAL;
-  if (T * d_out > 0 && z && (z == y || z == residual)) return FALQ_EINVAL;
-  if (!ws_ok(ws, ws_bytes, falq::linear_act_ws_bytes(T, d_in, d_out))) return FALQ_EINVAL;
+  const size_t need_ws = falq::linear_act_ws_bytes(T, d_in, d_out);
+  if (!ws_ok(ws, ws_bytes, need_ws)) return FALQ_EINVAL;
+  if (!apart({elements(y, T * d_out, dtype), elements(z, T * d_out, dtype), bytes(ws, need_ws)},
+             {bytes(xq, (size_t)(T * d_in)), bytes(wq, (size_t)(d_out * d_in)), floats(s_x, 1),
+              floats(s_w, 1), floats(bias, d_out)},
+             elements(residual, T * d_out, dtype)))
+    return FALQ_EINVAL;
   return hip_status(falq::launch_linear_act(xq, s_x, wq, s_w, bias, residual, T, d_in, d_out, act,
                                             dtype, y, z, ws,
                                             reinterpret_cast<hipStream_t>(stream)));
@@ -862,10 +910,13 @@ falq_status linear_act_bwd(const void* dy, int dy_dtype, const void* z, int z_dt
   if (d_out < 0 || !rows_ok(T, std::max<int64_t>(d_out, 1)) || !opt_f32(dbias)) return FALQ_EINVAL;
   if (d_out == 0) return FALQ_OK;
   if (!dz && !dbias) return FALQ_EINVAL;
-  if (T > 0 && (!elems(dy, dy_dtype) || !opt_elems(dz, dy_dtype) || (dz && dz == z)))
-    return FALQ_EINVAL;
+  if (T > 0 && (!elems(dy, dy_dtype) || !opt_elems(dz, dy_dtype))) return FALQ_EINVAL;
   if (T > 0 && act != FALQ_ACT_NONE && !elems(z, z_dtype)) return FALQ_EINVAL;
-  if (dbias && !ws_ok(ws, ws_bytes, falq::linear_act_bwd_ws_bytes(T, d_out))) return FALQ_EINVAL;
+  const size_t need_ws = dbias ? falq::linear_act_bwd_ws_bytes(T, d_out) : 0;
+  if (!ws_ok(ws, ws_bytes, need_ws)) return FALQ_EINVAL;
+  if (!apart({elements(dz, T * d_out, dy_dtype), floats(dbias, d_out), bytes(ws, need_ws)},
+             {elements(z, T * d_out, z_dtype)}, elements(dy, T * d_out, dy_dtype)))
+    return FALQ_EINVAL;
   return hip_status(falq::launch_linear_act_bwd(dy, dy_dtype, z, z_dtype, T, d_out, act, dz,
                                                 dbias, ws,
                                                 reinterpret_cast<hipStream_t>(stream)));

@@ -1,10 +1,11 @@
 // Loads and stores of float32 / bfloat16 elements as floats, and wave sums, for
 // the row-wise operators.
 //
-// E consecutive elements per lane: 4 or 8 (1 for rows shorter than that).  Stores of float32 take 4, 16 bytes a lane, so that a wave's store is
-// one run of whole 128-byte lines: 32 bytes of a lane are two stores of half
-// lines each, which the streaming hint below does not join again (backward of
-// an activation, 8192 x 11008, fp32 gradients: 216 us with 8, 175 with 4).
+// E consecutive elements per lane: 4 or 8 (1 for rows shorter than that).  Stores
+// of float32 take 4, 16 bytes a lane, so that a wave's store is one run of whole
+// 128-byte lines: 32 bytes of a lane are two stores of half lines each, which the
+// streaming hint below does not join again (backward of an activation, 8192 x
+// 11008, fp32 gradients: 216 us with 8, 175 with 4).
 #pragma once
 
 #include "common.hpp"

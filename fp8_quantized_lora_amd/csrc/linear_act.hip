@@ -5,7 +5,7 @@
 // residual are float32, and each output is rounded once.
 //
 // Tiles: the scheme of the direct-to-LDS kernel in gemm_fp8_kernel.hpp (two
-// LDS stages of 128 K-bytes, v_mfma_f32_16x16x128_f8f6f4, XOR-swizzled rows),
+// to four LDS stages of 128 K-bytes, v_mfma_f32_16x16x128_f8f6f4, swizzled rows),
 // for any tile size and any K that is a multiple of 16: in a last step of
 // fewer than 128 bytes the chunks past K are cleared in LDS.
 //
@@ -43,7 +43,8 @@ hipError_t launch_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N
                         int64_t n_first, int64_t n_end, const Epilogue& ep, hipStream_t s) {
   const int tM = (int)((M + C::BM - 1) / C::BM);
   const int tN = (int)((n_end - n_first + C::BN - 1) / C::BN);
-  const int64_t out = M * N * (int64_t)sizeof(OT) * (1 + (ep.z != nullptr) + (ep.residual != nullptr));
+  const int64_t out = M * N * (int64_t)sizeof(OT) *
+                      (1 + (ep.z != nullptr) + (ep.residual != nullptr));
   // the streaming hint needs whole lines: 16-byte stores, so bfloat16
   if (sizeof(OT) == 2 && out + M * K + N * K > kStreamBytes)
     linear_act_tile<C, OT, sizeof(OT) == 2><<<tM * tN, C::kThreads, 0, s>>>(

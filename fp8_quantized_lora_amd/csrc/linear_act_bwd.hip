@@ -19,9 +19,9 @@ constexpr int kLanes = 32;
 
 // part: the strips' sums, one row of d floats each (dbias itself with one strip)
 template <class GT, class ZT, int E, int ACT, int kRows, bool STREAM, bool ODD>
-__global__ __launch_bounds__(kRows * kLanes) void act_bwd_kernel(const GT* dy, const ZT* __restrict__ z,
-                                                      GT* dz, float* __restrict__ part, int64_t T,
-                                                      int64_t d, int64_t rows_per_strip) {
+__global__ __launch_bounds__(kRows * kLanes) void act_bwd_kernel(
+    const GT* dy, const ZT* __restrict__ z, GT* dz, float* __restrict__ part, int64_t T, int64_t d,
+    int64_t rows_per_strip) {
   __shared__ float sb[kRows][kLanes * E];
   const int cl = threadIdx.x % kLanes, rl = threadIdx.x / kLanes;
   const Piece<E, ODD> p(((uint32_t)blockIdx.x * kLanes + cl) * E, (uint32_t)d);

@@ -64,9 +64,8 @@ __device__ __forceinline__ void finish1(float v, float scale, float bias, const 
 // its NW waves take the 128-byte K steps in turn (adjacent waves read adjacent
 // memory), each with the loads of U steps in flight, straight into the
 // registers the matrix core reads; the waves' partial sums join in LDS in wave
-// order.  A
-// lane holds chunks g and g + 4 (16 bytes each) of row l % 16, g = l / 16, of
-// both operands, so whatever order the matrix core takes K in, the operands
+// order.  A lane holds chunks g and g + 4 (16 bytes each) of row l % 16, g = l / 16,
+// of both operands, so whatever order the matrix core takes K in, the operands
 // agree.  Chunks past K are cleared in both (a code there may be a NaN).
 template <int MT, int NB, int NW, int U, class OT>
 __global__ __launch_bounds__(NW * 64) void linear_act_few(const uint8_t* __restrict__ A,

@@ -225,7 +225,6 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
   }
 }
 
-
 // y (and z) from the S planes of partial sums
 template <int ACT, class OT>
 __device__ __forceinline__ void join8(const float* __restrict__ part, int S, int64_t plane,

@@ -609,8 +609,10 @@ falq_status lora_bf16_bwd(const float *dy, const uint8_t *gq, const float *s_g, 
  * float32 or wider and their order is fixed by the sizes, so results repeat
  * bit for bit.  These tensors need only their element's alignment (the FP8
  * codes 16 bytes as elsewhere), so rows may begin anywhere in a larger buffer;
- * 16-byte aligned rows are the fastest.  Two calls that may run at the same
- * time need a workspace each.
+ * 16-byte aligned rows are the fastest.  Outputs and the workspace lie apart
+ * from each other and from every input: a call where they overlap is refused,
+ * but for an output that may be its own input (in place), as stated there.
+ * Two calls that may run at the same time need a workspace each.
  */
 
 /*
@@ -619,7 +621,7 @@ falq_status lora_bf16_bwd(const float *dy, const uint8_t *gq, const float *s_g, 
  *     y = (x - mu) * rstd * weight + bias
  * rounded once to y's type.  A row with a NaN or an infinity is NaN.
  *
- *   x, y          [T x d] float32 or bfloat16 each, not the same memory;
+ *   x, y          [T x d] float32 or bfloat16 each;
  *                 1 <= d <= 2^24
  *   weight, bias  [d] float32, device, or NULL (1 and 0)
  *   mean, rstd    [T] float32, device (output), or NULL; the backward's inputs
@@ -667,7 +669,7 @@ typedef enum {
  *   act               falq_activation
  *   residual          [T x d_out] of type dtype, or NULL; may be y (added in place)
  *   y                 [T x d_out] of type dtype (output)
- *   z                 [T x d_out] of type dtype (output), or NULL; not y or residual
+ *   z                 [T x d_out] of type dtype (output), or NULL
  *   ws                melded_linear_fwd_act_workspace_bytes(T, d_in, d_out): 0
  *                     (ws may be NULL) unless few outputs meet a long d_in,
  *                     and always for T <= 16
@@ -685,8 +687,8 @@ falq_status melded_linear_fwd_act(const uint8_t *xq, const float *s_x, const uin
  * (relu'(z) = 1 for z > 0, else 0).  dz is what fp8_quantize and the product's
  * backward take as the upstream gradient; the residual's gradient is dy.
  *
- *   dy, dz   [T x d_out], one type; dz may be dy (in place), not z, or NULL
- *            where only dbias is wanted
+ *   dy, dz   [T x d_out], one type; dz may be dy (in place), or NULL where only
+ *            dbias is wanted
  *   z        [T x d_out] float32 or bfloat16: the forward's z; NULL allowed
  *            for FALQ_ACT_NONE; any d_out from 0 to 2^24
  *   dbias    [d_out] float32 (output), or NULL; zero for T = 0

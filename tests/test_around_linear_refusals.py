@@ -117,6 +117,50 @@ def test_grad_calls():
         assert both(**bad)[1] == EINVAL, bad
 
 
+def test_overlaps_are_refused():
+    """One element of an output in another tensor of the call, in the workspace or
+    in its own input but not at its start."""
+    lib = fq.load()
+    at = [(i + 1) << 24 for i in range(10)]                 # far apart
+    x, w, b, mu, rs, dy, o, dw, db, ws = at
+    T, d = 2000, 64
+    big = T * d * 4
+    fwd = [x, 0, w, b, T, d, 1e-5, o, 0, mu, rs, None]
+    refused(lib.layer_norm_fwd, fwd,
+            [(7, x), (7, x + big - 4), (7, x - big + 4), (7, w), (7, b + 4 * d - 4),
+             (7, mu + 4 * T - 4), (9, rs - 4 * T + 4), (9, x + 4), (9, w), (10, x), (10, mu)])
+    nb = fq.layer_norm_bwd_workspace_bytes(T, d)
+    bwd = [dy, 0, x, 0, w, mu, rs, T, d, o, dw, db, ws, nb, None]
+    refused(lib.layer_norm_bwd, bwd,
+            [(9, x), (9, dy + 4), (9, dy - 4), (9, w), (9, mu), (9, rs), (9, dw), (9, ws),
+             (10, db + 4), (10, db), (10, dy), (10, w), (11, ws + nb - 4), (11, x), (12, dy),
+             (12, x)])
+    xq, sx, wq, sw, b, res, y, z, ws = at[:9]
+    T, d_in, d_out = 64, 13824, 5120
+    nb, big = fq.melded_linear_fwd_act_workspace_bytes(T, d_in, d_out), T * d_out * 2
+    act = [xq, sx, wq, sw, b, 2, res, T, d_in, d_out, 1, y, z, ws, nb, None]
+    refused(lib.melded_linear_fwd_act, act,
+            [(11, res + 2), (11, res - 2), (11, z + big - 2), (11, xq + T * d_in - 2),
+             (11, wq - 2 + d_in * d_out), (11, sx), (11, sw), (11, b), (11, ws), (12, res),
+             (12, xq), (12, ws - 2), (12, b - big + 2), (13, xq), (13, wq), (13, res)])
+    dy, z, dz, db, ws = at[:5]
+    T, d = 1000, 48
+    nb = fq.linear_act_bwd_workspace_bytes(T, d)
+    ok = [dy, 0, z, 1, 2, T, d, dz, db, ws, nb, None]
+    refused(lib.linear_act_bwd, ok,
+            [(7, z), (7, z + T * d * 2 - 4), (7, dy + 4), (7, db), (7, ws), (8, dy), (8, z),
+             (8, ws), (8, dz + 4), (9, dy), (9, z)])
+    g0, g1, norm, ws, o0, o1 = at[:6]
+    nb = fq.grad_norm_workspace_bytes(2)
+    g, n, t = arrays((g0, g1), (100, 100), (0, 1))
+    out = arrays((o0, o1), (100, 100), (0, 1))[0]
+    for r, w in ((g0 + 396, ws), (g1, ws), (ws + nb - 4, ws), (norm, g0 & ~255), (norm, g1)):
+        assert lib.grad_norm(2, g, n, t, r, w, nb, None) == EINVAL
+        assert lib.grad_clip(2, g, n, t, 1.0, 0.0, out, r, w, nb, None) == EINVAL
+    for r, w in ((o0, ws), (o1 + 196, ws), (norm, o1)):
+        assert lib.grad_clip(2, g, n, t, 1.0, 0.0, out, r, w, nb, None) == EINVAL
+
+
 def test_binding_refuses_before_the_library():
     x = torch.zeros((4, 64))
     w, s, q = torch.zeros(64), torch.zeros(4), torch.zeros((4, 64), dtype=torch.uint8)

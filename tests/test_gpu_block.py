@@ -185,3 +185,52 @@ def test_layers_with_an_epilogue(gpu_lib):
     m.backward(dy)
     assert rel(m.dx, dec(m.gq, m.s_g) @ dec(m.wq, m.s_w)) <= 1e-3 and m.dz is None
     m.step(x, dy)
+
+
+@pytest.mark.parametrize("T, D", [(1, 16), (5, 48), (300, 272)])
+def test_tensors_side_by_side(gpu_lib, T, D):
+    """All tensors of a call carved from one buffer without gaps: nothing is
+    refused, and every output is what separate tensors give."""
+    fq, dev = gpu_lib, "cuda"
+    f32 = torch.float32
+    rows, vec, col = (f32, (T, D)), (f32, (D,)), (f32, (T,))
+    one = (f32, (1,))
+
+    def carved(*kinds):
+        need = sum(torch.empty(s, dtype=t).numel() * t.itemsize for t, s in kinds)
+        buf, at, out = torch.zeros(need, dtype=torch.uint8, device=dev), 0, []
+        for t, s in kinds:
+            k = math.prod(s) * t.itemsize
+            out.append(buf[at:at + k].view(t).view(s))
+            at += k
+        return out
+
+    def apart(*kinds):
+        return [torch.zeros(s, dtype=t, device=dev) for t, s in kinds]
+
+    g = torch.Generator().manual_seed(5)
+    draw = lambda s: torch.randn(s, generator=g).cuda()  # noqa: E731
+    X, DY, W, B, RES = draw((T, D)), draw((T, D)), draw(D), draw(D), draw((T, D))
+    Xq, sx = torch.empty((T, D), dtype=torch.uint8, device=dev), torch.empty(1, device=dev)
+    fq.fp8_quantize(X, Xq, sx)
+    Wq, sw = torch.empty((D, D), dtype=torch.uint8, device=dev), torch.empty(1, device=dev)
+    fq.fp8_quantize(draw((D, D)), Wq, sw)
+    got = []
+    for place in (carved, apart):
+        x, y, dy, w, b, dw, db, mean, rstd = place(rows, rows, rows, vec, vec, vec, vec, col, col)
+        x.copy_(X), dy.copy_(DY), w.copy_(W), b.copy_(B)
+        fq.layer_norm_fwd(x, w, b, y, mean, rstd)
+        fq.layer_norm_bwd(dy, x, w, mean, rstd, dy, dw, db)
+        xq, wq, res, o, z, bias, s1, s2 = place((torch.uint8, (T, D)), (torch.uint8, (D, D)), rows,
+                                                rows, rows, vec, one, one)
+        xq.copy_(Xq), wq.copy_(Wq), res.copy_(RES), bias.copy_(B), s1.copy_(sx), s2.copy_(sw)
+        fq.melded_linear_fwd_act(xq, s1, wq, s2, o, bias=bias, act="gelu", residual=res, z=z)
+        d2, z2, dbias = place(rows, rows, vec)
+        d2.copy_(DY), z2.copy_(z)
+        fq.linear_act_bwd(d2, z2, d2, dbias=dbias, act="gelu")
+        g0, g1, o0, o1, norm = place(rows, vec, rows, vec, one)
+        g0.copy_(d2), g1.copy_(dbias)
+        fq.grad_clip([g0, g1], 0.5, norm, out=[o0, o1])
+        got.append((y, mean, rstd, dy, dw, db, o, z, d2, dbias, o0, o1, norm, x, w, xq, res, g0))
+    for i, (a, b) in enumerate(zip(*got)):
+        assert torch.equal(a, b), i
