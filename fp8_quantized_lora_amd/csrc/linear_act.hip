@@ -4,19 +4,17 @@
 // caller keeps it for the backward.  Accumulation, bias, activation and
 // residual are float32, and each output is rounded once.
 //
-// Tiles: the scheme of the direct-to-LDS kernel in gemm_fp8_kernel.hpp (two
-// to four LDS stages of 128 K-bytes, v_mfma_f32_16x16x128_f8f6f4, swizzled rows),
-// for any tile size and any K that is a multiple of 16: in a last step of
-// fewer than 128 bytes the chunks past K are cleared in LDS.
+// Two kinds of tile kernel, for any tile size and any K that is a multiple of 16
+// (in a last step of fewer than 128 bytes the chunks past K are cleared in LDS),
+// both with v_mfma_f32_16x16x128_f8f6f4 on swizzled rows of 128 K-bytes that were
+// loaded straight into LDS: linear_act_pipe (linear_act_pipe.hpp) for many
+// outputs, linear_act_tile (linear_act_tile.hpp) for few.
 //
-// Long products are bound by the matrix cores (8192 x 11008 x 4096 with gelu and
-// z: 329 us, 2.2 PFLOP/s; 280 without the epilogue's work and stores; 4096 x 5120
-// x 13824 with a residual 228 us, 2.5 PFLOP/s), few tokens by reading W~ (1 x 4096
-// x 4096: 5.2 us on the GPU, 3.2 TB/s, of which a launch's latency is half).
-// Workgroups that keep their CU over several tiles, the next tile's first loads
-// under the last K step and the stores draining under the next tile, measured no
-// faster (354 us against 348 in one kind of tile): the long products run at the
-// card's power limit.
+// Long products are bound by the matrix cores, in part by their power, and by
+// the outputs (8192 x 11008 x 4096 with gelu and z: 307 us, 2.4 PFLOP/s; 275
+// without the epilogue's work and z; 4096 x 5120 x 13824 with a residual 206 us,
+// 2.8 PFLOP/s), few tokens by reading W~ (1 x 4096 x 4096: 5.2 us on the GPU, 3.2
+// TB/s, of which a launch's latency is half).
 //
 // Epilogue: a lane holds four columns of a row per 16 x 16 block, so a store
 // from the registers would be 8 or 16 bytes wide.  Each wave passes its
@@ -29,6 +27,7 @@
 #include "elem.hpp"
 #include "gemm_fp8_kernel.hpp"
 #include "kernels.hpp"
+#include "linear_act_pipe.hpp"
 #include "linear_act_tile.hpp"
 
 #include <algorithm>
@@ -37,21 +36,37 @@
 namespace falq {
 namespace {
 
-// output columns [n_first, n_end) in tiles of C
-template <class C, class OT>
+// Outputs above this go past the caches, which keeps the operands in them.
+// Below, the hint only moves the cost to the reader: with fp8_quantize of y
+// behind the product, 8192 x 11008 x 4096 gelu (172 MB) 417 us with it, 425
+// without (alone 306 and 335); 4096 x 8192 x 4096 (64 MB) 140 and 135.
+constexpr int64_t kStreamOut = (int64_t)80 << 20;
+
+// whether the outputs take the streaming hint, which needs whole lines: 16-byte
+// stores, so bfloat16
+template <class OT>
+bool stream_outputs(int64_t M, int64_t N, const Epilogue& ep) {
+  return sizeof(OT) == 2 && M * N * 2 * (1 + (ep.z != nullptr)) > kStreamOut;
+}
+
+// tiles of C: linear_act_tile, or PIPE workgroups of linear_act_pipe per CU
+template <class C, int PIPE, class OT>
 hipError_t launch_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
-                        int64_t n_first, int64_t n_end, const Epilogue& ep, hipStream_t s) {
-  const int tM = (int)((M + C::BM - 1) / C::BM);
-  const int tN = (int)((n_end - n_first + C::BN - 1) / C::BN);
-  const int64_t out = M * N * (int64_t)sizeof(OT) *
-                      (1 + (ep.z != nullptr) + (ep.residual != nullptr));
-  // the streaming hint needs whole lines: 16-byte stores, so bfloat16
-  if (sizeof(OT) == 2 && out + M * K + N * K > kStreamBytes)
-    linear_act_tile<C, OT, sizeof(OT) == 2><<<tM * tN, C::kThreads, 0, s>>>(
-        A, B, (int)M, (int)N, (int)K, (int)n_first, tM, tN, ep);
+                        const Epilogue& ep, hipStream_t s) {
+  const int tM = (int)((M + C::BM - 1) / C::BM), tN = (int)((N + C::BN - 1) / C::BN);
+  const auto go = [&](auto stream) {
+    constexpr bool STREAM = decltype(stream)::value;
+    if constexpr (PIPE > 0)
+      linear_act_pipe<C, PIPE, OT, STREAM><<<tM * tN, C::kThreads, 0, s>>>(
+          A, B, (int)M, (int)N, (int)K, tM, tN, ep);
+    else
+      linear_act_tile<C, OT, STREAM><<<tM * tN, C::kThreads, 0, s>>>(A, B, (int)M, (int)N, (int)K,
+                                                                     tM, tN, ep);
+  };
+  if (stream_outputs<OT>(M, N, ep))
+    go(std::bool_constant<sizeof(OT) == 2>{});
   else
-    linear_act_tile<C, OT, false><<<tM * tN, C::kThreads, 0, s>>>(
-        A, B, (int)M, (int)N, (int)K, (int)n_first, tM, tN, ep);
+    go(std::false_type{});
   return hipGetLastError();
 }
 
@@ -63,55 +78,72 @@ hipError_t launch_few(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, 
   return hipGetLastError();
 }
 
-// Which tile: the one whose rounds of the 256 CUs take least.  A K step of a
-// round of tiles costs (us, measured at 256 to 1024 tiles and 4096 and 8192
-// K-bytes)
-//     256 x 320  2.1      256 x 256  1.68     256 x 128  1.08     128 x 256  1.08
-//     192 x 128  0.82     128 x 192  0.82     128 x 128  0.62
-//      64 x  64  0.27      32 x  64  0.24
-// and a launch about 4 more for the first loads and the last stores: a larger
-// tile moves fewer bytes per product but leaves more of its last round empty.
-// 512 x 4096 x 4096: 15.5 in tiles of 64 x 64, 18.9 in 128 x 128 (half a round),
-// 17.5 in 32 x 128; 128 x 4096: 10.0 in 32 x 64, 10.9 in 64 x 64, 14 in 64 x
-// 128; 4096 x 5120 x 13824: 230 in 256 x 320 (one round), 252 in
-// a round of 256 x 256 and one of 128 x 128, 345 in 256 x 256; 512 x 11008 x 4096
-// with gelu and z: 31.5 in 128 x 192 (232 tiles), 36.7 in 128 x 256, 45 in 128 x
-// 128.
-enum TileKind {
-  k256, k256x320, k256x128, k128x256, k192x128, k128x192, k128, k64, k32x64, kTileKinds
+// Which tile: the one whose rounds of the 256 CUs take least, by this model of
+// them (us; gelu and z, 512 to 10240 columns, 4096 to 13824 K-bytes: within a
+// tenth of the measured times, mostly).  A larger tile moves fewer bytes per
+// product but leaves more of its last round empty, and where a CU holds one
+// workgroup, all of a round's outputs are stored at once, with the matrix cores
+// idle; where it holds two, one stores under the other's products.
+//   8192 x 11008 x 4096 with gelu and z: 305 in 256 x 128, 342 in 256 x 256,
+//     375 in 256 x 320 (a fifth round of 96 tiles), 345 in 128 x 128
+//   4096 x 5120 x 13824: 187 in 256 x 320 (one round), 265 in 256 x 256
+//   4096 x 4096 x 8192: 98 in 256 x 256 (one round), 110 in 256 x 128
+//   1024 x 5120 x 5120 with gelu and z: 31.8 in 192 x 128, 36.2 in 256 x 128
+//   512 x 11008 x 4096: 31.5 in 128 x 192, 36 in 256 x 128, 40 in 128 x 128
+//   512 x 4096 x 4096: 15.5 in 64 x 64, 128 x 4096 x 4096: 10.0 in 32 x 64
+// Fitted to 128 to 1024 tiles at 1024 and 4096 K-bytes, and 1056 and 4128 for rows
+// that begin inside a 128-byte line (each step's chunk of a row then lies in two),
+// between the times of a plain output and of gelu and z.
+struct TileCost {
+  int bm, bn;
+  int per_cu;          // workgroups of a round on a CU
+  float start, round;  // a launch, and a round of it, besides the K steps
+  // a K step, at most one workgroup on a CU and at per_cu: rows of whole lines
+  // and others
+  struct {
+    float alone, full;
+  } step[2];
 };
-constexpr int kTileM[kTileKinds] = {256, 256, 256, 128, 192, 128, 128, 64, 32};
-constexpr int kTileN[kTileKinds] = {256, 320, 128, 256, 128, 192, 128, 64, 64};
-constexpr float kStep[kTileKinds] = {1.68f, 2.1f,  1.08f, 1.08f, 0.82f,
-                                     0.82f, 0.62f, 0.27f, 0.24f};
-constexpr float kLaunch = 4.0f;
+// Down to 128 x 128 linear_act_pipe, but for w8 and the small ones, which are
+// linear_act_tile: more waves, which begin and end a tile faster.
+enum TileKind {
+  k256x320, k256, k256x128, k128x256, k192x128, k128x192w8, k128, k128w8, k64, k32x64, kTileKinds
+};
+constexpr TileCost kTile[kTileKinds] = {
+    {256, 320, 1, 4.0f, 23.0f, {{1.47f, 1.47f}, {1.75f, 1.75f}}},
+    {256, 256, 1, 3.0f, 15.0f, {{1.23f, 1.23f}, {1.50f, 1.50f}}},
+    {256, 128, 2, 2.0f, 10.0f, {{0.70f, 1.45f}, {1.07f, 2.05f}}},
+    {128, 256, 2, 2.0f, 10.0f, {{0.72f, 1.45f}, {1.08f, 2.05f}}},
+    {192, 128, 2, 4.0f, 7.0f, {{0.52f, 1.03f}, {0.88f, 1.65f}}},
+    {128, 192, 1, 2.5f, 6.0f, {{0.68f, 0.68f}, {0.85f, 0.85f}}},
+    {128, 128, 2, 4.5f, 4.5f, {{0.39f, 0.78f}, {0.69f, 1.30f}}},
+    {128, 128, 1, 3.0f, 3.0f, {{0.50f, 0.50f}, {0.68f, 0.68f}}},
+    {64, 64, 2, 2.0f, 1.5f, {{0.27f, 0.50f}, {0.31f, 0.61f}}},
+    {32, 64, 2, 2.0f, 1.0f, {{0.23f, 0.45f}, {0.23f, 0.48f}}}};
 constexpr int kCUs = 256;
+// the tiles of linear_act_pipe reach this far into a row by 32-bit offsets
+constexpr int64_t kFarK = (int64_t)1 << 23;
 
-int64_t tiles_of(TileKind k, int64_t M, int64_t n) {
-  return ((M + kTileM[k] - 1) / kTileM[k]) * ((n + kTileN[k] - 1) / kTileN[k]);
+int64_t tiles_of(TileKind k, int64_t M, int64_t N) {
+  return ((M + kTile[k].bm - 1) / kTile[k].bm) * ((N + kTile[k].bn - 1) / kTile[k].bn);
 }
 
-float tile_cost(TileKind k, int64_t M, int64_t n, int64_t steps) {
-  const int64_t nt = tiles_of(k, M, n);
+float tile_cost(TileKind k, int64_t M, int64_t N, int64_t K) {
+  const TileCost& t = kTile[k];
+  const int64_t nt = tiles_of(k, M, N), cap = (int64_t)t.per_cu * kCUs, rest = nt % cap;
   // a grid holds fewer than 2^32 threads: very long outputs take large tiles
   if (k != k256 && nt >= 1 << 23) return HUGE_VALF;
-  return kLaunch + kStep[k] * (float)steps * (float)((nt + kCUs - 1) / kCUs);
+  const auto& step = t.step[K % 128 != 0];
+  const float last = rest == 0 ? 0.0f : rest <= kCUs ? step.alone : step.full;
+  return t.start + (float)((nt + cap - 1) / cap) * t.round +
+         (float)((K + 127) / 128) * ((float)(nt / cap) * step.full + last);
 }
 
-TileKind best_tile(int64_t M, int64_t n, int64_t steps) {
-  int best = 0;
-  for (int k = 1; k < kTileKinds; ++k)
-    if (tile_cost((TileKind)k, M, n, steps) < tile_cost((TileKind)best, M, n, steps)) best = k;
-  return (TileKind)best;
-}
-
-// How a product runs: by few tokens, by tiles of one kind, by whole rounds of
-// 256 x 256 tiles (cols of their columns) and the remaining columns in tiles of
-// `kind`, or by 128 x 128 tiles split over K (`split` parts, kc steps each).
+// How a product runs: by few tokens, by tiles of one kind, or by 128 x 128 tiles
+// split over K (`split` parts, kc steps each).
 struct Plan {
   int few = 0;
   TileKind kind = k256;
-  int64_t cols = 0;
   int split = 1, kc = 0;
 };
 
@@ -124,34 +156,26 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   if (K > 0 && M <= 16) p.few = 1;
   if (K > 0 && M > 16 && M <= 32 && N <= 16 * kCUs) p.few = 2;
   if (p.few) return p;
-  p.kind = best_tile(M, N, steps);
-  float cost = tile_cost(p.kind, M, N, steps);
-  // whole rounds of large tiles, and the columns of a short last round in
-  // smaller ones by a second launch
-  const int64_t tM = (M + 255) / 256, tN = (N + 255) / 256;
-  const int64_t c = tM * tN / kCUs * kCUs / tM;              // tile columns in whole rounds
-  if (c > 0 && c < tN) {
-    const TileKind k2 = best_tile(M, N - c * 256, steps);
-    const float both = tile_cost(k256, M, c * 256, steps) + tile_cost(k2, M, N - c * 256, steps);
-    if (both < cost) {
-      cost = both;
-      p.kind = k2;
-      p.cols = c * 256;
-    }
+  float cost = HUGE_VALF;
+  for (int k = 0; k < kTileKinds; ++k) {
+    if (K > kFarK && k != k64 && k != k32x64) continue;
+    const float c = tile_cost((TileKind)k, M, N, K);
+    if (c >= cost) continue;
+    cost = c;
+    p.kind = (TileKind)k;
   }
   // few tiles and a long K: as many splits as give a workgroup to each CU, at
-  // least 8 steps each, and the planes written and read once at 4 TB/s.  64 x
+  // least 8 steps each, and the planes written and read once at 4 TB/s; two
+  // launches, 8 us.  64 x
   // 5120 x 13824: 22.5 us in 6 splits, 32.5 whole; 100 x 4096 x 11008: 19.8 in
   // 8, 25.8 whole; 512 x 4096 x 4096 21.1 in 2, 15.5 whole.
-  const int64_t nt = tiles_of(k128, M, N);
+  const int64_t nt = tiles_of(k128w8, M, N);
   const int64_t s = nt > 0 ? std::min<int64_t>(kCUs / nt, steps / 8) : 0;
   if (s >= 2) {
     const int64_t kc = (steps + s - 1) / s, parts = (steps + kc - 1) / kc;
-    const float split = 2 * kLaunch + kStep[k128] * (float)kc +
+    const float split = 8.0f + kTile[k128w8].step[0].alone * (float)kc +
                         (float)(parts * M * N) * 8.0f / 4e6f;
     if (parts >= 2 && split < cost) {
-      p.kind = k128;
-      p.cols = 0;
       p.split = (int)parts;
       p.kc = (int)kc;
     }
@@ -159,36 +183,32 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   return p;
 }
 
+using T128 = Tile<128, 128, 2, 4, 3>;
+
 template <class OT>
 hipError_t launch_kind(TileKind k, const uint8_t* A, const uint8_t* B, int64_t M, int64_t N,
-                       int64_t K, int64_t n_first, int64_t n_end, const Epilogue& ep,
-                       hipStream_t s) {
+                       int64_t K, const Epilogue& ep, hipStream_t s) {
   switch (k) {
-    case k256: return launch_tiles<Tile<256, 256, 2, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
-    case k256x320:
-      return launch_tiles<Tile<256, 320, 2, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
-    case k256x128:
-      return launch_tiles<Tile<256, 128, 4, 2, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
-    case k192x128:
-      return launch_tiles<Tile<192, 128, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
-    case k128x192:
-      return launch_tiles<Tile<128, 192, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
-    case k128x256:
-      return launch_tiles<Tile<128, 256, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
-    case k128:
-      return launch_tiles<Tile<128, 128, 2, 4, 3>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
-    case k64: return launch_tiles<Tile<64, 64, 2, 2, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
-    default: return launch_tiles<Tile<32, 64, 1, 4, 4>, OT>(A, B, M, N, K, n_first, n_end, ep, s);
+    case k256x320: return launch_tiles<Tile<256, 320, 2, 2>, 1, OT>(A, B, M, N, K, ep, s);
+    case k256: return launch_tiles<Tile<256, 256, 2, 2>, 1, OT>(A, B, M, N, K, ep, s);
+    case k256x128: return launch_tiles<Tile<256, 128, 2, 2>, 2, OT>(A, B, M, N, K, ep, s);
+    case k128x256: return launch_tiles<Tile<128, 256, 2, 2>, 2, OT>(A, B, M, N, K, ep, s);
+    case k192x128: return launch_tiles<Tile<192, 128, 2, 2>, 2, OT>(A, B, M, N, K, ep, s);
+    case k128x192w8: return launch_tiles<Tile<128, 192, 2, 4, 3>, 0, OT>(A, B, M, N, K, ep, s);
+    case k128: return launch_tiles<Tile<128, 128, 2, 2>, 2, OT>(A, B, M, N, K, ep, s);
+    case k128w8: return launch_tiles<T128, 0, OT>(A, B, M, N, K, ep, s);
+    case k64: return launch_tiles<Tile<64, 64, 2, 2, 4>, 0, OT>(A, B, M, N, K, ep, s);
+    default: return launch_tiles<Tile<32, 64, 1, 4, 4>, 0, OT>(A, B, M, N, K, ep, s);
   }
 }
 
 template <class OT>
 hipError_t launch_split(const Plan& p, const uint8_t* A, const uint8_t* B, int64_t M, int64_t N,
                         int64_t K, const Epilogue& ep, float* part, hipStream_t s) {
-  using C = Tile<128, 128, 2, 4, 3>;
+  using C = T128;
   const int tM = (int)((M + C::BM - 1) / C::BM), tN = (int)((N + C::BN - 1) / C::BN);
   linear_act_tile<C, OT, false, true><<<tM * tN * p.split, C::kThreads, 0, s>>>(
-      A, B, (int)M, (int)N, (int)K, 0, tM, tN, ep, part, p.kc);
+      A, B, (int)M, (int)N, (int)K, tM, tN, ep, part, p.kc);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int blocks = (int)std::min<int64_t>((M * N / 8 + 255) / 256, 2048);
@@ -203,11 +223,7 @@ hipError_t by_plan(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int
   if (p.few == 1) return launch_few<1, 1, 16, 1, OT>(A, B, M, N, K, ep, s);
   if (p.few == 2) return launch_few<2, 1, 8, 2, OT>(A, B, M, N, K, ep, s);
   if (p.split > 1) return launch_split<OT>(p, A, B, M, N, K, ep, part, s);
-  if (p.cols > 0) {
-    const hipError_t e = launch_kind<OT>(k256, A, B, M, N, K, 0, p.cols, ep, s);
-    if (e != hipSuccess) return e;
-  }
-  return launch_kind<OT>(p.kind, A, B, M, N, K, p.cols, N, ep, s);
+  return launch_kind<OT>(p.kind, A, B, M, N, K, ep, s);
 }
 
 }  // namespace

@@ -14,12 +14,12 @@ struct Tile {
   static constexpr int STAGE = (BM + BN) * BK;
   static constexpr int AI = BM / 8 / NW, BI = BN / 8 / NW;   // 1 KB loads per wave and stage
   static constexpr int LPS = AI + BI;
-  // the epilogue: rows of a wave's sub-tile per pass through its LDS
-  static constexpr int pass_of(int p) { return p * WTN * 4 * NW <= S * STAGE ? p : pass_of(p / 2); }
-  static constexpr int PASS = pass_of(WTM);
+  // the epilogue: rows of a wave's sub-tile per pass through its part of the LDS
+  static constexpr int pass_of(int p, int lds) {
+    return p * WTN * 4 * NW <= lds ? p : pass_of(p / 2, lds);
+  }
   static_assert(AI * 8 * NW == BM && BI * 8 * NW == BN, "whole loads");
   static_assert(S * STAGE <= 160 * 1024, "LDS");
-  static_assert(PASS % 16 == 0 && WTM % PASS == 0, "whole blocks per pass");
 };
 
 // waits until at most N vector-memory instructions of the wave are in flight
@@ -40,22 +40,76 @@ __device__ __forceinline__ void wait_stages(int ahead) {
   }
 }
 
-// STREAM: the outputs go past the caches, which keeps the operands in them
-// (kStreamBytes in elem.hpp; 8192 x 11008 x 4096 with two bf16 outputs: 336 us,
-// 386 without, one launch of 256 x 256 tiles)
+// The epilogue of a wave's accumulators, through its part of the LDS.
+template <class C, int LDS, class OT, bool STREAM, bool SPLIT>
+__device__ __forceinline__ void tile_out(uint8_t* smem, const v4f (&acc)[C::MB][C::NB], int m0,
+                                         int n0, int M, int N, float scale, const Epilogue& ep,
+                                         float* __restrict__ part, int sp) {
+  constexpr int NB = C::NB, PASS = C::pass_of(C::WTM, LDS);
+  static_assert(PASS % 16 == 0 && C::WTM % PASS == 0, "whole blocks per pass");
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wm = w / C::WGN, wn = w % C::WGN;
+  const int r16 = lane & 15, g = lane >> 4;
+  constexpr int CH = C::WTN / 4, LPR = C::WTN / 8, RPI = 64 / LPR;
+  // 16-byte chunk c of row r: swizzled where the rows' stride is a power of two
+  // (else the stride itself spreads the rows over the banks)
+  constexpr int SWZ = (CH & (CH - 1)) == 0 ? CH - 1 : 0;
+  auto slot = [](int r, int c) { return r * CH + (c ^ (r & SWZ)); };
+  v4f* mine = reinterpret_cast<v4f*>(smem + w * (LDS / C::NW / 16 * 16));
+  const int cl = lane % LPR, rl = lane / LPR;
+  const int col = n0 + wn * C::WTN + cl * 8;
+  const bool col_ok = rl < RPI && col < N;                   // N is a multiple of 16
+  float bias[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
+  if (!SPLIT && ep.bias && col_ok) load_elems<8>(ep.bias + col, bias);
+  auto rows = [&](auto act, int first) {
+    for (int r = rl; r < PASS; r += RPI) {                // lanes past RPI rows: idle
+      const int row = m0 + wm * C::WTM + first + r;
+      const v4f a = mine[slot(r, 2 * cl)];
+      const v4f b = mine[slot(r, 2 * cl + 1)];
+      if (!col_ok || row >= M) continue;
+      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      if constexpr (SPLIT)
+        store_elems<8>(part + ((int64_t)sp * M + row) * N + col, v);
+      else
+        finish8<decltype(act)::value, OT, STREAM>(v, scale, bias, ep, (int64_t)row * N + col);
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < C::WTM / PASS; ++p) {
+    // the wave's own LDS: its accesses are executed in order
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < PASS / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        mine[slot(i * 16 + r16, 4 * j + g)] = acc[p * (PASS / 16) + i][j];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int first = p * PASS;
+    switch (SPLIT ? (int)kNone : ep.act) {
+      case kRelu: rows(std::integral_constant<int, kRelu>{}, first); break;
+      case kGelu: rows(std::integral_constant<int, kGelu>{}, first); break;
+      case kGeluTanh: rows(std::integral_constant<int, kGeluTanh>{}, first); break;
+      case kSilu: rows(std::integral_constant<int, kSilu>{}, first); break;
+      default: rows(std::integral_constant<int, kNone>{}, first); break;
+    }
+  }
+}
+
+// STREAM: the outputs go past the caches (kStreamOut in linear_act.hip).
 // SPLIT (few tiles, long K): workgroup b takes tile b % tiles and the kc K steps
 // of split b / tiles, and writes its sums, unscaled, to that split's plane of
 // `part` ([M x N] floats each); linear_act_join adds the planes in order.
 template <class C, class OT, bool STREAM, bool SPLIT = false>
 __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
-    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int n_first,
-    int tilesM, int tilesN, Epilogue ep, float* __restrict__ part = nullptr, int kc = 0) {
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
+    int tilesN, Epilogue ep, float* __restrict__ part = nullptr, int kc = 0) {
   constexpr int BK = C::BK, MB = C::MB, NB = C::NB;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::S * C::STAGE];
   int tm, tn;
   const int nt = tilesM * tilesN, sp = SPLIT ? (int)blockIdx.x / nt : 0;
   gemm::tile_of(gemm::xcd_remap((int)blockIdx.x - sp * nt, nt), tilesM, tilesN, tm, tn);
-  const int m0 = tm * C::BM, n0 = n_first + tn * C::BN;
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w / C::WGN, wn = w % C::WGN;
   // the step at nk, if any, is the one of rem bytes
   const int nk = K / BK, rem = K % BK, all = nk + (rem > 0);
@@ -178,51 +232,7 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
   }
   __syncthreads();                                           // the stages are free
 
-  constexpr int CH = C::WTN / 4, LPR = C::WTN / 8, RPI = 64 / LPR;
-  // 16-byte chunk c of row r: swizzled where the rows' stride is a power of two
-  // (else the stride itself spreads the rows over the banks)
-  constexpr int SWZ = (CH & (CH - 1)) == 0 ? CH - 1 : 0;
-  auto slot = [](int r, int c) { return r * CH + (c ^ (r & SWZ)); };
-  v4f* mine = reinterpret_cast<v4f*>(smem + w * (C::S * C::STAGE / C::NW));
-  const int cl = lane % LPR, rl = lane / LPR;
-  const int col = n0 + wn * C::WTN + cl * 8;
-  const bool col_ok = rl < RPI && col < N;                   // N is a multiple of 16
-  float bias[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
-  if (!SPLIT && ep.bias && col_ok) load_elems<8>(ep.bias + col, bias);
-  auto rows = [&](auto act, int first) {
-    for (int r = rl; r < C::PASS; r += RPI) {                // lanes past RPI rows: idle
-      const int row = m0 + wm * C::WTM + first + r;
-      const v4f a = mine[slot(r, 2 * cl)];
-      const v4f b = mine[slot(r, 2 * cl + 1)];
-      if (!col_ok || row >= M) continue;
-      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      if constexpr (SPLIT)
-        store_elems<8>(part + ((int64_t)sp * M + row) * N + col, v);
-      else
-        finish8<decltype(act)::value, OT, STREAM>(v, scale, bias, ep, (int64_t)row * N + col);
-    }
-  };
-#pragma unroll
-  for (int p = 0; p < C::WTM / C::PASS; ++p) {
-    // the wave's own LDS: its accesses are executed in order
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < C::PASS / 16; ++i)
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        mine[slot(i * 16 + r16, 4 * j + g)] = acc[p * (C::PASS / 16) + i][j];
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const int first = p * C::PASS;
-    switch (SPLIT ? (int)kNone : ep.act) {
-      case kRelu: rows(std::integral_constant<int, kRelu>{}, first); break;
-      case kGelu: rows(std::integral_constant<int, kGelu>{}, first); break;
-      case kGeluTanh: rows(std::integral_constant<int, kGeluTanh>{}, first); break;
-      case kSilu: rows(std::integral_constant<int, kSilu>{}, first); break;
-      default: rows(std::integral_constant<int, kNone>{}, first); break;
-    }
-  }
+  tile_out<C, C::S * C::STAGE, OT, STREAM, SPLIT>(smem, acc, m0, n0, M, N, scale, ep, part, sp);
 }
 
 // y (and z) from the S planes of partial sums

@@ -128,18 +128,49 @@ def test_forward(gpu_lib, T, d_in, d_out, dtype):
     check(gy, y, ty + half_step(dtype) * (y.abs() + ty), "y")
 
 
-@pytest.mark.parametrize("T,d_in,d_out", [(1540, 656, 11600), (1287, 656, 14864)])
-def test_forward_in_two_launches(gpu_lib, T, d_in, d_out):
-    """Whole rounds of large tiles, the remaining columns in smaller ones:
-    a sample of the rows, the last ones among them."""
+# more outputs, for each of the larger tiles: one K step and part of one, two to
+# eleven, an odd and an even number of them, whole and not; ragged rows and columns
+LARGE = [
+    (579, 16, 11472), (514, 144, 11008), (578, 256, 9808), (517, 384, 10912),      # 128 x 128
+    (644, 528, 8224), (643, 784, 8288), (644, 1152, 8304), (650, 1296, 8224),
+    (978, 16, 10912), (257, 144, 9856), (258, 384, 9824), (129, 640, 11056),       # eight waves
+    (321, 272, 10912), (385, 384, 11824), (322, 528, 11008), (324, 1152, 10928),   # 128 x 192
+    (833, 16, 11744), (641, 144, 11936), (642, 256, 12064), (642, 272, 11984),     # 192 x 128
+    (643, 384, 11920), (513, 528, 9824), (641, 640, 10928), (520, 784, 9808),
+    (515, 1152, 9840), (518, 1296, 9856),
+    (1035, 16, 10896), (1028, 144, 10944), (967, 256, 10976), (968, 384, 11088),   # 256 x 128
+    (1154, 528, 9808), (977, 640, 11008), (1156, 784, 9760), (1033, 1152, 10896),
+    (1293, 16, 10912), (1287, 144, 10960), (1281, 256, 10896), (1298, 384, 11008),  # 128 x 256
+    (1300, 528, 11024), (1282, 640, 10896), (1288, 1152, 10896),
+    (1039, 1296, 10944), (1031, 2064, 10896), (963, 3088, 10944), (3841, 4096, 4096),  # 256 x 256
+    (2690, 784, 6544), (1538, 1296, 10976), (1288, 2064, 11808), (3841, 3584, 5104),   # 256 x 320
+]
+
+
+@pytest.mark.parametrize("T,d_in,d_out", LARGE)
+def test_forward_of_many_outputs(gpu_lib, T, d_in, d_out):
+    """Every seventh row and the last ones, all columns; the rest is written."""
     p = problem(17, T, d_in, d_out, BF16)
-    gy, gz = run(gpu_lib, p, "gelu_tanh", BF16)
-    rows = torch.tensor([0, 1, 255, 256, T // 2, T - 2, T - 1])
+    act = ACTS[(T + d_out // 16) % 5]
+    gy, gz = run(gpu_lib, p, act, BF16)
+    rows = torch.tensor(sorted({*range(0, T, 7 if T < 1000 else 23), T - 2, T - 1}))
     xq, s_x, wq, s_w, bias, res = p
-    z, tz, y, ty = reference((xq[rows], s_x, wq, s_w, bias, res[rows]), "gelu_tanh", True, True)
+    z, tz, y, ty = reference((xq[rows], s_x, wq, s_w, bias, res[rows]), act, True, True)
     check(gz.cpu()[rows], z, tz + half_step(BF16) * (z.abs() + tz), "z")
     check(gy.cpu()[rows], y, ty + half_step(BF16) * (y.abs() + ty), "y")
     assert torch.isfinite(gy).all() and torch.isfinite(gz).all()
+
+
+@pytest.mark.parametrize("T,d_in,d_out", [(3841, 4096, 4096), (3841, 3584, 5104),
+                                          (644, 1152, 8304), (1033, 1152, 10896)])
+def test_many_outputs_repeat(gpu_lib, T, d_in, d_out):
+    """The same bits from every call, float32 too, however the tiles overlap."""
+    for dtype in (BF16, F32):
+        p = problem(18, T, d_in, d_out, dtype)
+        first = run(gpu_lib, p, "silu", dtype)
+        for _ in range(4):
+            for a, b in zip(first, run(gpu_lib, p, "silu", dtype)):
+                assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("use_bias,use_res,keep_z", [(False, False, False), (True, False, True),
