@@ -112,9 +112,9 @@ enum TileKind {
 constexpr TileCost kTile[kTileKinds] = {
     {256, 320, 1, 4.0f, 23.0f, {{1.47f, 1.47f}, {1.75f, 1.75f}}},
     {256, 256, 1, 3.0f, 15.0f, {{1.23f, 1.23f}, {1.50f, 1.50f}}},
-    {256, 128, 2, 2.0f, 10.0f, {{0.70f, 1.45f}, {1.07f, 2.05f}}},
-    {128, 256, 2, 2.0f, 10.0f, {{0.72f, 1.45f}, {1.08f, 2.05f}}},
-    {192, 128, 2, 4.0f, 7.0f, {{0.52f, 1.03f}, {0.88f, 1.65f}}},
+    {256, 128, 2, 2.0f, 10.0f, {{0.70f, 1.42f}, {1.07f, 2.00f}}},
+    {128, 256, 2, 2.0f, 10.0f, {{0.72f, 1.42f}, {1.08f, 2.00f}}},
+    {192, 128, 2, 4.0f, 7.0f, {{0.52f, 1.08f}, {0.88f, 1.65f}}},
     {128, 192, 1, 2.5f, 6.0f, {{0.68f, 0.68f}, {0.85f, 0.85f}}},
     {128, 128, 2, 4.5f, 4.5f, {{0.39f, 0.78f}, {0.69f, 1.30f}}},
     {128, 128, 1, 3.0f, 3.0f, {{0.50f, 0.50f}, {0.68f, 0.68f}}},
