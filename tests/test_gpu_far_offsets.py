@@ -87,3 +87,32 @@ def test_clip(gpu_lib, big):
     keep = torch.ones(1000, dtype=torch.bool, device="cuda")
     keep[-7:-5] = False                              # between the views
     assert bool(((got - want).abs() <= 2.0 ** -7 * want.abs())[keep].all())
+
+
+@pytest.mark.parametrize("T, d_in, d_out", [(4096, 1 << 23, 5120), (40, (1 << 23) + 144, 64),
+                                            (3, (1 << 23) + 144, 64)])
+def test_product_over_long_rows(gpu_lib, T, d_in, d_out):
+    """Rows so long that a tile's last ones begin 2^31 bytes behind its first, and
+    rows past what the larger tiles' offsets reach.  Codes of +-1: every sum is an
+    integer below 2^24, exact in float32."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+
+    def signs(rows):
+        t = torch.empty((rows, d_in), dtype=torch.uint8, device="cuda")
+        t.random_(0, 2, generator=g)
+        return t.mul_(128).bitwise_or_(0x38)
+
+    xq, wq = signs(T), signs(d_out)
+    one = torch.ones(1, device="cuda")
+    y = torch.empty((T, d_out), device="cuda")
+    gpu_lib.melded_linear_fwd_act(xq, one, wq, one, y)
+    rows = sorted({0, 1, T // 2, T - 1})
+    ref = torch.zeros((len(rows), d_out), dtype=torch.float64, device="cuda")
+    for a in range(0, d_in, 1 << 16):
+        x = xq[rows, a:a + (1 << 16)].view(torch.float8_e4m3fn).float()
+        w = wq[:, a:a + (1 << 16)].contiguous().view(torch.float8_e4m3fn).float()
+        ref += (x @ w.T).double()
+    assert torch.equal(y[rows].double(), ref)
+    del xq, wq
+    torch.cuda.empty_cache()
