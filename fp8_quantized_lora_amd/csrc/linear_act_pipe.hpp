@@ -33,7 +33,8 @@ __device__ __forceinline__ void load16_to_lds_at(const uint8_t* base, uint32_t o
   const uint64_t p = reinterpret_cast<uint64_t>(base);
   const uint64_t s = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32)) << 32 |
                      (uint32_t)__builtin_amdgcn_readfirstlane((int)p);
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(s), "{m0}"(lds_addr) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(s), "{m0}"(lds_addr)
+               : "memory");
 }
 
 // d += a b^T of a 16 x 16 block, d in the same registers throughout (of the

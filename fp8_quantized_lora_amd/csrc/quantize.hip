@@ -292,7 +292,9 @@ __device__ __forceinline__ uint64_t get_word(uint64_t* p) {
 // a direct global -> LDS load of 16 bytes per lane with the streaming hint
 // (lane l's bytes land at lds_addr + 16 l; lds_addr wave-uniform)
 __device__ __forceinline__ void stream16_to_lds(const void* g, uint32_t lds_addr) {
-  asm volatile("global_load_lds_dwordx4 %0, off nt" ::"v"(g), "{m0}"(lds_addr) : "memory");
+  // s_nop: the wait state between the write of m0 and the load
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(g), "{m0}"(lds_addr)
+               : "memory");
 }
 
 // max |x| and the non-finite count of workgroup b's range (and the scalar
