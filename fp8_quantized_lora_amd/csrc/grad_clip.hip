@@ -246,8 +246,12 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(Tab t, const double* __
                                                          float* __restrict__ norm) {
   const double r = norm_of(part, P);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)r;
-  float c = (float)((double)max_norm / (r + (double)eps));
-  c = c > 1.0f ? 1.0f : c;                     // NaN stays NaN
+  // without a limit, or with nothing but zeros, nothing is scaled, also where the
+  // quotient is inf / inf or 0 / 0; a NaN among the elements stays one
+  const double to = r + (double)eps;
+  const bool free = to == 0.0 || (isinf(max_norm) && !isnan(r));
+  float c = free ? 1.0f : (float)((double)max_norm / to);
+  c = c > 1.0f ? 1.0f : c;
   walk<true>(t, [&](const Entry& e, int64_t a, int64_t b) {
     if (c == 1.0f && e.g == e.out) return;     // in place and not clipped
     if (e.bf16)

@@ -705,7 +705,9 @@ falq_status linear_act_bwd(const void *dy, int dy_dtype, const void *z, int z_dt
  * summed in float64.  grad_clip — the same, then with
  *     coef = min(1, max_norm / (norm + eps)):   out[i] = g[i] * coef
  * rounded once to the tensor's type.  A NaN anywhere makes norm and every
- * output NaN; an infinity makes norm infinite and coef 0.
+ * output NaN; an infinity makes norm infinite and coef 0 (so that element's
+ * output is NaN), or 1 with an infinite max_norm: without a limit nothing is
+ * scaled.  norm + eps = 0 leaves coef at 1 as well.
  *
  *   count    number of tensors, 0 <= count <= FALQ_GRAD_MAX_TENSORS
  *   g, out   HOST arrays of device pointers, read before the call returns;
