@@ -728,8 +728,10 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 GRAD_MAX_TENSORS = 65536
 
 _ELEM = {torch.float32: 0, torch.bfloat16: 1}
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (absent from a torch built without a GPU, where every call is refused before
+# they are needed)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _elem(t: torch.Tensor, name: str) -> int:
