@@ -31,7 +31,9 @@ With bias=True, act other than "none" or y_dtype bfloat16 the layer has an
 epilogue: the forward is melded_linear_fwd_act (bias, activation and, where
 forward is given one, a residual in the product's launch; z kept for the
 backward), the backward linear_act_bwd in front of fp8_quantize, then
-melded_linear_bwd, which forms X^ A^T itself.
+melded_linear_bwd, which forms X^ A^T itself.  The bias is trained: the adapter
+update steps it by dbias with the layer's optimizer (AdamW without weight
+decay, which is meant for matrices).
 
 clip_gradients clips the adapter (and bias) gradients of many layers by their
 global norm, between their backward calls and their adapter updates.
@@ -83,7 +85,7 @@ class MeldedLinear:
         merge_every: how often the caller will merge (update(merge=...)), which
         decides whether W~^T is kept (worth it from every second step on); bias
         adds a bias (self.bias, zero at the start; its gradient in self.dbias),
-        act an activation of melded_linear_fwd_act, y_dtype is the type of Y
+        which adapter_update steps, act an activation of melded_linear_fwd_act, y_dtype is the type of Y
         (and of a residual), dy_dtype that of the upstream gradient dY."""
         if optimizer not in ("sgd", "adamw"):
             raise ValueError(f"optimizer must be 'sgd' or 'adamw', not {optimizer!r}")
@@ -126,7 +128,7 @@ class MeldedLinear:
         self.dB = torch.empty((d_out, rank), dtype=f32, device=dev)
         # the epilogue: bias and its gradient, z for the backward, dz
         self.bias = torch.zeros(d_out, dtype=f32, device=dev) if bias else None
-        self.dbias = torch.empty(d_out, dtype=f32, device=dev) if bias else None
+        self.dbias = torch.zeros(d_out, dtype=f32, device=dev) if bias else None
         kept = act != "none"
         self.z = torch.empty((tokens, d_out), dtype=y_dtype, device=dev) if kept else None
         self.dz = torch.empty((tokens, d_out), dtype=dy_dtype, device=dev) if kept else None
@@ -140,6 +142,10 @@ class MeldedLinear:
             self.mB = torch.zeros((d_out, rank), dtype=f32, device=dev)
             self.vB = torch.zeros((d_out, rank), dtype=f32, device=dev)
             self.adam_state = adamw_state(dev)   # step count and beta powers, on the device
+            if bias:
+                self.mbias = torch.zeros(d_out, dtype=f32, device=dev)
+                self.vbias = torch.zeros(d_out, dtype=f32, device=dev)
+                self.bias_state = adamw_state(dev)
         self.sel = torch.empty(d_out, dtype=i32, device=dev)
         self.n_sel = torch.zeros(1, dtype=i32, device=dev)
         self.rho = torch.empty(d_out, dtype=f32, device=dev)
@@ -189,12 +195,18 @@ class MeldedLinear:
             nb = linear_act_bwd_workspace_bytes(tokens, d_out) if d_out else 0
             self.ws_act = torch.empty(max(1, nb), dtype=u8, device=dev)
 
-    def init_state(self, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, stream=None):
+    def init_state(self, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, stream=None,
+                   bias: Optional[torch.Tensor] = None):
         """W~ = E4M3(W * s_w), s_w = 448 / max|W| (the initial quantization
-        error is the implicit adapter); A and B copied in."""
+        error is the implicit adapter); A and B copied in, and the bias where
+        one is given."""
+        if bias is not None and self.bias is None:
+            raise ValueError("a bias needs a layer made with bias=True")
         fp8_quantize(W, self.wq, self.s_w, ws=self.ws_q, stream=stream)
         self.refresh_transpose(stream)
         self.B.copy_(B)
+        if bias is not None:
+            self.bias.copy_(bias)
         if self.fp8_a:                    # A~ = E4M3(A * s_a); the proxy's A is DQ(A~)
             self.A.copy_(A)
             fp8_quantize(self.A, self.aq, self.s_a, ws=self.ws_q, stream=stream)
@@ -255,7 +267,7 @@ class MeldedLinear:
 
     def backward_product(self, stream=None):
         """The backward call on the quantized upstream gradient (dX, dB and,
-        with A trained, dA)."""
+        with A trained, dA; dbias comes from backward only)."""
         if self.fp8_a:
             melded_linear_bwd_frozen_a(self.gq, self.s_g, self.wq, self.s_w, self.u, self.dx,
                                        self.dB, ws=self.ws_bwd, stream=stream, g_fmt=self.g_fmt)
@@ -281,6 +293,14 @@ class MeldedLinear:
         else:
             adapter_step_adamw(self.A, self.B, self.dA, self.dB, self.mA, self.vA, self.mB,
                                self.vB, self.adam_state, lr, stream=stream, **self.adamw)
+        if self.bias is not None:         # in B's place, as a column; A frozen
+            row, col, grad = self.bias[None], self.bias[:, None], self.dbias[:, None]
+            if self.optimizer == "sgd":
+                adapter_step(row, col, None, grad, lr, stream=stream)
+            else:
+                adapter_step_adamw(row, col, None, grad, None, None, self.mbias[:, None],
+                                   self.vbias[:, None], self.bias_state, lr, stream=stream,
+                                   **{**self.adamw, "weight_decay": 0.0})
 
     def merge(self, tau: float, k_max: int = 0, stream=None):
         if self.topk_rank:
@@ -296,7 +316,7 @@ class MeldedLinear:
                                  self.n_sel, rho=self.rho, ws=self.ws_px, stream=stream)
 
     def update(self, lr: float, tau: float, k_max: int = 0, stream=None, merge: bool = True):
-        """Adapter step, then (if `merge`) the row-wise proxy update.  Between
+        """Adapter step (and the bias's), then (if `merge`) the row-wise proxy update.  Between
         merges B keeps accumulating the adapter updates: B is the proxy, merged
         into W~ periodically."""
         self.adapter_update(lr, stream)
@@ -304,12 +324,13 @@ class MeldedLinear:
             self.merge(tau, k_max, stream)
 
     def step(self, X: torch.Tensor, dY: torch.Tensor, lr: float = 1e-3, tau: float = 0.5,
-             k_max: int = 0, stream=None, merge_every: int = 1):
+             k_max: int = 0, stream=None, merge_every: int = 1,
+             residual: Optional[torch.Tensor] = None):
         """One training step; the proxy is merged into W~ on every
         `merge_every`-th step (counted by this layer)."""
         if merge_every < 1:
             raise ValueError("merge_every must be >= 1")
         self.n_steps = getattr(self, "n_steps", 0) + 1
-        self.forward(X, stream)
+        self.forward(X, stream, residual)
         self.backward(dY, stream)
         self.update(lr, tau, k_max, stream, merge=self.n_steps % merge_every == 0)
