@@ -26,7 +26,7 @@ __device__ __forceinline__ void finish8(float (&v)[8], float scale, const float 
   for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], scale, bias[i]);
   if (e.z) store_elems<8, STREAM>((OT*)e.z + at, v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = act_value<ACT>(v[i]);
+  for (int i = 0; i < 8; ++i) v[i] = act_value<ACT, OT>(v[i]);
   if (e.residual) {
     float r[8];
     load_elems<8>((const OT*)e.residual + at, r);
@@ -42,7 +42,7 @@ __device__ __forceinline__ void finish1(float v, float scale, float bias, const 
                                         int64_t at) {
   float o[1] = {fmaf(v, scale, bias)};
   if (e.z) store_elems<1>((OT*)e.z + at, o);
-  o[0] = act_value<ACT>(o[0]);
+  o[0] = act_value<ACT, OT>(o[0]);
   if (e.residual) o[0] += (float)((const OT*)e.residual)[at];
   store_elems<1>((OT*)e.y + at, o);
 }
