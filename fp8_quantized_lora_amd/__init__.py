@@ -742,7 +742,7 @@ def _elem(t: torch.Tensor, name: str) -> int:
 
 
 def _act(act) -> int:
-    if act not in ACTIVATIONS:
+    if not isinstance(act, str) or act not in ACTIVATIONS:
         raise FalqError(f"act must be one of {sorted(ACTIVATIONS)}, not {act!r}")
     return ACTIVATIONS[act]
 
