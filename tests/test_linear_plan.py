@@ -1,8 +1,11 @@
 """The rule that picks the FP8 product's kernel, on the host."""
+import random
+
 import pytest
 
 import fp8_quantized_lora_amd as fq
-from tests.linear_plan import plan
+from tests.linear_kinds import STREAM_BYTES, STREAMED, WHOLE
+from tests.linear_plan import KINDS, plan
 
 # d_in and d_out up to 2^30 and as many 256 x 256 tiles as the call accepts
 DIMS = [16, 48, 4096, 11008, 65536, 1 << 20, (1 << 22) - 16, 1 << 22, 1 << 24, (1 << 26) - 16,
@@ -33,3 +36,25 @@ def test_few_tokens_need_no_workspace():
                 assert plan(T, d_in, d_out).split == 1
                 if accepted(T, d_in, d_out):
                     assert fq.melded_linear_fwd_act_workspace_bytes(T, d_in, d_out) == 0
+
+
+def test_tested_shapes_reach_their_kernel():
+    """The shapes that the GPU tests list for a kernel get it, none is left out, and
+    the streamed ones are streamed."""
+    for table in (WHOLE, STREAMED):
+        for how, shapes in table.items():
+            for T, d_in, d_out in shapes:
+                assert plan(T, d_in, d_out).how == how, (T, d_in, d_out)
+                assert (4 * T * d_out > STREAM_BYTES) == (table is STREAMED)
+    assert set(WHOLE) == {"few1", "few2", "split", *KINDS}
+
+
+def test_streamed_kinds():
+    """No other tile is picked for outputs that are streamed."""
+    rng, seen = random.Random(4), set()
+    for _ in range(60000):
+        T = int(2 ** rng.uniform(0, 26))
+        d_out = int(2 ** rng.uniform(0, 22)) * 16
+        if 4 * T * d_out > STREAM_BYTES:
+            seen.add(plan(T, int(2 ** rng.uniform(0, 12)) * 16, d_out).how)
+    assert seen - {"few1"} <= set(STREAMED), seen - set(STREAMED)
