@@ -49,8 +49,9 @@ bool stream_outputs(int64_t M, int64_t N, const Epilogue& ep) {
   return sizeof(OT) == 2 && M * N * 2 * (1 + (ep.z != nullptr)) > kStreamOut;
 }
 
-// tiles of C: linear_act_tile, or PIPE workgroups of linear_act_pipe per CU
-template <class C, int PIPE, class OT>
+// tiles of C: linear_act_tile, or PIPE workgroups of linear_act_pipe per CU.  MANY:
+// the rule takes them for outputs that are streamed, too.
+template <class C, int PIPE, class OT, bool MANY = true>
 hipError_t launch_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
                         const Epilogue& ep, hipStream_t s) {
   const int tM = (int)((M + C::BM - 1) / C::BM), tN = (int)((N + C::BN - 1) / C::BN);
@@ -63,8 +64,8 @@ hipError_t launch_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N
       linear_act_tile<C, OT, STREAM><<<tM * tN, C::kThreads, 0, s>>>(A, B, (int)M, (int)N, (int)K,
                                                                      tM, tN, ep);
   };
-  if (stream_outputs<OT>(M, N, ep))
-    go(std::bool_constant<sizeof(OT) == 2>{});
+  if (MANY && stream_outputs<OT>(M, N, ep))
+    go(std::bool_constant<MANY && sizeof(OT) == 2>{});
   else
     go(std::false_type{});
   return hipGetLastError();
@@ -91,7 +92,7 @@ hipError_t launch_kind(TileKind k, const uint8_t* A, const uint8_t* B, int64_t M
     case k192x128: return launch_tiles<Tile<192, 128, 2, 2>, 2, OT>(A, B, M, N, K, ep, s);
     case k128x192w8: return launch_tiles<Tile<128, 192, 2, 4, 3>, 0, OT>(A, B, M, N, K, ep, s);
     case k128: return launch_tiles<Tile<128, 128, 2, 2>, 2, OT>(A, B, M, N, K, ep, s);
-    case k128w8: return launch_tiles<T128, 0, OT>(A, B, M, N, K, ep, s);
+    case k128w8: return launch_tiles<T128, 0, OT, false>(A, B, M, N, K, ep, s);
     case k64: return launch_tiles<Tile<64, 64, 2, 2, 4>, 0, OT>(A, B, M, N, K, ep, s);
     default: return launch_tiles<Tile<32, 64, 1, 4, 4>, 0, OT>(A, B, M, N, K, ep, s);
   }
