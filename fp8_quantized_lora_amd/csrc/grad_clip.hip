@@ -4,7 +4,7 @@
 //   g' = g coef.
 // Squares are summed in float64 (no overflow below 1e154, no loss over long
 // sums; the conversion and the fused multiply-add are far below the memory
-// time), in an order that the sizes fix.
+// time), in an order that the sizes and the tensors' places within 16 bytes fix.
 //
 // The tensors' addresses travel in kernel arguments, so a captured graph holds
 // them and nothing is copied from the host: up to kTable tensors directly, more

@@ -85,8 +85,8 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   Plan p;
   const int64_t steps = (K + 127) / 128;
   // few tokens: 4096 x 4096 5.6 us at 1 token and 6.6 at 16 (tiles of 32 x 64:
-  // 9.5); at 32 tokens 8.3 against 9.6 while one workgroup per CU holds all
-  // columns, 21 against 14.4 at 11008 columns
+  // 9.5); at 32 tokens 7.7 against 9.6 while one workgroup per CU holds all
+  // columns, 18.7 against 9.7 at 11008 columns
   // (a grid holds fewer than 2^32 threads: beyond that the tiles, which then are
   // too many for a split)
   if (K > 0 && M <= 16 && (N + 15) / 16 * kFewWaves[1] * 64 < (int64_t)1 << 32) p.few = 1;

@@ -606,8 +606,9 @@ falq_status lora_bf16_bwd(const float *dy, const uint8_t *gq, const float *s_g, 
  * residual of a product, the backward of both, and the clipping of every
  * layer's dA and dB by their global norm before the adapter step.  Elements
  * are float32 or bfloat16 (falq_dtype); sums, statistics and norms are
- * float32 or wider and their order is fixed by the sizes, so results repeat
- * bit for bit.  These tensors need only their element's alignment (the FP8
+ * float32 or wider and their order is fixed by the sizes and types (and, for
+ * grad_norm and grad_clip, by each tensor's place within 16 bytes), so results
+ * repeat bit for bit.  These tensors need only their element's alignment (the FP8
  * codes 16 bytes as elsewhere), so rows may begin anywhere in a larger buffer;
  * 16-byte aligned rows are the fastest.  Outputs and the workspace lie apart
  * from each other and from every input: a call where they overlap is refused,
