@@ -35,10 +35,13 @@ __device__ __forceinline__ float logistic_pair(float x, float& rest) {
   return s;
 }
 
+// where every activation has reached its limit
+constexpr float kFar = 100.0f;
+
 // Phi(z), and exp(-z^2 / 2) in `ex`
 __device__ __forceinline__ float normal_cdf(float z, float& ex) {
   constexpr float kP = 0.4f;
-  const float a = fabsf(z);
+  const float a = fminf(fabsf(z), kFar);       // inf * 0 does not arise in v
   const float v = -kP * a * rcp_fast(fmaf(kP, a, 1.0f));
   ex = exp2_fast(-0.7213475204f * z * z);
   float p = fmaf(-0.0392525159f, v, -0.114942111f);
