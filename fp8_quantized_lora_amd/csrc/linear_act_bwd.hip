@@ -40,7 +40,7 @@ __global__ __launch_bounds__(kRows * kLanes) void act_bwd_kernel(
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         g[e] = gr[e];
-        if constexpr (ACT != kNone) g[e] *= act_slope<ACT>(v[e]);
+        if constexpr (ACT != kNone) g[e] *= act_slope<ACT, GT>(v[e]);
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) ab[e] += g[e];
