@@ -45,13 +45,13 @@ class Plan(NamedTuple):
 
 @functools.lru_cache(maxsize=1)
 def _lib():
-    d = tempfile.mkdtemp()
-    src, so = os.path.join(d, "plan.cpp"), os.path.join(d, "plan.so")
-    with open(src, "w") as f:
-        f.write(SOURCE)
-    subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", f"-I{CSRC}", src, "-o", so],
-                   check=True)
-    lib = ctypes.CDLL(so)
+    with tempfile.TemporaryDirectory() as d:
+        src, so = os.path.join(d, "plan.cpp"), os.path.join(d, "plan.so")
+        with open(src, "w") as f:
+            f.write(SOURCE)
+        subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", f"-I{CSRC}", src, "-o", so],
+                       check=True)
+        lib = ctypes.CDLL(so)
     assert lib.kinds() == len(KINDS)
     return lib
 
