@@ -11,7 +11,7 @@
 // outputs, linear_act_tile (linear_act_tile.hpp) for few.
 //
 // Long products are bound by the matrix cores, in part by their power, and by
-// the outputs (8192 x 11008 x 4096 with gelu and z: 305 to 314 us, 2.4 PFLOP/s; 275
+// the outputs (8192 x 11008 x 4096 with gelu and z: 305 to 316 us, 2.4 PFLOP/s; 275
 // without the epilogue's work and z; 4096 x 5120 x 13824 with a residual 201 to 213
 // us, 2.8 PFLOP/s), few tokens by reading W~ (1 x 4096 x 4096: 5.2 us on the GPU, 3.2
 // TB/s, of which a launch's latency is half).
