@@ -39,7 +39,12 @@ __all__ = ["load", "FalqError", "fp8_quantize", "fp8_quantize_workspace_bytes",
            "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "ACTIVATIONS",
            "melded_linear_fwd_act", "melded_linear_fwd_act_workspace_bytes",
            "linear_act_bwd", "linear_act_bwd_workspace_bytes",
-           "grad_norm", "grad_clip", "grad_norm_workspace_bytes", "GRAD_MAX_TENSORS"]
+           "grad_norm", "grad_clip", "grad_norm_workspace_bytes", "GRAD_MAX_TENSORS",
+           "mxfp4_scales_shape", "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_dequantize", "melded_linear_fwd_mxfp4",
+           "melded_linear_fwd_mxfp4_workspace_bytes", "checkpoint_scales_shape",
+           "checkpoint_save", "checkpoint_restore", "linear_act_bwd_ckpt", "layer_norm_bwd_ckpt",
+           "linear_cross_entropy_fwd", "linear_cross_entropy_fwd_workspace_bytes",
+           "linear_cross_entropy_bwd", "linear_cross_entropy_bwd_workspace_bytes"]
 
 #: bytes of the per-device scratch array behind fp8_quantize_noalloc
 QUANTIZE_SCRATCH_BYTES = 16384
@@ -130,6 +135,24 @@ _SIGS = {
     "linear_act_bwd_workspace_bytes": (_sz, [_i64, _i64]),
     "linear_act_bwd": (_i32, [_c_p, _i32, _c_p, _i32, _i32, _i64, _i64, _c_p, _c_p, _c_p, _sz,
                               _c_p]),
+    "mxfp4_scale_bytes": (_sz, [_i64, _i64]),
+    "mxfp4_quantize": (_i32, [_c_p, _i32, _i64, _i64, _c_p, _c_p, _c_p]),
+    "mxfp4_dequantize": (_i32, [_c_p, _c_p, _i64, _i64, _c_p, _i32, _c_p]),
+    "melded_linear_fwd_mxfp4_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "melded_linear_fwd_mxfp4": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _i32, _c_p, _i64, _i64, _i64,
+                                       _i32, _c_p, _c_p, _c_p, _sz, _c_p]),
+    "checkpoint_save": (_i32, [_c_p, _i32, _i64, _i64, _c_p, _c_p, _c_p]),
+    "checkpoint_restore": (_i32, [_c_p, _c_p, _i64, _i64, _c_p, _i32, _c_p]),
+    "linear_act_bwd_ckpt": (_i32, [_c_p, _i32, _c_p, _c_p, _i32, _i64, _i64, _c_p, _c_p, _c_p,
+                                   _sz, _c_p]),
+    "layer_norm_bwd_ckpt": (_i32, [_c_p, _i32, _c_p, _c_p, _c_p, _c_p, _c_p, _i64, _i64, _c_p,
+                                   _c_p, _c_p, _c_p, _sz, _c_p]),
+    "linear_cross_entropy_fwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "linear_cross_entropy_fwd": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _i64, _i64, _i64, _c_p,
+                                        _c_p, _c_p, _sz, _c_p]),
+    "linear_cross_entropy_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "linear_cross_entropy_bwd": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _i64, _i64,
+                                        _i64, _c_p, _i32, _c_p, _sz, _c_p]),
     "grad_norm_workspace_bytes": (_sz, [_i64]),
     "grad_norm": (_i32, [_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _sz, _c_p]),
     "grad_clip": (_i32, [_i64, _c_p, _c_p, _c_p, _f32, _f32, _c_p, _c_p, _c_p, _sz, _c_p]),
@@ -957,6 +980,200 @@ def grad_clip(grads, max_norm: float, norm: torch.Tensor, out=None, eps: float =
     w = _scratch(ws, lib.grad_norm_workspace_bytes(count), dev, stream, st)
     _run(lib.grad_clip, "grad_clip", dev, count, _at(p), _at(n), _at(t), max_norm, eps,
          None if q is None else _at(q), norm_at, *_span(w), st)
+
+
+# ---------------------------------------------------------------------------
+# Microscaled formats (a power of two per block of 32), activations kept in 8 bits,
+# and the loss over the vocabulary; as above, on the device of their tensors.
+
+def mxfp4_scales_shape(rows: int, K: int):
+    """The shape of the exponent bytes of FP4 operands [rows x K]: steps of 256
+    elements, rows up to a multiple of 16, the eight blocks of a step (block b at
+    2 (b % 4) + b // 4)."""
+    return ((K + 255) // 256, (rows + 15) // 16 * 16, 8)
+
+
+def mxfp4_scale_bytes(rows: int, K: int) -> int:
+    return int(load().mxfp4_scale_bytes(rows, K))
+
+
+def _mx_operand(q: torch.Tensor, e: torch.Tensor, K: int, dev: int, name: str, ename: str):
+    rows = q.shape[0]
+    return (_arg(q, torch.uint8, (rows, K // 2), dev, name),
+            _arg(e, torch.uint8, mxfp4_scales_shape(rows, K), dev, ename))
+
+
+def _mx_width(K: int, name: str) -> int:
+    if K % 32:
+        raise FalqError(f"{name}: rows must be whole blocks of 32, not {K} elements")
+    return K
+
+
+def mxfp4_quantize(x: torch.Tensor, q: torch.Tensor, e: torch.Tensor, stream=None) -> None:
+    """FP4 E2M1 codes q [rows x K / 2] (two a byte, the lower index in the low half)
+    and exponent bytes e (mxfp4_scales_shape) of x [rows x K], float32 or bfloat16: a
+    power of two per block of 32, floor(log2(largest)) - 2; values to nearest, ties to
+    the even code, saturating at 6."""
+    rows, K = _matrix(x, "x")
+    _matrix(q, "q")
+    t, dev = _elem(x, "x"), _device(x, "x")
+    args = (_arg(x, x.dtype, (rows, _mx_width(K, "x")), dev, "x"), t, rows, K,
+            _arg(q, torch.uint8, (rows, K // 2), dev, "q"),
+            _arg(e, torch.uint8, mxfp4_scales_shape(rows, K), dev, "e"))
+    _run(load().mxfp4_quantize, "mxfp4_quantize", dev, *args, _stream_of(dev, stream))
+
+
+def mxfp4_dequantize(q: torch.Tensor, e: torch.Tensor, x: torch.Tensor, stream=None) -> None:
+    """x [rows x K], float32 or bfloat16, from mxfp4_quantize's codes and exponents."""
+    rows, K = _matrix(x, "x")
+    _matrix(q, "q")
+    t, dev = _elem(x, "x"), _device(q, "q")
+    args = (_arg(q, torch.uint8, (rows, _mx_width(K, "x") // 2), dev, "q"),
+            _arg(e, torch.uint8, mxfp4_scales_shape(rows, K), dev, "e"), rows, K,
+            _arg(x, x.dtype, (rows, K), dev, "x"), t)
+    _run(load().mxfp4_dequantize, "mxfp4_dequantize", dev, *args, _stream_of(dev, stream))
+
+
+def melded_linear_fwd_mxfp4_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
+    return int(load().melded_linear_fwd_mxfp4_workspace_bytes(T, d_in, d_out))
+
+
+def melded_linear_fwd_mxfp4(xq: torch.Tensor, x_e: torch.Tensor, wq: torch.Tensor,
+                            w_e: torch.Tensor, y: torch.Tensor,
+                            bias: Optional[torch.Tensor] = None, act: str = "none",
+                            residual: Optional[torch.Tensor] = None,
+                            z: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """melded_linear_fwd_act of mxfp4_quantize's operands: z = dec(xq) dec(wq)^T + bias
+    and y = act(z) + residual; xq [T x d_in / 2], wq [d_out x d_in / 2]."""
+    T, half = _matrix(xq, "xq")
+    d_in, d_out = _mx_width(2 * half, "xq"), _matrix(wq, "wq")[0]
+    t, a, dev = _elem(y, "y"), _act(act), _device(xq, "xq")
+    f32, out = torch.float32, (T, d_out)
+    lib, st = load(), _stream_of(dev, stream)
+    args = (*_mx_operand(xq, x_e, d_in, dev, "xq", "x_e"),
+            *_mx_operand(wq, w_e, d_in, dev, "wq", "w_e"), _arg(bias, f32, (d_out,), dev, "bias"),
+            a, _arg(residual, y.dtype, out, dev, "residual"), T, d_in, d_out, t,
+            _arg(y, y.dtype, out, dev, "y"), _arg(z, y.dtype, out, dev, "z"))
+    need = 0 if T <= 16 else lib.melded_linear_fwd_mxfp4_workspace_bytes(T, d_in, d_out)
+    w = _scratch(ws, need, dev, stream, st)
+    _run(lib.melded_linear_fwd_mxfp4, "melded_linear_fwd_mxfp4", dev, *args, *_span(w), st)
+
+
+def checkpoint_scales_shape(T: int, d: int):
+    """The shape of an 8-bit checkpoint's exponent bytes."""
+    return (T, (d + 31) // 32)
+
+
+def _checkpoint(q: torch.Tensor, e: torch.Tensor, T: int, d: int, dev: int, name: str,
+                ename: str):
+    return (_arg(q, torch.uint8, (T, d), dev, name),
+            _arg(e, torch.uint8, checkpoint_scales_shape(T, d), dev, ename))
+
+
+def checkpoint_save(x: torch.Tensor, q: torch.Tensor, e: torch.Tensor, stream=None) -> None:
+    """An activation x [T x d], float32 or bfloat16, kept in 8 bits: E4M3 codes q
+    [T x d] and exponent bytes e (checkpoint_scales_shape), a power of two per block of
+    32 of a row, the smallest under which the block does not saturate."""
+    T, d = _matrix(x, "x")
+    t, dev = _elem(x, "x"), _device(x, "x")
+    _run(load().checkpoint_save, "checkpoint_save", dev, _arg(x, x.dtype, (T, d), dev, "x"), t, T,
+         d, *_checkpoint(q, e, T, d, dev, "q", "e"), _stream_of(dev, stream))
+
+
+def checkpoint_restore(q: torch.Tensor, e: torch.Tensor, x: torch.Tensor, stream=None) -> None:
+    """x [T x d], float32 or bfloat16, from checkpoint_save's codes and exponents."""
+    T, d = _matrix(x, "x")
+    t, dev = _elem(x, "x"), _device(q, "q")
+    _run(load().checkpoint_restore, "checkpoint_restore", dev,
+         *_checkpoint(q, e, T, d, dev, "q", "e"), T, d, _arg(x, x.dtype, (T, d), dev, "x"), t,
+         _stream_of(dev, stream))
+
+
+def linear_act_bwd_ckpt(dy: torch.Tensor, z_q: torch.Tensor, z_e: torch.Tensor,
+                        dz: Optional[torch.Tensor], dbias: Optional[torch.Tensor] = None,
+                        act: str = "none", ws: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """linear_act_bwd with the z of a checkpoint (checkpoint_save's z_q and z_e)."""
+    T, d_out = _matrix(dy, "dy")
+    gt, a, dev, lib = _elem(dy, "dy"), _act(act), _device(dy, "dy"), load()
+    st = _stream_of(dev, stream)
+    args = (_arg(dy, dy.dtype, (T, d_out), dev, "dy"), gt,
+            *_checkpoint(z_q, z_e, T, d_out, dev, "z_q", "z_e"), a, T, d_out,
+            _arg(dz, dy.dtype, (T, d_out), dev, "dz"),
+            _arg(dbias, torch.float32, (d_out,), dev, "dbias"))
+    need = 0 if dbias is None else lib.linear_act_bwd_workspace_bytes(T, d_out)
+    w = _scratch(ws, need, dev, stream, st)
+    _run(lib.linear_act_bwd_ckpt, "linear_act_bwd_ckpt", dev, *args, *_span(w), st)
+
+
+def layer_norm_bwd_ckpt(dy: torch.Tensor, x_q: torch.Tensor, x_e: torch.Tensor,
+                        weight: Optional[torch.Tensor], mean: torch.Tensor, rstd: torch.Tensor,
+                        dx: Optional[torch.Tensor], dweight: Optional[torch.Tensor] = None,
+                        dbias: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """layer_norm_bwd with the x of a checkpoint (checkpoint_save's x_q and x_e); mean
+    and rstd are the forward's."""
+    T, d = _matrix(dy, "dy")
+    gt, dev, f32, lib = _elem(dy, "dy"), _device(dy, "dy"), torch.float32, load()
+    st = _stream_of(dev, stream)
+    args = (_arg(dy, dy.dtype, (T, d), dev, "dy"), gt,
+            *_checkpoint(x_q, x_e, T, d, dev, "x_q", "x_e"), _arg(weight, f32, (d,), dev, "weight"),
+            _arg(mean, f32, (T,), dev, "mean"), _arg(rstd, f32, (T,), dev, "rstd"), T, d,
+            _arg(dx, dy.dtype, (T, d), dev, "dx"), _arg(dweight, f32, (d,), dev, "dweight"),
+            _arg(dbias, f32, (d,), dev, "dbias"))
+    need = (0 if dweight is None and dbias is None
+            else lib.layer_norm_bwd_workspace_bytes(T, d))
+    w = _scratch(ws, need, dev, stream, st)
+    _run(lib.layer_norm_bwd_ckpt, "layer_norm_bwd_ckpt", dev, *args, *_span(w), st)
+
+
+def linear_cross_entropy_fwd_workspace_bytes(T: int, d: int, V: int) -> int:
+    return int(load().linear_cross_entropy_fwd_workspace_bytes(T, d, V))
+
+
+def linear_cross_entropy_fwd(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tensor,
+                             s_w: torch.Tensor, target: torch.Tensor, loss: torch.Tensor,
+                             lse: Optional[torch.Tensor] = None,
+                             ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """loss [T] = lse - z[t][target[t]] with the logits z = dec(xq) dec(wq)^T /
+    (s_x s_w) over the V rows of wq [V x d], which are not kept, and lse [T] =
+    log sum_v exp(z), the backward's input.  target [T] int64; a negative one does
+    not count (loss 0)."""
+    T, d = _matrix(xq, "xq")
+    V, dev = _matrix(wq, "wq")[0], _device(xq, "xq")
+    u8, f32, lib, st = torch.uint8, torch.float32, load(), _stream_of(dev, stream)
+    args = (_arg(xq, u8, (T, d), dev, "xq"), _arg(s_x, f32, (1,), dev, "s_x"),
+            _arg(wq, u8, (V, d), dev, "wq"), _arg(s_w, f32, (1,), dev, "s_w"),
+            _arg(target, torch.int64, (T,), dev, "target"), T, d, V,
+            _arg(loss, f32, (T,), dev, "loss"), _arg(lse, f32, (T,), dev, "lse"))
+    w = _scratch(ws, lib.linear_cross_entropy_fwd_workspace_bytes(T, d, V), dev, stream, st)
+    _run(lib.linear_cross_entropy_fwd, "linear_cross_entropy_fwd", dev, *args, *_span(w), st)
+
+
+def linear_cross_entropy_bwd_workspace_bytes(T: int, d: int, V: int,
+                                             dx_dtype=torch.float32) -> int:
+    return int(load().linear_cross_entropy_bwd_workspace_bytes(T, d, V, _ELEM[dx_dtype]))
+
+
+def linear_cross_entropy_bwd(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tensor,
+                             s_w: torch.Tensor, target: torch.Tensor, lse: torch.Tensor,
+                             dloss: torch.Tensor, dx: torch.Tensor,
+                             ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dx [T x d] (float32 or bfloat16), the gradient in x of sum_t dloss[t] loss[t]:
+    dloss[t] sum_v (exp(z[t][v] - lse[t]) - [v = target[t]]) dec(wq[v]) / s_w, the
+    logits z formed again a piece of the vocabulary at a time."""
+    T, d = _matrix(xq, "xq")
+    V, dev = _matrix(wq, "wq")[0], _device(xq, "xq")
+    u8, f32, lib, st = torch.uint8, torch.float32, load(), _stream_of(dev, stream)
+    t = _elem(dx, "dx")
+    args = (_arg(xq, u8, (T, d), dev, "xq"), _arg(s_x, f32, (1,), dev, "s_x"),
+            _arg(wq, u8, (V, d), dev, "wq"), _arg(s_w, f32, (1,), dev, "s_w"),
+            _arg(target, torch.int64, (T,), dev, "target"), _arg(lse, f32, (T,), dev, "lse"),
+            _arg(dloss, f32, (T,), dev, "dloss"), T, d, V, _arg(dx, dx.dtype, (T, d), dev, "dx"),
+            t)
+    w = _scratch(ws, lib.linear_cross_entropy_bwd_workspace_bytes(T, d, V, t), dev, stream, st)
+    _run(lib.linear_cross_entropy_bwd, "linear_cross_entropy_bwd", dev, *args, *_span(w), st)
 
 
 from .step import MeldedLinear, clip_gradients  # noqa: E402  (buffers + the call sequence)

@@ -3,6 +3,7 @@
 // launched; launches are asynchronous on the caller's stream.
 #include "../../include/falqon.h"
 #include "kernels.hpp"
+#include "mx_layout.hpp"
 
 #include <hip/hip_runtime.h>
 
@@ -729,6 +730,17 @@ inline bool rows_ok(int64_t T, int64_t d) {
   return T >= 0 && T <= (int64_t)1 << 30 && d >= 1 && d <= (int64_t)1 << 24;
 }
 
+// FP4 operands: rows of whole blocks of 32
+inline bool mx_dims_ok(int64_t rows, int64_t K) {
+  return rows >= 0 && rows <= (int64_t)1 << 30 && K >= 0 && K <= (int64_t)1 << 30 && K % 32 == 0;
+}
+// exponent bytes of an 8-bit checkpoint
+inline size_t kept_scale_bytes(int64_t T, int64_t d) { return (size_t)T * (size_t)((d + 31) / 32); }
+// an output layer of V rows of d codes
+inline bool loss_dims_ok(int64_t T, int64_t d, int64_t V) {
+  return T >= 0 && d >= 16 && d % 16 == 0 && V >= 1 && falq::cross_entropy_fits(T, d, V);
+}
+
 // memory of a call: count elements of size bytes (NULL: not given)
 struct Mem {
   uintptr_t lo, hi;
@@ -863,8 +875,8 @@ falq_status layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x_dt
              {elements(x, T * d, x_dtype), floats(weight, d), floats(mean, T), floats(rstd, T)},
              elements(dy, T * d, dy_dtype)))
     return FALQ_EINVAL;
-  return hip_status(falq::launch_layer_norm_bwd(dy, dy_dtype, x, x_dtype, weight, mean, rstd, T,
-                                                d, dx, dweight, dbias, ws,
+  return hip_status(falq::launch_layer_norm_bwd(dy, dy_dtype, x, x_dtype, nullptr, weight, mean,
+                                                rstd, T, d, dx, dweight, dbias, ws,
                                                 reinterpret_cast<hipStream_t>(stream)));
 }
 
@@ -917,8 +929,8 @@ falq_status linear_act_bwd(const void* dy, int dy_dtype, const void* z, int z_dt
   if (!apart({elements(dz, T * d_out, dy_dtype), floats(dbias, d_out), bytes(ws, need_ws)},
              {elements(z, T * d_out, z_dtype)}, elements(dy, T * d_out, dy_dtype)))
     return FALQ_EINVAL;
-  return hip_status(falq::launch_linear_act_bwd(dy, dy_dtype, z, z_dtype, T, d_out, act, dz,
-                                                dbias, ws,
+  return hip_status(falq::launch_linear_act_bwd(dy, dy_dtype, z, z_dtype, nullptr, T, d_out, act,
+                                                dz, dbias, ws,
                                                 reinterpret_cast<hipStream_t>(stream)));
 }
 
@@ -936,6 +948,180 @@ falq_status grad_clip(int64_t count, void* const* g, const int64_t* n, const int
                       size_t ws_bytes, falq_stream stream) {
   return grad_norm_impl(count, g, n, dtype, max_norm, eps, out ? out : g, norm, ws,
                         ws_bytes, stream);
+}
+
+// ---- microscaled formats ----------------------------------------------------
+
+size_t mxfp4_scale_bytes(int64_t rows, int64_t K) {
+  return mx_dims_ok(rows, K) ? (size_t)(falq::mx_steps(K) * falq::mx_rows16(rows) * 8) : 0;
+}
+
+falq_status mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, uint8_t* q,
+                           uint8_t* e, falq_stream stream) {
+  if (!mx_dims_ok(rows, K) || !dtype_ok(dtype)) return FALQ_EINVAL;
+  if (rows * K > 0 && (!elems(x, dtype) || !need(q) || !need(e))) return FALQ_EINVAL;
+  if (!apart({bytes(q, (size_t)(rows * K / 2)), bytes(e, mxfp4_scale_bytes(rows, K))},
+             {elements(x, rows * K, dtype)}, floats(nullptr, 0)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_mxfp4_quantize(x, dtype, rows, K, q, e,
+                                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+falq_status mxfp4_dequantize(const uint8_t* q, const uint8_t* e, int64_t rows, int64_t K, void* x,
+                             int dtype, falq_stream stream) {
+  if (!mx_dims_ok(rows, K) || !dtype_ok(dtype)) return FALQ_EINVAL;
+  if (rows * K > 0 && (!elems(x, dtype) || !need(q) || !need(e))) return FALQ_EINVAL;
+  if (!apart({elements(x, rows * K, dtype)},
+             {bytes(q, (size_t)(rows * K / 2)), bytes(e, mxfp4_scale_bytes(rows, K))},
+             floats(nullptr, 0)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_mxfp4_dequantize(q, e, rows, K, x, dtype,
+                                                  reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t melded_linear_fwd_mxfp4_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out) {
+  return gemm_dims_ok(T, d_in, d_out) && d_in % 32 == 0 ? falq::mx_linear_ws_bytes(T, d_in, d_out)
+                                                        : 0;
+}
+
+falq_status melded_linear_fwd_mxfp4(const uint8_t* xq, const uint8_t* x_e, const uint8_t* wq,
+                                    const uint8_t* w_e, const float* bias, int act,
+                                    const void* residual, int64_t T, int64_t d_in, int64_t d_out,
+                                    int dtype, void* y, void* z, void* ws, size_t ws_bytes,
+                                    falq_stream stream) {
+  if (!gemm_dims_ok(T, d_in, d_out) || d_in % 32 != 0 || !dtype_ok(dtype)) return FALQ_EINVAL;
+  if (act < FALQ_ACT_NONE || act > FALQ_ACT_SILU || !opt_f32(bias)) return FALQ_EINVAL;
+  if (T * d_in > 0 && (!need(xq) || !need(x_e))) return FALQ_EINVAL;
+  if (d_out * d_in > 0 && (!need(wq) || !need(w_e))) return FALQ_EINVAL;
+  if (T * d_out > 0 && (!elems(y, dtype) || !opt_elems(z, dtype) || !opt_elems(residual, dtype)))
+    return FALQ_EINVAL;
+  const size_t need_ws = falq::mx_linear_ws_bytes(T, d_in, d_out);
+  if (!ws_ok(ws, ws_bytes, need_ws)) return FALQ_EINVAL;
+  if (!apart({elements(y, T * d_out, dtype), elements(z, T * d_out, dtype), bytes(ws, need_ws)},
+             {bytes(xq, (size_t)(T * d_in / 2)), bytes(wq, (size_t)(d_out * d_in / 2)),
+              bytes(x_e, mxfp4_scale_bytes(T, d_in)), bytes(w_e, mxfp4_scale_bytes(d_out, d_in)),
+              floats(bias, d_out)},
+             elements(residual, T * d_out, dtype)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_mx_linear(xq, x_e, wq, w_e, bias, residual, T, d_in, d_out, act,
+                                           dtype, y, z, ws,
+                                           reinterpret_cast<hipStream_t>(stream)));
+}
+
+// ---- 8-bit checkpoints --------------------------------------------------------
+
+falq_status checkpoint_save(const void* x, int dtype, int64_t T, int64_t d, uint8_t* q, uint8_t* e,
+                            falq_stream stream) {
+  if (!rows_ok(T, d) || !dtype_ok(dtype)) return FALQ_EINVAL;
+  if (T > 0 && (!elems(x, dtype) || !q || !e)) return FALQ_EINVAL;
+  if (!apart({bytes(q, (size_t)(T * d)), bytes(e, kept_scale_bytes(T, d))},
+             {elements(x, T * d, dtype)}, floats(nullptr, 0)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_checkpoint_save(x, dtype, T, d, q, e,
+                                                 reinterpret_cast<hipStream_t>(stream)));
+}
+
+falq_status checkpoint_restore(const uint8_t* q, const uint8_t* e, int64_t T, int64_t d, void* x,
+                               int dtype, falq_stream stream) {
+  if (!rows_ok(T, d) || !dtype_ok(dtype)) return FALQ_EINVAL;
+  if (T > 0 && (!elems(x, dtype) || !q || !e)) return FALQ_EINVAL;
+  if (!apart({elements(x, T * d, dtype)},
+             {bytes(q, (size_t)(T * d)), bytes(e, kept_scale_bytes(T, d))}, floats(nullptr, 0)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_checkpoint_restore(q, e, T, d, x, dtype,
+                                                    reinterpret_cast<hipStream_t>(stream)));
+}
+
+falq_status linear_act_bwd_ckpt(const void* dy, int dy_dtype, const uint8_t* z_q,
+                                const uint8_t* z_e, int act, int64_t T, int64_t d_out, void* dz,
+                                float* dbias, void* ws, size_t ws_bytes, falq_stream stream) {
+  if (!dtype_ok(dy_dtype) || act < FALQ_ACT_NONE || act > FALQ_ACT_SILU) return FALQ_EINVAL;
+  if (!rows_ok(T, d_out) || !opt_f32(dbias) || (!dz && !dbias)) return FALQ_EINVAL;
+  if (T > 0 && (!elems(dy, dy_dtype) || !opt_elems(dz, dy_dtype) || !z_q || !z_e))
+    return FALQ_EINVAL;
+  const size_t need_ws = dbias ? falq::linear_act_bwd_ws_bytes(T, d_out) : 0;
+  if (!ws_ok(ws, ws_bytes, need_ws)) return FALQ_EINVAL;
+  if (!apart({elements(dz, T * d_out, dy_dtype), floats(dbias, d_out), bytes(ws, need_ws)},
+             {bytes(z_q, (size_t)(T * d_out)), bytes(z_e, kept_scale_bytes(T, d_out))},
+             elements(dy, T * d_out, dy_dtype)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_linear_act_bwd(dy, dy_dtype, z_q, 0, z_e, T, d_out, act, dz,
+                                                dbias, ws,
+                                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+falq_status layer_norm_bwd_ckpt(const void* dy, int dy_dtype, const uint8_t* x_q,
+                                const uint8_t* x_e, const float* weight, const float* mean,
+                                const float* rstd, int64_t T, int64_t d, void* dx, float* dweight,
+                                float* dbias, void* ws, size_t ws_bytes, falq_stream stream) {
+  if (!rows_ok(T, d) || !dtype_ok(dy_dtype)) return FALQ_EINVAL;
+  if (!opt_f32(weight) || !opt_elems(dx, dy_dtype) || !opt_f32(dweight) || !opt_f32(dbias))
+    return FALQ_EINVAL;
+  if (T > 0 && (!elems(dy, dy_dtype) || !x_q || !x_e || !scalar(mean) || !scalar(rstd)))
+    return FALQ_EINVAL;
+  const size_t need_ws = dweight || dbias ? falq::layer_norm_bwd_ws_bytes(T, d) : 0;
+  if (!ws_ok(ws, ws_bytes, need_ws)) return FALQ_EINVAL;
+  if (!apart({elements(dx, T * d, dy_dtype), floats(dweight, d), floats(dbias, d),
+              bytes(ws, need_ws)},
+             {bytes(x_q, (size_t)(T * d)), bytes(x_e, kept_scale_bytes(T, d)), floats(weight, d),
+              floats(mean, T), floats(rstd, T)},
+             elements(dy, T * d, dy_dtype)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_layer_norm_bwd(dy, dy_dtype, x_q, 0, x_e, weight, mean, rstd, T,
+                                                d, dx, dweight, dbias, ws,
+                                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+// ---- cross entropy over the vocabulary ----------------------------------------
+
+size_t linear_cross_entropy_fwd_workspace_bytes(int64_t T, int64_t d, int64_t V) {
+  return loss_dims_ok(T, d, V) ? falq::cross_entropy_fwd_ws_bytes(T, d, V) : 0;
+}
+
+falq_status linear_cross_entropy_fwd(const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                     const float* s_w, const int64_t* target, int64_t T,
+                                     int64_t d, int64_t V, float* loss, float* lse, void* ws,
+                                     size_t ws_bytes, falq_stream stream) {
+  if (!loss_dims_ok(T, d, V)) return FALQ_EINVAL;
+  if (!scalar(s_x) || !scalar(s_w) || !need(wq) || !opt_f32(lse)) return FALQ_EINVAL;
+  if (T > 0 && (!need(xq) || !target || !aligned(target, 8) || !scalar(loss))) return FALQ_EINVAL;
+  const size_t need_ws = falq::cross_entropy_fwd_ws_bytes(T, d, V);
+  if (!ws_ok(ws, ws_bytes, need_ws)) return FALQ_EINVAL;
+  if (!apart({floats(loss, T), floats(lse, T), bytes(ws, need_ws)},
+             {bytes(xq, (size_t)(T * d)), bytes(wq, (size_t)(V * d)), floats(s_x, 1),
+              floats(s_w, 1), bytes(target, (size_t)T * 8)},
+             floats(nullptr, 0)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_cross_entropy_fwd(xq, s_x, wq, s_w, target, T, d, V, loss, lse,
+                                                   ws, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t linear_cross_entropy_bwd_workspace_bytes(int64_t T, int64_t d, int64_t V, int dx_dtype) {
+  return loss_dims_ok(T, d, V) && dtype_ok(dx_dtype)
+             ? falq::cross_entropy_bwd_ws_bytes(T, d, V, dx_dtype)
+             : 0;
+}
+
+falq_status linear_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                     const float* s_w, const int64_t* target, const float* lse,
+                                     const float* dloss, int64_t T, int64_t d, int64_t V,
+                                     void* dx, int dx_dtype, void* ws, size_t ws_bytes,
+                                     falq_stream stream) {
+  if (!loss_dims_ok(T, d, V) || !dtype_ok(dx_dtype)) return FALQ_EINVAL;
+  if (!scalar(s_x) || !scalar(s_w) || !need(wq)) return FALQ_EINVAL;
+  if (T > 0 && (!need(xq) || !target || !aligned(target, 8) || !scalar(lse) || !scalar(dloss) ||
+                !elems(dx, dx_dtype)))
+    return FALQ_EINVAL;
+  const size_t need_ws = falq::cross_entropy_bwd_ws_bytes(T, d, V, dx_dtype);
+  if (!ws_ok(ws, ws_bytes, need_ws)) return FALQ_EINVAL;
+  if (!apart({elements(dx, T * d, dx_dtype), bytes(ws, need_ws)},
+             {bytes(xq, (size_t)(T * d)), bytes(wq, (size_t)(V * d)), floats(s_x, 1),
+              floats(s_w, 1), bytes(target, (size_t)T * 8), floats(lse, T), floats(dloss, T)},
+             floats(nullptr, 0)))
+    return FALQ_EINVAL;
+  return hip_status(falq::launch_cross_entropy_bwd(xq, s_x, wq, s_w, target, lse, dloss, T, d, V,
+                                                   dx, dx_dtype, ws,
+                                                   reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,665 @@
+// Softmax cross entropy over the vocabulary of an FP8 output layer, the logits
+//   z[t][v] = dec(xq[t]) . dec(wq[v]) / (s_x s_w)
+// never kept:
+//   lse[t] = log sum_v exp z[t][v],   loss[t] = lse[t] - z[t][target[t]],
+//   dx[t] = dloss[t] sum_v (exp(z[t][v] - lse[t]) - [v = target[t]]) dec(wq[v]) / s_w.
+//
+// Forward: the FP8 product in tiles (linear_act_pipe.hpp, linear_act_tile.hpp; few
+// tokens: linear_act_few.hpp), whose epilogue leaves of each row and each wave's
+// columns the maximum and the sum of exponentials under it, straight from the
+// accumulators, 8 bytes for 64 to 128 logits; a second launch joins them.  All of it
+// in float32 and base 2.
+//
+// Backward, a piece of the vocabulary after the other: the product again, whose
+// epilogue now leaves G = 2^15 (p - [v = target]) of the piece as float16; the piece's
+// rows of W as float16, transposed; and the product of the two, added onto dx.  G is
+// float16 because its 11 bits keep the gradient to 2^-12 of its terms (bfloat16: 2^-9),
+// and 2^15 because p may be as small as 1 / V: under it float16 has its full precision
+// down to 2^-29 and absolute steps of 2^-39 below, while 1 still fits; E4M3 codes are
+// exact in it.  The row's factor dloss / s_w is applied at the end, in float32.
+#include "elem.hpp"
+#include "kernels.hpp"
+#include "linear_act_pipe.hpp"
+#include "linear_act_plan.hpp"
+#include "linear_act_tile.hpp"
+
+#include <algorithm>
+
+namespace falq {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kGradScale = 32768.0f;
+
+// What the epilogues of the logits take.  V: columns there are (from the piece's
+// first on); k: base-2 logits per unit of the accumulators.
+struct Logits {
+  const float* sx;
+  const float* sw;
+  const int64_t* target;
+  __device__ __forceinline__ float k() const { return kLog2e / (sx[0] * sw[0]); }
+};
+
+// over the lanes l, l ^ 32 (and l ^ 16, l ^ 48 with blocks of 16)
+template <int BLK>
+__device__ __forceinline__ float max_over_g(float v) {
+  if constexpr (BLK == 16) v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+template <int BLK>
+__device__ __forceinline__ float sum_over_g(float v) {
+  if constexpr (BLK == 16) v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// ---- forward --------------------------------------------------------------
+// part[i][row] = (maximum, sum of 2^(z - maximum)) of the row's columns in the i-th
+// run; at_target[row] = the target's base-2 logit.
+struct Stats {
+  float2* part;
+  float* at_target;
+};
+
+template <class C, int MB, int NB, class ACC>
+__device__ __forceinline__ void stats_out(const ACC (&acc)[MB][NB], int m0, int n0, int M, int V,
+                                          float k, const Logits& lg, const Stats& st, int tn) {
+  // a lane's elements of a block: its row's columns 4 g + (e & 3) + (e >> 2) * SKIP
+  constexpr int E = sizeof(ACC) / 4, BLK = E == 4 ? 16 : 32, SKIP = BLK / 4;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wm = w / C::WGN, wn = w % C::WGN;
+  const int r = lane % BLK, g = lane / BLK;
+  const int col0 = n0 + wn * C::WTN + 4 * g;
+  const auto column = [](int j, int e) { return BLK * j + (e & 3) + (e >> 2) * SKIP; };
+  const bool whole = n0 + wn * C::WTN + C::WTN <= V;
+  float2* to = st.part + (int64_t)(tn * C::WGN + wn) * M;
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    const int row = m0 + wm * C::WTM + i * BLK + r;
+    float m = -INFINITY, s = 0.0f;
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e) m = fmaxf(m, acc[i][j][e]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (col0 + column(j, e) < V) m = fmaxf(m, acc[i][j][e]);
+    }
+    m = max_over_g<BLK>(m) * k;
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], k, -m));
+    } else {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (col0 + column(j, e) < V) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], k, -m));
+    }
+    s = sum_over_g<BLK>(s);
+    if (g == 0 && row < M) to[row] = make_float2(m, s);
+    // the target's logit, where it is among the wave's columns
+    const int64_t t = row < M ? lg.target[row] : -1;
+    const int64_t at = t - col0;
+    if (t < V && at >= 0 && at < C::WTN) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (at == column(j, e)) st.at_target[row] = acc[i][j][e] * k;
+    }
+  }
+}
+
+template <class C, int PER_CU>
+__global__ __launch_bounds__(C::kThreads, PER_CU) void loss_pipe(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
+    int tilesN, Logits lg, Stats st) {
+  int tm, tn;
+  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
+  const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
+  const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
+  pipe_product<E4M3AsF16Wide, C, PER_CU>(
+      A, B, M, N, K, m0, n0, Exponents{}, [&] { return lg.k(); },
+      [&](const auto& acc, float k, uint8_t*) {
+        stats_out<C>(acc, m0, n0, M, N, k, lg, st, tn);
+      });
+}
+template <class C>
+__global__ __launch_bounds__(C::kThreads) void loss_tile(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
+    int tilesN, Logits lg, Stats st) {
+  int tm, tn;
+  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  tile_product<E4M3AsF16, C>(
+      A, B, M, N, K, m0, n0, 0, INT32_MAX, Exponents{}, [&] { return lg.k(); },
+      [&](const auto& acc, float k, uint8_t*) {
+        stats_out<C>(acc, m0, n0, M, N, k, lg, st, tn);
+      });
+}
+// up to 16 tokens: a run of 16 columns a workgroup, a column of a row a lane
+template <int NW>
+__global__ __launch_bounds__(NW * 64) void loss_few(const uint8_t* __restrict__ A,
+                                                    const uint8_t* __restrict__ B, int M, int N,
+                                                    int K, Logits lg, Stats st) {
+  static_assert(NW * 64 >= 256, "a lane for each of 16 x 16");
+  __shared__ FewParts<1, 1, NW> part;
+  const int n0 = blockIdx.x * 16;
+  few_product<E4M3AsF16, 1, 1, NW, 1>(part, A, B, M, N, K, n0, Exponents{});
+  const float k = lg.k();
+  const int row = threadIdx.x / 16, c = threadIdx.x % 16, col = n0 + c;
+  if (row >= M) return;                                      // 16 lanes together
+  const float v = few_sum<1, 1, NW>(part, row, c) * k;
+  float m = col < N ? v : -INFINITY;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  float s = col < N ? __builtin_amdgcn_exp2f(v - m) : 0.0f;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) s += __shfl_xor(s, o, 64);
+  if (c == 0) st.part[(int64_t)blockIdx.x * M + row] = make_float2(m, s);
+  if (col < N && lg.target[row] == col) st.at_target[row] = v;
+}
+
+// (m, s) of two runs
+__device__ __forceinline__ void join_runs(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  // a run without a column is (-inf, 0)
+  const float a = m == -INFINITY ? 0.0f : s * __builtin_amdgcn_exp2f(m - top);
+  const float b = m2 == -INFINITY ? 0.0f : s2 * __builtin_amdgcn_exp2f(m2 - top);
+  m = top;
+  s = a + b;
+}
+
+// R rows of P runs each per workgroup, the runs dealt to 256 / R lanes in order
+template <int R>
+__global__ __launch_bounds__(256) void loss_join(const float2* __restrict__ part, int P, int M,
+                                                 int64_t V, const int64_t* __restrict__ target,
+                                                 const float* __restrict__ at_target,
+                                                 float* __restrict__ loss,
+                                                 float* __restrict__ lse) {
+  constexpr int L = 256 / R;
+  __shared__ float2 red[L][R];
+  const int r = threadIdx.x % R, l = threadIdx.x / R;
+  const int row = blockIdx.x * R + r;
+  float m = -INFINITY, s = 0.0f;
+  if (row < M)
+#pragma unroll 4
+    for (int i = l; i < P; i += L) {
+      const float2 p = part[(int64_t)i * M + row];
+      join_runs(m, s, p.x, p.y);
+    }
+  red[l][r] = make_float2(m, s);
+  __syncthreads();
+  for (int n = L / 2; n > 0; n /= 2) {
+    if (l < n) {
+      const float2 p = red[l + n][r];
+      join_runs(m, s, p.x, p.y);
+      red[l][r] = make_float2(m, s);
+    }
+    __syncthreads();
+  }
+  if (l != 0 || row >= M) return;
+  const float bits = __builtin_amdgcn_logf(s);               // log2
+  const int64_t t = target[row];
+  if (lse) lse[row] = (m + bits) * kLn2;
+  loss[row] = t < 0 ? 0.0f : t >= V ? NAN : ((m - at_target[row]) + bits) * kLn2;
+}
+
+// ---- backward -------------------------------------------------------------
+// G of a piece, [M x ldg] float16, columns past the vocabulary 0
+struct Grads {
+  const float* lse;
+  _Float16* G;
+  int64_t ldg;
+  int v0;              // the piece's first column
+};
+
+// the row's -lse in base 2, and its target's column in the piece; columns of a row
+// that is not counted are 0
+struct GradRow {
+  float neg;
+  int64_t t;
+  bool counts;
+  __device__ __forceinline__ GradRow(const Logits& lg, const Grads& gr, int row) {
+    t = lg.target[row];
+    counts = t >= 0;
+    t -= gr.v0;
+    neg = -gr.lse[row] * kLog2e;
+  }
+  __device__ __forceinline__ float of(float acc, float k, int col, int V) const {
+    const float p = __builtin_amdgcn_exp2f(fmaf(acc, k, neg));
+    const float v = (p - (col == t ? 1.0f : 0.0f)) * kGradScale;
+    return counts && col < V ? v : 0.0f;
+  }
+};
+
+// through the wave's part of the LDS, as tile_out: eight columns of a row per lane
+template <class C, int LDS, int MB, int NB, class ACC>
+__device__ __forceinline__ void grads_out(uint8_t* smem, const ACC (&acc)[MB][NB], int m0, int n0,
+                                          int M, int V, float k, const Logits& lg,
+                                          const Grads& gr) {
+  rows_through_lds<C, LDS>(smem, acc, m0, n0, M, (int)gr.ldg, [&](int row, int col, float(&v)[8]) {
+    const GradRow r(lg, gr, row);
+    typedef _Float16 H8 __attribute__((ext_vector_type(8)));
+    H8 h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (_Float16)r.of(v[i], k, col + i, V);
+    *reinterpret_cast<H8*>(gr.G + (int64_t)row * gr.ldg + col) = h;
+  });
+}
+
+template <class C, int PER_CU>
+__global__ __launch_bounds__(C::kThreads, PER_CU) void grads_pipe(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
+    int tilesN, Logits lg, Grads gr) {
+  int tm, tn;
+  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
+  const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
+  const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
+  pipe_product<E4M3, C, PER_CU>(
+      A, B, M, N, K, m0, n0, Exponents{}, [&] { return lg.k(); },
+      [&](const auto& acc, float k, uint8_t* smem) {
+        grads_out<C, Ring<E4M3, C, PER_CU>::kLds>(smem, acc, m0, n0, M, N, k, lg, gr);
+      });
+}
+template <class C>
+__global__ __launch_bounds__(C::kThreads) void grads_tile(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
+    int tilesN, Logits lg, Grads gr) {
+  int tm, tn;
+  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  tile_product<E4M3, C>(
+      A, B, M, N, K, m0, n0, 0, INT32_MAX, Exponents{}, [&] { return lg.k(); },
+      [&](const auto& acc, float k, uint8_t* smem) {
+        grads_out<C, kTileLds<E4M3, C>>(smem, acc, m0, n0, M, N, k, lg, gr);
+      });
+}
+template <int NW>
+__global__ __launch_bounds__(NW * 64) void grads_few(const uint8_t* __restrict__ A,
+                                                     const uint8_t* __restrict__ B, int M, int N,
+                                                     int K, Logits lg, Grads gr) {
+  __shared__ FewParts<1, 1, NW> part;
+  const int n0 = blockIdx.x * 16;
+  few_product<E4M3, 1, 1, NW, 1>(part, A, B, M, N, K, n0, Exponents{});
+  const float k = lg.k();
+  const int row = threadIdx.x / 16, c = threadIdx.x % 16;
+  if (row >= M) return;
+  const GradRow r(lg, gr, row);
+  gr.G[(int64_t)row * gr.ldg + n0 + c] =
+      (_Float16)r.of(few_sum<1, 1, NW>(part, row, c), k, n0 + c, N);
+}
+
+// out[d x ld] = dec(w[V x d])^T as float16, columns V .. ld - 1 zero (ld a multiple of
+// 64, d of 16): 64 x 128 elements a workgroup, turned in LDS
+__global__ __launch_bounds__(256) void weight_turn(const uint8_t* __restrict__ w, int V, int d,
+                                                   _Float16* __restrict__ out, int64_t ld) {
+  constexpr int ROWS = 64, COLS = 128, PAD = COLS + 2;
+  __shared__ _Float16 t[ROWS][PAD];
+  const int v0 = blockIdx.x * ROWS, c0 = blockIdx.y * COLS;
+  typedef _Float16 H2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = threadIdx.x / 8 + h * 32, c = threadIdx.x % 8 * 16;
+    const bool live = v0 + r < V && c0 + c < d;
+    const uint4 q = live ? *reinterpret_cast<const uint4*>(w + (int64_t)(v0 + r) * d + c0 + c)
+                         : make_uint4(0, 0, 0, 0);
+    const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      *reinterpret_cast<H2*>(&t[r][c + 4 * i]) =
+          __builtin_bit_cast(H2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[i], 1.0f, false));
+      *reinterpret_cast<H2*>(&t[r][c + 4 * i + 2]) =
+          __builtin_bit_cast(H2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[i], 1.0f, true));
+    }
+  }
+  __syncthreads();
+  typedef _Float16 H8 __attribute__((ext_vector_type(8)));
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int c = threadIdx.x / 8 + p * 32, r = threadIdx.x % 8 * 8;
+    if (c0 + c >= d) continue;
+    H8 h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = t[r + i][c];
+    *reinterpret_cast<H8*>(out + (int64_t)(c0 + c) * ld + v0 + r) = h;
+  }
+}
+
+// dx of all pieces up to this one: sums in `sums` between pieces, dx itself at the last
+struct DxOut {
+  const int64_t* target;
+  const float* dloss;
+  const float* sw;
+  float* sums;         // [M x N]: read unless this is the first piece
+  void* dx;            // [M x N]; null: not the last piece
+  int64_t V;
+  bool first;
+};
+
+template <class OT>
+__device__ __forceinline__ void dx_out8(float (&v)[8], int row, int64_t at, const DxOut& o) {
+  if (!o.first) {
+    float t[8];
+    load_elems<8>(o.sums + at, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+  if (!o.dx) {
+    store_elems<8>(o.sums + at, v);
+    return;
+  }
+  const int64_t t = o.target[row];
+  const float f = t >= o.V ? NAN : o.dloss[row] / (o.sw[0] * kGradScale);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = t < 0 ? 0.0f : v[i] * f;
+  store_elems<8>((OT*)o.dx + at, v);
+}
+
+template <class C, int PER_CU, class OT>
+__global__ __launch_bounds__(C::kThreads, PER_CU) void dx_pipe(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
+    int tilesN, DxOut o) {
+  int tm, tn;
+  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
+  const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
+  const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
+  pipe_product<F16Wide, C, PER_CU>(
+      A, B, M, N, K, m0, n0, Exponents{}, [] { return 0; },
+      [&](const auto& acc, int, uint8_t* smem) {
+        rows_through_lds<C, Ring<F16Wide, C, PER_CU>::kLds>(
+            smem, acc, m0, n0, M, N, [&](int row, int col, float(&v)[8]) {
+              dx_out8<OT>(v, row, (int64_t)row * N + col, o);
+            });
+      });
+}
+// SPLIT: as linear_act_tile, each split's sums to its plane of `part`
+template <class C, class OT, bool SPLIT>
+__global__ __launch_bounds__(C::kThreads) void dx_tile(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
+    int tilesN, DxOut o, float* __restrict__ part, int kc) {
+  int tm, tn;
+  const int nt = tilesM * tilesN, sp = SPLIT ? (int)blockIdx.x / nt : 0;
+  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x - sp * nt, nt), tilesM, tilesN, tm, tn);
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  tile_product<F16, C>(
+      A, B, M, N, K, m0, n0, SPLIT ? sp * kc : 0, SPLIT ? sp * kc + kc : INT32_MAX, Exponents{},
+      [] { return 0; }, [&](const auto& acc, int, uint8_t* smem) {
+        rows_through_lds<C, kTileLds<F16, C>>(
+            smem, acc, m0, n0, M, N, [&](int row, int col, float(&v)[8]) {
+              if constexpr (SPLIT)
+                store_elems<8>(part + ((int64_t)sp * M + row) * N + col, v);
+              else
+                dx_out8<OT>(v, row, (int64_t)row * N + col, o);
+            });
+      });
+}
+template <class OT>
+__global__ __launch_bounds__(256) void dx_join(const float* __restrict__ part, int S, int64_t M,
+                                               int N, DxOut o) {
+  const int64_t plane = M * N;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < plane / 8;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t at = i * 8;
+    float v[8];
+    load_elems<8>(part + at, v);
+    for (int s = 1; s < S; ++s) {
+      float t[8];
+      load_elems<8>(part + s * plane + at, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += t[e];
+    }
+    dx_out8<OT>(v, (int)(at / N), at, o);
+  }
+}
+
+// ---- host -----------------------------------------------------------------
+using P256 = Tile<256, 256, 2, 2>;
+using P256x128 = Tile<256, 128, 2, 2>;
+using P128 = Tile<128, 128, 2, 2>;
+using T128 = Tile<128, 128, 2, 4, 3>;
+using T64 = Tile<64, 64, 2, 2, 4>;
+using T32 = Tile<32, 64, 1, 4, 4>;
+
+constexpr int kFew = 16, kFewNW = 16;
+constexpr TileKind kLossKinds[] = {k256, k128, k64, k32x64};
+constexpr TileKind kGradKinds[] = {k256x128, k128, k64, k32x64};
+constexpr TileKind kDxKinds[] = {k256, k256x128, k128, k64, k32x64};
+
+template <int N>
+TileKind cheapest(const TileKind (&kinds)[N], int64_t M, int64_t n, int64_t K) {
+  TileKind best = kinds[N - 1];
+  float cost = HUGE_VALF;
+  for (const TileKind k : kinds) {
+    if (K > kFarK && k != k64 && k != k32x64) continue;
+    const float c = tile_cost(k, M, n, K);
+    if (c < cost) {
+      cost = c;
+      best = k;
+    }
+  }
+  return best;
+}
+
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up(int64_t a, int64_t b) { return ceil_div64(a, b) * b; }
+
+// Rows are taken in strips, so that no workspace grows with T beyond a strip's.
+constexpr int64_t kStrip = 16384;
+int64_t strip_of(int64_t T) { return std::min(T, kStrip); }
+
+// runs of columns of the forward's partial sums
+int64_t runs_of(int64_t T, int64_t d, int64_t V) {
+  if (T <= kFew) return ceil_div64(V, 16);
+  switch (cheapest(kLossKinds, T, V, 2 * d)) {
+    case k256: return ceil_div64(V, 256) * P256::WGN;
+    case k128: return ceil_div64(V, 128) * P128::WGN;
+    case k64: return ceil_div64(V, 64) * T64::WGN;
+    default: return ceil_div64(V, 64) * T32::WGN;
+  }
+}
+
+// pieces of the vocabulary: as many as keep G and the turned weight within kPiece
+// bytes each, of one width, a multiple of 64
+constexpr int64_t kPiece = (int64_t)128 << 20;
+int64_t piece_width(int64_t T, int64_t d, int64_t V) {
+  const int64_t most = std::clamp<int64_t>(kPiece / (2 * std::max(T, d)), 2048, 1 << 21);
+  return up(ceil_div64(V, ceil_div64(V, most)), 64);
+}
+
+// splits of the product with G over the piece: where its tiles leave CUs without work
+int dx_splits(int64_t T, int64_t d, int64_t width, int& kc) {
+  const int64_t nt = tiles_of(k128w8, T, d), steps = ceil_div64(width * 2, 128);
+  const int64_t s = std::min<int64_t>(kCUs / nt, steps / 8);
+  kc = 0;
+  if (s < 2) return 1;
+  kc = (int)ceil_div64(steps, s);
+  return (int)ceil_div64(steps, kc);
+}
+
+struct BwdPlan {
+  int64_t width;
+  int splits, kc;
+  size_t g, w, sums, part;                                   // bytes, multiples of 256
+  size_t bytes() const { return g + w + sums + part; }
+};
+BwdPlan bwd_plan(int64_t T, int64_t d, int64_t V, int dx_type) {
+  BwdPlan p;
+  p.width = piece_width(T, d, V);
+  p.splits = dx_splits(T, d, p.width, p.kc);
+  p.g = (size_t)up(T * p.width * 2, 256);
+  p.w = (size_t)up(d * p.width * 2, 256);
+  // float32 gradients collect in place
+  p.sums = dx_type != 0 && p.width < V ? (size_t)up(T * d * 4, 256) : 0;
+  p.part = p.splits > 1 ? (size_t)up(p.splits * T * d * 4, 256) : 0;
+  return p;
+}
+
+template <class C, int PIPE>
+void launch_logits_fwd(const uint8_t* x, const uint8_t* w, int64_t T, int64_t d, int64_t V,
+                       const Logits& lg, const Stats& st, hipStream_t s) {
+  const int tM = (int)ceil_div64(T, C::BM), tN = (int)ceil_div64(V, C::BN);
+  if constexpr (PIPE > 0)
+    loss_pipe<C, PIPE><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM, tN, lg,
+                                                       st);
+  else
+    loss_tile<C><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM, tN, lg, st);
+}
+// V: rows of w from the piece's first on, and columns counted
+template <class C, int PIPE>
+void launch_logits_bwd(const uint8_t* x, const uint8_t* w, int64_t T, int64_t d, int64_t V,
+                       const Logits& lg, const Grads& gr, hipStream_t s) {
+  const int tM = (int)ceil_div64(T, C::BM), tN = (int)ceil_div64(gr.ldg, C::BN);
+  if constexpr (PIPE > 0)
+    grads_pipe<C, PIPE><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM, tN, lg,
+                                                        gr);
+  else
+    grads_tile<C><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM, tN, lg, gr);
+}
+
+template <class C, int PIPE, class OT>
+void launch_dx(const uint8_t* g, const uint8_t* w, int64_t T, int64_t d, int64_t K,
+               const DxOut& o, hipStream_t s) {
+  const int tM = (int)ceil_div64(T, C::BM), tN = (int)ceil_div64(d, C::BN);
+  if constexpr (PIPE > 0)
+    dx_pipe<C, PIPE, OT><<<tM * tN, C::kThreads, 0, s>>>(g, w, (int)T, (int)d, (int)K, tM, tN, o);
+  else
+    dx_tile<C, OT, false><<<tM * tN, C::kThreads, 0, s>>>(g, w, (int)T, (int)d, (int)K, tM, tN, o,
+                                                          nullptr, 0);
+}
+
+template <class OT>
+hipError_t run_dx_product(const BwdPlan& p, const uint8_t* g, const uint8_t* w, int64_t T,
+                          int64_t d, int64_t K, const DxOut& o, float* part, hipStream_t s) {
+  if (p.splits > 1) {
+    using C = T128;
+    const int tM = (int)ceil_div64(T, C::BM), tN = (int)ceil_div64(d, C::BN);
+    dx_tile<C, OT, true><<<tM * tN * p.splits, C::kThreads, 0, s>>>(
+        g, w, (int)T, (int)d, (int)K, tM, tN, o, part, p.kc);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int blocks = (int)std::min<int64_t>((T * d / 8 + 255) / 256, 2048);
+    dx_join<OT><<<blocks, 256, 0, s>>>(part, p.splits, T, (int)d, o);
+    return hipGetLastError();
+  }
+  switch (cheapest(kDxKinds, T, d, K)) {
+    case k256: launch_dx<P256, 1, OT>(g, w, T, d, K, o, s); break;
+    case k256x128: launch_dx<P256x128, 2, OT>(g, w, T, d, K, o, s); break;
+    case k128: launch_dx<P128, 2, OT>(g, w, T, d, K, o, s); break;
+    case k64: launch_dx<T64, 0, OT>(g, w, T, d, K, o, s); break;
+    default: launch_dx<T32, 0, OT>(g, w, T, d, K, o, s); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// the largest sizes whose tiles, of strips of rows, a grid holds
+bool cross_entropy_fits(int64_t T, int64_t d, int64_t V) {
+  return T <= (int64_t)1 << 30 && d <= (int64_t)1 << 22 && V <= (int64_t)1 << 22;
+}
+
+size_t cross_entropy_fwd_ws_bytes(int64_t T, int64_t d, int64_t V) {
+  const int64_t n = strip_of(T);
+  // (a strip shorter than the others may have more runs: of 16 columns at most)
+  const int64_t tail = T % kStrip;
+  size_t most = 0;
+  for (const int64_t m : {n, tail})
+    if (m > 0) most = std::max(most, (size_t)(runs_of(m, d, V) * m) * sizeof(float2));
+  return T == 0 ? 0 : (size_t)up(n * 4, 256) + most;
+}
+
+hipError_t launch_cross_entropy_fwd(const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                    const float* s_w, const int64_t* target, int64_t T, int64_t d,
+                                    int64_t V, float* loss, float* lse, void* ws, hipStream_t s) {
+  const size_t first = (size_t)up(strip_of(T) * 4, 256);
+  for (int64_t r0 = 0; r0 < T; r0 += kStrip) {
+    const int64_t n = std::min(kStrip, T - r0);
+    const uint8_t* x = xq + r0 * d;
+    const Logits lg{s_x, s_w, target + r0};
+    const Stats st{(float2*)((char*)ws + first), (float*)ws};
+    if (n <= kFew) {
+      loss_few<kFewNW><<<(int)ceil_div64(V, 16), kFewNW * 64, 0, s>>>(x, wq, (int)n, (int)V, (int)d,
+                                                                      lg, st);
+    } else {
+      switch (cheapest(kLossKinds, n, V, 2 * d)) {
+        case k256: launch_logits_fwd<P256, 1>(x, wq, n, d, V, lg, st, s); break;
+        case k128: launch_logits_fwd<P128, 2>(x, wq, n, d, V, lg, st, s); break;
+        case k64: launch_logits_fwd<T64, 0>(x, wq, n, d, V, lg, st, s); break;
+        default: launch_logits_fwd<T32, 0>(x, wq, n, d, V, lg, st, s); break;
+      }
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int P = (int)runs_of(n, d, V);
+    float* const out = lse ? lse + r0 : nullptr;
+    if (n <= kFew)
+      loss_join<1><<<(int)n, 256, 0, s>>>(st.part, P, (int)n, V, lg.target, st.at_target,
+                                          loss + r0, out);
+    else
+      loss_join<16><<<(int)ceil_div64(n, 16), 256, 0, s>>>(st.part, P, (int)n, V, lg.target,
+                                                           st.at_target, loss + r0, out);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+size_t cross_entropy_bwd_ws_bytes(int64_t T, int64_t d, int64_t V, int dx_type) {
+  size_t most = 0;
+  for (const int64_t n : {strip_of(T), T % kStrip})
+    if (n > 0) most = std::max(most, bwd_plan(n, d, V, dx_type).bytes());
+  return most;
+}
+
+hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                    const float* s_w, const int64_t* target, const float* lse,
+                                    const float* dloss, int64_t T, int64_t d, int64_t V, void* dx,
+                                    int dx_type, void* ws, hipStream_t s) {
+  for (int64_t r0 = 0; r0 < T; r0 += kStrip) {
+    const int64_t n = std::min(kStrip, T - r0);
+    const uint8_t* x = xq + r0 * d;
+    const BwdPlan p = bwd_plan(n, d, V, dx_type);
+    const Logits lg{s_x, s_w, target + r0};
+    uint8_t* const g = (uint8_t*)ws;
+    uint8_t* const wt = g + p.g;
+    void* const to = (uint8_t*)dx + r0 * d * (dx_type == 0 ? 4 : 2);
+    float* const sums = dx_type == 0 ? (float*)to : (float*)(wt + p.w);
+    float* const part = (float*)(wt + p.w + p.sums);
+    for (int64_t v0 = 0; v0 < V; v0 += p.width) {
+      const int64_t cols = std::min(p.width, V - v0), ld = up(cols, 64);
+      const uint8_t* w = wq + v0 * d;
+      const Grads gr{lse + r0, (_Float16*)g, ld, (int)v0};
+      if (n <= kFew) {
+        grads_few<kFewNW><<<(int)(ld / 16), kFewNW * 64, 0, s>>>(x, w, (int)n, (int)cols, (int)d,
+                                                                 lg, gr);
+      } else {
+        switch (cheapest(kGradKinds, n, ld, d)) {
+          case k256x128: launch_logits_bwd<P256x128, 2>(x, w, n, d, cols, lg, gr, s); break;
+          case k128: launch_logits_bwd<P128, 2>(x, w, n, d, cols, lg, gr, s); break;
+          case k64: launch_logits_bwd<T64, 0>(x, w, n, d, cols, lg, gr, s); break;
+          default: launch_logits_bwd<T32, 0>(x, w, n, d, cols, lg, gr, s); break;
+        }
+      }
+      hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      weight_turn<<<dim3((unsigned)(ld / 64), (unsigned)ceil_div64(d, 128)), 256, 0, s>>>(
+          w, (int)cols, (int)d, (_Float16*)wt, ld);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      const bool last = v0 + p.width >= V;
+      const DxOut o{lg.target, dloss + r0, s_w, sums, last ? to : nullptr, V, v0 == 0};
+      e = dx_type == 0 ? run_dx_product<float>(p, g, wt, n, d, ld * 2, o, part, s)
+                       : run_dx_product<__bf16>(p, g, wt, n, d, ld * 2, o, part, s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace falq

@@ -9,6 +9,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "mx.hpp"
 
 #include <type_traits>
 
@@ -151,6 +152,73 @@ struct Piece {
     }
   }
 };
+
+// A lane's elements of a row: of float32 or bfloat16, or of an 8-bit checkpoint
+// (T = kept_t: E4M3 codes, and a power of two per block of 32 in `scales`).
+typedef uint8_t kept_t;
+template <class T, int E, bool ODD>
+struct RowElems {
+  Raw<T, E> v;
+  template <bool STREAM = false>
+  __device__ __forceinline__ void load(const T* x, const uint8_t*, int64_t row, int64_t d,
+                                       uint32_t base) {
+    v.template load<STREAM>(x + row * d + base);
+  }
+  __device__ __forceinline__ void clear() { v.clear(); }
+  __device__ __forceinline__ float operator[](int e) const { return v[e]; }
+};
+template <int E, bool ODD>
+struct RowElems<kept_t, E, ODD> {
+  typedef typename std::conditional<E == 8, v2i, typename std::conditional<E == 4, int, uint8_t>::type>::type V;
+  typedef V V_any __attribute__((aligned(1)));
+  V v;
+  uint8_t s0, s1;                              // of the first element's block, of the last's
+  int turn;                                    // elements of the first
+  template <bool STREAM = false>
+  __device__ __forceinline__ void load(const kept_t* x, const uint8_t* scales, int64_t row,
+                                       int64_t d, uint32_t base) {
+    const V_any* p = reinterpret_cast<const V_any*>(x + row * d + base);
+    if constexpr (STREAM && E > 1)
+      v = __builtin_nontemporal_load(p);
+    else
+      v = *p;
+    const uint8_t* s = scales + row * ((d + 31) / 32);
+    s0 = s[base / 32];
+    if constexpr (ODD && E > 1) {              // the row's last piece may lie in two
+      s1 = s[(base + E - 1) / 32];
+      turn = 32 - (int)(base & 31);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+    v = V{};
+    s0 = s1 = 127;
+    turn = 32;
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    uint32_t w;
+    if constexpr (E == 8)
+      w = (uint32_t)v[e / 4];
+    else
+      w = (uint32_t)v;
+    const float2 p = (e & 2) ? dec2(w, true) : dec2(w, false);
+    const float s = e8m0_value(ODD && E > 1 && e >= turn ? s1 : s0);
+    return ((e & 1) ? p.y : p.x) * s;
+  }
+};
+
+// elements base .. base + E - 1 of a row (all of one block where E > 1), as floats
+template <int E, class T>
+__device__ __forceinline__ void load_row_elems(const T* x, const uint8_t* scales, int64_t row,
+                                               int64_t d, int64_t base, float (&v)[E]) {
+  if constexpr (std::is_same_v<T, kept_t>) {
+    RowElems<kept_t, E, false> r;
+    r.load(x, scales, row, d, (uint32_t)base);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = r[e];
+  } else {
+    load_elems<E>(x + row * d + base, v);
+  }
+}
 
 // Sum over the wave's 64 lanes, in every lane.  Within rows of 16 lanes by
 // shifts, then across the rows: cross-lane operands of ordinary additions,

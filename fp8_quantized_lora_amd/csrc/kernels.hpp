@@ -233,10 +233,12 @@ size_t layer_norm_bwd_ws_bytes(int64_t T, int64_t d);
 hipError_t launch_layer_norm_fwd(const void* x, int xt, const float* w, const float* b, int64_t T,
                                  int64_t d, float eps, void* y, int yt, float* mean, float* rstd,
                                  hipStream_t s);
-// dx, dw and db may each be null; dx may be dy
-hipError_t launch_layer_norm_bwd(const void* dy, int gt, const void* x, int xt, const float* w,
-                                 const float* mean, const float* rstd, int64_t T, int64_t d,
-                                 void* dx, float* dw, float* db, void* ws, hipStream_t s);
+// dx, dw and db may each be null; dx may be dy.  xs: null, or x is an 8-bit
+// checkpoint's codes (xt is not used) and these are its exponent bytes
+hipError_t launch_layer_norm_bwd(const void* dy, int gt, const void* x, int xt, const uint8_t* xs,
+                                 const float* w, const float* mean, const float* rstd, int64_t T,
+                                 int64_t d, void* dx, float* dw, float* db, void* ws,
+                                 hipStream_t s);
 
 // ---- linear layer with an epilogue, and the epilogue's backward -------------
 size_t linear_act_ws_bytes(int64_t T, int64_t d_in, int64_t d_out);
@@ -245,10 +247,41 @@ hipError_t launch_linear_act(const uint8_t* xq, const float* s_x, const uint8_t*
                              int64_t d_in, int64_t d_out, int act, int dtype, void* y, void* z,
                              void* ws, hipStream_t s);
 size_t linear_act_bwd_ws_bytes(int64_t T, int64_t d);
-// dz or dbias may be null (without dbias ws is not used); dz may be dy
-hipError_t launch_linear_act_bwd(const void* dy, int gt, const void* z, int zt, int64_t T,
-                                 int64_t d, int act, void* dz, float* dbias, void* ws,
+// dz or dbias may be null (without dbias ws is not used); dz may be dy.  zs: as xs
+// above, of z
+hipError_t launch_linear_act_bwd(const void* dy, int gt, const void* z, int zt, const uint8_t* zs,
+                                 int64_t T, int64_t d, int act, void* dz, float* dbias, void* ws,
                                  hipStream_t s);
+
+// ---- microscaled formats (mx.hpp) --------------------------------------------
+// K a multiple of 32; e in the packed layout of mx.hpp
+hipError_t launch_mxfp4_quantize(const void* x, int xt, int64_t rows, int64_t K, uint8_t* q,
+                                 uint8_t* e, hipStream_t s);
+hipError_t launch_mxfp4_dequantize(const uint8_t* q, const uint8_t* e, int64_t rows, int64_t K,
+                                   void* y, int yt, hipStream_t s);
+size_t mx_linear_ws_bytes(int64_t T, int64_t d_in, int64_t d_out);
+hipError_t launch_mx_linear(const uint8_t* xq, const uint8_t* x_e, const uint8_t* wq,
+                            const uint8_t* w_e, const float* bias, const void* residual, int64_t T,
+                            int64_t d_in, int64_t d_out, int act, int dtype, void* y, void* z,
+                            void* ws, hipStream_t s);
+// 8-bit checkpoints: codes [T x d], exponent bytes [T x ceil(d / 32)]
+hipError_t launch_checkpoint_save(const void* x, int xt, int64_t T, int64_t d, uint8_t* q,
+                                  uint8_t* e, hipStream_t s);
+hipError_t launch_checkpoint_restore(const uint8_t* q, const uint8_t* e, int64_t T, int64_t d,
+                                     void* y, int yt, hipStream_t s);
+
+// ---- cross entropy over the vocabulary ---------------------------------------
+bool cross_entropy_fits(int64_t T, int64_t d, int64_t V);
+size_t cross_entropy_fwd_ws_bytes(int64_t T, int64_t d, int64_t V);
+// lse may be null
+hipError_t launch_cross_entropy_fwd(const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                    const float* s_w, const int64_t* target, int64_t T, int64_t d,
+                                    int64_t V, float* loss, float* lse, void* ws, hipStream_t s);
+size_t cross_entropy_bwd_ws_bytes(int64_t T, int64_t d, int64_t V, int dx_type);
+hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                    const float* s_w, const int64_t* target, const float* lse,
+                                    const float* dloss, int64_t T, int64_t d, int64_t V, void* dx,
+                                    int dx_type, void* ws, hipStream_t s);
 
 // ---- gradient norm and clipping ---------------------------------------------
 size_t grad_norm_ws_bytes(int64_t count);

@@ -91,19 +91,18 @@ __global__ __launch_bounds__(1024) void ln_fwd_long(const XT* __restrict__ x,
 // dx of one row per workgroup, which it reads twice
 template <class XT, class GT, int E>
 __global__ __launch_bounds__(1024) void ln_bwd_dx_long(
-    const GT* dy, const XT* __restrict__ x, const float* __restrict__ w,
-    const float* __restrict__ mean, const float* __restrict__ rstd, GT* dx, int64_t T,
-    int64_t d) {
+    const GT* dy, const XT* __restrict__ x, const uint8_t* __restrict__ xs,
+    const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
+    GT* dx, int64_t T, int64_t d) {
   __shared__ float red[16];
   for (int64_t row = blockIdx.x; row < T; row += gridDim.x) {
     const float mu = mean[row], rs = rstd[row];
     const GT* gr = dy + row * d;
-    const XT* xr = x + row * d;
     float s1 = 0.0f, s2 = 0.0f;
     for (int64_t i = (int64_t)threadIdx.x * E; i < d; i += 1024 * E) {
       float g[E], v[E], t[E];
       load_elems<E>(gr + i, g);
-      load_elems<E>(xr + i, v);
+      load_row_elems<E>(x, xs, row, d, i, v);
       if (w) load_elems<E>(w + i, t);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -117,7 +116,7 @@ __global__ __launch_bounds__(1024) void ln_bwd_dx_long(
     for (int64_t i = (int64_t)threadIdx.x * E; i < d; i += 1024 * E) {
       float g[E], v[E], t[E];
       load_elems<E>(gr + i, g);
-      load_elems<E>(xr + i, v);
+      load_row_elems<E>(x, xs, row, d, i, v);
       if (w) load_elems<E>(w + i, t);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -244,6 +243,7 @@ __global__ __launch_bounds__(1024) void ln_fwd_rows(const XT* __restrict__ x,
 // in registers as it lies in memory.
 template <class XT, class GT, int E, int C, int MOST, bool STREAM, bool ODD>
 __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __restrict__ x,
+                                                    const uint8_t* __restrict__ xs,
                                                     const float* __restrict__ w,
                                                     const float* __restrict__ mean,
                                                     const float* __restrict__ rstd, GT* dx,
@@ -271,13 +271,12 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
   // zeros in the threads past its end
   struct Row {
     Raw<GT, E> g[C];
-    Raw<XT, E> v[C];
+    RowElems<XT, E, ODD> v[C];
     float mu, rs;
   };
   auto load = [&](Row& o, int64_t r) {
     const int64_t row = __builtin_amdgcn_readfirstlane((int)(r < T ? r : T - 1));
     const GT* dyr = dy + row * d;
-    const XT* xr = x + row * d;
     o.mu = mean[row];
     o.rs = rstd[row];
 #pragma unroll
@@ -285,7 +284,7 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
       const Piece<E, ODD> p(gr.at<E>(c), d);
       if (p.any) {
         o.g[c].template load<STREAM>(dyr + p.base);
-        o.v[c].template load<STREAM>(xr + p.base);
+        o.v[c].template load<STREAM>(x, xs, row, d, p.base);
       } else {
         o.g[c].clear();
         o.v[c].clear();
@@ -389,8 +388,9 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
 constexpr int kShortCols = 32;
 template <class XT, class GT, int E, int C, bool ODD>
 __global__ __launch_bounds__(1024) void ln_bwd_short(
-    const GT* dy, const XT* __restrict__ x, const float* __restrict__ w,
-    const float* __restrict__ mean, const float* __restrict__ rstd, GT* dx,
+    const GT* dy, const XT* __restrict__ x, const uint8_t* __restrict__ xs,
+    const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
+    GT* dx,
     float* __restrict__ dw, float* __restrict__ db, int T, int d, int nt, int row_blocks) {
   if ((int)blockIdx.x < row_blocks) {
     __shared__ float red[16][2];
@@ -407,12 +407,13 @@ __global__ __launch_bounds__(1024) void ln_bwd_short(
       if (!p.any) continue;
       float f[E];
       load_elems<E>(dy + from + p.base, gw[c]);
-      load_elems<E>(x + from + p.base, xh[c]);
+      RowElems<XT, E, ODD> v;
+      v.load(x, xs, live ? row : T - 1, d, p.base);
       if (w) load_elems<E>(w + p.base, f);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         if (w) gw[c][e] *= f[e];
-        xh[c][e] = (xh[c][e] - mu) * rs;
+        xh[c][e] = (v[e] - mu) * rs;
         if (!p.own(e)) continue;
         s[0] += gw[c][e];
         s[1] = fmaf(gw[c][e], xh[c][e], s[1]);
@@ -440,7 +441,9 @@ __global__ __launch_bounds__(1024) void ln_bwd_short(
 #pragma unroll 8
     for (int r = rl; r < T; r += lanes) {
       const float g = (float)dy[(int64_t)r * d + col];
-      a = fmaf(g, ((float)x[(int64_t)r * d + col] - mean[r]) * rstd[r], a);
+      float v[1];
+      load_row_elems<1>(x, xs, r, d, col, v);
+      a = fmaf(g, (v[0] - mean[r]) * rstd[r], a);
       b += g;
     }
   }
@@ -462,8 +465,8 @@ __global__ __launch_bounds__(1024) void ln_bwd_short(
 constexpr int kColRows = 8, kColLanes = 32;
 template <class XT, class GT, int E>
 __global__ __launch_bounds__(256) void ln_bwd_cols(
-    const GT* __restrict__ dy, const XT* __restrict__ x, const float* __restrict__ mean,
-    const float* __restrict__ rstd, float* __restrict__ part, int64_t T, int64_t d,
+    const GT* __restrict__ dy, const XT* __restrict__ x, const uint8_t* __restrict__ xs,
+    const float* __restrict__ mean, const float* __restrict__ rstd, float* __restrict__ part, int64_t T, int64_t d,
     int64_t rows_per_strip) {
   __shared__ float sw[kColRows][kColLanes * E], sb[kColRows][kColLanes * E];
   const int cl = threadIdx.x % kColLanes, rl = threadIdx.x / kColLanes;
@@ -476,7 +479,7 @@ __global__ __launch_bounds__(256) void ln_bwd_cols(
     for (int64_t r = r0 + rl; r < r1; r += kColRows) {
       float g[E], v[E];
       load_elems<E>(dy + r * d + col, g);
-      load_elems<E>(x + r * d + col, v);
+      load_row_elems<E>(x, xs, r, d, col, v);
       const float mu = mean[r], rs = rstd[r];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -542,16 +545,16 @@ BwdPlan bwd_plan(int64_t T, int64_t d) {
 }
 
 template <class XT, class GT, int E, int C, bool STREAM, bool ODD>
-hipError_t bwd_rows(const BwdPlan& p, const GT* dy, const XT* x, const float* w, const float* mean,
+hipError_t bwd_rows(const BwdPlan& p, const GT* dy, const XT* x, const uint8_t* xs, const float* w, const float* mean,
                     const float* rstd, int64_t T, int64_t d, GT* dx, float* part, hipStream_t s) {
   const size_t lds = (size_t)C * E * (p.G / 2) * p.nt * 4;
   // a workgroup of at most 512 threads may use twice the registers
   if (p.nt <= 512)
     ln_bwd_rows<XT, GT, E, C, 512, STREAM, ODD><<<p.blocks, p.nt * p.G, lds, s>>>(
-        dy, x, w, mean, rstd, dx, part, T, (int)d, p.nt);
+        dy, x, xs, w, mean, rstd, dx, part, T, (int)d, p.nt);
   else
     ln_bwd_rows<XT, GT, E, C, 1024, STREAM, ODD><<<p.blocks, p.nt, lds, s>>>(
-        dy, x, w, mean, rstd, dx, part, T, (int)d, p.nt);
+        dy, x, xs, w, mean, rstd, dx, part, T, (int)d, p.nt);
   return hipGetLastError();
 }
 
@@ -561,7 +564,7 @@ bool bwd_short_fits(int64_t T, int64_t d) {
 }
 
 template <class XT, class GT, int E, bool ODD>
-hipError_t bwd_short(const GT* dy, const XT* x, const float* w, const float* mean,
+hipError_t bwd_short(const GT* dy, const XT* x, const uint8_t* xs, const float* w, const float* mean,
                      const float* rstd, int64_t T, int64_t d, GT* dx, float* dw, float* db,
                      hipStream_t s) {
   const int nt = row_threads(d, 8, 1024), G = 1024 / nt;
@@ -570,7 +573,7 @@ hipError_t bwd_short(const GT* dy, const XT* x, const float* w, const float* mea
   auto launch = [&](int row_blocks, int col_blocks) {
     if (row_blocks + col_blocks > 0)
       ln_bwd_short<XT, GT, E, 8 / E, ODD><<<row_blocks + col_blocks, nt * G, 0, s>>>(
-          dy, x, w, mean, rstd, dx, dw, db, (int)T, (int)d, nt, row_blocks);
+          dy, x, xs, w, mean, rstd, dx, dw, db, (int)T, (int)d, nt, row_blocks);
   };
   if ((const GT*)dx == dy) {                   // in place: the columns are read first
     launch(0, cols);
@@ -584,24 +587,24 @@ hipError_t bwd_short(const GT* dy, const XT* x, const float* w, const float* mea
 // rows that no group of threads holds in registers (or shorter than a piece):
 // dx in two passes over the row, dw and db in strips of rows
 template <class XT, class GT, int E>
-hipError_t bwd_long(const GT* dy, const XT* x, const float* w, const float* mean,
+hipError_t bwd_long(const GT* dy, const XT* x, const uint8_t* xs, const float* w, const float* mean,
                     const float* rstd, int64_t T, int64_t d, GT* dx, float* part, hipStream_t s) {
   if (part) {                                  // before dx, which may overwrite dy
     const Strips st = strips_of(T, d);
     const dim3 grid((unsigned)((d + kColLanes * E - 1) / (kColLanes * E)), (unsigned)st.n);
-    ln_bwd_cols<XT, GT, E><<<grid, 256, 0, s>>>(dy, x, mean, rstd, part, T, d, st.rows);
+    ln_bwd_cols<XT, GT, E><<<grid, 256, 0, s>>>(dy, x, xs, mean, rstd, part, T, d, st.rows);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (dx) ln_bwd_dx_long<XT, GT, E><<<row_grid(T), 1024, 0, s>>>(dy, x, w, mean, rstd, dx, T, d);
+  if (dx) ln_bwd_dx_long<XT, GT, E><<<row_grid(T), 1024, 0, s>>>(dy, x, xs, w, mean, rstd, dx, T, d);
   return hipGetLastError();
 }
 
 template <class XT, class GT, int E, bool ODD>
-hipError_t bwd(const GT* dy, const XT* x, const float* w, const float* mean, const float* rstd,
+hipError_t bwd(const GT* dy, const XT* x, const uint8_t* xs, const float* w, const float* mean, const float* rstd,
                int64_t T, int64_t d, GT* dx, float* dw, float* db, float* part, hipStream_t s) {
   if (bwd_short_fits(T, d))
-    return bwd_short<XT, GT, E, ODD>(dy, x, w, mean, rstd, T, d, dx, dw, db, s);
+    return bwd_short<XT, GT, E, ODD>(dy, x, xs, w, mean, rstd, T, d, dx, dw, db, s);
   if (!dw && !db) part = nullptr;
   const BwdPlan p = bwd_plan(T, d);
   // the streaming hint needs whole lines
@@ -609,28 +612,28 @@ hipError_t bwd(const GT* dy, const XT* x, const float* w, const float* mean, con
   const bool stream = HINT && T * d * (int64_t)(2 * sizeof(GT) + sizeof(XT)) > kStreamBytes;
   hipError_t e;
   if (p.n == 16)
-    e = stream ? bwd_rows<XT, GT, E, 16 / E, HINT, ODD>(p, dy, x, w, mean, rstd, T, d, dx, part, s)
-               : bwd_rows<XT, GT, E, 16 / E, false, ODD>(p, dy, x, w, mean, rstd, T, d, dx, part,
+    e = stream ? bwd_rows<XT, GT, E, 16 / E, HINT, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx, part, s)
+               : bwd_rows<XT, GT, E, 16 / E, false, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx, part,
                                                          s);
   else if (p.n)
-    e = stream ? bwd_rows<XT, GT, E, 8 / E, HINT, ODD>(p, dy, x, w, mean, rstd, T, d, dx, part, s)
-               : bwd_rows<XT, GT, E, 8 / E, false, ODD>(p, dy, x, w, mean, rstd, T, d, dx, part,
+    e = stream ? bwd_rows<XT, GT, E, 8 / E, HINT, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx, part, s)
+               : bwd_rows<XT, GT, E, 8 / E, false, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx, part,
                                                         s);
   else
-    e = bwd_long<XT, GT, ODD ? 1 : E>(dy, x, w, mean, rstd, T, d, dx, part, s);
+    e = bwd_long<XT, GT, ODD ? 1 : E>(dy, x, xs, w, mean, rstd, T, d, dx, part, s);
   if (e != hipSuccess || !part) return e;
   return launch_column_sum(part, p.n ? p.blocks : strips_of(T, d).n, d, 2, dw, db, s);
 }
 
 template <class XT, class GT>
-hipError_t bwd_by_width(const void* dy, const void* x, const float* w, const float* mean,
+hipError_t bwd_by_width(const void* dy, const void* x, const uint8_t* xs, const float* w, const float* mean,
                         const float* rstd, int64_t T, int64_t d, void* dx, float* dw, float* db,
                         float* part, hipStream_t s) {
   const GT* g = (const GT*)dy;
   const XT* v = (const XT*)x;
-  constexpr int E = sizeof(XT) + sizeof(GT) == 4 ? 8 : 4;
-  return d % 8 == 0 ? bwd<XT, GT, E, false>(g, v, w, mean, rstd, T, d, (GT*)dx, dw, db, part, s)
-                    : bwd<XT, GT, 4, true>(g, v, w, mean, rstd, T, d, (GT*)dx, dw, db, part, s);
+  constexpr int E = sizeof(XT) + sizeof(GT) <= 4 ? 8 : 4;
+  return d % 8 == 0 ? bwd<XT, GT, E, false>(g, v, xs, w, mean, rstd, T, d, (GT*)dx, dw, db, part, s)
+                    : bwd<XT, GT, 4, true>(g, v, xs, w, mean, rstd, T, d, (GT*)dx, dw, db, part, s);
 }
 
 template <class XT, class YT, int E, int N, bool STREAM, bool ODD>
@@ -739,8 +742,8 @@ hipError_t launch_layer_norm_fwd(const void* x, int xt, const float* w, const fl
                  : fwd<__bf16, __bf16>(x, w, b, T, d, eps, y, mean, rstd, s);
 }
 
-hipError_t launch_layer_norm_bwd(const void* dy, int gt, const void* x, int xt, const float* w,
-                                 const float* mean, const float* rstd, int64_t T, int64_t d,
+hipError_t launch_layer_norm_bwd(const void* dy, int gt, const void* x, int xt, const uint8_t* xs,
+                                 const float* w, const float* mean, const float* rstd, int64_t T, int64_t d,
                                  void* dx, float* dw, float* db, void* ws, hipStream_t s) {
   if (T == 0) {
     hipError_t e = dw ? launch_fill_f32(dw, d, 0.0f, s) : hipSuccess;
@@ -748,12 +751,13 @@ hipError_t launch_layer_norm_bwd(const void* dy, int gt, const void* x, int xt, 
     return db ? launch_fill_f32(db, d, 0.0f, s) : hipSuccess;
   }
   float* part = (float*)ws;
-  if (xt == 0)
-    return gt == 0
-               ? bwd_by_width<float, float>(dy, x, w, mean, rstd, T, d, dx, dw, db, part, s)
-               : bwd_by_width<float, __bf16>(dy, x, w, mean, rstd, T, d, dx, dw, db, part, s);
-  return gt == 0 ? bwd_by_width<__bf16, float>(dy, x, w, mean, rstd, T, d, dx, dw, db, part, s)
-                 : bwd_by_width<__bf16, __bf16>(dy, x, w, mean, rstd, T, d, dx, dw, db, part, s);
+  const auto run = [&](auto v, auto g) {
+    return bwd_by_width<decltype(v), decltype(g)>(dy, x, xs, w, mean, rstd, T, d, dx, dw, db, part,
+                                                  s);
+  };
+  if (xs) return gt == 0 ? run(kept_t{}, float{}) : run(kept_t{}, __bf16{});
+  if (xt == 0) return gt == 0 ? run(float{}, float{}) : run(float{}, __bf16{});
+  return gt == 0 ? run(__bf16{}, float{}) : run(__bf16{}, __bf16{});
 }
 
 }  // namespace falq

@@ -58,11 +58,11 @@ hipError_t launch_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N
   const auto go = [&](auto stream) {
     constexpr bool STREAM = decltype(stream)::value;
     if constexpr (PIPE > 0)
-      linear_act_pipe<C, PIPE, OT, STREAM><<<tM * tN, C::kThreads, 0, s>>>(
-          A, B, (int)M, (int)N, (int)K, tM, tN, ep);
+      linear_act_pipe<E4M3, C, PIPE, OT, STREAM><<<tM * tN, C::kThreads, 0, s>>>(
+          A, B, (int)M, (int)N, (int)K, tM, tN, ep, Exponents{});
     else
-      linear_act_tile<C, OT, STREAM><<<tM * tN, C::kThreads, 0, s>>>(A, B, (int)M, (int)N, (int)K,
-                                                                     tM, tN, ep);
+      linear_act_tile<E4M3, C, OT, STREAM><<<tM * tN, C::kThreads, 0, s>>>(
+          A, B, (int)M, (int)N, (int)K, tM, tN, ep, Exponents{});
   };
   if (MANY && stream_outputs<OT>(M, N, ep))
     go(std::bool_constant<MANY && sizeof(OT) == 2>{});
@@ -74,8 +74,9 @@ hipError_t launch_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N
 template <int MT, int NB, int NW, int U, class OT>
 hipError_t launch_few(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
                       const Epilogue& ep, hipStream_t s) {
-  linear_act_few<MT, NB, NW, U, OT><<<(int)((N + NB * 16 - 1) / (NB * 16)), NW * 64, 0, s>>>(
-      A, B, (int)M, (int)N, (int)K, ep);
+  linear_act_few<E4M3, MT, NB, NW, U, OT>
+      <<<(int)((N + NB * 16 - 1) / (NB * 16)), NW * 64, 0, s>>>(A, B, (int)M, (int)N, (int)K, ep,
+                                                                Exponents{});
   return hipGetLastError();
 }
 
@@ -103,12 +104,12 @@ hipError_t launch_split(const Plan& p, const uint8_t* A, const uint8_t* B, int64
                         int64_t K, const Epilogue& ep, float* part, hipStream_t s) {
   using C = T128;
   const int tM = (int)((M + C::BM - 1) / C::BM), tN = (int)((N + C::BN - 1) / C::BN);
-  linear_act_tile<C, OT, false, true><<<tM * tN * p.split, C::kThreads, 0, s>>>(
-      A, B, (int)M, (int)N, (int)K, tM, tN, ep, part, p.kc);
+  linear_act_tile<E4M3, C, OT, false, true><<<tM * tN * p.split, C::kThreads, 0, s>>>(
+      A, B, (int)M, (int)N, (int)K, tM, tN, ep, Exponents{}, part, p.kc);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int blocks = (int)std::min<int64_t>((M * N / 8 + 255) / 256, 2048);
-  linear_act_join<OT><<<blocks, 256, 0, s>>>(part, p.split, M, (int)N, ep);
+  linear_act_join<E4M3, OT><<<blocks, 256, 0, s>>>(part, p.split, M, (int)N, ep);
   return hipGetLastError();
 }
 

@@ -37,20 +37,14 @@ __device__ __forceinline__ void load16_to_lds_at(const uint8_t* base, uint32_t o
                : "memory");
 }
 
-// d += a b^T of a 16 x 16 block, d in the same registers throughout (of the
-// accumulation half of the file, ACC, or the other): left to itself the compiler
-// moves the accumulators of a large tile through others at every loop turn
-template <bool ACC>
-__device__ __forceinline__ void mfma_in_place(v4f& d, const v8i& a, const v8i& b) {
-  if constexpr (ACC)
-    asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, %0" : "+a"(d) : "v"(a), "v"(b));
-  else
-    asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
-}
-// whether column block j of MB rows' blocks lies there: 64 blocks fill it
-template <int MB>
+// The products keep their accumulators in the same registers throughout
+// (mma_in_place): left to itself the compiler moves those of a large tile through
+// others at every loop turn.
+// whether the accumulators of column block j of MB rows' blocks lie in the
+// accumulation half, which 256 of a lane's registers fill
+template <class ACC, int MB>
 constexpr bool in_acc(int j) {
-  return (j + 1) * MB <= 64;
+  return (j + 1) * MB * (int)sizeof(ACC) <= 64 * 16;
 }
 
 // f(0), ..., f(N - 1), each index a constant of its type
@@ -63,63 +57,117 @@ __device__ __forceinline__ void each(F&& f) {
 }
 #define FALQ_INLINE __attribute__((always_inline))
 
-// d += a b^T of 16 x 16 blocks for every row fragment of a and column fragment of
-// b; with(t) goes between product t and the next
-template <int I0, int J0, int MB, int NB, int HM, int HN, class F>
-__device__ __forceinline__ void quarter(v4f (&acc)[MB][NB], const v8i (&a)[HM],
-                                        const v8i (&b)[HN], F&& with) {
-  each<HM * HN>([&](auto t) FALQ_INLINE {
-    constexpr int T = decltype(t)::value;
-    mfma_in_place<in_acc<MB>(J0 + T % HN)>(acc[I0 + T / HN][J0 + T % HN], b[T % HN], a[T / HN]);
-    with(t);
+// d += a b^T of the blocks for every row fragment of a and column fragment of b
+// (first of all blocks' first products, where a step takes several); with(t) goes
+// between product t and the next.
+template <class OP, int I0, int J0, int MB, int NB, int HM, int HN, class F>
+__device__ __forceinline__ void quarter(typename OP::Acc (&acc)[MB][NB],
+                                        const typename OP::Frag (&a)[HM],
+                                        const typename OP::Frag (&b)[HN], F&& with) {
+  typedef typename OP::Acc Acc;
+  constexpr int BLOCKS = HM * HN;
+  if constexpr (!OP::kConverted) {
+    each<BLOCKS * OP::kProducts>([&](auto t) FALQ_INLINE {
+      constexpr int T = decltype(t)::value, P = T % BLOCKS;
+      OP::template mma_in_place<in_acc<Acc, MB>(J0 + P % HN), T / BLOCKS>(
+          acc[I0 + P / HN][J0 + P % HN], b[P % HN], a[P / HN]);
+      with(t);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  } else {
+    // the next product's operands are converted between this one's blocks
+    v4i ca[2][HM], cb[2][HN];
+    auto convert = [&](auto to, auto o) FALQ_INLINE {        // operand o, A's first
+      constexpr int P = decltype(to)::value, O = decltype(o)::value;
+      if constexpr (O < HM)
+        ca[P % 2][O] = OP::template convert<P>(a[O]);
+      else
+        cb[P % 2][O - HM] = OP::template convert<P>(b[O - HM]);
+    };
+    using First = std::integral_constant<int, 0>;
+    each<HM + HN>([&](auto o) FALQ_INLINE { convert(First{}, o); });
     __builtin_amdgcn_sched_barrier(0);
-  });
+    asm volatile("s_nop 1");                                 // an operand's two wait states
+    each<BLOCKS * OP::kProducts>([&](auto t) FALQ_INLINE {
+      constexpr int T = decltype(t)::value, B = T % BLOCKS, P = T / BLOCKS;
+      static_assert(in_acc<Acc, MB>(J0 + B % HN), "accumulators");
+      mfma_f16_in_place(acc[I0 + B / HN][J0 + B % HN], cb[P % 2][B % HN], ca[P % 2][B / HN]);
+      if constexpr (P + 1 < OP::kProducts) {
+        using Next = std::integral_constant<int, P + 1>;
+        constexpr int O0 = B * (HM + HN) / BLOCKS, O1 = (B + 1) * (HM + HN) / BLOCKS;
+        each<O1 - O0>([&](auto o) FALQ_INLINE {
+          convert(Next{}, std::integral_constant<int, O0 + decltype(o)::value>{});
+        });
+      }
+      with(t);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (B + 1 == BLOCKS) asm volatile("s_nop 1");
+    });
+  }
 }
 
 // Between an asm product and whatever else may touch its result (a copy, where
 // the compiler sees fit) pass the product's eight passes, which the compiler,
 // not knowing the instruction, does not wait for: to be called where blocks of
 // code meet, for copies arise there.
-template <int MB, int NB>
-__device__ __forceinline__ void settle(v4f (&acc)[MB][NB]) {
+template <int MB, int NB, class ACC>
+__device__ __forceinline__ void settle(ACC (&acc)[MB][NB]) {
   asm volatile("s_nop 15" ::: "memory");
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      if (in_acc<MB>(j))
+      if (in_acc<ACC, MB>(j))
         asm volatile("" : "+a"(acc[i][j]));
       else
         asm volatile("" : "+v"(acc[i][j]));
     }
 }
 
-template <class C, int PER_CU, class OT, bool STREAM>
-__global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
-    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
-    int tilesN, Epilogue ep) {
-  constexpr int BK = C::BK, MB = C::MB, NB = C::NB, HM = MB / 2, HN = NB / 2;
-  // a slot: half the rows of either operand for one K step
-  constexpr int UA = C::BM / 2 * BK, SLOT = UA + C::BN / 2 * BK;
-  constexpr int FIT = 160 * 1024 / PER_CU / SLOT, SLOTS = FIT < 5 ? FIT : 5, AHEAD = SLOTS - 2;
-  constexpr int LA = C::AI / 2, LB = C::BI / 2, LPP = LA + LB;
-  static_assert(C::AI % 2 == 0 && C::BI % 2 == 0 && C::NW == 4, "whole loads per slot");
+// The LDS of pipe_product: a ring of slots, each half the rows of either operand
+// for one K step, and their exponent bytes, where there are any (8 a row).
+template <class OP, class C, int PER_CU>
+struct Ring {
+  static constexpr int UA = C::BM / 2 * C::BK, CODES = UA + C::BN / 2 * C::BK;
+  static constexpr int SLOT = CODES + (OP::kScaled ? (C::BM + C::BN) / 2 * 8 : 0);
+  static constexpr int FIT = 160 * 1024 / PER_CU / SLOT, SLOTS = FIT < 5 ? FIT : 5;
+  static constexpr int kLds = SLOTS * SLOT;
   static_assert(SLOTS >= 3, "LDS");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[SLOTS * SLOT];
-  int tm, tn;
-  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
-  const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
-  const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
+};
+
+// The tile at (m0, n0), wave-uniform: before() is called ahead of the loop, out(acc,
+// what it gave, LDS) behind it, with the LDS (the ring's kLds) free.
+template <class OP, class C, int PER_CU, class BEFORE, class OUT>
+__device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
+                                             const uint8_t* __restrict__ B, int M, int N, int K,
+                                             int m0, int n0, const Exponents& ex, BEFORE&& before,
+                                             OUT&& out) {
+  using R = Ring<OP, C, PER_CU>;
+  typedef typename OP::Frag Frag;
+  // (declared here: through a pointer the compiler keeps an address per fragment, and
+  // spills)
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[R::kLds];
+  constexpr int BK = C::BK, BLK = OP::kBlock, MB = C::WTM / BLK, NB = C::WTN / BLK;
+  constexpr int HM = MB / 2, HN = NB / 2, H = OP::kProducts;
+  static_assert(MB % 2 == 0 && NB % 2 == 0, "quarters");
+  constexpr int UA = R::UA, SLOT = R::SLOT, SLOTS = R::SLOTS, AHEAD = SLOTS - 2;
+  constexpr int LA = C::AI / 2, LB = C::BI / 2, LPP = LA + LB + OP::kScaled;
+  // exponents of a slot: a lane loads those of two rows, ELA of a wave's lanes A's
+  constexpr int ELA = C::BM / 16, ELB = C::BN / 16, EWAVE = (ELA + ELB) * 16;
+  static_assert(C::AI % 2 == 0 && C::BI % 2 == 0 && C::NW == 4, "whole loads per slot");
+  static_assert(!OP::kScaled || (ELA + ELB <= 64 && BLK % (C::BM / 8) == 0 &&
+                                 BLK % (C::BN / 8) == 0),
+                "a fragment's rows begin with a wave's rows of exponents");
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = w / C::WGN, wn = w % C::WGN;
   const int nk = K / BK, rem = K % BK, all = nk + (rem > 0), last = 2 * all - 1;
 
-  v4f acc[MB][NB];
+  typename OP::Acc acc[MB][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < NB; ++j) acc[i][j] = typename OP::Acc{};
 
   // direct loads: the tile's first row as a scalar address, a lane's row (clamped
   // into the matrix) and swizzled chunk as its offset.  Half h of an operand is
@@ -143,6 +191,21 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
       vB[h][j] = (uint32_t)min(row, N - 1 - n0) * (uint32_t)K + (lslot ^ gemm::dma::swz(r)) * 16;
     }
   }
+  // exponents: the lane's two rows of half h, and a K step's stride
+  const uint8_t* pE = nullptr;
+  uint32_t vE[2];
+  int64_t estep = 0;
+  const bool e_of_a = lane < ELA;
+  if constexpr (OP::kScaled) {
+    const int r = e_of_a ? (w * ELA + lane) * 2 : (w * ELB + min(lane - ELA, ELB - 1)) * 2;
+    const int half = e_of_a ? C::WTM / 2 : C::WTN / 2, rows = e_of_a ? ex.rows_a : ex.rows_b;
+    pE = e_of_a ? ex.a : ex.b;
+    estep = (int64_t)rows * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)                             // rows are multiples of 16
+      vE[h] = (uint32_t)min((e_of_a ? m0 : n0) + (r / half * 2 + h) * half + r % half, rows - 2);
+  }
+  const uint32_t ldsE = lds_offset(smem) + R::CODES + w * EWAVE;
   const uint32_t ldsA = lds_offset(smem) + w * LA * 1024;
   const uint32_t ldsB = lds_offset(smem) + UA + w * LB * 1024;
   // load J of the wave's LPP: half HA of A's and half HB of B's rows, whole step kt
@@ -151,9 +214,14 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
     if constexpr (J < LA)
       load16_to_lds_at(tA + (int64_t)kt * BK, vA[decltype(ha)::value][J],
                        ldsA + slot * SLOT + J * 1024);
-    else if constexpr (J < LPP)
+    else if constexpr (J < LA + LB)
       load16_to_lds_at(tB + (int64_t)kt * BK, vB[decltype(hb)::value][J - LA],
                        ldsB + slot * SLOT + (J - LA) * 1024);
+    else if constexpr (J < LPP)
+      if (lane < ELA + ELB)
+        load16_to_lds(pE + ((int64_t)(e_of_a ? vE[decltype(ha)::value] : vE[decltype(hb)::value]) * 8 +
+                            kt * estep),
+                      ldsE + slot * SLOT);
   };
   // all of them, for any step; chunks past K load the row's last chunk
   auto fetch = [&](auto ha, auto hb, int kt, int slot) FALQ_INLINE {
@@ -168,17 +236,19 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
         const int co = (lslot ^ gemm::dma::swz((w * LA + J) * 8 + lrow)) * 16;
         load16_to_lds_at(tA + (int64_t)nk * BK, vA[decltype(ha)::value][J] - co + min(co, rem - 16),
                          ldsA + slot * SLOT + J * 1024);
-      } else {
+      } else if constexpr (J < LA + LB) {
         const int co = (lslot ^ gemm::dma::swz((w * LB + J - LA) * 8 + lrow)) * 16;
         load16_to_lds_at(tB + (int64_t)nk * BK,
                          vB[decltype(hb)::value][J - LA] - co + min(co, rem - 16),
                          ldsB + slot * SLOT + (J - LA) * 1024);
+      } else {
+        load(ha, hb, j, nk, slot);
       }
     });
   };
   // chunks past K of a slot of the step of rem bytes, once it has landed
   auto clear = [&](int slot) {
-    for (int i = threadIdx.x; i < SLOT / 16; i += C::kThreads) {
+    for (int i = threadIdx.x; i < R::CODES / 16; i += C::kThreads) {
       const int row = i >> 3, c = i & 7;                     // UA is a multiple of 16 rows
       if (c >= rem / 16)
         *reinterpret_cast<uint4*>(smem + slot * SLOT + row * BK +
@@ -187,19 +257,44 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
     __syncthreads();
   };
 
-  const int r16 = lane & 15, g = lane >> 4, sw = gemm::dma::swz(r16);
-  const int o0 = ((2 * g) ^ sw) * 16, o1 = ((2 * g + 1) ^ sw) * 16;
-  const int offA = (wm * (C::WTM / 2) + r16) * BK, offB = UA + (wn * (C::WTN / 2) + r16) * BK;
-  auto frag = [&](int at) FALQ_INLINE {
-    return gemm::join(*reinterpret_cast<const uint4*>(smem + at + o0),
-                      *reinterpret_cast<const uint4*>(smem + at + o1));
+  const int r = lane % BLK, g = lane / BLK;
+  // the chunks of the lane's row, swizzled by the row's place among 16
+  int o[OP::kParts];
+#pragma unroll
+  for (int p = 0; p < OP::kParts; ++p) o[p] = (OP::chunk(g, p) ^ gemm::dma::swz(r & 15)) * 16;
+  const int offA = (wm * (C::WTM / 2) + r) * BK, offB = UA + (wn * (C::WTN / 2) + r) * BK;
+  // the lane's exponents of fragment 0 of A and of B in a slot: EWAVE bytes for each
+  // BM / 8 rows of A and BN / 8 of B, A's ahead
+  constexpr int EA = C::BM / 8, EB = C::BN / 8, EPL = 8 * BLK / 64;
+  const int rA = wm * (C::WTM / 2) + r, rB = wn * (C::WTN / 2) + r;
+  const int eA = R::CODES + rA / EA * EWAVE + rA % EA * 8 + EPL * g;
+  const int eB = R::CODES + rB / EB * EWAVE + ELA * 16 + rB % EB * 8 + EPL * g;
+  // fragment I of a half of A, of B, of the slot that begins at byte `at`
+  auto frag_at = [&](int codes, int exps) FALQ_INLINE {
+    int e = 0;
+    if constexpr (OP::kScaled)
+      e = (int)*reinterpret_cast<const typename OP::Scales*>(smem + exps);
+    uint4 q[OP::kParts];
+#pragma unroll
+    for (int p = 0; p < OP::kParts; ++p) q[p] = *reinterpret_cast<const uint4*>(smem + codes + o[p]);
+    return OP::make(q, e);
   };
-  // with every second product a fragment of the group f at `at`
-  auto read = [&](auto t, auto& f, int at) FALQ_INLINE {
-    constexpr int T = decltype(t)::value, I = T / 2;
-    if constexpr (T % 2 == 0 && I < sizeof(f) / sizeof(f[0])) f[I] = frag(at + I * 16 * BK);
+  auto fragA = [&](auto i, int at) FALQ_INLINE {
+    constexpr int I = decltype(i)::value * BLK;
+    return frag_at(at + offA + I * BK, at + eA + I / EA * EWAVE);
   };
-  v8i a0[HM], a1[HM], b0[HN], b1[HN];
+  auto fragB = [&](auto i, int at) FALQ_INLINE {
+    constexpr int I = decltype(i)::value * BLK;
+    return frag_at(at + offB + I * BK, at + eB + I / EB * EWAVE);
+  };
+  // with every second product a fragment of the group f (of 32 rows: every eighth)
+  constexpr int EVERY = OP::kBlock == 16 ? 2 : HM * HN * H >= 16 ? 8 : 4;
+  auto read = [&](auto t, auto& f, auto&& of, int at) FALQ_INLINE {
+    constexpr int T = decltype(t)::value, I = T / EVERY, N = sizeof(f) / sizeof(f[0]);
+    static_assert(T > 0 || (N - 1) * EVERY < HM * HN * H, "all within the quarter");
+    if constexpr (T % EVERY == 0 && I < N) f[I] = of(std::integral_constant<int, I>{}, at);
+  };
+  Frag a0[HM], a1[HM], b0[HN], b1[HN];
   auto next = [](int slot) { return slot == SLOTS - 1 ? 0 : slot + 1; };
   // pair n, whose AHEAD successors are under way, is in its slot, and all waves are
   // done with pair n - 1
@@ -219,10 +314,10 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
   auto step = [&](auto par, auto whole, int k, int& slot) FALQ_INLINE {
     constexpr bool P = decltype(par)::value, WHOLE = decltype(whole)::value;
     constexpr int jf = P ? HN : 0, jo = HN - jf;
-    v8i(&f)[HN] = P ? b1 : b0;
-    v8i(&o)[HN] = P ? b0 : b1;
+    Frag(&f)[HN] = P ? b1 : b0;
+    Frag(&other)[HN] = P ? b0 : b1;
     // the pairs that take the slots freed: SLOTS - 1 on from those read
-    constexpr int D1 = SLOTS / 2, D2 = (SLOTS + 1) / 2, U = 2 * HM * HN / LPP;
+    constexpr int D1 = SLOTS / 2, D2 = (SLOTS + 1) / 2, U = 2 * HM * HN * H / LPP;
     using HA1 = std::integral_constant<int, SLOTS % 2>;
     using HA2 = std::integral_constant<int, (SLOTS + 1) % 2>;
     using HB1 = std::integral_constant<int, (P + D1 + SLOTS) % 2>;
@@ -234,16 +329,16 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
         load(ha, hb, std::integral_constant<int, T / U>{}, kt, to);
     };
     using T0 = std::integral_constant<int, 0>;
-    using T1 = std::integral_constant<int, HM * HN>;
+    using T1 = std::integral_constant<int, HM * HN * H>;
     arrive(whole, 2 * k + 1, slot, k);
     int at = slot * SLOT, to = slot == 0 ? SLOTS - 1 : slot - 1;
     if constexpr (!WHOLE) fetch(HA1{}, HB1{}, k + D1, to);
-    quarter<0, jf>(acc, a0, f, [&](auto t) FALQ_INLINE {
-      read(t, o, at + offB);
+    quarter<OP, 0, jf>(acc, a0, f, [&](auto t) FALQ_INLINE {
+      read(t, other, fragB, at);
       send(t, T0{}, HA1{}, HB1{}, k + D1, to);
     });
-    quarter<0, jo>(acc, a0, o, [&](auto t) FALQ_INLINE {
-      read(t, a1, at + offA);
+    quarter<OP, 0, jo>(acc, a0, other, [&](auto t) FALQ_INLINE {
+      read(t, a1, fragA, at);
       send(t, T1{}, HA1{}, HB1{}, k + D1, to);
     });
     to = slot;
@@ -251,12 +346,12 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
     at = slot * SLOT;
     arrive(whole, 2 * k + 2, slot, k + 1);
     if constexpr (!WHOLE) fetch(HA2{}, HB2{}, k + D2, to);
-    quarter<HM, jo>(acc, a1, o, [&](auto t) FALQ_INLINE {
-      read(t, a0, at + offA);
+    quarter<OP, HM, jo>(acc, a1, other, [&](auto t) FALQ_INLINE {
+      read(t, a0, fragA, at);
       send(t, T0{}, HA2{}, HB2{}, k + D2, to);
     });
-    quarter<HM, jf>(acc, a1, f, [&](auto t) FALQ_INLINE {
-      read(t, o, at + offB);
+    quarter<OP, HM, jf>(acc, a1, f, [&](auto t) FALQ_INLINE {
+      read(t, other, fragB, at);
       send(t, T1{}, HA2{}, HB2{}, k + D2, to);
     });
     slot = next(slot);
@@ -272,12 +367,10 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
     wait_stages<SLOTS - 1, LPP>(last);
     barrier_no_drain();
     if (nk == 0) clear(0);
-#pragma unroll
-    for (int i = 0; i < HM; ++i) a0[i] = frag(offA + i * 16 * BK);
-#pragma unroll
-    for (int j = 0; j < HN; ++j) b0[j] = frag(offB + j * 16 * BK);
+    each<HM>([&](auto i) FALQ_INLINE { a0[decltype(i)::value] = fragA(i, 0); });
+    each<HN>([&](auto j) FALQ_INLINE { b0[decltype(j)::value] = fragB(j, 0); });
   }
-  const float scale = 1.0f / (ep.sa[0] * ep.sb[0]);
+  const auto kept = before();
   __builtin_amdgcn_s_waitcnt(0xC07F);                        // lgkmcnt(0)
   int k = 0, slot = 1;
   for (; k + 1 + (SLOTS + 1) / 2 < nk; k += 2) {
@@ -293,7 +386,23 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
   }
   settle(acc);
   __syncthreads();                                           // the slots are free
-  tile_out<C, SLOTS * SLOT, OT, STREAM, false>(smem, acc, m0, n0, M, N, scale, ep, nullptr, 0);
+  out(acc, kept, smem);
+}
+
+template <class OP, class C, int PER_CU, class OT, bool STREAM>
+__global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
+    int tilesN, Epilogue ep, Exponents ex) {
+  int tm, tn;
+  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
+  const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
+  const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
+  pipe_product<OP, C, PER_CU>(
+      A, B, M, N, K, m0, n0, ex, [&] { return scale_of<OP>(ep); },
+      [&](const auto& acc, float scale, uint8_t* smem) {
+        tile_out<C, Ring<OP, C, PER_CU>::kLds, OT, STREAM, false>(smem, acc, m0, n0, M, N, scale,
+                                                                  ep, nullptr, 0);
+      });
 }
 
 }  // namespace

@@ -40,15 +40,71 @@ __device__ __forceinline__ void wait_stages(int ahead) {
   }
 }
 
-// The epilogue of a wave's accumulators, through its part of the LDS.
-template <class C, int LDS, class OT, bool STREAM, bool SPLIT>
-__device__ __forceinline__ void tile_out(uint8_t* smem, const v4f (&acc)[C::MB][C::NB], int m0,
-                                         int n0, int M, int N, float scale, const Epilogue& ep,
-                                         float* __restrict__ part, int sp) {
-  constexpr int NB = C::NB, PASS = C::pass_of(C::WTM, LDS);
-  static_assert(PASS % 16 == 0 && C::WTM % PASS == 0, "whole blocks per pass");
+// A wave's accumulators of rows first .. first + PASS - 1 into its part of the LDS,
+// four columns of a row at slot(row, column / 4).  A lane holds of a block row
+// lane % BLK, and columns 4 g .. 4 g + 3 (g = lane / 16) of 16, or 8 q + 4 g .. + 3
+// (g = lane / 32) of 32.
+template <int PASS, int MB, int NB, class ACC, class SLOT>
+__device__ __forceinline__ void put_rows(v4f* mine, const ACC (&acc)[MB][NB], int pass,
+                                         SLOT&& slot) {
+  constexpr int Q = sizeof(ACC) / 16, BLK = Q == 1 ? 16 : 32;
+  const int lane = threadIdx.x & 63, r = lane % BLK, g = lane / BLK;
+#pragma unroll
+  for (int i = 0; i < PASS / BLK; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const ACC& c = acc[pass * (PASS / BLK) + i][j];
+      if constexpr (Q == 1) {
+        mine[slot(i * BLK + r, 4 * j + g)] = c;
+      } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          mine[slot(i * BLK + r, 8 * j + 2 * q + g)] =
+              v4f{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+      }
+    }
+}
+
+// A wave's accumulators through its part of the LDS: each(row, column, eight columns'
+// values) for eight columns of a row at a time, the columns below N.
+template <class C, int LDS, int MB, int NB, class ACC, class EACH>
+__device__ __forceinline__ void rows_through_lds(uint8_t* smem, const ACC (&acc)[MB][NB], int m0,
+                                                 int n0, int M, int N, EACH&& each) {
+  constexpr int PASS = C::pass_of(C::WTM, LDS);
+  static_assert(PASS % (C::WTM / MB) == 0 && C::WTM % PASS == 0, "whole blocks per pass");
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wm = w / C::WGN, wn = w % C::WGN;
-  const int r16 = lane & 15, g = lane >> 4;
+  constexpr int CH = C::WTN / 4, LPR = C::WTN / 8, RPI = 64 / LPR;
+  constexpr int SWZ = (CH & (CH - 1)) == 0 ? CH - 1 : 0;     // as tile_out
+  auto slot = [](int r, int c) { return r * CH + (c ^ (r & SWZ)); };
+  v4f* mine = reinterpret_cast<v4f*>(smem + w * (LDS / C::NW / 16 * 16));
+  const int cl = lane % LPR, rl = lane / LPR;
+  const int col = n0 + wn * C::WTN + cl * 8;
+  const bool col_ok = rl < RPI && col < N;                   // N is a multiple of 8
+#pragma unroll
+  for (int p = 0; p < C::WTM / PASS; ++p) {
+    // the wave's own LDS: its accesses are executed in order
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    put_rows<PASS>(mine, acc, p, slot);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    for (int r = rl; r < PASS; r += RPI) {
+      const int row = m0 + wm * C::WTM + p * PASS + r;
+      const v4f a = mine[slot(r, 2 * cl)];
+      const v4f b = mine[slot(r, 2 * cl + 1)];
+      if (!col_ok || row >= M) continue;
+      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      each(row, col, v);
+    }
+  }
+}
+
+// The epilogue of a wave's accumulators, through its part of the LDS.
+template <class C, int LDS, class OT, bool STREAM, bool SPLIT, int MB, int NB, class ACC>
+__device__ __forceinline__ void tile_out(uint8_t* smem, const ACC (&acc)[MB][NB], int m0, int n0,
+                                         int M, int N, float scale, const Epilogue& ep,
+                                         float* __restrict__ part, int sp) {
+  constexpr int PASS = C::pass_of(C::WTM, LDS);
+  static_assert(PASS % (C::WTM / MB) == 0 && C::WTM % PASS == 0, "whole blocks per pass");
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wm = w / C::WGN, wn = w % C::WGN;
   constexpr int CH = C::WTN / 4, LPR = C::WTN / 8, RPI = 64 / LPR;
   // 16-byte chunk c of row r: swizzled where the rows' stride is a power of two
   // (else the stride itself spreads the rows over the banks)
@@ -79,11 +135,7 @@ __device__ __forceinline__ void tile_out(uint8_t* smem, const v4f (&acc)[C::MB][
   for (int p = 0; p < C::WTM / PASS; ++p) {
     // the wave's own LDS: its accesses are executed in order
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < PASS / 16; ++i)
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        mine[slot(i * 16 + r16, 4 * j + g)] = acc[p * (PASS / 16) + i][j];
+    put_rows<PASS>(mine, acc, p, slot);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int first = p * PASS;
     switch (SPLIT ? (int)kNone : ep.act) {
@@ -96,24 +148,27 @@ __device__ __forceinline__ void tile_out(uint8_t* smem, const v4f (&acc)[C::MB][
   }
 }
 
-// STREAM: the outputs go past the caches (kStreamOut in linear_act.hip).
-// SPLIT (few tiles, long K): workgroup b takes tile b % tiles and the kc K steps
-// of split b / tiles, and writes its sums, unscaled, to that split's plane of
-// `part` ([M x N] floats each); linear_act_join adds the planes in order.
-template <class C, class OT, bool STREAM, bool SPLIT = false>
-__global__ __launch_bounds__(C::kThreads) void linear_act_tile(
-    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
-    int tilesN, Epilogue ep, float* __restrict__ part = nullptr, int kc = 0) {
+// LDS of tile_product: the stages, then their exponent bytes, where there are any.
+template <class OP, class C>
+constexpr int kTileLds = C::S * (C::STAGE + (OP::kScaled ? (C::BM + C::BN) * 8 : 0));
+
+// The tile at (m0, n0) over K steps k_lo .. steps - 1 (of all that K has): before()
+// is called ahead of the loop, out(acc, what it gave, LDS) behind it, with the LDS
+// (kTileLds) free.
+template <class OP, class C, class BEFORE, class OUT>
+__device__ __forceinline__ void tile_product(const uint8_t* __restrict__ A,
+                                             const uint8_t* __restrict__ B, int M, int N, int K,
+                                             int m0, int n0, int k_lo, int k_end,
+                                             const Exponents& ex, BEFORE&& before, OUT&& out) {
   constexpr int BK = C::BK, MB = C::MB, NB = C::NB;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::S * C::STAGE];
-  int tm, tn;
-  const int nt = tilesM * tilesN, sp = SPLIT ? (int)blockIdx.x / nt : 0;
-  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x - sp * nt, nt), tilesM, tilesN, tm, tn);
-  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  // exponent bytes of a stage: 8 a row, a lane loads those of two rows
+  constexpr int EROWS = C::BM + C::BN, ELANES = EROWS / 2 / C::NW, LPS = C::LPS + OP::kScaled;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kTileLds<OP, C>];
+  static_assert(!OP::kScaled || (ELANES * 2 * C::NW == EROWS && ELANES <= 64), "whole rows");
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w / C::WGN, wn = w % C::WGN;
   // the step at nk, if any, is the one of rem bytes
   const int nk = K / BK, rem = K % BK, all = nk + (rem > 0);
-  const int k_lo = SPLIT ? sp * kc : 0, steps = SPLIT ? min(all, k_lo + kc) : all;
+  const int steps = min(all, k_end);
 
   v4f acc[MB][NB];
 #pragma unroll
@@ -138,6 +193,22 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
     const int row = (w * C::BI + j) * 8 + lrow;
     gB[j] = B + (int64_t)min(n0 + row, N - 1) * K + ((lslot ^ gemm::dma::swz(row)) * 16);
   }
+  const uint8_t* gE = nullptr;
+  int64_t estep = 0;
+  if constexpr (OP::kScaled) {
+    const int r = (w * ELANES + min(lane, ELANES - 1)) * 2;  // of A's rows, then B's
+    const bool of_a = r < C::BM;
+    const int rows = of_a ? ex.rows_a : ex.rows_b;           // multiples of 16
+    gE = (of_a ? ex.a : ex.b) + (int64_t)min(of_a ? m0 + r : n0 + r - C::BM, rows - 2) * 8;
+    estep = (int64_t)rows * 8;
+  }
+  auto issue_exponents = [&](int stage, int kt) {
+    if constexpr (OP::kScaled)
+      if (lane < ELANES)
+        load16_to_lds(gE + kt * estep,
+                      __builtin_amdgcn_readfirstlane(lds_offset(smem) + C::S * C::STAGE +
+                                                     (stage * EROWS + w * ELANES * 2) * 8));
+  };
   auto issue = [&](int stage, int k0) {
     const uint32_t base = lds_offset(smem + stage * C::STAGE);
     const uint32_t la = __builtin_amdgcn_readfirstlane(base + w * C::AI * 1024);
@@ -169,6 +240,7 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
       issue(stage, kt * BK);
     else
       issue_rem(stage);
+    issue_exponents(stage, kt);
   };
 #pragma unroll
   for (int s = 0; s < C::S - 1; ++s)
@@ -176,32 +248,37 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
 
   const int r16 = lane & 15, g = lane >> 4;
   const int sw = gemm::dma::swz(r16);
-  const int o0 = ((2 * g) ^ sw) * 16, o1 = ((2 * g + 1) ^ sw) * 16;
+  const int o0 = (OP::chunk(g, 0) ^ sw) * 16, o1 = (OP::chunk(g, 1) ^ sw) * 16;
   const int offA = (wm * C::WTM + r16) * BK, offB = C::BM * BK + (wn * C::WTN + r16) * BK;
-  auto frag = [&](const uint8_t* p) {
-    return gemm::join(*reinterpret_cast<const uint4*>(p + o0),
-                      *reinterpret_cast<const uint4*>(p + o1));
+  // the fragment of the 16 rows from byte `at` of a stage on
+  auto frag = [&](int stage, int at) {
+    const uint8_t* p = smem + stage * C::STAGE + at;
+    int e = 0;
+    if constexpr (OP::kScaled)
+      e = *reinterpret_cast<const typename OP::Scales*>(smem + C::S * C::STAGE +
+                                                        stage * EROWS * 8 + at / BK * 8 + 2 * g);
+    const uint4 q[2] = {*reinterpret_cast<const uint4*>(p + o0),
+                        *reinterpret_cast<const uint4*>(p + o1)};
+    return OP::make(q, e);
   };
-  const float scale = 1.0f / (ep.sa[0] * ep.sb[0]);
+  const auto kept = before();
   // fragment reads in the order the MFMAs consume them; next(): the loads of
   // the following stage, sent once the first fragments are in registers
-  auto step = [&](const uint8_t* st, auto&& next) {
-    v8i bf[NB], af[2];
-    af[0] = frag(st + offA);
+  auto step = [&](int st, auto&& next) {
+    typename OP::Frag bf[NB], af[2];
+    af[0] = frag(st, offA);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      bf[j] = frag(st + offB + j * 16 * BK);
+      bf[j] = frag(st, offB + j * 16 * BK);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      if (i + 1 < MB) af[(i + 1) & 1] = frag(st + offA + (i + 1) * 16 * BK);
+      if (i + 1 < MB) af[(i + 1) & 1] = frag(st, offA + (i + 1) * 16 * BK);
       __builtin_amdgcn_sched_barrier(0);
       // D = B A^T per block: a lane ends with four columns of one row
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i & 1], acc[i][j],
-                                                                     0, 0, 0, 0, 0, 0);
+      for (int j = 0; j < NB; ++j) acc[i][j] = OP::mma(bf[j], af[i & 1], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
       if (i == 0) next();
       __builtin_amdgcn_sched_barrier(0);
@@ -210,9 +287,9 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
   __builtin_amdgcn_s_waitcnt(0xC07F);                        // lgkmcnt(0)
   const int k_whole = min(steps, nk);
   for (int kt = k_lo; kt < k_whole; ++kt) {
-    wait_stages<C::S - 2, C::LPS>(steps - 1 - kt);
+    wait_stages<C::S - 2, LPS>(steps - 1 - kt);
     barrier_no_drain();
-    step(smem + (kt - k_lo) % C::S * C::STAGE, [&] {
+    step((kt - k_lo) % C::S, [&] {
       if (kt + C::S - 1 < steps) fetch(kt + C::S - 1);
     });
   }
@@ -228,11 +305,31 @@ __global__ __launch_bounds__(C::kThreads) void linear_act_tile(
             make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
-    step(st, [] {});
+    step((nk - k_lo) % C::S, [] {});
   }
   __syncthreads();                                           // the stages are free
+  out(acc, kept, smem);
+}
 
-  tile_out<C, C::S * C::STAGE, OT, STREAM, SPLIT>(smem, acc, m0, n0, M, N, scale, ep, part, sp);
+// STREAM: the outputs go past the caches (kStreamOut in linear_act.hip).
+// SPLIT (few tiles, long K): workgroup b takes tile b % tiles and the kc K steps
+// of split b / tiles, and writes its sums, unscaled, to that split's plane of
+// `part` ([M x N] floats each); linear_act_join adds the planes in order.
+template <class OP, class C, class OT, bool STREAM, bool SPLIT = false>
+__global__ __launch_bounds__(C::kThreads) void linear_act_tile(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
+    int tilesN, Epilogue ep, Exponents ex, float* __restrict__ part = nullptr, int kc = 0) {
+  int tm, tn;
+  const int nt = tilesM * tilesN, sp = SPLIT ? (int)blockIdx.x / nt : 0;
+  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x - sp * nt, nt), tilesM, tilesN, tm, tn);
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  tile_product<OP, C>(
+      A, B, M, N, K, m0, n0, SPLIT ? sp * kc : 0, SPLIT ? sp * kc + kc : INT32_MAX, ex,
+      [&] { return scale_of<OP>(ep); },
+      [&](const v4f (&acc)[C::MB][C::NB], float scale, uint8_t* smem) {
+        tile_out<C, kTileLds<OP, C>, OT, STREAM, SPLIT>(smem, acc, m0, n0, M, N, scale, ep, part,
+                                                        sp);
+      });
 }
 
 // y (and z) from the S planes of partial sums
@@ -252,11 +349,11 @@ __device__ __forceinline__ void join8(const float* __restrict__ part, int S, int
   if (ep.bias) load_elems<8>(ep.bias + col, bias);
   finish8<ACT, OT, false>(v, scale, bias, ep, at);
 }
-template <class OT>
+template <class OP, class OT>
 __global__ __launch_bounds__(256) void linear_act_join(const float* __restrict__ part, int S,
                                                        int64_t M, int N, Epilogue ep) {
   const int64_t plane = M * N;
-  const float scale = 1.0f / (ep.sa[0] * ep.sb[0]);
+  const float scale = scale_of<OP>(ep);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < plane / 8;
        i += (int64_t)gridDim.x * 256) {
     const int64_t at = i * 8;

@@ -1,0 +1,90 @@
+// The product of FP4 operands with a power of two per block of 32 (mx.hpp):
+//   z = dec(Xq) dec(Wq)^T + bias,   y = act(z) + residual,
+// with the epilogue, the kernels and the rule of linear_act.hip; the matrix core
+// applies the blocks' scales itself (v_mfma_scale_f32_16x16x128_f8f6f4), whose bytes
+// ride along with the codes of a K step, eight for a row.
+#include "activation.hpp"
+#include "elem.hpp"
+#include "kernels.hpp"
+#include "linear_act_pipe.hpp"
+#include "linear_act_plan.hpp"
+#include "linear_act_tile.hpp"
+
+#include <algorithm>
+
+namespace falq {
+namespace {
+
+template <class C, int PIPE, class OT>
+hipError_t mx_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
+                    const Epilogue& ep, const Exponents& ex, hipStream_t s) {
+  const int tM = (int)((M + C::BM - 1) / C::BM), tN = (int)((N + C::BN - 1) / C::BN);
+  if constexpr (PIPE > 0)
+    linear_act_pipe<Fp4Wide, C, PIPE, OT, false><<<tM * tN, C::kThreads, 0, s>>>(
+        A, B, (int)M, (int)N, (int)K, tM, tN, ep, ex);
+  else
+    linear_act_tile<Fp4, C, OT, false><<<tM * tN, C::kThreads, 0, s>>>(
+        A, B, (int)M, (int)N, (int)K, tM, tN, ep, ex);
+  return hipGetLastError();
+}
+
+template <int MT, int NB, int NW, int U, class OT>
+hipError_t mx_few(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
+                  const Epilogue& ep, const Exponents& ex, hipStream_t s) {
+  linear_act_few<Fp4, MT, NB, NW, U, OT>
+      <<<(int)((N + NB * 16 - 1) / (NB * 16)), NW * 64, 0, s>>>(A, B, (int)M, (int)N, (int)K, ep,
+                                                                ex);
+  return hipGetLastError();
+}
+
+using T128 = Tile<128, 128, 2, 4, 3>;
+
+template <class OT>
+hipError_t mx_by_plan(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
+                      const Epilogue& ep, const Exponents& ex, float* part, hipStream_t s) {
+  const Plan p = plan_of(M, N, K);
+  if (p.few == 1) return mx_few<1, 1, kFewWaves[1], 1, OT>(A, B, M, N, K, ep, ex, s);
+  if (p.few == 2) return mx_few<2, 1, kFewWaves[2], 2, OT>(A, B, M, N, K, ep, ex, s);
+  if (p.split > 1) {
+    using C = T128;
+    const int tM = (int)((M + C::BM - 1) / C::BM), tN = (int)((N + C::BN - 1) / C::BN);
+    linear_act_tile<Fp4, C, OT, false, true><<<tM * tN * p.split, C::kThreads, 0, s>>>(
+        A, B, (int)M, (int)N, (int)K, tM, tN, ep, ex, part, p.kc);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int blocks = (int)std::min<int64_t>((M * N / 8 + 255) / 256, 2048);
+    linear_act_join<Fp4, OT><<<blocks, 256, 0, s>>>(part, p.split, M, (int)N, ep);
+    return hipGetLastError();
+  }
+  switch (p.kind) {
+    case k256x320:
+    case k256:
+    case k256x128:
+    case k128x256:
+    case k192x128: return mx_tiles<Tile<256, 256, 2, 2>, 1, OT>(A, B, M, N, K, ep, ex, s);
+    case k128x192w8:
+    case k128: return mx_tiles<Tile<128, 128, 2, 2>, 2, OT>(A, B, M, N, K, ep, ex, s);
+    case k128w8: return mx_tiles<T128, 0, OT>(A, B, M, N, K, ep, ex, s);
+    case k64: return mx_tiles<Tile<64, 64, 2, 2, 4>, 0, OT>(A, B, M, N, K, ep, ex, s);
+    default: return mx_tiles<Tile<32, 64, 1, 4, 4>, 0, OT>(A, B, M, N, K, ep, ex, s);
+  }
+}
+
+}  // namespace
+
+size_t mx_linear_ws_bytes(int64_t T, int64_t d_in, int64_t d_out) {
+  return linear_act_ws_bytes(T, d_in / 2, d_out);
+}
+
+hipError_t launch_mx_linear(const uint8_t* xq, const uint8_t* x_e, const uint8_t* wq,
+                            const uint8_t* w_e, const float* bias, const void* residual, int64_t T,
+                            int64_t d_in, int64_t d_out, int act, int dtype, void* y, void* z,
+                            void* ws, hipStream_t s) {
+  if (T == 0 || d_out == 0) return hipSuccess;
+  const Epilogue ep{nullptr, nullptr, bias, residual, y, z, act};
+  const Exponents ex{x_e, w_e, (int)mx_rows16(T), (int)mx_rows16(d_out)};
+  return dtype == 0 ? mx_by_plan<float>(xq, wq, T, d_out, d_in / 2, ep, ex, (float*)ws, s)
+                    : mx_by_plan<__bf16>(xq, wq, T, d_out, d_in / 2, ep, ex, (float*)ws, s);
+}
+
+}  // namespace falq

@@ -730,6 +730,124 @@ falq_status grad_clip(int64_t count, void *const *g, const int64_t *n, const int
                       float max_norm, float eps, void *const *out, float *norm, void *ws,
                       size_t ws_bytes, falq_stream stream);
 
+/*
+ * ---- Microscaled formats, 8-bit checkpoints, the loss ------------------------
+ * Blocks of 32 elements along a row with a power of two each, held as an E8M0 byte
+ * (exponent + 127; 255: NaN).  Conventions as in the part around the linear.
+ */
+
+/*
+ * mxfp4_quantize — FP4 E2M1 codes with a power of two for each block of 32 of a row,
+ * as the OCP microscaling specification has it:
+ *     e = floor(log2(amax)) - 2, amax the block's largest finite magnitude
+ *         (0 for a block without a non-zero one; at least -127),
+ *     q[i] = E2M1(x[i] 2^-e), nearest, ties to the even code, saturating at 6:
+ * the block's largest elements may saturate (those of 6 2^e to 8 2^e).  An infinity
+ * saturates, a NaN gives a zero.  mxfp4_dequantize — x[i] = dec(q[i]) 2^e, rounded
+ * once to x's type.
+ *
+ *   x   [rows x K] float32 or bfloat16; K a multiple of 32
+ *   q   [rows x K / 2] codes, two a byte (the lower index in the low half), 16-byte
+ *       aligned
+ *   e   exponent bytes, mxfp4_scale_bytes(rows, K) of them, 16-byte aligned, in the
+ *       order that the product reads: [steps x rows16 x 8], a step of 256 elements
+ *       having eight blocks, rows16 = rows rounded up to a multiple of 16; block b
+ *       of step s of row i at (s rows16 + i) 8 + 2 (b % 4) + b / 4.  Those of blocks
+ *       past K and of rows past the last are 127.
+ */
+size_t mxfp4_scale_bytes(int64_t rows, int64_t K);
+falq_status mxfp4_quantize(const void *x, int dtype, int64_t rows, int64_t K, uint8_t *q,
+                           uint8_t *e, falq_stream stream);
+falq_status mxfp4_dequantize(const uint8_t *q, const uint8_t *e, int64_t rows, int64_t K, void *x,
+                             int dtype, falq_stream stream);
+
+/*
+ * melded_linear_fwd_mxfp4 — melded_linear_fwd_act with such operands:
+ *     z = dec(xq) dec(wq)^T + bias,   y = act(z) + residual
+ * with the blocks' scales applied by the matrix core; sums in float32.
+ *
+ *   xq, x_e   T rows of d_in;  wq, w_e  d_out rows of d_in (the weight's codes are
+ *             mxfp4_quantize's of W, or of W^T for the product with the upstream
+ *             gradient); d_in a multiple of 32, d_out of 16
+ *   the rest  as melded_linear_fwd_act
+ */
+size_t melded_linear_fwd_mxfp4_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
+falq_status melded_linear_fwd_mxfp4(const uint8_t *xq, const uint8_t *x_e, const uint8_t *wq,
+                                    const uint8_t *w_e, const float *bias, int act,
+                                    const void *residual, int64_t T, int64_t d_in, int64_t d_out,
+                                    int dtype, void *y, void *z, void *ws, size_t ws_bytes,
+                                    falq_stream stream);
+
+/*
+ * checkpoint_save — an activation kept in 8 bits between forward and backward:
+ * E4M3 codes with a power of two for each block of 32 of a row,
+ *     e = the smallest with amax <= 448 2^e, amax the block's largest finite
+ *         magnitude (0 for a block without a non-zero one; at least -127),
+ *     q[i] = E4M3(x[i] 2^-e)
+ * (nearest, ties to even; infinities saturate at 448, a NaN stays one).
+ * checkpoint_restore — x[i] = dec(q[i]) 2^e, rounded once to x's type.
+ *
+ *   x   [T x d] float32 or bfloat16; 1 <= d <= 2^24
+ *   q   [T x d] codes;  e  [T x ceil(d / 32)] exponent bytes, any alignment
+ */
+falq_status checkpoint_save(const void *x, int dtype, int64_t T, int64_t d, uint8_t *q, uint8_t *e,
+                            falq_stream stream);
+falq_status checkpoint_restore(const uint8_t *q, const uint8_t *e, int64_t T, int64_t d, void *x,
+                               int dtype, falq_stream stream);
+
+/*
+ * linear_act_bwd_ckpt — linear_act_bwd with the z of a checkpoint; layer_norm_bwd_ckpt —
+ * layer_norm_bwd with the x of one (mean and rstd the forward's, of the x that was
+ * saved).  The restored values are not stored anywhere.
+ *
+ *   z_q, z_e; x_q, x_e   checkpoint_save's of [T x d_out], of [T x d]
+ *   ws                   linear_act_bwd_workspace_bytes(T, d_out),
+ *                        layer_norm_bwd_workspace_bytes(T, d)
+ *   the rest             as there; 1 <= d_out <= 2^24
+ */
+falq_status linear_act_bwd_ckpt(const void *dy, int dy_dtype, const uint8_t *z_q,
+                                const uint8_t *z_e, int act, int64_t T, int64_t d_out, void *dz,
+                                float *dbias, void *ws, size_t ws_bytes, falq_stream stream);
+falq_status layer_norm_bwd_ckpt(const void *dy, int dy_dtype, const uint8_t *x_q,
+                                const uint8_t *x_e, const float *weight, const float *mean,
+                                const float *rstd, int64_t T, int64_t d, void *dx, float *dweight,
+                                float *dbias, void *ws, size_t ws_bytes, falq_stream stream);
+
+/*
+ * linear_cross_entropy_fwd — the loss of T tokens over the V rows of an output layer,
+ * with the logits z = dec(xq) dec(wq)^T / (s_x s_w), which are not kept:
+ *     lse[t] = log(sum_v exp(z[t][v])),   loss[t] = lse[t] - z[t][target[t]].
+ * A token whose target is negative does not count: its loss is 0.  A target of V or
+ * more gives a NaN.
+ * linear_cross_entropy_bwd — the gradient in x of sum_t dloss[t] loss[t], the logits
+ * formed again a piece of the vocabulary at a time:
+ *     dx[t] = dloss[t] sum_v (exp(z[t][v] - lse[t]) - [v = target[t]]) dec(wq[v]) / s_w
+ * (0 for a token that does not count, NaN for a target of V or more).  The factors of
+ * dec(wq[v]) are rounded to float16, 2^-12 of each, before the sum over v, which is
+ * float32's.
+ *
+ *   xq, s_x   [T x d] E4M3 codes and their scale (fp8_quantize's, positive)
+ *   wq, s_w   [V x d] likewise: the output layer; d a multiple of 16, 16 to 2^22;
+ *             1 <= V <= 2^22
+ *   target    [T] int64, device
+ *   loss, lse [T] float32, device (output); lse may be NULL, and is the backward's
+ *             input
+ *   dloss     [T] float32, device: 1 / (tokens that count) for their mean
+ *   dx        [T x d] float32 or bfloat16 (output)
+ *   ws        the call's *_workspace_bytes
+ */
+size_t linear_cross_entropy_fwd_workspace_bytes(int64_t T, int64_t d, int64_t V);
+falq_status linear_cross_entropy_fwd(const uint8_t *xq, const float *s_x, const uint8_t *wq,
+                                     const float *s_w, const int64_t *target, int64_t T,
+                                     int64_t d, int64_t V, float *loss, float *lse, void *ws,
+                                     size_t ws_bytes, falq_stream stream);
+size_t linear_cross_entropy_bwd_workspace_bytes(int64_t T, int64_t d, int64_t V, int dx_dtype);
+falq_status linear_cross_entropy_bwd(const uint8_t *xq, const float *s_x, const uint8_t *wq,
+                                     const float *s_w, const int64_t *target, const float *lse,
+                                     const float *dloss, int64_t T, int64_t d, int64_t V,
+                                     void *dx, int dx_dtype, void *ws, size_t ws_bytes,
+                                     falq_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
