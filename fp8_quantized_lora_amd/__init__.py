@@ -1176,5 +1176,6 @@ def linear_cross_entropy_bwd(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tens
     _run(lib.linear_cross_entropy_bwd, "linear_cross_entropy_bwd", dev, *args, *_span(w), st)
 
 
-from .step import MeldedLinear, clip_gradients  # noqa: E402  (buffers + the call sequence)
-__all__ += ["MeldedLinear", "clip_gradients"]
+from .step import (LinearCrossEntropy, MeldedLinear,  # noqa: E402  (buffers + the call
+                   clip_gradients)                    # sequence)
+__all__ += ["MeldedLinear", "LinearCrossEntropy", "clip_gradients"]

@@ -10,17 +10,19 @@
 // accumulators, 8 bytes for 64 to 128 logits; a second launch joins them.  All of it
 // in float32 and base 2.
 //
-// Backward, a piece of the vocabulary after the other: the product again, whose
-// epilogue now leaves G = 2^15 (p - [v = target]) of the piece as float16; the piece's
+// Backward, a piece of the vocabulary after the other: the product again, as FP8's
+// (p is then off by some 2^-13 of itself), whose epilogue now leaves G = 2^15 (p - [v =
+// target]) of the piece as float16, the target's from its own logit, summed in float32,
+// as 2^15 expm1(z - lse): a sure token's gradient is a small difference; the piece's
 // rows of W as float16, transposed; and the product of the two, added onto dx.  G is
-// float16 because its 11 bits keep the gradient to 2^-12 of its terms (bfloat16: 2^-9),
+// float16 because its 11 bits keep the gradient to 2^-11 of its terms (bfloat16: 2^-8),
 // and 2^15 because p may be as small as 1 / V: under it float16 has its full precision
 // down to 2^-29 and absolute steps of 2^-39 below, while 1 still fits; E4M3 codes are
 // exact in it.  The row's factor dloss / s_w is applied at the end, in float32.
+#include "cross_entropy_plan.hpp"
 #include "elem.hpp"
 #include "kernels.hpp"
 #include "linear_act_pipe.hpp"
-#include "linear_act_plan.hpp"
 #include "linear_act_tile.hpp"
 
 #include <algorithm>
@@ -211,9 +213,40 @@ __global__ __launch_bounds__(256) void loss_join(const float2* __restrict__ part
 }
 
 // ---- backward -------------------------------------------------------------
+// at_target[row] = 2^15 (p - 1) of the row's target: a wave a row
+__global__ __launch_bounds__(256) void target_grads(const uint8_t* __restrict__ x,
+                                                    const uint8_t* __restrict__ w, int M, int d,
+                                                    int64_t V, const float* __restrict__ sx,
+                                                    const float* __restrict__ sw,
+                                                    const int64_t* __restrict__ target,
+                                                    const float* __restrict__ lse,
+                                                    float* __restrict__ at_target) {
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (row >= M) return;
+  const int64_t t = target[row];
+  if (t < 0 || t >= V) return;                               // not read
+  const uint8_t* a = x + (int64_t)row * d;
+  const uint8_t* b = w + t * d;
+  float sum = 0.0f;
+  for (int i = lane * 16; i < d; i += 1024) {
+    const uint4 p = *reinterpret_cast<const uint4*>(a + i);
+    const uint4 q = *reinterpret_cast<const uint4*>(b + i);
+    const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 u0 = dec2(u[j], false), u1 = dec2(u[j], true);
+      const float2 v0 = dec2(v[j], false), v1 = dec2(v[j], true);
+      sum = fmaf(u0.x, v0.x, fmaf(u0.y, v0.y, fmaf(u1.x, v1.x, fmaf(u1.y, v1.y, sum))));
+    }
+  }
+  sum = wave_sum_f32(sum);
+  if (lane == 0) at_target[row] = expm1f(sum / (sx[0] * sw[0]) - lse[row]) * kGradScale;
+}
+
 // G of a piece, [M x ldg] float16, columns past the vocabulary 0
 struct Grads {
   const float* lse;
+  const float* at_target;
   _Float16* G;
   int64_t ldg;
   int v0;              // the piece's first column
@@ -222,7 +255,7 @@ struct Grads {
 // the row's -lse in base 2, and its target's column in the piece; columns of a row
 // that is not counted are 0
 struct GradRow {
-  float neg;
+  float neg, at_target;
   int64_t t;
   bool counts;
   __device__ __forceinline__ GradRow(const Logits& lg, const Grads& gr, int row) {
@@ -230,11 +263,11 @@ struct GradRow {
     counts = t >= 0;
     t -= gr.v0;
     neg = -gr.lse[row] * kLog2e;
+    at_target = gr.at_target[row];
   }
   __device__ __forceinline__ float of(float acc, float k, int col, int V) const {
-    const float p = __builtin_amdgcn_exp2f(fmaf(acc, k, neg));
-    const float v = (p - (col == t ? 1.0f : 0.0f)) * kGradScale;
-    return counts && col < V ? v : 0.0f;
+    const float p = __builtin_amdgcn_exp2f(fmaf(acc, k, neg)) * kGradScale;
+    return !counts || col >= V ? 0.0f : col == t ? at_target : p;
   }
 };
 
@@ -426,80 +459,6 @@ using T128 = Tile<128, 128, 2, 4, 3>;
 using T64 = Tile<64, 64, 2, 2, 4>;
 using T32 = Tile<32, 64, 1, 4, 4>;
 
-constexpr int kFew = 16, kFewNW = 16;
-constexpr TileKind kLossKinds[] = {k256, k128, k64, k32x64};
-constexpr TileKind kGradKinds[] = {k256x128, k128, k64, k32x64};
-constexpr TileKind kDxKinds[] = {k256, k256x128, k128, k64, k32x64};
-
-template <int N>
-TileKind cheapest(const TileKind (&kinds)[N], int64_t M, int64_t n, int64_t K) {
-  TileKind best = kinds[N - 1];
-  float cost = HUGE_VALF;
-  for (const TileKind k : kinds) {
-    if (K > kFarK && k != k64 && k != k32x64) continue;
-    const float c = tile_cost(k, M, n, K);
-    if (c < cost) {
-      cost = c;
-      best = k;
-    }
-  }
-  return best;
-}
-
-int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t up(int64_t a, int64_t b) { return ceil_div64(a, b) * b; }
-
-// Rows are taken in strips, so that no workspace grows with T beyond a strip's.
-constexpr int64_t kStrip = 16384;
-int64_t strip_of(int64_t T) { return std::min(T, kStrip); }
-
-// runs of columns of the forward's partial sums
-int64_t runs_of(int64_t T, int64_t d, int64_t V) {
-  if (T <= kFew) return ceil_div64(V, 16);
-  switch (cheapest(kLossKinds, T, V, 2 * d)) {
-    case k256: return ceil_div64(V, 256) * P256::WGN;
-    case k128: return ceil_div64(V, 128) * P128::WGN;
-    case k64: return ceil_div64(V, 64) * T64::WGN;
-    default: return ceil_div64(V, 64) * T32::WGN;
-  }
-}
-
-// pieces of the vocabulary: as many as keep G and the turned weight within kPiece
-// bytes each, of one width, a multiple of 64
-constexpr int64_t kPiece = (int64_t)128 << 20;
-int64_t piece_width(int64_t T, int64_t d, int64_t V) {
-  const int64_t most = std::clamp<int64_t>(kPiece / (2 * std::max(T, d)), 2048, 1 << 21);
-  return up(ceil_div64(V, ceil_div64(V, most)), 64);
-}
-
-// splits of the product with G over the piece: where its tiles leave CUs without work
-int dx_splits(int64_t T, int64_t d, int64_t width, int& kc) {
-  const int64_t nt = tiles_of(k128w8, T, d), steps = ceil_div64(width * 2, 128);
-  const int64_t s = std::min<int64_t>(kCUs / nt, steps / 8);
-  kc = 0;
-  if (s < 2) return 1;
-  kc = (int)ceil_div64(steps, s);
-  return (int)ceil_div64(steps, kc);
-}
-
-struct BwdPlan {
-  int64_t width;
-  int splits, kc;
-  size_t g, w, sums, part;                                   // bytes, multiples of 256
-  size_t bytes() const { return g + w + sums + part; }
-};
-BwdPlan bwd_plan(int64_t T, int64_t d, int64_t V, int dx_type) {
-  BwdPlan p;
-  p.width = piece_width(T, d, V);
-  p.splits = dx_splits(T, d, p.width, p.kc);
-  p.g = (size_t)up(T * p.width * 2, 256);
-  p.w = (size_t)up(d * p.width * 2, 256);
-  // float32 gradients collect in place
-  p.sums = dx_type != 0 && p.width < V ? (size_t)up(T * d * 4, 256) : 0;
-  p.part = p.splits > 1 ? (size_t)up(p.splits * T * d * 4, 256) : 0;
-  return p;
-}
-
 template <class C, int PIPE>
 void launch_logits_fwd(const uint8_t* x, const uint8_t* w, int64_t T, int64_t d, int64_t V,
                        const Logits& lg, const Stats& st, hipStream_t s) {
@@ -587,10 +546,10 @@ hipError_t launch_cross_entropy_fwd(const uint8_t* xq, const float* s_x, const u
       loss_few<kFewNW><<<(int)ceil_div64(V, 16), kFewNW * 64, 0, s>>>(x, wq, (int)n, (int)V, (int)d,
                                                                       lg, st);
     } else {
-      switch (cheapest(kLossKinds, n, V, 2 * d)) {
-        case k256: launch_logits_fwd<P256, 1>(x, wq, n, d, V, lg, st, s); break;
-        case k128: launch_logits_fwd<P128, 2>(x, wq, n, d, V, lg, st, s); break;
-        case k64: launch_logits_fwd<T64, 0>(x, wq, n, d, V, lg, st, s); break;
+      switch (loss_kind(n, V, d)) {
+        case kLoss256: launch_logits_fwd<P256, 1>(x, wq, n, d, V, lg, st, s); break;
+        case kLoss128: launch_logits_fwd<P128, 2>(x, wq, n, d, V, lg, st, s); break;
+        case kLoss64: launch_logits_fwd<T64, 0>(x, wq, n, d, V, lg, st, s); break;
         default: launch_logits_fwd<T32, 0>(x, wq, n, d, V, lg, st, s); break;
       }
     }
@@ -598,12 +557,19 @@ hipError_t launch_cross_entropy_fwd(const uint8_t* xq, const float* s_x, const u
     if (e != hipSuccess) return e;
     const int P = (int)runs_of(n, d, V);
     float* const out = lse ? lse + r0 : nullptr;
-    if (n <= kFew)
-      loss_join<1><<<(int)n, 256, 0, s>>>(st.part, P, (int)n, V, lg.target, st.at_target,
-                                          loss + r0, out);
+    // few rows a workgroup, so that there are workgroups for all CUs, but 16 where there
+    // are: 8-byte partials of adjacent rows are one line
+    const auto join = [&](auto rows) {
+      constexpr int R = decltype(rows)::value;
+      loss_join<R><<<(int)ceil_div64(n, R), 256, 0, s>>>(st.part, P, (int)n, V, lg.target,
+                                                         st.at_target, loss + r0, out);
+    };
+    if (n < 4 * kCUs)
+      join(std::integral_constant<int, 1>{});
+    else if (n < 16 * kCUs)
+      join(std::integral_constant<int, 4>{});
     else
-      loss_join<16><<<(int)ceil_div64(n, 16), 256, 0, s>>>(st.part, P, (int)n, V, lg.target,
-                                                           st.at_target, loss + r0, out);
+      join(std::integral_constant<int, 16>{});
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -631,10 +597,15 @@ hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const u
     void* const to = (uint8_t*)dx + r0 * d * (dx_type == 0 ? 4 : 2);
     float* const sums = dx_type == 0 ? (float*)to : (float*)(wt + p.w);
     float* const part = (float*)(wt + p.w + p.sums);
+    float* const at_target = (float*)(wt + p.w + p.sums + p.part);
+    target_grads<<<(unsigned)ceil_div64(n, 4), 256, 0, s>>>(x, wq, (int)n, (int)d, V, s_x, s_w,
+                                                            lg.target, lse + r0, at_target);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     for (int64_t v0 = 0; v0 < V; v0 += p.width) {
       const int64_t cols = std::min(p.width, V - v0), ld = up(cols, 64);
       const uint8_t* w = wq + v0 * d;
-      const Grads gr{lse + r0, (_Float16*)g, ld, (int)v0};
+      const Grads gr{lse + r0, at_target, (_Float16*)g, ld, (int)v0};
       if (n <= kFew) {
         grads_few<kFewNW><<<(int)(ld / 16), kFewNW * 64, 0, s>>>(x, w, (int)n, (int)cols, (int)d,
                                                                  lg, gr);
@@ -646,7 +617,7 @@ hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const u
           default: launch_logits_bwd<T32, 0>(x, w, n, d, cols, lg, gr, s); break;
         }
       }
-      hipError_t e = hipGetLastError();
+      e = hipGetLastError();
       if (e != hipSuccess) return e;
       weight_turn<<<dim3((unsigned)(ld / 64), (unsigned)ceil_div64(d, 128)), 256, 0, s>>>(
           w, (int)cols, (int)d, (_Float16*)wt, ld);

@@ -1,0 +1,121 @@
+// How the cross entropy over the vocabulary and its gradient run (cross_entropy.hip).
+// Host code only.
+#pragma once
+
+#include "linear_act_plan.hpp"
+
+#include <cstddef>
+
+namespace falq {
+namespace {
+
+// up to kFew tokens one kernel of 16 waves a workgroup streams the weight
+constexpr int kFew = 16, kFewNW = 16;
+
+// The forward's tiles, by the model of linear_act_plan.hpp with its own costs: the
+// products as float16 take twice the steps' time, and there is nothing to store.
+//   4096 x 32000 x 4096: 747 us in 256 x 256, 827 in 128 x 128
+//   4096 x 50000 x 1024: 386 and 365; 333 x 131071 x 1040 174 and 109
+//   128 x 32000 x 4096: 35 in 128 x 128, 50 in 64 x 64; 64 tokens 34 and 26
+//   17 x 32000 x 4096: 26 in 64 x 64, 23 in 32 x 64
+enum LossKind { kLoss256, kLoss128, kLoss64, kLoss32x64, kLossKinds };
+constexpr TileCost kLossTile[kLossKinds] = {
+    {256, 256, 1, 5.0f, 8.0f, {{2.65f, 2.65f}, {2.90f, 2.90f}}},
+    {128, 128, 2, 5.0f, 2.3f, {{0.82f, 1.58f}, {0.90f, 1.70f}}},
+    {64, 64, 2, 4.0f, 1.2f, {{0.35f, 0.62f}, {0.38f, 0.68f}}},
+    {32, 64, 2, 6.0f, 0.8f, {{0.25f, 0.39f}, {0.28f, 0.43f}}}};
+LossKind loss_kind(int64_t T, int64_t V, int64_t d) {
+  LossKind best = kLoss64;
+  float cost = HUGE_VALF;
+  for (int k = 0; k < kLossKinds; ++k) {
+    const TileCost& t = kLossTile[k];
+    const int64_t nt = ((T + t.bm - 1) / t.bm) * ((V + t.bn - 1) / t.bn);
+    const float c = cost_of(t, nt, d);
+    if (nt >= 1 << 23 || c >= cost) continue;
+    cost = c;
+    best = (LossKind)k;
+  }
+  return best;
+}
+
+// The gradient's two products, by linear_act_plan.hpp's costs: G's (E4M3) and dx's
+// (float16, K in bytes), those kinds that are cheapest somewhere.
+//   G, 16000 columns of 4096: 205 us in 256 x 128 at 4096 tokens (128 x 128: 246), 35
+//   and 37 at 512, 17 in 64 x 64 at 128 (128 x 128: 20), 12.1 in 32 x 64 at 17 (12.8)
+//   dx from them: 388 in 256 x 256 at 4096 tokens (256 x 128: 417), 217 in 256 x 128 at
+//   2048 (280; 128 x 128: 234), 125 in 128 x 128 at 1024 (157)
+constexpr TileKind kGradKinds[] = {k256x128, k128, k64, k32x64};
+constexpr TileKind kDxKinds[] = {k256, k256x128, k128, k64, k32x64};
+
+template <int N>
+TileKind cheapest(const TileKind (&kinds)[N], int64_t M, int64_t n, int64_t K) {
+  TileKind best = k64;
+  float cost = HUGE_VALF;
+  for (const TileKind k : kinds) {
+    if (K > kFarK && k != k64 && k != k32x64) continue;
+    const float c = tile_cost(k, M, n, K);
+    if (c < cost) {
+      cost = c;
+      best = k;
+    }
+  }
+  return best;
+}
+
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up(int64_t a, int64_t b) { return ceil_div64(a, b) * b; }
+
+// Rows are taken in strips, so that no workspace grows with T beyond a strip's.
+constexpr int64_t kStrip = 16384;
+int64_t strip_of(int64_t T) { return std::min(T, kStrip); }
+
+// runs of columns of the forward's partial sums: a wave's of a tile, or 16
+int64_t runs_of(int64_t T, int64_t d, int64_t V) {
+  if (T <= kFew) return ceil_div64(V, 16);
+  switch (loss_kind(T, V, d)) {
+    case kLoss256: return ceil_div64(V, 256) * 2;
+    case kLoss128: return ceil_div64(V, 128) * 2;
+    case kLoss64: return ceil_div64(V, 64) * 2;
+    default: return ceil_div64(V, 64) * 4;
+  }
+}
+
+// pieces of the vocabulary: as many as keep G and the turned weight within kPiece
+// bytes each, of one width, a multiple of 64
+constexpr int64_t kPiece = (int64_t)128 << 20;
+int64_t piece_width(int64_t T, int64_t d, int64_t V) {
+  const int64_t most = std::clamp<int64_t>(kPiece / (2 * std::max(T, d)), 2048, 1 << 21);
+  return up(ceil_div64(V, ceil_div64(V, most)), 64);
+}
+
+// splits of the product with G over the piece: where its tiles leave CUs without work
+int dx_splits(int64_t T, int64_t d, int64_t width, int& kc) {
+  const int64_t nt = tiles_of(k128w8, T, d), steps = ceil_div64(width * 2, 128);
+  const int64_t s = std::min<int64_t>(kCUs / nt, steps / 8);
+  kc = 0;
+  if (s < 2) return 1;
+  kc = (int)ceil_div64(steps, s);
+  return (int)ceil_div64(steps, kc);
+}
+
+struct BwdPlan {
+  int64_t width;
+  int splits, kc;
+  size_t g, w, sums, part, at_target;                        // bytes, multiples of 256
+  size_t bytes() const { return g + w + sums + part + at_target; }
+};
+BwdPlan bwd_plan(int64_t T, int64_t d, int64_t V, int dx_type) {
+  BwdPlan p;
+  p.width = piece_width(T, d, V);
+  p.splits = dx_splits(T, d, p.width, p.kc);
+  p.g = (size_t)up(T * p.width * 2, 256);
+  p.w = (size_t)up(d * p.width * 2, 256);
+  // float32 gradients collect in place
+  p.sums = dx_type != 0 && p.width < V ? (size_t)up(T * d * 4, 256) : 0;
+  p.part = p.splits > 1 ? (size_t)up(p.splits * T * d * 4, 256) : 0;
+  p.at_target = (size_t)up(T * 4, 256);
+  return p;
+}
+
+}  // namespace
+}  // namespace falq

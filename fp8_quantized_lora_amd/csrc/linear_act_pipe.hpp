@@ -129,7 +129,8 @@ __device__ __forceinline__ void settle(ACC (&acc)[MB][NB]) {
 template <class OP, class C, int PER_CU>
 struct Ring {
   static constexpr int UA = C::BM / 2 * C::BK, CODES = UA + C::BN / 2 * C::BK;
-  static constexpr int SLOT = CODES + (OP::kScaled ? (C::BM + C::BN) / 2 * 8 : 0);
+  static constexpr int EXPS = 1024;                          // of half the rows, 8 each
+  static constexpr int SLOT = CODES + (OP::kScaled ? 2 * EXPS : 0);
   static constexpr int FIT = 160 * 1024 / PER_CU / SLOT, SLOTS = FIT < 5 ? FIT : 5;
   static constexpr int kLds = SLOTS * SLOT;
   static_assert(SLOTS >= 3, "LDS");
@@ -137,7 +138,10 @@ struct Ring {
 
 // The tile at (m0, n0), wave-uniform: before() is called ahead of the loop, out(acc,
 // what it gave, LDS) behind it, with the LDS (the ring's kLds) free.
-template <class OP, class C, int PER_CU, class BEFORE, class OUT>
+//
+// LEAN: one set of fragments of A instead of two, read between the quarters, where the
+// registers do not hold two: the other workgroup of the CU multiplies meanwhile.
+template <class OP, class C, int PER_CU, bool LEAN = false, class BEFORE, class OUT>
 __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
                                              const uint8_t* __restrict__ B, int M, int N, int K,
                                              int m0, int n0, const Exponents& ex, BEFORE&& before,
@@ -151,13 +155,9 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
   constexpr int HM = MB / 2, HN = NB / 2, H = OP::kProducts;
   static_assert(MB % 2 == 0 && NB % 2 == 0, "quarters");
   constexpr int UA = R::UA, SLOT = R::SLOT, SLOTS = R::SLOTS, AHEAD = SLOTS - 2;
-  constexpr int LA = C::AI / 2, LB = C::BI / 2, LPP = LA + LB + OP::kScaled;
-  // exponents of a slot: a lane loads those of two rows, ELA of a wave's lanes A's
-  constexpr int ELA = C::BM / 16, ELB = C::BN / 16, EWAVE = (ELA + ELB) * 16;
+  constexpr int LA = C::AI / 2, LB = C::BI / 2, LPP = LA + LB;
   static_assert(C::AI % 2 == 0 && C::BI % 2 == 0 && C::NW == 4, "whole loads per slot");
-  static_assert(!OP::kScaled || (ELA + ELB <= 64 && BLK % (C::BM / 8) == 0 &&
-                                 BLK % (C::BN / 8) == 0),
-                "a fragment's rows begin with a wave's rows of exponents");
+  static_assert(!OP::kScaled || (C::BM * 4 <= R::EXPS && C::BN * 4 <= R::EXPS), "exponents");
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = w / C::WGN, wn = w % C::WGN;
@@ -191,21 +191,21 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
       vB[h][j] = (uint32_t)min(row, N - 1 - n0) * (uint32_t)K + (lslot ^ gemm::dma::swz(r)) * 16;
     }
   }
-  // exponents: the lane's two rows of half h, and a K step's stride
-  const uint8_t* pE = nullptr;
+  // exponents: wave 0 loads A's of a slot, wave 1 B's, two rows a lane
+  const bool loads_e = OP::kScaled && w < 2;
+  const uint8_t* tE = nullptr;
   uint32_t vE[2];
   int64_t estep = 0;
-  const bool e_of_a = lane < ELA;
   if constexpr (OP::kScaled) {
-    const int r = e_of_a ? (w * ELA + lane) * 2 : (w * ELB + min(lane - ELA, ELB - 1)) * 2;
-    const int half = e_of_a ? C::WTM / 2 : C::WTN / 2, rows = e_of_a ? ex.rows_a : ex.rows_b;
-    pE = e_of_a ? ex.a : ex.b;
+    const int half = (w == 0 ? C::WTM : C::WTN) / 2, rows = w == 0 ? ex.rows_a : ex.rows_b;
+    const int first = w == 0 ? m0 : n0, r = min(lane * 2, (w == 0 ? C::BM : C::BN) / 2 - 2);
+    tE = (w == 0 ? ex.a : ex.b) + (int64_t)first * 8;
     estep = (int64_t)rows * 8;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)                             // rows are multiples of 16
-      vE[h] = (uint32_t)min((e_of_a ? m0 : n0) + (r / half * 2 + h) * half + r % half, rows - 2);
+    for (int h = 0; h < 2; ++h)                             // rows is a multiple of 16
+      vE[h] = (uint32_t)min((r / half * 2 + h) * half + r % half, rows - 2 - first) * 8;
   }
-  const uint32_t ldsE = lds_offset(smem) + R::CODES + w * EWAVE;
+  const uint32_t ldsE = lds_offset(smem) + R::CODES + w * R::EXPS;
   const uint32_t ldsA = lds_offset(smem) + w * LA * 1024;
   const uint32_t ldsB = lds_offset(smem) + UA + w * LB * 1024;
   // load J of the wave's LPP: half HA of A's and half HB of B's rows, whole step kt
@@ -214,18 +214,20 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
     if constexpr (J < LA)
       load16_to_lds_at(tA + (int64_t)kt * BK, vA[decltype(ha)::value][J],
                        ldsA + slot * SLOT + J * 1024);
-    else if constexpr (J < LA + LB)
+    else if constexpr (J < LPP)
       load16_to_lds_at(tB + (int64_t)kt * BK, vB[decltype(hb)::value][J - LA],
                        ldsB + slot * SLOT + (J - LA) * 1024);
-    else if constexpr (J < LPP)
-      if (lane < ELA + ELB)
-        load16_to_lds(pE + ((int64_t)(e_of_a ? vE[decltype(ha)::value] : vE[decltype(hb)::value]) * 8 +
-                            kt * estep),
-                      ldsE + slot * SLOT);
+  };
+  auto load_exponents = [&](auto ha, auto hb, int kt, int slot) FALQ_INLINE {
+    if constexpr (OP::kScaled)
+      if (loads_e)
+        load16_to_lds_at(tE + kt * estep, w == 0 ? vE[decltype(ha)::value] : vE[decltype(hb)::value],
+                         ldsE + slot * SLOT);
   };
   // all of them, for any step; chunks past K load the row's last chunk
   auto fetch = [&](auto ha, auto hb, int kt, int slot) FALQ_INLINE {
     if (kt >= all) return;
+    load_exponents(ha, hb, kt, slot);
     if (kt < nk) {
       each<LPP>([&](auto j) FALQ_INLINE { load(ha, hb, j, kt, slot); });
       return;
@@ -236,13 +238,11 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
         const int co = (lslot ^ gemm::dma::swz((w * LA + J) * 8 + lrow)) * 16;
         load16_to_lds_at(tA + (int64_t)nk * BK, vA[decltype(ha)::value][J] - co + min(co, rem - 16),
                          ldsA + slot * SLOT + J * 1024);
-      } else if constexpr (J < LA + LB) {
+      } else {
         const int co = (lslot ^ gemm::dma::swz((w * LB + J - LA) * 8 + lrow)) * 16;
         load16_to_lds_at(tB + (int64_t)nk * BK,
                          vB[decltype(hb)::value][J - LA] - co + min(co, rem - 16),
                          ldsB + slot * SLOT + (J - LA) * 1024);
-      } else {
-        load(ha, hb, j, nk, slot);
       }
     });
   };
@@ -263,12 +263,10 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
 #pragma unroll
   for (int p = 0; p < OP::kParts; ++p) o[p] = (OP::chunk(g, p) ^ gemm::dma::swz(r & 15)) * 16;
   const int offA = (wm * (C::WTM / 2) + r) * BK, offB = UA + (wn * (C::WTN / 2) + r) * BK;
-  // the lane's exponents of fragment 0 of A and of B in a slot: EWAVE bytes for each
-  // BM / 8 rows of A and BN / 8 of B, A's ahead
-  constexpr int EA = C::BM / 8, EB = C::BN / 8, EPL = 8 * BLK / 64;
-  const int rA = wm * (C::WTM / 2) + r, rB = wn * (C::WTN / 2) + r;
-  const int eA = R::CODES + rA / EA * EWAVE + rA % EA * 8 + EPL * g;
-  const int eB = R::CODES + rB / EB * EWAVE + ELA * 16 + rB % EB * 8 + EPL * g;
+  // the lane's exponents of fragment 0 of A and of B in a slot
+  constexpr int EPL = 8 * BLK / 64;
+  const int eA = R::CODES + (wm * (C::WTM / 2) + r) * 8 + EPL * g;
+  const int eB = R::CODES + R::EXPS + (wn * (C::WTN / 2) + r) * 8 + EPL * g;
   // fragment I of a half of A, of B, of the slot that begins at byte `at`
   auto frag_at = [&](int codes, int exps) FALQ_INLINE {
     int e = 0;
@@ -281,11 +279,11 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
   };
   auto fragA = [&](auto i, int at) FALQ_INLINE {
     constexpr int I = decltype(i)::value * BLK;
-    return frag_at(at + offA + I * BK, at + eA + I / EA * EWAVE);
+    return frag_at(at + offA + I * BK, at + eA + I * 8);
   };
   auto fragB = [&](auto i, int at) FALQ_INLINE {
     constexpr int I = decltype(i)::value * BLK;
-    return frag_at(at + offB + I * BK, at + eB + I / EB * EWAVE);
+    return frag_at(at + offB + I * BK, at + eB + I * 8);
   };
   // with every second product a fragment of the group f (of 32 rows: every eighth)
   constexpr int EVERY = OP::kBlock == 16 ? 2 : HM * HN * H >= 16 ? 8 : 4;
@@ -294,18 +292,34 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
     static_assert(T > 0 || (N - 1) * EVERY < HM * HN * H, "all within the quarter");
     if constexpr (T % EVERY == 0 && I < N) f[I] = of(std::integral_constant<int, I>{}, at);
   };
-  Frag a0[HM], a1[HM], b0[HN], b1[HN];
+  Frag a0[HM], a_next[LEAN ? 1 : HM], b0[HN], b1[HN];
+  Frag(&a1)[HM] = *(Frag(*)[HM])(LEAN ? a0 : a_next);
+  auto read_a = [&](int at) FALQ_INLINE {
+    each<HM>([&](auto i) FALQ_INLINE { a0[decltype(i)::value] = fragA(i, at); });
+  };
   auto next = [](int slot) { return slot == SLOTS - 1 ? 0 : slot + 1; };
+  // until at most the loads of `ahead` pairs, at most A of them, are in flight
+  auto wait_pairs = [&](auto most, int ahead) FALQ_INLINE {
+    constexpr int A = decltype(most)::value;
+    if (loads_e)
+      wait_stages<A, LPP + 1>(ahead);
+    else
+      wait_stages<A, LPP>(ahead);
+  };
   // pair n, whose AHEAD successors are under way, is in its slot, and all waves are
   // done with pair n - 1
   auto arrive = [&](auto whole, int n, int slot, int kt) FALQ_INLINE {
     if constexpr (decltype(whole)::value) {
-      __builtin_amdgcn_s_waitcnt(0x70 | ((AHEAD * LPP) & 0xF) | ((AHEAD * LPP) >> 4) << 14);
+      constexpr int MOST = AHEAD * LPP, MOST_E = AHEAD * (LPP + 1);
+      if (loads_e)
+        __builtin_amdgcn_s_waitcnt(0x70 | (MOST_E & 0xF) | (MOST_E >> 4) << 14);
+      else
+        __builtin_amdgcn_s_waitcnt(0x70 | (MOST & 0xF) | (MOST >> 4) << 14);
       barrier_no_drain();
     } else {
       settle(acc);
       __builtin_amdgcn_s_waitcnt(0xC07F);                    // lgkmcnt(0)
-      wait_stages<AHEAD, LPP>(last - n);
+      wait_pairs(std::integral_constant<int, AHEAD>{}, last - n);
       barrier_no_drain();
       if (kt == nk && rem) clear(slot);
     }
@@ -318,6 +332,7 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
     Frag(&other)[HN] = P ? b0 : b1;
     // the pairs that take the slots freed: SLOTS - 1 on from those read
     constexpr int D1 = SLOTS / 2, D2 = (SLOTS + 1) / 2, U = 2 * HM * HN * H / LPP;
+    static_assert(U > 0, "a product for each load");
     using HA1 = std::integral_constant<int, SLOTS % 2>;
     using HA2 = std::integral_constant<int, (SLOTS + 1) % 2>;
     using HB1 = std::integral_constant<int, (P + D1 + SLOTS) % 2>;
@@ -325,7 +340,8 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
     // load t / U of the pair's with every U-th product of a half step
     auto send = [&](auto t, auto first, auto ha, auto hb, int kt, int to) FALQ_INLINE {
       constexpr int T = decltype(t)::value + decltype(first)::value;
-      if constexpr (WHOLE && T % U == 1)
+      if constexpr (WHOLE && T == 0) load_exponents(ha, hb, kt, to);
+      if constexpr (WHOLE && T % U == (U > 1))
         load(ha, hb, std::integral_constant<int, T / U>{}, kt, to);
     };
     using T0 = std::integral_constant<int, 0>;
@@ -338,22 +354,24 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
       send(t, T0{}, HA1{}, HB1{}, k + D1, to);
     });
     quarter<OP, 0, jo>(acc, a0, other, [&](auto t) FALQ_INLINE {
-      read(t, a1, fragA, at);
+      if constexpr (!LEAN) read(t, a1, fragA, at);
       send(t, T1{}, HA1{}, HB1{}, k + D1, to);
     });
+    if constexpr (LEAN) read_a(at);
     to = slot;
     slot = next(slot);
     at = slot * SLOT;
     arrive(whole, 2 * k + 2, slot, k + 1);
     if constexpr (!WHOLE) fetch(HA2{}, HB2{}, k + D2, to);
     quarter<OP, HM, jo>(acc, a1, other, [&](auto t) FALQ_INLINE {
-      read(t, a0, fragA, at);
+      if constexpr (!LEAN) read(t, a0, fragA, at);
       send(t, T0{}, HA2{}, HB2{}, k + D2, to);
     });
     quarter<OP, HM, jf>(acc, a1, f, [&](auto t) FALQ_INLINE {
       read(t, other, fragB, at);
       send(t, T1{}, HA2{}, HB2{}, k + D2, to);
     });
+    if constexpr (LEAN) read_a(at);
     slot = next(slot);
   };
 
@@ -364,10 +382,10 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
       using HB = std::integral_constant<int, (Q % 2 + Q / 2) % 2>;
       fetch(HA{}, HB{}, Q / 2, Q);
     });
-    wait_stages<SLOTS - 1, LPP>(last);
+    wait_pairs(std::integral_constant<int, SLOTS - 1>{}, last);
     barrier_no_drain();
     if (nk == 0) clear(0);
-    each<HM>([&](auto i) FALQ_INLINE { a0[decltype(i)::value] = fragA(i, 0); });
+    read_a(0);
     each<HN>([&](auto j) FALQ_INLINE { b0[decltype(j)::value] = fragB(j, 0); });
   }
   const auto kept = before();
@@ -389,7 +407,7 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
   out(acc, kept, smem);
 }
 
-template <class OP, class C, int PER_CU, class OT, bool STREAM>
+template <class OP, class C, int PER_CU, class OT, bool STREAM, bool LEAN = false>
 __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
     int tilesN, Epilogue ep, Exponents ex) {
@@ -397,7 +415,7 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
   gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
   const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
   const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
-  pipe_product<OP, C, PER_CU>(
+  pipe_product<OP, C, PER_CU, LEAN>(
       A, B, M, N, K, m0, n0, ex, [&] { return scale_of<OP>(ep); },
       [&](const auto& acc, float scale, uint8_t* smem) {
         tile_out<C, Ring<OP, C, PER_CU>::kLds, OT, STREAM, false>(smem, acc, m0, n0, M, N, scale,

@@ -59,15 +59,20 @@ int64_t tiles_of(TileKind k, int64_t M, int64_t N) {
   return ((M + kTile[k].bm - 1) / kTile[k].bm) * ((N + kTile[k].bn - 1) / kTile[k].bn);
 }
 
-float tile_cost(TileKind k, int64_t M, int64_t N, int64_t K) {
-  const TileCost& t = kTile[k];
-  const int64_t nt = tiles_of(k, M, N), cap = (int64_t)t.per_cu * kCUs, rest = nt % cap;
-  // a grid holds fewer than 2^32 threads: very long outputs take large tiles
-  if (k != k256 && nt >= 1 << 23) return HUGE_VALF;
+// nt tiles of t over K bytes
+float cost_of(const TileCost& t, int64_t nt, int64_t K) {
+  const int64_t cap = (int64_t)t.per_cu * kCUs, rest = nt % cap;
   const auto& step = t.step[K % 128 != 0];
   const float last = rest == 0 ? 0.0f : rest <= kCUs ? step.alone : step.full;
   return t.start + (float)((nt + cap - 1) / cap) * t.round +
          (float)((K + 127) / 128) * ((float)(nt / cap) * step.full + last);
+}
+
+float tile_cost(TileKind k, int64_t M, int64_t N, int64_t K) {
+  const int64_t nt = tiles_of(k, M, N);
+  // a grid holds fewer than 2^32 threads: very long outputs take large tiles
+  if (k != k256 && nt >= 1 << 23) return HUGE_VALF;
+  return cost_of(kTile[k], nt, K);
 }
 
 // How a product runs: by few tokens, by tiles of one kind, or by 128 x 128 tiles

@@ -7,20 +7,20 @@
 #include "elem.hpp"
 #include "kernels.hpp"
 #include "linear_act_pipe.hpp"
-#include "linear_act_plan.hpp"
 #include "linear_act_tile.hpp"
+#include "mx_linear_plan.hpp"
 
 #include <algorithm>
 
 namespace falq {
 namespace {
 
-template <class C, int PIPE, class OT>
+template <class C, int PIPE, class OT, bool LEAN = false>
 hipError_t mx_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
                     const Epilogue& ep, const Exponents& ex, hipStream_t s) {
   const int tM = (int)((M + C::BM - 1) / C::BM), tN = (int)((N + C::BN - 1) / C::BN);
   if constexpr (PIPE > 0)
-    linear_act_pipe<Fp4Wide, C, PIPE, OT, false><<<tM * tN, C::kThreads, 0, s>>>(
+    linear_act_pipe<Fp4Wide, C, PIPE, OT, false, LEAN><<<tM * tN, C::kThreads, 0, s>>>(
         A, B, (int)M, (int)N, (int)K, tM, tN, ep, ex);
   else
     linear_act_tile<Fp4, C, OT, false><<<tM * tN, C::kThreads, 0, s>>>(
@@ -42,7 +42,7 @@ using T128 = Tile<128, 128, 2, 4, 3>;
 template <class OT>
 hipError_t mx_by_plan(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
                       const Epilogue& ep, const Exponents& ex, float* part, hipStream_t s) {
-  const Plan p = plan_of(M, N, K);
+  const MxPlan p = mx_plan_of(M, N, K);
   if (p.few == 1) return mx_few<1, 1, kFewWaves[1], 1, OT>(A, B, M, N, K, ep, ex, s);
   if (p.few == 2) return mx_few<2, 1, kFewWaves[2], 2, OT>(A, B, M, N, K, ep, ex, s);
   if (p.split > 1) {
@@ -57,15 +57,9 @@ hipError_t mx_by_plan(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, 
     return hipGetLastError();
   }
   switch (p.kind) {
-    case k256x320:
-    case k256:
-    case k256x128:
-    case k128x256:
-    case k192x128: return mx_tiles<Tile<256, 256, 2, 2>, 1, OT>(A, B, M, N, K, ep, ex, s);
-    case k128x192w8:
-    case k128: return mx_tiles<Tile<128, 128, 2, 2>, 2, OT>(A, B, M, N, K, ep, ex, s);
-    case k128w8: return mx_tiles<T128, 0, OT>(A, B, M, N, K, ep, ex, s);
-    case k64: return mx_tiles<Tile<64, 64, 2, 2, 4>, 0, OT>(A, B, M, N, K, ep, ex, s);
+    case kMx256x128: return mx_tiles<Tile<256, 128, 2, 2>, 2, OT, true>(A, B, M, N, K, ep, ex, s);
+    case kMx128: return mx_tiles<Tile<128, 128, 2, 2>, 2, OT>(A, B, M, N, K, ep, ex, s);
+    case kMx64: return mx_tiles<Tile<64, 64, 2, 2, 4>, 0, OT>(A, B, M, N, K, ep, ex, s);
     default: return mx_tiles<Tile<32, 64, 1, 4, 4>, 0, OT>(A, B, M, N, K, ep, ex, s);
   }
 }
@@ -73,7 +67,9 @@ hipError_t mx_by_plan(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, 
 }  // namespace
 
 size_t mx_linear_ws_bytes(int64_t T, int64_t d_in, int64_t d_out) {
-  return linear_act_ws_bytes(T, d_in / 2, d_out);
+  if (T == 0 || d_out == 0) return 0;
+  const MxPlan p = mx_plan_of(T, d_out, d_in / 2);
+  return p.split > 1 ? (size_t)p.split * (size_t)T * (size_t)d_out * 4 : 0;
 }
 
 hipError_t launch_mx_linear(const uint8_t* xq, const uint8_t* x_e, const uint8_t* wq,

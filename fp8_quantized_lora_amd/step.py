@@ -35,6 +35,14 @@ melded_linear_bwd, which forms X^ A^T itself.  The bias is trained: the adapter
 update steps it by dbias with the layer's optimizer (AdamW without weight
 decay, which is meant for matrices).
 
+With keep_z="fp8" a layer with an activation keeps its z in 8 bits between forward
+and backward (checkpoint_save, linear_act_bwd_ckpt): half of bfloat16's memory.  The
+product writes z itself into `z_scratch`, which layers that run one after the other
+may share.
+
+LinearCrossEntropy is the loss behind the last layer: an output layer frozen in FP8,
+whose logits are never kept, and the gradient that the last layer's backward takes.
+
 clip_gradients clips the adapter (and bias) gradients of many layers by their
 global norm, between their backward calls and their adapter updates.
 
@@ -60,7 +68,10 @@ from . import (fp8_quantize, fp8_quantize_workspace_bytes, fp8_dequantize, melde
                adapter_pieces_bytes, adapter_pieces, adapter_step_pieces,
                melded_linear_fwd_xa_pieces, melded_linear_fwd_act,
                melded_linear_fwd_act_workspace_bytes, linear_act_bwd,
-               linear_act_bwd_workspace_bytes, grad_clip, ACTIVATIONS)
+               linear_act_bwd_workspace_bytes, grad_clip, ACTIVATIONS, checkpoint_save,
+               checkpoint_scales_shape, linear_act_bwd_ckpt, linear_cross_entropy_fwd,
+               linear_cross_entropy_fwd_workspace_bytes, linear_cross_entropy_bwd,
+               linear_cross_entropy_bwd_workspace_bytes)
 
 
 def clip_gradients(layers, max_norm: float, norm: torch.Tensor, extra=(), eps: float = 1e-6,
@@ -76,7 +87,8 @@ class MeldedLinear:
                  x_dtype=torch.float32, train_a: bool = True, optimizer: str = "sgd",
                  adamw: Optional[dict] = None, fp8_a: bool = False, g_fmt: str = "e4m3",
                  topk_rank: int = 0, merge_every: int = 1, bias: bool = False,
-                 act: str = "none", y_dtype=torch.float32, dy_dtype=torch.float32):
+                 act: str = "none", y_dtype=torch.float32, dy_dtype=torch.float32,
+                 keep_z: str = "exact", z_scratch: Optional[torch.Tensor] = None):
         """optimizer "sgd" (adapter_step) or "adamw" (adapter_step_adamw, with
         hyper-parameters `adamw`: beta1, beta2, eps, weight_decay); fp8_a
         freezes A in FP8 (implies train_a=False); g_fmt is the FP8 format of the
@@ -86,7 +98,10 @@ class MeldedLinear:
         decides whether W~^T is kept (worth it from every second step on); bias
         adds a bias (self.bias, zero at the start; its gradient in self.dbias),
         which adapter_update steps, act an activation of melded_linear_fwd_act, y_dtype is the type of Y
-        (and of a residual), dy_dtype that of the upstream gradient dY."""
+        (and of a residual), dy_dtype that of the upstream gradient dY; keep_z "fp8"
+        keeps z for the backward in 8 bits instead of y_dtype ("exact"), and z_scratch
+        is then the memory z passes through: contiguous, of y_dtype and at least tokens
+        x d_out elements (None: the layer's own)."""
         if optimizer not in ("sgd", "adamw"):
             raise ValueError(f"optimizer must be 'sgd' or 'adamw', not {optimizer!r}")
         if act not in ACTIVATIONS:
@@ -94,6 +109,13 @@ class MeldedLinear:
         if y_dtype not in (torch.float32, torch.bfloat16) or dy_dtype not in (torch.float32,
                                                                               torch.bfloat16):
             raise ValueError("y_dtype and dy_dtype must be float32 or bfloat16")
+        if keep_z not in ("exact", "fp8"):
+            raise ValueError(f"keep_z must be 'exact' or 'fp8', not {keep_z!r}")
+        if keep_z == "fp8" and act == "none":
+            raise ValueError("without an activation no z is kept")
+        if z_scratch is not None and keep_z != "fp8":
+            raise ValueError("z_scratch is for layers that keep z in 8 bits")
+        self.keep_z = keep_z
         self.act = act
         self.epilogue = bias or act != "none" or y_dtype != torch.float32
         if fp8_a and self.epilogue:
@@ -130,7 +152,18 @@ class MeldedLinear:
         self.bias = torch.zeros(d_out, dtype=f32, device=dev) if bias else None
         self.dbias = torch.zeros(d_out, dtype=f32, device=dev) if bias else None
         kept = act != "none"
-        self.z = torch.empty((tokens, d_out), dtype=y_dtype, device=dev) if kept else None
+        if z_scratch is not None:
+            if (z_scratch.dtype != y_dtype or z_scratch.numel() < tokens * d_out
+                    or not z_scratch.is_contiguous()
+                    or z_scratch.device.type != dev.type):
+                raise ValueError("z_scratch must be contiguous, of y_dtype, on the layer's device "
+                                 "and hold tokens x d_out elements")
+            self.z = z_scratch.view(-1)[:tokens * d_out].view(tokens, d_out)
+        else:
+            self.z = torch.empty((tokens, d_out), dtype=y_dtype, device=dev) if kept else None
+        if keep_z == "fp8":
+            self.z_q = torch.empty((tokens, d_out), dtype=u8, device=dev)
+            self.z_e = torch.empty(checkpoint_scales_shape(tokens, d_out), dtype=u8, device=dev)
         self.dz = torch.empty((tokens, d_out), dtype=dy_dtype, device=dev) if kept else None
         if fp8_a:                         # A~, its scale, and U = X~ A~^T of the forward
             self.aq = torch.empty((rank, d_in), dtype=u8, device=dev)
@@ -242,6 +275,8 @@ class MeldedLinear:
             melded_linear_fwd_act(self.xq, self.s_x, self.wq, self.s_w, self.y, bias=self.bias,
                                   act=self.act, residual=residual, z=self.z, ws=self.ws_fwd,
                                   stream=stream)
+            if self.keep_z == "fp8":
+                checkpoint_save(self.z, self.z_q, self.z_e, stream=stream)
         elif self.fp8_a:
             melded_linear_fwd_frozen_a(self.xq, self.s_x, self.wq, self.s_w, self.aq, self.s_a,
                                        self.y, self.u, ws=self.ws_fwd, stream=stream)
@@ -257,8 +292,13 @@ class MeldedLinear:
     def backward(self, dY: torch.Tensor, stream=None):
         if self.dz is not None or self.dbias is not None:
             # through the activation, and the bias's gradient
-            linear_act_bwd(dY, self.z, self.dz, dbias=self.dbias, act=self.act,
-                           ws=self.ws_act if self.dbias is not None else None, stream=stream)
+            ws = self.ws_act if self.dbias is not None else None
+            if self.keep_z == "fp8":
+                linear_act_bwd_ckpt(dY, self.z_q, self.z_e, self.dz, dbias=self.dbias,
+                                    act=self.act, ws=ws, stream=stream)
+            else:
+                linear_act_bwd(dY, self.z, self.dz, dbias=self.dbias, act=self.act, ws=ws,
+                               stream=stream)
         if self.dz is not None:
             dY = self.dz
         fp8_quantize(dY, self.gq, self.s_g, ws=self.ws_q, stream=stream, fmt=self.g_fmt)
@@ -334,3 +374,49 @@ class MeldedLinear:
         self.forward(X, stream, residual)
         self.backward(dY, stream)
         self.update(lr, tau, k_max, stream, merge=self.n_steps % merge_every == 0)
+
+
+class LinearCrossEntropy:
+    """Softmax cross entropy over the `vocab` rows of an output layer that is frozen in
+    FP8, for `tokens` rows of d features, every buffer allocated once: forward gives the
+    loss of each token, backward the gradient in its input."""
+
+    def __init__(self, vocab: int, d: int, tokens: int, device="cuda", dx_dtype=torch.float32):
+        if dx_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("dx_dtype must be float32 or bfloat16")
+        dev = torch.device(device)
+        u8, f32 = torch.uint8, torch.float32
+        self.vocab, self.d, self.T = vocab, d, tokens
+        self.wq = torch.empty((vocab, d), dtype=u8, device=dev)
+        self.s_w = torch.empty(1, dtype=f32, device=dev)
+        self.xq = torch.empty((tokens, d), dtype=u8, device=dev)
+        self.s_x = torch.empty(1, dtype=f32, device=dev)
+        self.loss = torch.empty(tokens, dtype=f32, device=dev)
+        self.lse = torch.empty(tokens, dtype=f32, device=dev)
+        self.dx = torch.empty((tokens, d), dtype=dx_dtype, device=dev)
+        nb = fp8_quantize_workspace_bytes(max(tokens * d, vocab * d))
+        self.ws_q = torch.empty(nb, dtype=u8, device=dev)
+        nb = linear_cross_entropy_fwd_workspace_bytes(tokens, d, vocab)
+        self.ws_fwd = torch.empty(max(1, nb), dtype=u8, device=dev)
+        nb = linear_cross_entropy_bwd_workspace_bytes(tokens, d, vocab, dx_dtype)
+        self.ws_bwd = torch.empty(max(1, nb), dtype=u8, device=dev)
+
+    def init_state(self, W: torch.Tensor, stream=None):
+        """W~ = E4M3(W * s_w), s_w = 448 / max|W|, of the output layer [vocab x d]."""
+        fp8_quantize(W, self.wq, self.s_w, ws=self.ws_q, stream=stream)
+
+    def forward(self, X: torch.Tensor, target: torch.Tensor, stream=None):
+        """The loss of each row of X [tokens x d] (float32 or bfloat16) for the class
+        target [tokens] (int64; negative: it does not count, its loss is 0)."""
+        fp8_quantize(X, self.xq, self.s_x, ws=self.ws_q, stream=stream)
+        self.target = target
+        linear_cross_entropy_fwd(self.xq, self.s_x, self.wq, self.s_w, target, self.loss, self.lse,
+                                 ws=self.ws_fwd, stream=stream)
+        return self.loss
+
+    def backward(self, dloss: torch.Tensor, stream=None):
+        """dX of sum_t dloss[t] loss[t] (1 / tokens that count for their mean), through
+        the quantisation as melded_linear_bwd's."""
+        linear_cross_entropy_bwd(self.xq, self.s_x, self.wq, self.s_w, self.target, self.lse,
+                                 dloss, self.dx, ws=self.ws_bwd, stream=stream)
+        return self.dx

@@ -823,8 +823,9 @@ falq_status layer_norm_bwd_ckpt(const void *dy, int dy_dtype, const uint8_t *x_q
  * formed again a piece of the vocabulary at a time:
  *     dx[t] = dloss[t] sum_v (exp(z[t][v] - lse[t]) - [v = target[t]]) dec(wq[v]) / s_w
  * (0 for a token that does not count, NaN for a target of V or more).  The factors of
- * dec(wq[v]) are rounded to float16, 2^-12 of each, before the sum over v, which is
- * float32's.
+ * dec(wq[v]) are rounded to float16, 2^-11 of each at most, before the sum over v, which
+ * is float32's; but for the target's, they come from logits of the FP8 product, which
+ * is off as melded_linear_fwd is.
  *
  *   xq, s_x   [T x d] E4M3 codes and their scale (fp8_quantize's, positive)
  *   wq, s_w   [V x d] likewise: the output layer; d a multiple of 16, 16 to 2^22;
