@@ -4,17 +4,16 @@
 //   lse[t] = log sum_v exp z[t][v],   loss[t] = lse[t] - z[t][target[t]],
 //   dx[t] = dloss[t] sum_v (exp(z[t][v] - lse[t]) - [v = target[t]]) dec(wq[v]) / s_w.
 //
-// Forward: the FP8 product in tiles (linear_act_pipe.hpp, linear_act_tile.hpp; few
-// tokens: linear_act_few.hpp), whose epilogue leaves of each row and each wave's
-// columns the maximum and the sum of exponentials under it, straight from the
-// accumulators, 8 bytes for 64 to 128 logits; a second launch joins them.  All of it
-// in float32 and base 2.
+// Forward: the product in tiles (linear_act_pipe.hpp, linear_act_tile.hpp), whose
+// epilogue leaves of each row the maximum and the sum of exponentials under it over the
+// tile's columns, straight from the accumulators, 8 bytes for 64 to 256 logits; a second
+// launch joins them.  All of it in float32 and base 2.
 //
 // Backward, a piece of the vocabulary after the other: the product again, as FP8's
 // (p is then off by some 2^-13 of itself), whose epilogue now leaves G = 2^15 (p - [v =
 // target]) of the piece as float16, the target's from its own logit, summed in float32,
-// as 2^15 expm1(z - lse): a sure token's gradient is a small difference; the piece's
-// rows of W as float16, transposed; and the product of the two, added onto dx.  G is
+// as 2^15 expm1(z - lse): a sure token's gradient is a small difference; then G times
+// the piece's rows of W, which are read as they lie (F16ByE4M3), added onto dx.  G is
 // float16 because its 11 bits keep the gradient to 2^-11 of its terms (bfloat16: 2^-8),
 // and 2^15 because p may be as small as 1 / V: under it float16 has its full precision
 // down to 2^-29 and absolute steps of 2^-39 below, while 1 still fits; E4M3 codes are
@@ -62,9 +61,20 @@ struct Stats {
   float* at_target;
 };
 
+// (m, s) of two runs
+__device__ __forceinline__ void join_runs(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  // a run without a column is (-inf, 0)
+  const float a = m == -INFINITY ? 0.0f : s * __builtin_amdgcn_exp2f(m - top);
+  const float b = m2 == -INFINITY ? 0.0f : s2 * __builtin_amdgcn_exp2f(m2 - top);
+  m = top;
+  s = a + b;
+}
+
 template <class C, int MB, int NB, class ACC>
-__device__ __forceinline__ void stats_out(const ACC (&acc)[MB][NB], int m0, int n0, int M, int V,
-                                          float k, const Logits& lg, const Stats& st, int tn) {
+__device__ __forceinline__ void stats_out(uint8_t* smem, const ACC (&acc)[MB][NB], int m0, int n0,
+                                          int M, int V, float k, const Logits& lg, const Stats& st,
+                                          int tn) {
   // a lane's elements of a block: its row's columns 4 g + (e & 3) + (e >> 2) * SKIP
   constexpr int E = sizeof(ACC) / 4, BLK = E == 4 ? 16 : 32, SKIP = BLK / 4;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wm = w / C::WGN, wn = w % C::WGN;
@@ -72,7 +82,7 @@ __device__ __forceinline__ void stats_out(const ACC (&acc)[MB][NB], int m0, int 
   const int col0 = n0 + wn * C::WTN + 4 * g;
   const auto column = [](int j, int e) { return BLK * j + (e & 3) + (e >> 2) * SKIP; };
   const bool whole = n0 + wn * C::WTN + C::WTN <= V;
-  float2* to = st.part + (int64_t)(tn * C::WGN + wn) * M;
+  float2* const runs = reinterpret_cast<float2*>(smem);      // [WGN][BM]: the waves'
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     const int row = m0 + wm * C::WTM + i * BLK + r;
@@ -103,7 +113,7 @@ __device__ __forceinline__ void stats_out(const ACC (&acc)[MB][NB], int m0, int 
           if (col0 + column(j, e) < V) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], k, -m));
     }
     s = sum_over_g<BLK>(s);
-    if (g == 0 && row < M) to[row] = make_float2(m, s);
+    if (g == 0) runs[wn * C::BM + wm * C::WTM + i * BLK + r] = make_float2(m, s);
     // the target's logit, where it is among the wave's columns
     const int64_t t = row < M ? lg.target[row] : -1;
     const int64_t at = t - col0;
@@ -114,6 +124,16 @@ __device__ __forceinline__ void stats_out(const ACC (&acc)[MB][NB], int m0, int 
         for (int e = 0; e < E; ++e)
           if (at == column(j, e)) st.at_target[row] = acc[i][j][e] * k;
     }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < C::BM && m0 + i < M; i += C::kThreads) {
+    float2 a = runs[i];
+#pragma unroll
+    for (int n = 1; n < C::WGN; ++n) {
+      const float2 b = runs[n * C::BM + i];
+      join_runs(a.x, a.y, b.x, b.y);
+    }
+    st.part[(int64_t)tn * M + m0 + i] = a;
   }
 }
 
@@ -127,8 +147,8 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void loss_pipe(
   const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
   pipe_product<E4M3AsF16Wide, C, PER_CU>(
       A, B, M, N, K, m0, n0, Exponents{}, [&] { return lg.k(); },
-      [&](const auto& acc, float k, uint8_t*) {
-        stats_out<C>(acc, m0, n0, M, N, k, lg, st, tn);
+      [&](const auto& acc, float k, uint8_t* smem) {
+        stats_out<C>(smem, acc, m0, n0, M, N, k, lg, st, tn);
       });
 }
 template <class C>
@@ -140,43 +160,10 @@ __global__ __launch_bounds__(C::kThreads) void loss_tile(
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   tile_product<E4M3AsF16, C>(
       A, B, M, N, K, m0, n0, 0, INT32_MAX, Exponents{}, [&] { return lg.k(); },
-      [&](const auto& acc, float k, uint8_t*) {
-        stats_out<C>(acc, m0, n0, M, N, k, lg, st, tn);
+      [&](const auto& acc, float k, uint8_t* smem) {
+        stats_out<C>(smem, acc, m0, n0, M, N, k, lg, st, tn);
       });
 }
-// up to 16 tokens: a run of 16 columns a workgroup, a column of a row a lane
-template <int NW>
-__global__ __launch_bounds__(NW * 64) void loss_few(const uint8_t* __restrict__ A,
-                                                    const uint8_t* __restrict__ B, int M, int N,
-                                                    int K, Logits lg, Stats st) {
-  static_assert(NW * 64 >= 256, "a lane for each of 16 x 16");
-  __shared__ FewParts<1, 1, NW> part;
-  const int n0 = blockIdx.x * 16;
-  few_product<E4M3AsF16, 1, 1, NW, 1>(part, A, B, M, N, K, n0, Exponents{});
-  const float k = lg.k();
-  const int row = threadIdx.x / 16, c = threadIdx.x % 16, col = n0 + c;
-  if (row >= M) return;                                      // 16 lanes together
-  const float v = few_sum<1, 1, NW>(part, row, c) * k;
-  float m = col < N ? v : -INFINITY;
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-  float s = col < N ? __builtin_amdgcn_exp2f(v - m) : 0.0f;
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) s += __shfl_xor(s, o, 64);
-  if (c == 0) st.part[(int64_t)blockIdx.x * M + row] = make_float2(m, s);
-  if (col < N && lg.target[row] == col) st.at_target[row] = v;
-}
-
-// (m, s) of two runs
-__device__ __forceinline__ void join_runs(float& m, float& s, float m2, float s2) {
-  const float top = fmaxf(m, m2);
-  // a run without a column is (-inf, 0)
-  const float a = m == -INFINITY ? 0.0f : s * __builtin_amdgcn_exp2f(m - top);
-  const float b = m2 == -INFINITY ? 0.0f : s2 * __builtin_amdgcn_exp2f(m2 - top);
-  m = top;
-  s = a + b;
-}
-
 // R rows of P runs each per workgroup, the runs dealt to 256 / R lanes in order
 template <int R>
 __global__ __launch_bounds__(256) void loss_join(const float2* __restrict__ part, int P, int M,
@@ -313,57 +300,6 @@ __global__ __launch_bounds__(C::kThreads) void grads_tile(
         grads_out<C, kTileLds<E4M3, C>>(smem, acc, m0, n0, M, N, k, lg, gr);
       });
 }
-template <int NW>
-__global__ __launch_bounds__(NW * 64) void grads_few(const uint8_t* __restrict__ A,
-                                                     const uint8_t* __restrict__ B, int M, int N,
-                                                     int K, Logits lg, Grads gr) {
-  __shared__ FewParts<1, 1, NW> part;
-  const int n0 = blockIdx.x * 16;
-  few_product<E4M3, 1, 1, NW, 1>(part, A, B, M, N, K, n0, Exponents{});
-  const float k = lg.k();
-  const int row = threadIdx.x / 16, c = threadIdx.x % 16;
-  if (row >= M) return;
-  const GradRow r(lg, gr, row);
-  gr.G[(int64_t)row * gr.ldg + n0 + c] =
-      (_Float16)r.of(few_sum<1, 1, NW>(part, row, c), k, n0 + c, N);
-}
-
-// out[d x ld] = dec(w[V x d])^T as float16, columns V .. ld - 1 zero (ld a multiple of
-// 64, d of 16): 64 x 128 elements a workgroup, turned in LDS
-__global__ __launch_bounds__(256) void weight_turn(const uint8_t* __restrict__ w, int V, int d,
-                                                   _Float16* __restrict__ out, int64_t ld) {
-  constexpr int ROWS = 64, COLS = 128, PAD = COLS + 2;
-  __shared__ _Float16 t[ROWS][PAD];
-  const int v0 = blockIdx.x * ROWS, c0 = blockIdx.y * COLS;
-  typedef _Float16 H2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = threadIdx.x / 8 + h * 32, c = threadIdx.x % 8 * 16;
-    const bool live = v0 + r < V && c0 + c < d;
-    const uint4 q = live ? *reinterpret_cast<const uint4*>(w + (int64_t)(v0 + r) * d + c0 + c)
-                         : make_uint4(0, 0, 0, 0);
-    const uint32_t x[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      *reinterpret_cast<H2*>(&t[r][c + 4 * i]) =
-          __builtin_bit_cast(H2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[i], 1.0f, false));
-      *reinterpret_cast<H2*>(&t[r][c + 4 * i + 2]) =
-          __builtin_bit_cast(H2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[i], 1.0f, true));
-    }
-  }
-  __syncthreads();
-  typedef _Float16 H8 __attribute__((ext_vector_type(8)));
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int c = threadIdx.x / 8 + p * 32, r = threadIdx.x % 8 * 8;
-    if (c0 + c >= d) continue;
-    H8 h;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = t[r + i][c];
-    *reinterpret_cast<H8*>(out + (int64_t)(c0 + c) * ld + v0 + r) = h;
-  }
-}
-
 // dx of all pieces up to this one: sums in `sums` between pieces, dx itself at the last
 struct DxOut {
   const int64_t* target;
@@ -397,15 +333,15 @@ __device__ __forceinline__ void dx_out8(float (&v)[8], int row, int64_t at, cons
 template <class C, int PER_CU, class OT>
 __global__ __launch_bounds__(C::kThreads, PER_CU) void dx_pipe(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
-    int tilesN, DxOut o) {
+    int tilesN, int rows, DxOut o) {
   int tm, tn;
   gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
   const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
   const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
-  pipe_product<F16Wide, C, PER_CU>(
-      A, B, M, N, K, m0, n0, Exponents{}, [] { return 0; },
+  pipe_product<F16ByE4M3Wide, C, PER_CU>(
+      A, B, M, N, K, m0, n0, Exponents{nullptr, nullptr, 0, rows}, [] { return 0; },
       [&](const auto& acc, int, uint8_t* smem) {
-        rows_through_lds<C, Ring<F16Wide, C, PER_CU>::kLds>(
+        rows_through_lds<C, Ring<F16ByE4M3Wide, C, PER_CU>::kLds>(
             smem, acc, m0, n0, M, N, [&](int row, int col, float(&v)[8]) {
               dx_out8<OT>(v, row, (int64_t)row * N + col, o);
             });
@@ -415,15 +351,15 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void dx_pipe(
 template <class C, class OT, bool SPLIT>
 __global__ __launch_bounds__(C::kThreads) void dx_tile(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
-    int tilesN, DxOut o, float* __restrict__ part, int kc) {
+    int tilesN, int rows, DxOut o, float* __restrict__ part, int kc) {
   int tm, tn;
   const int nt = tilesM * tilesN, sp = SPLIT ? (int)blockIdx.x / nt : 0;
   gemm::tile_of(gemm::xcd_remap((int)blockIdx.x - sp * nt, nt), tilesM, tilesN, tm, tn);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
-  tile_product<F16, C>(
-      A, B, M, N, K, m0, n0, SPLIT ? sp * kc : 0, SPLIT ? sp * kc + kc : INT32_MAX, Exponents{},
-      [] { return 0; }, [&](const auto& acc, int, uint8_t* smem) {
-        rows_through_lds<C, kTileLds<F16, C>>(
+  tile_product<F16ByE4M3, C>(
+      A, B, M, N, K, m0, n0, SPLIT ? sp * kc : 0, SPLIT ? sp * kc + kc : INT32_MAX,
+      Exponents{nullptr, nullptr, 0, rows}, [] { return 0; }, [&](const auto& acc, int, uint8_t* smem) {
+        rows_through_lds<C, kTileLds<F16ByE4M3, C>>(
             smem, acc, m0, n0, M, N, [&](int row, int col, float(&v)[8]) {
               if constexpr (SPLIT)
                 store_elems<8>(part + ((int64_t)sp * M + row) * N + col, v);
@@ -482,24 +418,26 @@ void launch_logits_bwd(const uint8_t* x, const uint8_t* w, int64_t T, int64_t d,
 }
 
 template <class C, int PIPE, class OT>
-void launch_dx(const uint8_t* g, const uint8_t* w, int64_t T, int64_t d, int64_t K,
+void launch_dx(const uint8_t* g, const uint8_t* w, int64_t T, int64_t d, int64_t K, int64_t rows,
                const DxOut& o, hipStream_t s) {
   const int tM = (int)ceil_div64(T, C::BM), tN = (int)ceil_div64(d, C::BN);
   if constexpr (PIPE > 0)
-    dx_pipe<C, PIPE, OT><<<tM * tN, C::kThreads, 0, s>>>(g, w, (int)T, (int)d, (int)K, tM, tN, o);
+    dx_pipe<C, PIPE, OT><<<tM * tN, C::kThreads, 0, s>>>(g, w, (int)T, (int)d, (int)K, tM, tN,
+                                                         (int)rows, o);
   else
-    dx_tile<C, OT, false><<<tM * tN, C::kThreads, 0, s>>>(g, w, (int)T, (int)d, (int)K, tM, tN, o,
-                                                          nullptr, 0);
+    dx_tile<C, OT, false><<<tM * tN, C::kThreads, 0, s>>>(g, w, (int)T, (int)d, (int)K, tM, tN,
+                                                          (int)rows, o, nullptr, 0);
 }
 
 template <class OT>
 hipError_t run_dx_product(const BwdPlan& p, const uint8_t* g, const uint8_t* w, int64_t T,
-                          int64_t d, int64_t K, const DxOut& o, float* part, hipStream_t s) {
+                          int64_t d, int64_t K, int64_t rows, const DxOut& o, float* part,
+                          hipStream_t s) {
   if (p.splits > 1) {
     using C = T128;
     const int tM = (int)ceil_div64(T, C::BM), tN = (int)ceil_div64(d, C::BN);
     dx_tile<C, OT, true><<<tM * tN * p.splits, C::kThreads, 0, s>>>(
-        g, w, (int)T, (int)d, (int)K, tM, tN, o, part, p.kc);
+        g, w, (int)T, (int)d, (int)K, tM, tN, (int)rows, o, part, p.kc);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int blocks = (int)std::min<int64_t>((T * d / 8 + 255) / 256, 2048);
@@ -507,11 +445,11 @@ hipError_t run_dx_product(const BwdPlan& p, const uint8_t* g, const uint8_t* w, 
     return hipGetLastError();
   }
   switch (cheapest(kDxKinds, T, d, K)) {
-    case k256: launch_dx<P256, 1, OT>(g, w, T, d, K, o, s); break;
-    case k256x128: launch_dx<P256x128, 2, OT>(g, w, T, d, K, o, s); break;
-    case k128: launch_dx<P128, 2, OT>(g, w, T, d, K, o, s); break;
-    case k64: launch_dx<T64, 0, OT>(g, w, T, d, K, o, s); break;
-    default: launch_dx<T32, 0, OT>(g, w, T, d, K, o, s); break;
+    case k256: launch_dx<P256, 1, OT>(g, w, T, d, K, rows, o, s); break;
+    case k256x128: launch_dx<P256x128, 2, OT>(g, w, T, d, K, rows, o, s); break;
+    case k128: launch_dx<P128, 2, OT>(g, w, T, d, K, rows, o, s); break;
+    case k64: launch_dx<T64, 0, OT>(g, w, T, d, K, rows, o, s); break;
+    default: launch_dx<T32, 0, OT>(g, w, T, d, K, rows, o, s); break;
   }
   return hipGetLastError();
 }
@@ -542,16 +480,11 @@ hipError_t launch_cross_entropy_fwd(const uint8_t* xq, const float* s_x, const u
     const uint8_t* x = xq + r0 * d;
     const Logits lg{s_x, s_w, target + r0};
     const Stats st{(float2*)((char*)ws + first), (float*)ws};
-    if (n <= kFew) {
-      loss_few<kFewNW><<<(int)ceil_div64(V, 16), kFewNW * 64, 0, s>>>(x, wq, (int)n, (int)V, (int)d,
-                                                                      lg, st);
-    } else {
-      switch (loss_kind(n, V, d)) {
-        case kLoss256: launch_logits_fwd<P256, 1>(x, wq, n, d, V, lg, st, s); break;
-        case kLoss128: launch_logits_fwd<P128, 2>(x, wq, n, d, V, lg, st, s); break;
-        case kLoss64: launch_logits_fwd<T64, 0>(x, wq, n, d, V, lg, st, s); break;
-        default: launch_logits_fwd<T32, 0>(x, wq, n, d, V, lg, st, s); break;
-      }
+    switch (loss_kind(n, V, d)) {
+      case kLoss256: launch_logits_fwd<P256, 1>(x, wq, n, d, V, lg, st, s); break;
+      case kLoss128: launch_logits_fwd<P128, 2>(x, wq, n, d, V, lg, st, s); break;
+      case kLoss64: launch_logits_fwd<T64, 0>(x, wq, n, d, V, lg, st, s); break;
+      default: launch_logits_fwd<T32, 0>(x, wq, n, d, V, lg, st, s); break;
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -593,11 +526,10 @@ hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const u
     const BwdPlan p = bwd_plan(n, d, V, dx_type);
     const Logits lg{s_x, s_w, target + r0};
     uint8_t* const g = (uint8_t*)ws;
-    uint8_t* const wt = g + p.g;
     void* const to = (uint8_t*)dx + r0 * d * (dx_type == 0 ? 4 : 2);
-    float* const sums = dx_type == 0 ? (float*)to : (float*)(wt + p.w);
-    float* const part = (float*)(wt + p.w + p.sums);
-    float* const at_target = (float*)(wt + p.w + p.sums + p.part);
+    float* const sums = dx_type == 0 ? (float*)to : (float*)(g + p.g);
+    float* const part = (float*)(g + p.g + p.sums);
+    float* const at_target = (float*)(g + p.g + p.sums + p.part);
     target_grads<<<(unsigned)ceil_div64(n, 4), 256, 0, s>>>(x, wq, (int)n, (int)d, V, s_x, s_w,
                                                             lg.target, lse + r0, at_target);
     hipError_t e = hipGetLastError();
@@ -606,27 +538,18 @@ hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const u
       const int64_t cols = std::min(p.width, V - v0), ld = up(cols, 64);
       const uint8_t* w = wq + v0 * d;
       const Grads gr{lse + r0, at_target, (_Float16*)g, ld, (int)v0};
-      if (n <= kFew) {
-        grads_few<kFewNW><<<(int)(ld / 16), kFewNW * 64, 0, s>>>(x, w, (int)n, (int)cols, (int)d,
-                                                                 lg, gr);
-      } else {
-        switch (cheapest(kGradKinds, n, ld, d)) {
-          case k256x128: launch_logits_bwd<P256x128, 2>(x, w, n, d, cols, lg, gr, s); break;
-          case k128: launch_logits_bwd<P128, 2>(x, w, n, d, cols, lg, gr, s); break;
-          case k64: launch_logits_bwd<T64, 0>(x, w, n, d, cols, lg, gr, s); break;
-          default: launch_logits_bwd<T32, 0>(x, w, n, d, cols, lg, gr, s); break;
-        }
+      switch (cheapest(kGradKinds, n, ld, d)) {
+        case k256x128: launch_logits_bwd<P256x128, 2>(x, w, n, d, cols, lg, gr, s); break;
+        case k128: launch_logits_bwd<P128, 2>(x, w, n, d, cols, lg, gr, s); break;
+        case k64: launch_logits_bwd<T64, 0>(x, w, n, d, cols, lg, gr, s); break;
+        default: launch_logits_bwd<T32, 0>(x, w, n, d, cols, lg, gr, s); break;
       }
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      weight_turn<<<dim3((unsigned)(ld / 64), (unsigned)ceil_div64(d, 128)), 256, 0, s>>>(
-          w, (int)cols, (int)d, (_Float16*)wt, ld);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
       const bool last = v0 + p.width >= V;
       const DxOut o{lg.target, dloss + r0, s_w, sums, last ? to : nullptr, V, v0 == 0};
-      e = dx_type == 0 ? run_dx_product<float>(p, g, wt, n, d, ld * 2, o, part, s)
-                       : run_dx_product<__bf16>(p, g, wt, n, d, ld * 2, o, part, s);
+      e = dx_type == 0 ? run_dx_product<float>(p, g, w, n, d, ld * 2, cols, o, part, s)
+                       : run_dx_product<__bf16>(p, g, w, n, d, ld * 2, cols, o, part, s);
       if (e != hipSuccess) return e;
     }
   }

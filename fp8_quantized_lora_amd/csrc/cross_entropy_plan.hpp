@@ -9,15 +9,13 @@
 namespace falq {
 namespace {
 
-// up to kFew tokens one kernel of 16 waves a workgroup streams the weight
-constexpr int kFew = 16, kFewNW = 16;
-
 // The forward's tiles, by the model of linear_act_plan.hpp with its own costs: the
 // products as float16 take twice the steps' time, and there is nothing to store.
 //   4096 x 32000 x 4096: 747 us in 256 x 256, 827 in 128 x 128
 //   4096 x 50000 x 1024: 386 and 365; 333 x 131071 x 1040 174 and 109
 //   128 x 32000 x 4096: 35 in 128 x 128, 50 in 64 x 64; 64 tokens 34 and 26
-//   17 x 32000 x 4096: 26 in 64 x 64, 23 in 32 x 64
+//   17 x 32000 x 4096: 26 in 64 x 64, 23 in 32 x 64; 1 token 21.3 (with the weight
+//   streamed through the registers as in linear_act_few.hpp 23.6, and 31 for 16)
 enum LossKind { kLoss256, kLoss128, kLoss64, kLoss32x64, kLossKinds };
 constexpr TileCost kLossTile[kLossKinds] = {
     {256, 256, 1, 5.0f, 8.0f, {{2.65f, 2.65f}, {2.90f, 2.90f}}},
@@ -69,22 +67,16 @@ int64_t up(int64_t a, int64_t b) { return ceil_div64(a, b) * b; }
 constexpr int64_t kStrip = 16384;
 int64_t strip_of(int64_t T) { return std::min(T, kStrip); }
 
-// runs of columns of the forward's partial sums: a wave's of a tile, or 16
+// runs of columns of the forward's partial sums: the tiles'
 int64_t runs_of(int64_t T, int64_t d, int64_t V) {
-  if (T <= kFew) return ceil_div64(V, 16);
-  switch (loss_kind(T, V, d)) {
-    case kLoss256: return ceil_div64(V, 256) * 2;
-    case kLoss128: return ceil_div64(V, 128) * 2;
-    case kLoss64: return ceil_div64(V, 64) * 2;
-    default: return ceil_div64(V, 64) * 4;
-  }
+  return ceil_div64(V, kLossTile[loss_kind(T, V, d)].bn);
 }
 
-// pieces of the vocabulary: as many as keep G and the turned weight within kPiece
-// bytes each, of one width, a multiple of 64
+// pieces of the vocabulary: as many as keep G within kPiece bytes, of one width, a
+// multiple of 64
 constexpr int64_t kPiece = (int64_t)128 << 20;
-int64_t piece_width(int64_t T, int64_t d, int64_t V) {
-  const int64_t most = std::clamp<int64_t>(kPiece / (2 * std::max(T, d)), 2048, 1 << 21);
+int64_t piece_width(int64_t T, int64_t V) {
+  const int64_t most = std::clamp<int64_t>(kPiece / (2 * T), 2048, 1 << 21);
   return up(ceil_div64(V, ceil_div64(V, most)), 64);
 }
 
@@ -101,15 +93,14 @@ int dx_splits(int64_t T, int64_t d, int64_t width, int& kc) {
 struct BwdPlan {
   int64_t width;
   int splits, kc;
-  size_t g, w, sums, part, at_target;                        // bytes, multiples of 256
-  size_t bytes() const { return g + w + sums + part + at_target; }
+  size_t g, sums, part, at_target;                        // bytes, multiples of 256
+  size_t bytes() const { return g + sums + part + at_target; }
 };
 BwdPlan bwd_plan(int64_t T, int64_t d, int64_t V, int dx_type) {
   BwdPlan p;
-  p.width = piece_width(T, d, V);
+  p.width = piece_width(T, V);
   p.splits = dx_splits(T, d, p.width, p.kc);
   p.g = (size_t)up(T * p.width * 2, 256);
-  p.w = (size_t)up(d * p.width * 2, 256);
   // float32 gradients collect in place
   p.sums = dx_type != 0 && p.width < V ? (size_t)up(T * d * 4, 256) : 0;
   p.part = p.splits > 1 ? (size_t)up(p.splits * T * d * 4, 256) : 0;

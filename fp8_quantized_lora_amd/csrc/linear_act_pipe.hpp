@@ -63,7 +63,7 @@ __device__ __forceinline__ void each(F&& f) {
 template <class OP, int I0, int J0, int MB, int NB, int HM, int HN, class F>
 __device__ __forceinline__ void quarter(typename OP::Acc (&acc)[MB][NB],
                                         const typename OP::Frag (&a)[HM],
-                                        const typename OP::Frag (&b)[HN], F&& with) {
+                                        const typename OP::FragB (&b)[HN], F&& with) {
   typedef typename OP::Acc Acc;
   constexpr int BLOCKS = HM * HN;
   if constexpr (!OP::kConverted) {
@@ -76,25 +76,27 @@ __device__ __forceinline__ void quarter(typename OP::Acc (&acc)[MB][NB],
     });
   } else {
     // the next product's operands are converted between this one's blocks
+    constexpr int CA = OP::kConvertsA ? HM : 0;              // A's operands, then B's
     v4i ca[2][HM], cb[2][HN];
-    auto convert = [&](auto to, auto o) FALQ_INLINE {        // operand o, A's first
+    auto convert = [&](auto to, auto o) FALQ_INLINE {
       constexpr int P = decltype(to)::value, O = decltype(o)::value;
-      if constexpr (O < HM)
-        ca[P % 2][O] = OP::template convert<P>(a[O]);
+      if constexpr (O < CA)
+        ca[P % 2][O] = OP::template a_of<P>(a[O]);
       else
-        cb[P % 2][O - HM] = OP::template convert<P>(b[O - HM]);
+        cb[P % 2][O - CA] = OP::template b_of<P>(b[O - CA]);
     };
     using First = std::integral_constant<int, 0>;
-    each<HM + HN>([&](auto o) FALQ_INLINE { convert(First{}, o); });
+    each<CA + HN>([&](auto o) FALQ_INLINE { convert(First{}, o); });
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_nop 1");                                 // an operand's two wait states
     each<BLOCKS * OP::kProducts>([&](auto t) FALQ_INLINE {
       constexpr int T = decltype(t)::value, B = T % BLOCKS, P = T / BLOCKS;
       static_assert(in_acc<Acc, MB>(J0 + B % HN), "accumulators");
-      mfma_f16_in_place(acc[I0 + B / HN][J0 + B % HN], cb[P % 2][B % HN], ca[P % 2][B / HN]);
+      const v4i& row = OP::kConvertsA ? ca[P % 2][B / HN] : OP::template a_of<P>(a[B / HN]);
+      mfma_f16_in_place(acc[I0 + B / HN][J0 + B % HN], cb[P % 2][B % HN], row);
       if constexpr (P + 1 < OP::kProducts) {
         using Next = std::integral_constant<int, P + 1>;
-        constexpr int O0 = B * (HM + HN) / BLOCKS, O1 = (B + 1) * (HM + HN) / BLOCKS;
+        constexpr int O0 = B * (CA + HN) / BLOCKS, O1 = (B + 1) * (CA + HN) / BLOCKS;
         each<O1 - O0>([&](auto o) FALQ_INLINE {
           convert(Next{}, std::integral_constant<int, O0 + decltype(o)::value>{});
         });
@@ -125,10 +127,12 @@ __device__ __forceinline__ void settle(ACC (&acc)[MB][NB]) {
 }
 
 // The LDS of pipe_product: a ring of slots, each half the rows of either operand
-// for one K step, and their exponent bytes, where there are any (8 a row).
+// for one K step (of a turned B the step's 64 rows of half the columns), and their
+// exponent bytes, where there are any (8 a row).
 template <class OP, class C, int PER_CU>
 struct Ring {
-  static constexpr int UA = C::BM / 2 * C::BK, CODES = UA + C::BN / 2 * C::BK;
+  static constexpr int UA = C::BM / 2 * C::BK;
+  static constexpr int CODES = UA + C::BN / 2 * (OP::kTurned ? 64 : C::BK);
   static constexpr int EXPS = 1024;                          // of half the rows, 8 each
   static constexpr int SLOT = CODES + (OP::kScaled ? 2 * EXPS : 0);
   static constexpr int FIT = 160 * 1024 / PER_CU / SLOT, SLOTS = FIT < 5 ? FIT : 5;
@@ -148,6 +152,7 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
                                              OUT&& out) {
   using R = Ring<OP, C, PER_CU>;
   typedef typename OP::Frag Frag;
+  typedef typename OP::FragB FragB;
   // (declared here: through a pointer the compiler keeps an address per fragment, and
   // spills)
   __shared__ __attribute__((aligned(1024))) uint8_t smem[R::kLds];
@@ -155,13 +160,20 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
   constexpr int HM = MB / 2, HN = NB / 2, H = OP::kProducts;
   static_assert(MB % 2 == 0 && NB % 2 == 0, "quarters");
   constexpr int UA = R::UA, SLOT = R::SLOT, SLOTS = R::SLOTS, AHEAD = SLOTS - 2;
-  constexpr int LA = C::AI / 2, LB = C::BI / 2, LPP = LA + LB;
+  constexpr bool TURNED = OP::kTurned;
+  constexpr int LA = C::AI / 2, LB = TURNED ? C::BN / 2 * 64 / 1024 / 4 : C::BI / 2;
+  constexpr int LPP = LA + LB;
+  // turned: bytes and chunks of a row of half the columns, a wave's chunks of it, rows a load
+  constexpr int RB = C::BN / 2, CPR = RB / 16, CPW = C::WTN / 2 / 16, RPL = 64 / CPR;
+  static_assert(!TURNED || (LB * 4 * 1024 == RB * 64 && CPW == NB), "whole loads");
   static_assert(C::AI % 2 == 0 && C::BI % 2 == 0 && C::NW == 4, "whole loads per slot");
   static_assert(!OP::kScaled || (C::BM * 4 <= R::EXPS && C::BN * 4 <= R::EXPS), "exponents");
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = w / C::WGN, wn = w % C::WGN;
-  const int nk = K / BK, rem = K % BK, all = nk + (rem > 0), last = 2 * all - 1;
+  // whole K steps, and the bytes or (turned) the rows of B of one that is not
+  const int nk = TURNED ? ex.rows_b / 64 : K / BK, rem = TURNED ? 0 : K % BK;
+  const int all = (K + BK - 1) / BK, last = 2 * all - 1;
 
   typename OP::Acc acc[MB][NB];
 #pragma unroll
@@ -173,7 +185,8 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
   // into the matrix) and swizzled chunk as its offset.  Half h of an operand is
   // half h of each wave's rows.
   const uint8_t* tA = A + (int64_t)m0 * K;
-  const uint8_t* tB = B + (int64_t)n0 * K;
+  const uint8_t* tB = TURNED ? B + n0 : B + (int64_t)n0 * K;
+  const int64_t stepB = TURNED ? (int64_t)64 * N : BK;
   const int lrow = lane >> 3, lslot = lane & 7;
   uint32_t vA[2][LA], vB[2][LB];
 #pragma unroll
@@ -186,6 +199,12 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
     }
 #pragma unroll
     for (int j = 0; j < LB; ++j) {
+      if constexpr (TURNED) {
+        const int r = (w * LB + j) * RPL + lane / CPR, c = (lane % CPR) ^ turned_swz<CPR>(r);
+        vB[h][j] = (uint32_t)r * (uint32_t)N +
+                   min(c / CPW * C::WTN + (h * CPW + c % CPW) * 16, N - 16 - n0);
+        continue;
+      }
       const int r = (w * LB + j) * 8 + lrow, row = (r / (C::WTN / 2) * 2 + h) * (C::WTN / 2) +
                                                    r % (C::WTN / 2);
       vB[h][j] = (uint32_t)min(row, N - 1 - n0) * (uint32_t)K + (lslot ^ gemm::dma::swz(r)) * 16;
@@ -215,7 +234,7 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
       load16_to_lds_at(tA + (int64_t)kt * BK, vA[decltype(ha)::value][J],
                        ldsA + slot * SLOT + J * 1024);
     else if constexpr (J < LPP)
-      load16_to_lds_at(tB + (int64_t)kt * BK, vB[decltype(hb)::value][J - LA],
+      load16_to_lds_at(tB + kt * stepB, vB[decltype(hb)::value][J - LA],
                        ldsB + slot * SLOT + (J - LA) * 1024);
   };
   auto load_exponents = [&](auto ha, auto hb, int kt, int slot) FALQ_INLINE {
@@ -234,7 +253,13 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
     }
     each<LPP>([&](auto j) FALQ_INLINE {
       constexpr int J = decltype(j)::value;
-      if constexpr (J < LA) {
+      if constexpr (TURNED && J < LA) {
+        load(ha, hb, j, kt, slot);
+      } else if constexpr (TURNED) {                         // rows past the last: the last
+        const int r = (w * LB + J - LA) * RPL + lane / CPR, back = max(0, nk * 64 + r + 1 - ex.rows_b);
+        load16_to_lds_at(tB + kt * stepB, vB[decltype(hb)::value][J - LA] - (uint32_t)back * (uint32_t)N,
+                         ldsB + slot * SLOT + (J - LA) * 1024);
+      } else if constexpr (J < LA) {
         const int co = (lslot ^ gemm::dma::swz((w * LA + J) * 8 + lrow)) * 16;
         load16_to_lds_at(tA + (int64_t)nk * BK, vA[decltype(ha)::value][J] - co + min(co, rem - 16),
                          ldsA + slot * SLOT + J * 1024);
@@ -281,9 +306,25 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
     constexpr int I = decltype(i)::value * BLK;
     return frag_at(at + offA + I * BK, at + eA + I * 8);
   };
+  // turned: the lane's eight bytes of fragment 0 and 1 of a half of B
+  int tB0 = 0, tB1 = 0;
+  if constexpr (TURNED) {
+    const int row = turned_row(lane), c = wn * CPW + ((lane >> 4) & 1), sz = turned_swz<CPR>(row);
+    const int base = UA + (g * 8 + row) * RB + (lane & 1) * 8;
+    tB0 = base + (c ^ sz) * 16;
+    tB1 = base + ((c + 2) ^ sz) * 16;
+  }
   auto fragB = [&](auto i, int at) FALQ_INLINE {
     constexpr int I = decltype(i)::value * BLK;
-    return frag_at(at + offB + I * BK, at + eB + I * 8);
+    if constexpr (TURNED) {
+      static_assert(HN <= 2, "offsets");
+      FragB f;
+#pragma unroll
+      for (int p = 0; p < OP::kParts; ++p)
+        f.h[p] = read_turned(smem + at + (I == 0 ? tB0 : tB1) + p * 16 * RB);
+      return f;
+    } else
+      return frag_at(at + offB + I * BK, at + eB + I * 8);
   };
   // with every second product a fragment of the group f (of 32 rows: every eighth)
   constexpr int EVERY = OP::kBlock == 16 ? 2 : HM * HN * H >= 16 ? 8 : 4;
@@ -292,7 +333,8 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
     static_assert(T > 0 || (N - 1) * EVERY < HM * HN * H, "all within the quarter");
     if constexpr (T % EVERY == 0 && I < N) f[I] = of(std::integral_constant<int, I>{}, at);
   };
-  Frag a0[HM], a_next[LEAN ? 1 : HM], b0[HN], b1[HN];
+  Frag a0[HM], a_next[LEAN ? 1 : HM];
+  FragB b0[HN], b1[HN];
   Frag(&a1)[HM] = *(Frag(*)[HM])(LEAN ? a0 : a_next);
   auto read_a = [&](int at) FALQ_INLINE {
     each<HM>([&](auto i) FALQ_INLINE { a0[decltype(i)::value] = fragA(i, at); });
@@ -328,8 +370,8 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
   auto step = [&](auto par, auto whole, int k, int& slot) FALQ_INLINE {
     constexpr bool P = decltype(par)::value, WHOLE = decltype(whole)::value;
     constexpr int jf = P ? HN : 0, jo = HN - jf;
-    Frag(&f)[HN] = P ? b1 : b0;
-    Frag(&other)[HN] = P ? b0 : b1;
+    FragB(&f)[HN] = P ? b1 : b0;
+    FragB(&other)[HN] = P ? b0 : b1;
     // the pairs that take the slots freed: SLOTS - 1 on from those read
     constexpr int D1 = SLOTS / 2, D2 = (SLOTS + 1) / 2, U = 2 * HM * HN * H / LPP;
     static_assert(U > 0, "a product for each load");
@@ -384,7 +426,7 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
     });
     wait_pairs(std::integral_constant<int, SLOTS - 1>{}, last);
     barrier_no_drain();
-    if (nk == 0) clear(0);
+    if (nk == 0 && rem) clear(0);
     read_a(0);
     each<HN>([&](auto j) FALQ_INLINE { b0[decltype(j)::value] = fragB(j, 0); });
   }

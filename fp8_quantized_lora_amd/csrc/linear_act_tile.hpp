@@ -148,9 +148,12 @@ __device__ __forceinline__ void tile_out(uint8_t* smem, const ACC (&acc)[MB][NB]
   }
 }
 
-// LDS of tile_product: the stages, then their exponent bytes, where there are any.
+// LDS of tile_product: the stages (a step's rows of either operand; of a turned B the
+// step's 64 rows of the tile's columns), then their exponent bytes, where there are any.
 template <class OP, class C>
-constexpr int kTileLds = C::S * (C::STAGE + (OP::kScaled ? (C::BM + C::BN) * 8 : 0));
+constexpr int kTileStage = OP::kTurned ? C::BM * C::BK + 64 * C::BN : C::STAGE;
+template <class OP, class C>
+constexpr int kTileLds = C::S * (kTileStage<OP, C> + (OP::kScaled ? (C::BM + C::BN) * 8 : 0));
 
 // The tile at (m0, n0) over K steps k_lo .. steps - 1 (of all that K has): before()
 // is called ahead of the loop, out(acc, what it gave, LDS) behind it, with the LDS
@@ -162,13 +165,18 @@ __device__ __forceinline__ void tile_product(const uint8_t* __restrict__ A,
                                              const Exponents& ex, BEFORE&& before, OUT&& out) {
   constexpr int BK = C::BK, MB = C::MB, NB = C::NB;
   // exponent bytes of a stage: 8 a row, a lane loads those of two rows
-  constexpr int EROWS = C::BM + C::BN, ELANES = EROWS / 2 / C::NW, LPS = C::LPS + OP::kScaled;
+  constexpr int EROWS = C::BM + C::BN, ELANES = EROWS / 2 / C::NW;
+  constexpr bool TURNED = OP::kTurned;
+  constexpr int STAGE = kTileStage<OP, C>, BI = TURNED ? 64 * C::BN / 1024 / C::NW : C::BI;
+  constexpr int LPS = C::AI + BI + OP::kScaled, CPR = C::BN / 16, RPL = 64 / CPR;
+  static_assert(!TURNED || BI * C::NW * 1024 == 64 * C::BN, "whole loads");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kTileLds<OP, C>];
   static_assert(!OP::kScaled || (ELANES * 2 * C::NW == EROWS && ELANES <= 64), "whole rows");
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w / C::WGN, wn = w % C::WGN;
   // the step at nk, if any, is the one of rem bytes
-  const int nk = K / BK, rem = K % BK, all = nk + (rem > 0);
-  const int steps = min(all, k_end);
+  // (turned: the one of fewer than 64 rows of B, whose columns of A are zeros)
+  const int nk = TURNED ? ex.rows_b / 64 : K / BK, rem = TURNED ? 0 : K % BK;
+  const int all = (K + BK - 1) / BK, steps = min(all, k_end);
 
   v4f acc[MB][NB];
 #pragma unroll
@@ -182,16 +190,24 @@ __device__ __forceinline__ void tile_product(const uint8_t* __restrict__ A,
   // the swizzled chunk
   const int lrow = lane >> 3, lslot = lane & 7;
   const uint8_t* gA[C::AI];
-  const uint8_t* gB[C::BI];
+  const uint8_t* gB[BI];
 #pragma unroll
   for (int j = 0; j < C::AI; ++j) {
     const int row = (w * C::AI + j) * 8 + lrow;
     gA[j] = A + (int64_t)min(m0 + row, M - 1) * K + ((lslot ^ gemm::dma::swz(row)) * 16);
   }
+  // turned: row lane / CPR of RPL, its chunk of columns clamped into the matrix
+  const int trow = lane / CPR;
 #pragma unroll
-  for (int j = 0; j < C::BI; ++j) {
-    const int row = (w * C::BI + j) * 8 + lrow;
-    gB[j] = B + (int64_t)min(n0 + row, N - 1) * K + ((lslot ^ gemm::dma::swz(row)) * 16);
+  for (int j = 0; j < BI; ++j) {
+    if constexpr (TURNED) {
+      const int row = (w * BI + j) * RPL + trow;
+      const int chunk = (lane % CPR) ^ turned_swz<CPR>(row);
+      gB[j] = B + (int64_t)row * N + min(n0 + chunk * 16, N - 16);
+    } else {
+      const int row = (w * BI + j) * 8 + lrow;
+      gB[j] = B + (int64_t)min(n0 + row, N - 1) * K + ((lslot ^ gemm::dma::swz(row)) * 16);
+    }
   }
   const uint8_t* gE = nullptr;
   int64_t estep = 0;
@@ -206,37 +222,44 @@ __device__ __forceinline__ void tile_product(const uint8_t* __restrict__ A,
     if constexpr (OP::kScaled)
       if (lane < ELANES)
         load16_to_lds(gE + kt * estep,
-                      __builtin_amdgcn_readfirstlane(lds_offset(smem) + C::S * C::STAGE +
+                      __builtin_amdgcn_readfirstlane(lds_offset(smem) + C::S * STAGE +
                                                      (stage * EROWS + w * ELANES * 2) * 8));
   };
   auto issue = [&](int stage, int k0) {
-    const uint32_t base = lds_offset(smem + stage * C::STAGE);
+    const uint32_t base = lds_offset(smem + stage * STAGE);
     const uint32_t la = __builtin_amdgcn_readfirstlane(base + w * C::AI * 1024);
-    const uint32_t lb = __builtin_amdgcn_readfirstlane(base + C::BM * BK + w * C::BI * 1024);
+    const uint32_t lb = __builtin_amdgcn_readfirstlane(base + C::BM * BK + w * BI * 1024);
 #pragma unroll
     for (int j = 0; j < C::AI; ++j) load16_to_lds(gA[j] + k0, la + j * 1024);
 #pragma unroll
-    for (int j = 0; j < C::BI; ++j) load16_to_lds(gB[j] + k0, lb + j * 1024);
+    for (int j = 0; j < BI; ++j) {
+      int64_t at = k0;
+      if constexpr (TURNED) {                                // rows past the last: the last
+        const int row = (w * BI + j) * RPL + trow, first = k0 / 2;
+        at = (int64_t)(first + min(0, ex.rows_b - 1 - first - row)) * N;
+      }
+      load16_to_lds(gB[j] + at, lb + j * 1024);
+    }
   };
   // the step of fewer than BK bytes: chunks past K load the row's last chunk
   auto issue_rem = [&](int stage) {
-    const uint32_t base = lds_offset(smem + stage * C::STAGE);
+    const uint32_t base = lds_offset(smem + stage * STAGE);
     const uint32_t la = __builtin_amdgcn_readfirstlane(base + w * C::AI * 1024);
-    const uint32_t lb = __builtin_amdgcn_readfirstlane(base + C::BM * BK + w * C::BI * 1024);
+    const uint32_t lb = __builtin_amdgcn_readfirstlane(base + C::BM * BK + w * BI * 1024);
 #pragma unroll
     for (int j = 0; j < C::AI; ++j) {
       const int co = (lslot ^ gemm::dma::swz((w * C::AI + j) * 8 + lrow)) * 16;
       load16_to_lds(gA[j] + nk * BK - max(0, co - (rem - 16)), la + j * 1024);
     }
 #pragma unroll
-    for (int j = 0; j < C::BI; ++j) {
-      const int co = (lslot ^ gemm::dma::swz((w * C::BI + j) * 8 + lrow)) * 16;
+    for (int j = 0; j < BI; ++j) {
+      const int co = (lslot ^ gemm::dma::swz((w * BI + j) * 8 + lrow)) * 16;
       load16_to_lds(gB[j] + nk * BK - max(0, co - (rem - 16)), lb + j * 1024);
     }
   };
   auto fetch = [&](int kt) {
     const int stage = (kt - k_lo) % C::S;
-    if (kt < nk)
+    if (TURNED || kt < nk)
       issue(stage, kt * BK);
     else
       issue_rem(stage);
@@ -252,24 +275,45 @@ __device__ __forceinline__ void tile_product(const uint8_t* __restrict__ A,
   const int offA = (wm * C::WTM + r16) * BK, offB = C::BM * BK + (wn * C::WTN + r16) * BK;
   // the fragment of the 16 rows from byte `at` of a stage on
   auto frag = [&](int stage, int at) {
-    const uint8_t* p = smem + stage * C::STAGE + at;
+    const uint8_t* p = smem + stage * STAGE + at;
     int e = 0;
     if constexpr (OP::kScaled)
-      e = *reinterpret_cast<const typename OP::Scales*>(smem + C::S * C::STAGE +
+      e = *reinterpret_cast<const typename OP::Scales*>(smem + C::S * STAGE +
                                                         stage * EROWS * 8 + at / BK * 8 + 2 * g);
     const uint4 q[2] = {*reinterpret_cast<const uint4*>(p + o0),
                         *reinterpret_cast<const uint4*>(p + o1)};
     return OP::make(q, e);
   };
+  // of B, block j of the wave's columns
+  int tB[NB];
+  if constexpr (TURNED) {
+    const int row = turned_row(lane);
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      tB[j] = C::BM * BK + (g * 8 + row) * C::BN + (lane & 1) * 8 +
+              (((wn * C::WTN) / 16 + j) ^ turned_swz<CPR>(row)) * 16;
+  }
+  auto frag_b = [&](int stage, int j) {
+    if constexpr (TURNED) {
+      typename OP::FragB f;
+#pragma unroll
+      for (int p = 0; p < OP::kParts; ++p)
+        f.h[p] = read_turned(smem + stage * STAGE + tB[j] + p * 32 * C::BN);
+      return f;
+    } else {
+      return frag(stage, offB + j * 16 * BK);
+    }
+  };
   const auto kept = before();
   // fragment reads in the order the MFMAs consume them; next(): the loads of
   // the following stage, sent once the first fragments are in registers
   auto step = [&](int st, auto&& next) {
-    typename OP::Frag bf[NB], af[2];
+    typename OP::FragB bf[NB];
+    typename OP::Frag af[2];
     af[0] = frag(st, offA);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      bf[j] = frag(st, offB + j * 16 * BK);
+      bf[j] = frag_b(st, j);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -285,7 +329,7 @@ __device__ __forceinline__ void tile_product(const uint8_t* __restrict__ A,
     }
   };
   __builtin_amdgcn_s_waitcnt(0xC07F);                        // lgkmcnt(0)
-  const int k_whole = min(steps, nk);
+  const int k_whole = TURNED ? steps : min(steps, nk);
   for (int kt = k_lo; kt < k_whole; ++kt) {
     wait_stages<C::S - 2, LPS>(steps - 1 - kt);
     barrier_no_drain();
@@ -294,7 +338,7 @@ __device__ __forceinline__ void tile_product(const uint8_t* __restrict__ A,
     });
   }
   if (rem && steps == all) {
-    uint8_t* st = smem + (nk - k_lo) % C::S * C::STAGE;
+    uint8_t* st = smem + (nk - k_lo) % C::S * STAGE;
     wait_vmem(0);
     barrier_no_drain();
     const int valid = rem / 16;                              // chunks of K in the step

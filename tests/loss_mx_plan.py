@@ -26,8 +26,8 @@ extern "C" void loss(int64_t T, int64_t d, int64_t V, int64_t* out) {
   const int64_t n = strip_of(T);
   const BwdPlan p = bwd_plan(n, d, V, 1);
   const int64_t ld = up(std::min(p.width, V), 64);
-  out[0] = n <= kFew ? -1 : loss_kind(n, V, d);
-  out[1] = n <= kFew ? -1 : cheapest(kGradKinds, n, ld, d);
+  out[0] = loss_kind(n, V, d);
+  out[1] = cheapest(kGradKinds, n, ld, d);
   out[2] = p.splits > 1 ? -1 : cheapest(kDxKinds, n, d, ld * 2);
   out[3] = ceil_div64(V, p.width);
   out[4] = p.splits;
@@ -66,5 +66,4 @@ def mx(T, d_in, d_out):
 def loss(T, d, V):
     """(forward's kernel, G's, dx's, pieces, strips)"""
     f, g, x, pieces, _, strips = _call(_lib().loss, T, d, V)
-    return ("few" if f < 0 else LOSS_KINDS[f], "few" if g < 0 else TILE_KINDS[g],
-            "split" if x < 0 else TILE_KINDS[x], pieces, strips)
+    return LOSS_KINDS[f], TILE_KINDS[g], "split" if x < 0 else TILE_KINDS[x], pieces, strips
