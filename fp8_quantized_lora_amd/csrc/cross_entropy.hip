@@ -146,7 +146,7 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void loss_pipe(
   const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
   const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
   pipe_product<E4M3AsF16Wide, C, PER_CU>(
-      A, B, M, N, K, m0, n0, Exponents{}, [&] { return lg.k(); },
+      A, B, M, N, K, m0, n0, 0, INT32_MAX, Exponents{}, [&] { return lg.k(); },
       [&](const auto& acc, float k, uint8_t* smem) {
         stats_out<C>(smem, acc, m0, n0, M, N, k, lg, st, tn);
       });
@@ -282,7 +282,7 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void grads_pipe(
   const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
   const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
   pipe_product<E4M3, C, PER_CU>(
-      A, B, M, N, K, m0, n0, Exponents{}, [&] { return lg.k(); },
+      A, B, M, N, K, m0, n0, 0, INT32_MAX, Exponents{}, [&] { return lg.k(); },
       [&](const auto& acc, float k, uint8_t* smem) {
         grads_out<C, Ring<E4M3, C, PER_CU>::kLds>(smem, acc, m0, n0, M, N, k, lg, gr);
       });
@@ -330,20 +330,38 @@ __device__ __forceinline__ void dx_out8(float (&v)[8], int row, int64_t at, cons
   store_elems<8>((OT*)o.dx + at, v);
 }
 
-template <class C, int PER_CU, class OT>
+// The split and the tile of a workgroup: workgroups go round the eight XCDs, and the
+// tiles of a split, which share its columns of G and rows of W, stay on one, whose L2
+// then reads them once (where the splits are a multiple of eight).
+__device__ __forceinline__ int split_tile(int tilesM, int tilesN, int& tm, int& tn) {
+  const int nt = tilesM * tilesN, S = (int)gridDim.x / nt, b = (int)blockIdx.x;
+  const int j = S % 8 == 0 ? b / 8 : b;
+  const int sp = j / nt + (S % 8 == 0 ? b % 8 * (S / 8) : 0);
+  gemm::tile_of(j % nt, tilesM, tilesN, tm, tn);
+  return sp;
+}
+
+// SPLIT: as linear_act_tile, each split's sums to its plane of `part`
+template <class C, int PER_CU, class OT, bool SPLIT>
 __global__ __launch_bounds__(C::kThreads, PER_CU) void dx_pipe(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
-    int tilesN, int rows, DxOut o) {
+    int tilesN, int rows, DxOut o, float* __restrict__ part, int kc) {
   int tm, tn;
-  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
+  const int sp = SPLIT ? split_tile(tilesM, tilesN, tm, tn) : 0;
+  if constexpr (!SPLIT)
+    gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
   const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
   const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
   pipe_product<F16ByE4M3Wide, C, PER_CU>(
-      A, B, M, N, K, m0, n0, Exponents{nullptr, nullptr, 0, rows}, [] { return 0; },
+      A, B, M, N, K, m0, n0, SPLIT ? sp * kc : 0, SPLIT ? sp * kc + kc : INT32_MAX,
+      Exponents{nullptr, nullptr, 0, rows}, [] { return 0; },
       [&](const auto& acc, int, uint8_t* smem) {
         rows_through_lds<C, Ring<F16ByE4M3Wide, C, PER_CU>::kLds>(
             smem, acc, m0, n0, M, N, [&](int row, int col, float(&v)[8]) {
-              dx_out8<OT>(v, row, (int64_t)row * N + col, o);
+              if constexpr (SPLIT)
+                store_elems<8>(part + ((int64_t)sp * M + row) * N + col, v);
+              else
+                dx_out8<OT>(v, row, (int64_t)row * N + col, o);
             });
       });
 }
@@ -353,8 +371,9 @@ __global__ __launch_bounds__(C::kThreads) void dx_tile(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
     int tilesN, int rows, DxOut o, float* __restrict__ part, int kc) {
   int tm, tn;
-  const int nt = tilesM * tilesN, sp = SPLIT ? (int)blockIdx.x / nt : 0;
-  gemm::tile_of(gemm::xcd_remap((int)blockIdx.x - sp * nt, nt), tilesM, tilesN, tm, tn);
+  const int sp = SPLIT ? split_tile(tilesM, tilesN, tm, tn) : 0;
+  if constexpr (!SPLIT)
+    gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   tile_product<F16ByE4M3, C>(
       A, B, M, N, K, m0, n0, SPLIT ? sp * kc : 0, SPLIT ? sp * kc + kc : INT32_MAX,
@@ -391,7 +410,6 @@ __global__ __launch_bounds__(256) void dx_join(const float* __restrict__ part, i
 using P256 = Tile<256, 256, 2, 2>;
 using P256x128 = Tile<256, 128, 2, 2>;
 using P128 = Tile<128, 128, 2, 2>;
-using T128 = Tile<128, 128, 2, 4, 3>;
 using T64 = Tile<64, 64, 2, 2, 4>;
 using T32 = Tile<32, 64, 1, 4, 4>;
 
@@ -417,40 +435,45 @@ void launch_logits_bwd(const uint8_t* x, const uint8_t* w, int64_t T, int64_t d,
     grads_tile<C><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM, tN, lg, gr);
 }
 
-template <class C, int PIPE, class OT>
-void launch_dx(const uint8_t* g, const uint8_t* w, int64_t T, int64_t d, int64_t K, int64_t rows,
-               const DxOut& o, hipStream_t s) {
+template <class C, int PIPE, class OT, bool SPLIT>
+void launch_dx(const BwdPlan& p, const uint8_t* g, const uint8_t* w, int64_t T, int64_t d,
+               int64_t K, int64_t rows, const DxOut& o, float* part, hipStream_t s) {
   const int tM = (int)ceil_div64(T, C::BM), tN = (int)ceil_div64(d, C::BN);
   if constexpr (PIPE > 0)
-    dx_pipe<C, PIPE, OT><<<tM * tN, C::kThreads, 0, s>>>(g, w, (int)T, (int)d, (int)K, tM, tN,
-                                                         (int)rows, o);
+    dx_pipe<C, PIPE, OT, SPLIT><<<tM * tN * p.splits, C::kThreads, 0, s>>>(
+        g, w, (int)T, (int)d, (int)K, tM, tN, (int)rows, o, part, p.kc);
   else
-    dx_tile<C, OT, false><<<tM * tN, C::kThreads, 0, s>>>(g, w, (int)T, (int)d, (int)K, tM, tN,
-                                                          (int)rows, o, nullptr, 0);
+    dx_tile<C, OT, SPLIT><<<tM * tN * p.splits, C::kThreads, 0, s>>>(
+        g, w, (int)T, (int)d, (int)K, tM, tN, (int)rows, o, part, p.kc);
+}
+
+template <class OT, bool SPLIT>
+void launch_dx_kind(const BwdPlan& p, const uint8_t* g, const uint8_t* w, int64_t T, int64_t d,
+                    int64_t K, int64_t rows, const DxOut& o, float* part, hipStream_t s) {
+  switch (p.kind) {
+    case kDx256:
+      if constexpr (!SPLIT) launch_dx<P256, 1, OT, false>(p, g, w, T, d, K, rows, o, part, s);
+      break;
+    case kDx256x128: launch_dx<P256x128, 2, OT, SPLIT>(p, g, w, T, d, K, rows, o, part, s); break;
+    case kDx128: launch_dx<P128, 2, OT, SPLIT>(p, g, w, T, d, K, rows, o, part, s); break;
+    case kDx64: launch_dx<T64, 0, OT, SPLIT>(p, g, w, T, d, K, rows, o, part, s); break;
+    default: launch_dx<T32, 0, OT, SPLIT>(p, g, w, T, d, K, rows, o, part, s); break;
+  }
 }
 
 template <class OT>
 hipError_t run_dx_product(const BwdPlan& p, const uint8_t* g, const uint8_t* w, int64_t T,
                           int64_t d, int64_t K, int64_t rows, const DxOut& o, float* part,
                           hipStream_t s) {
-  if (p.splits > 1) {
-    using C = T128;
-    const int tM = (int)ceil_div64(T, C::BM), tN = (int)ceil_div64(d, C::BN);
-    dx_tile<C, OT, true><<<tM * tN * p.splits, C::kThreads, 0, s>>>(
-        g, w, (int)T, (int)d, (int)K, tM, tN, (int)rows, o, part, p.kc);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int blocks = (int)std::min<int64_t>((T * d / 8 + 255) / 256, 2048);
-    dx_join<OT><<<blocks, 256, 0, s>>>(part, p.splits, T, (int)d, o);
+  if (p.splits == 1) {
+    launch_dx_kind<OT, false>(p, g, w, T, d, K, rows, o, part, s);
     return hipGetLastError();
   }
-  switch (cheapest(kDxKinds, T, d, K)) {
-    case k256: launch_dx<P256, 1, OT>(g, w, T, d, K, rows, o, s); break;
-    case k256x128: launch_dx<P256x128, 2, OT>(g, w, T, d, K, rows, o, s); break;
-    case k128: launch_dx<P128, 2, OT>(g, w, T, d, K, rows, o, s); break;
-    case k64: launch_dx<T64, 0, OT>(g, w, T, d, K, rows, o, s); break;
-    default: launch_dx<T32, 0, OT>(g, w, T, d, K, rows, o, s); break;
-  }
+  launch_dx_kind<float, true>(p, g, w, T, d, K, rows, o, part, s);   // sums are float32
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int blocks = (int)std::min<int64_t>((T * d / 8 + 255) / 256, 2048);
+  dx_join<OT><<<blocks, 256, 0, s>>>(part, p.splits, T, (int)d, o);
   return hipGetLastError();
 }
 
@@ -538,10 +561,10 @@ hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const u
       const int64_t cols = std::min(p.width, V - v0), ld = up(cols, 64);
       const uint8_t* w = wq + v0 * d;
       const Grads gr{lse + r0, at_target, (_Float16*)g, ld, (int)v0};
-      switch (cheapest(kGradKinds, n, ld, d)) {
-        case k256x128: launch_logits_bwd<P256x128, 2>(x, w, n, d, cols, lg, gr, s); break;
-        case k128: launch_logits_bwd<P128, 2>(x, w, n, d, cols, lg, gr, s); break;
-        case k64: launch_logits_bwd<T64, 0>(x, w, n, d, cols, lg, gr, s); break;
+      switch (grad_kind(n, ld, d)) {
+        case kGrad256x128: launch_logits_bwd<P256x128, 2>(x, w, n, d, cols, lg, gr, s); break;
+        case kGrad128: launch_logits_bwd<P128, 2>(x, w, n, d, cols, lg, gr, s); break;
+        case kGrad64: launch_logits_bwd<T64, 0>(x, w, n, d, cols, lg, gr, s); break;
         default: launch_logits_bwd<T32, 0>(x, w, n, d, cols, lg, gr, s); break;
       }
       e = hipGetLastError();

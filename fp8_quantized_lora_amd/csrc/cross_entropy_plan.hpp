@@ -36,26 +36,19 @@ LossKind loss_kind(int64_t T, int64_t V, int64_t d) {
   return best;
 }
 
-// The gradient's two products, by linear_act_plan.hpp's costs: G's (E4M3) and dx's
-// (float16, K in bytes), those kinds that are cheapest somewhere.
-//   G, 16000 columns of 4096: 205 us in 256 x 128 at 4096 tokens (128 x 128: 246), 35
-//   and 37 at 512, 17 in 64 x 64 at 128 (128 x 128: 20), 12.1 in 32 x 64 at 17 (12.8)
-//   dx from them: 388 in 256 x 256 at 4096 tokens (256 x 128: 417), 217 in 256 x 128 at
-//   2048 (280; 128 x 128: 234), 125 in 128 x 128 at 1024 (157)
-constexpr TileKind kGradKinds[] = {k256x128, k128, k64, k32x64};
-constexpr TileKind kDxKinds[] = {k256, k256x128, k128, k64, k32x64};
-
-template <int N>
-TileKind cheapest(const TileKind (&kinds)[N], int64_t M, int64_t n, int64_t K) {
-  TileKind best = k64;
+// G's tiles, by linear_act_plan.hpp's costs, those kinds that are cheapest somewhere:
+// 16000 columns of 4096 205 us in 256 x 128 at 4096 tokens (128 x 128: 246), 35 and 37 at
+// 512, 17 in 64 x 64 at 128 (128 x 128: 20), 12.1 in 32 x 64 at 17 (12.8).
+enum GradKind { kGrad256x128, kGrad128, kGrad64, kGrad32x64, kGradKinds };
+constexpr TileKind kGradTile[kGradKinds] = {k256x128, k128, k64, k32x64};
+GradKind grad_kind(int64_t T, int64_t n, int64_t d) {
+  GradKind best = kGrad64;
   float cost = HUGE_VALF;
-  for (const TileKind k : kinds) {
-    if (K > kFarK && k != k64 && k != k32x64) continue;
-    const float c = tile_cost(k, M, n, K);
-    if (c < cost) {
-      cost = c;
-      best = k;
-    }
+  for (int k = 0; k < kGradKinds; ++k) {
+    const float c = tile_cost(kGradTile[k], T, n, d);
+    if (c >= cost) continue;
+    cost = c;
+    best = (GradKind)k;
   }
   return best;
 }
@@ -80,26 +73,55 @@ int64_t piece_width(int64_t T, int64_t V) {
   return up(ceil_div64(V, ceil_div64(V, most)), 64);
 }
 
-// splits of the product with G over the piece: where its tiles leave CUs without work
-int dx_splits(int64_t T, int64_t d, int64_t width, int& kc) {
-  const int64_t nt = tiles_of(k128w8, T, d), steps = ceil_div64(width * 2, 128);
-  const int64_t s = std::min<int64_t>(kCUs / nt, steps / 8);
-  kc = 0;
-  if (s < 2) return 1;
-  kc = (int)ceil_div64(steps, s);
-  return (int)ceil_div64(steps, kc);
-}
+// dx's tiles and splits over the piece's columns, by the same model; a split's sums are
+// written and read once at 4 TB/s and joined by a launch of their own.
+//   32000 columns: 4096 x 4096 800 us in 256 x 256 (256 x 128: 830); 2048 x 4096 420 in
+//     256 x 128 (588; 128 x 128: 483)
+//   1024 x 4096: 222 in 2 splits of 256 x 128, 252 in 128 x 128 whole; 2048 x 1024 120
+//     in 4, 205 whole
+//   128 x 4096: 45 in 8 splits of 128 x 128, 67 of 64 x 64; 64 x 4096: 39 and 37; 17 x
+//     4096: 36 in 8 of 64 x 64, 29 of 32 x 64
+//   131071 columns, 333 x 1040: 127 in 8 splits of 128 x 128, 161 of 256 x 128
+enum DxKind { kDx256, kDx256x128, kDx128, kDx64, kDx32x64, kDxKinds };
+constexpr TileCost kDxTile[kDxKinds] = {
+    {256, 256, 1, 3.0f, 15.0f, {{1.50f, 1.50f}, {1.50f, 1.50f}}},
+    {256, 128, 2, 2.0f, 10.0f, {{0.80f, 1.60f}, {0.80f, 1.60f}}},
+    {128, 128, 2, 4.5f, 4.5f, {{0.47f, 0.94f}, {0.47f, 0.94f}}},
+    {64, 64, 2, 2.0f, 1.5f, {{0.32f, 0.42f}, {0.32f, 0.42f}}},
+    {32, 64, 2, 2.0f, 1.0f, {{0.27f, 0.35f}, {0.27f, 0.35f}}}};
 
 struct BwdPlan {
   int64_t width;
-  int splits, kc;
-  size_t g, sums, part, at_target;                        // bytes, multiples of 256
+  DxKind kind;
+  int splits, kc;                                            // kc K steps each
+  size_t g, sums, part, at_target;                           // bytes, multiples of 256
   size_t bytes() const { return g + sums + part + at_target; }
 };
 BwdPlan bwd_plan(int64_t T, int64_t d, int64_t V, int dx_type) {
   BwdPlan p;
   p.width = piece_width(T, V);
-  p.splits = dx_splits(T, d, p.width, p.kc);
+  p.kind = kDx64;
+  p.splits = 1;
+  p.kc = 0;
+  const int64_t steps = ceil_div64(p.width, 64);
+  float cost = HUGE_VALF;
+  for (int k = 0; k < kDxKinds; ++k) {
+    const TileCost& t = kDxTile[k];
+    const int64_t nt = ceil_div64(T, t.bm) * ceil_div64(d, t.bn);
+    // (pipelined tiles reach this far into a row of G by 32-bit offsets)
+    if (p.width * 2 > kFarK && k < kDx64) continue;
+    for (int s = 1; s <= 32; s *= 2) {
+      if (s > 1 && (k == kDx256 || steps / s < 8)) break;
+      const int64_t kc = ceil_div64(steps, s);
+      const float join = s == 1 ? 0.0f : 3.0f + (float)(s * T * d) * 8.0f / 4e6f;
+      const float c = cost_of(t, nt * s, kc * 128) + join;
+      if (nt * s >= 1 << 22 || c >= cost) continue;
+      cost = c;
+      p.kind = (DxKind)k;
+      p.splits = s;
+      p.kc = (int)kc;
+    }
+  }
   p.g = (size_t)up(T * p.width * 2, 256);
   // float32 gradients collect in place
   p.sums = dx_type != 0 && p.width < V ? (size_t)up(T * d * 4, 256) : 0;

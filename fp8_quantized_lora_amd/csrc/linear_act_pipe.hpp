@@ -140,16 +140,17 @@ struct Ring {
   static_assert(SLOTS >= 3, "LDS");
 };
 
-// The tile at (m0, n0), wave-uniform: before() is called ahead of the loop, out(acc,
-// what it gave, LDS) behind it, with the LDS (the ring's kLds) free.
+// The tile at (m0, n0), wave-uniform, over K steps k_lo .. k_end - 1 (of all that K has;
+// a k_lo that is not 0 with a turned B only): before() is called ahead of the loop,
+// out(acc, what it gave, LDS) behind it, with the LDS (the ring's kLds) free.
 //
 // LEAN: one set of fragments of A instead of two, read between the quarters, where the
 // registers do not hold two: the other workgroup of the CU multiplies meanwhile.
 template <class OP, class C, int PER_CU, bool LEAN = false, class BEFORE, class OUT>
 __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
                                              const uint8_t* __restrict__ B, int M, int N, int K,
-                                             int m0, int n0, const Exponents& ex, BEFORE&& before,
-                                             OUT&& out) {
+                                             int m0, int n0, int k_lo, int k_end,
+                                             const Exponents& ex, BEFORE&& before, OUT&& out) {
   using R = Ring<OP, C, PER_CU>;
   typedef typename OP::Frag Frag;
   typedef typename OP::FragB FragB;
@@ -172,8 +173,9 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = w / C::WGN, wn = w % C::WGN;
   // whole K steps, and the bytes or (turned) the rows of B of one that is not
-  const int nk = TURNED ? ex.rows_b / 64 : K / BK, rem = TURNED ? 0 : K % BK;
-  const int all = (K + BK - 1) / BK, last = 2 * all - 1;
+  const int rows_b = TURNED ? ex.rows_b - k_lo * 64 : 0;
+  const int nk = TURNED ? min(rows_b / 64, k_end - k_lo) : K / BK, rem = TURNED ? 0 : K % BK;
+  const int all = min((K + BK - 1) / BK, k_end) - k_lo, last = 2 * all - 1;
 
   typename OP::Acc acc[MB][NB];
 #pragma unroll
@@ -184,9 +186,9 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
   // direct loads: the tile's first row as a scalar address, a lane's row (clamped
   // into the matrix) and swizzled chunk as its offset.  Half h of an operand is
   // half h of each wave's rows.
-  const uint8_t* tA = A + (int64_t)m0 * K;
-  const uint8_t* tB = TURNED ? B + n0 : B + (int64_t)n0 * K;
   const int64_t stepB = TURNED ? (int64_t)64 * N : BK;
+  const uint8_t* tA = A + (int64_t)m0 * K + (int64_t)k_lo * BK;
+  const uint8_t* tB = (TURNED ? B + n0 : B + (int64_t)n0 * K) + k_lo * stepB;
   const int lrow = lane >> 3, lslot = lane & 7;
   uint32_t vA[2][LA], vB[2][LB];
 #pragma unroll
@@ -256,7 +258,7 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
       if constexpr (TURNED && J < LA) {
         load(ha, hb, j, kt, slot);
       } else if constexpr (TURNED) {                         // rows past the last: the last
-        const int r = (w * LB + J - LA) * RPL + lane / CPR, back = max(0, nk * 64 + r + 1 - ex.rows_b);
+        const int r = (w * LB + J - LA) * RPL + lane / CPR, back = max(0, nk * 64 + r + 1 - rows_b);
         load16_to_lds_at(tB + kt * stepB, vB[decltype(hb)::value][J - LA] - (uint32_t)back * (uint32_t)N,
                          ldsB + slot * SLOT + (J - LA) * 1024);
       } else if constexpr (J < LA) {
@@ -458,7 +460,7 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void linear_act_pipe(
   const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
   const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
   pipe_product<OP, C, PER_CU, LEAN>(
-      A, B, M, N, K, m0, n0, ex, [&] { return scale_of<OP>(ep); },
+      A, B, M, N, K, m0, n0, 0, INT32_MAX, ex, [&] { return scale_of<OP>(ep); },
       [&](const auto& acc, float scale, uint8_t* smem) {
         tile_out<C, Ring<OP, C, PER_CU>::kLds, OT, STREAM, false>(smem, acc, m0, n0, M, N, scale,
                                                                   ep, nullptr, 0);

@@ -21,14 +21,14 @@ extern "C" void mx(int64_t M, int64_t N, int64_t K, int64_t* out) {
   out[2] = p.split;
   out[3] = p.kc;
 }
-// the forward's kernel, G's, dx's (of the first piece), pieces, splits, strips
+// the forward's kernel, G's (of the first piece), dx's, pieces, splits, strips
 extern "C" void loss(int64_t T, int64_t d, int64_t V, int64_t* out) {
   const int64_t n = strip_of(T);
   const BwdPlan p = bwd_plan(n, d, V, 1);
   const int64_t ld = up(std::min(p.width, V), 64);
   out[0] = loss_kind(n, V, d);
-  out[1] = cheapest(kGradKinds, n, ld, d);
-  out[2] = p.splits > 1 ? -1 : cheapest(kDxKinds, n, d, ld * 2);
+  out[1] = grad_kind(n, ld, d);
+  out[2] = p.kind;
   out[3] = ceil_div64(V, p.width);
   out[4] = p.splits;
   out[5] = ceil_div64(T, kStrip);
@@ -37,8 +37,8 @@ extern "C" void loss(int64_t T, int64_t d, int64_t V, int64_t* out) {
 
 MX_KINDS = ("256x128", "128", "64", "32x64")
 LOSS_KINDS = ("256", "128", "64", "32x64")
-TILE_KINDS = ("256x320", "256", "256x128", "128x256", "192x128", "128x192w8", "128", "128w8", "64",
-              "32x64")
+GRAD_KINDS = ("256x128", "128", "64", "32x64")
+DX_KINDS = ("256", "256x128", "128", "64", "32x64")
 
 
 @functools.lru_cache(maxsize=1)
@@ -64,6 +64,6 @@ def mx(T, d_in, d_out):
 
 
 def loss(T, d, V):
-    """(forward's kernel, G's, dx's, pieces, strips)"""
-    f, g, x, pieces, _, strips = _call(_lib().loss, T, d, V)
-    return LOSS_KINDS[f], TILE_KINDS[g], "split" if x < 0 else TILE_KINDS[x], pieces, strips
+    """(forward's kernel, G's, dx's, "*" behind those split, pieces, strips)"""
+    f, g, x, pieces, splits, strips = _call(_lib().loss, T, d, V)
+    return (LOSS_KINDS[f], GRAD_KINDS[g], DX_KINDS[x] + "*" * (splits > 1), pieces, strips)
