@@ -64,9 +64,9 @@ struct Stats {
 // (m, s) of two runs
 __device__ __forceinline__ void join_runs(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
-  // a run without a column is (-inf, 0)
-  const float a = m == -INFINITY ? 0.0f : s * __builtin_amdgcn_exp2f(m - top);
-  const float b = m2 == -INFINITY ? 0.0f : s2 * __builtin_amdgcn_exp2f(m2 - top);
+  // a run without a column is (-inf, 0); one of NaN alone is (-inf, NaN) and stays
+  const float a = s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f(m - top);
+  const float b = s2 == 0.0f ? 0.0f : s2 * __builtin_amdgcn_exp2f(m2 - top);
   m = top;
   s = a + b;
 }
@@ -486,7 +486,7 @@ bool cross_entropy_fits(int64_t T, int64_t d, int64_t V) {
 
 size_t cross_entropy_fwd_ws_bytes(int64_t T, int64_t d, int64_t V) {
   const int64_t n = strip_of(T);
-  // (a strip shorter than the others may have more runs: of 16 columns at most)
+  // (a strip shorter than the others may have more runs: its tiles may be narrower)
   const int64_t tail = T % kStrip;
   size_t most = 0;
   for (const int64_t m : {n, tail})

@@ -207,6 +207,25 @@ def test_targets_out_of_range_and_nan(gpu_lib, T):
     assert float(loss[0]) == 0 and not bool(c.backward(gpu_lib, lse, F32)[0].any())
 
 
+@pytest.mark.parametrize("T,d,V", [(3, 16, 65), (3, 16, 64), (50, 64, 129), (700, 64, 1025),
+                                   (1, 4112, 2049)])
+def test_nan_logits_reach_lse(gpu_lib, T, d, V):
+    """A NaN in a row of the weight is in every token's sum, though it stand alone in the
+    last run of columns; all logits of a token NaN give a NaN, not the empty sum's -inf."""
+    c = Case(T, d, V, ignored=0.0)
+    c.target.fill_(0)
+    w = c.wq.clone()
+    c.wq[-1, 3] = 0x7F
+    loss, lse = c.forward(gpu_lib)
+    assert bool(lse.isnan().all()) and bool(loss.isnan().all())
+    assert bool(c.backward(gpu_lib, lse, F32).isnan().all())
+    c.wq.copy_(w)
+    c.xq[T // 2, 5] = 0xFF
+    c.target[T // 2] = -1
+    loss, lse = c.forward(gpu_lib)
+    assert lse.isnan().nonzero().tolist() == [[T // 2]] and not bool(loss.isnan().any())
+
+
 def test_gradient_against_differences(gpu_lib):
     """Central differences of the float64 loss along random directions, in the values
     that the codes stand for."""
