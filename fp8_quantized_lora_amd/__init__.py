@@ -1015,7 +1015,6 @@ def mxfp4_quantize(x: torch.Tensor, q: torch.Tensor, e: torch.Tensor, stream=Non
     power of two per block of 32, floor(log2(largest)) - 2; values to nearest, ties to
     the even code, saturating at 6."""
     rows, K = _matrix(x, "x")
-    _matrix(q, "q")
     t, dev = _elem(x, "x"), _device(x, "x")
     args = (_arg(x, x.dtype, (rows, _mx_width(K, "x")), dev, "x"), t, rows, K,
             _arg(q, torch.uint8, (rows, K // 2), dev, "q"),
@@ -1026,7 +1025,6 @@ def mxfp4_quantize(x: torch.Tensor, q: torch.Tensor, e: torch.Tensor, stream=Non
 def mxfp4_dequantize(q: torch.Tensor, e: torch.Tensor, x: torch.Tensor, stream=None) -> None:
     """x [rows x K], float32 or bfloat16, from mxfp4_quantize's codes and exponents."""
     rows, K = _matrix(x, "x")
-    _matrix(q, "q")
     t, dev = _elem(x, "x"), _device(q, "q")
     args = (_arg(q, torch.uint8, (rows, _mx_width(K, "x") // 2), dev, "q"),
             _arg(e, torch.uint8, mxfp4_scales_shape(rows, K), dev, "e"), rows, K,
