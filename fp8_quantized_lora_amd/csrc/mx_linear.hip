@@ -15,16 +15,32 @@
 namespace falq {
 namespace {
 
+// Outputs from this on, the Infinity Cache's size, go past the caches (bfloat16's 16-byte
+// stores, whole lines): they do not fit, and each line written back for another waits.
+// Alone, and with mxfp4_quantize of y behind: 8192 x 11008 x 4096 with gelu and z
+// (344 MB) 227 and 271 us, 269 and 301 without the hint; 8192 x 8192 x 4096 with gelu and
+// z (256 MB) 160 and 200, 169 and 222; 65536 x 4096 x 256 (512 MB) 123 and 258, 131 and
+// 286.  Smaller ones do fit: 8192 x 11008 x 4096 with gelu (172 MB) 219 and 267, 208 and
+// 263 without.
+constexpr int64_t kStreamOut = (int64_t)256 << 20;
+
 template <class C, int PIPE, class OT, bool LEAN = false>
 hipError_t mx_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
                     const Epilogue& ep, const Exponents& ex, hipStream_t s) {
   const int tM = (int)((M + C::BM - 1) / C::BM), tN = (int)((N + C::BN - 1) / C::BN);
-  if constexpr (PIPE > 0)
-    linear_act_pipe<Fp4Wide, C, PIPE, OT, false, LEAN><<<tM * tN, C::kThreads, 0, s>>>(
-        A, B, (int)M, (int)N, (int)K, tM, tN, ep, ex);
-  else
+  if constexpr (PIPE > 0) {
+    const auto go = [&](auto stream) {
+      linear_act_pipe<Fp4Wide, C, PIPE, OT, decltype(stream)::value, LEAN>
+          <<<tM * tN, C::kThreads, 0, s>>>(A, B, (int)M, (int)N, (int)K, tM, tN, ep, ex);
+    };
+    if (sizeof(OT) == 2 && M * N * 2 * (1 + (ep.z != nullptr)) >= kStreamOut)
+      go(std::bool_constant<sizeof(OT) == 2>{});
+    else
+      go(std::false_type{});
+  } else {
     linear_act_tile<Fp4, C, OT, false><<<tM * tN, C::kThreads, 0, s>>>(
         A, B, (int)M, (int)N, (int)K, tM, tN, ep, ex);
+  }
   return hipGetLastError();
 }
 

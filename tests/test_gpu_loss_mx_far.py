@@ -6,6 +6,8 @@ import math
 import pytest
 import torch
 
+from tests.loss_mx_plan import mx as plan
+
 pytestmark = pytest.mark.gpu
 
 F32, BF16, U8 = torch.float32, torch.bfloat16, torch.uint8
@@ -140,10 +142,14 @@ def test_cross_entropy_of_a_far_weight(gpu_lib):
     assert not bool(dx[4].any())
 
 
-def test_fp4_product_of_far_outputs(gpu_lib):
-    """2.2e9 outputs; 64 products each, so that float32's sums are off by 64 half steps of
-    their absolute sum at most."""
-    tokens, d_in, d_out = 66000, 64, 33008
+@pytest.mark.parametrize("tokens,d_out,kind", [(66000, 33008, "256x128"), (8192, 11008, "128"),
+                                               (8190, 16400, "128")])
+def test_fp4_product_of_far_outputs(gpu_lib, tokens, d_out, kind):
+    """2.2e9 outputs, and outputs that go past the caches in either kind of tile; 64
+    products each, so that float32's sums are off by 64 half steps of their absolute sum
+    at most."""
+    d_in = 64
+    assert plan(tokens, d_in, d_out) == kind
     x, w = filled(tokens, d_in), filled(d_out, d_in)
     ops = []
     for t in (x, w):
@@ -155,7 +161,7 @@ def test_fp4_product_of_far_outputs(gpu_lib):
     (xq, x_e, xv), (wq, w_e, wv) = ops
     y, z = new(tokens, d_out, t=BF16), new(tokens, d_out, t=BF16)
     gpu_lib.melded_linear_fwd_mxfp4(xq, x_e, wq, w_e, y, act="relu", z=z)
-    for at in (0, 2 ** 31 // d_out - 20, tokens - 40):
+    for at in (0, min(2 ** 31 // d_out, tokens - 60) - 20, tokens - 40):
         s = slice(at, at + 40)
         ref, S = xv[s].double() @ wv.double().T, xv[s].abs().double() @ wv.abs().double().T
         tol = S * 64 * 2.0 ** -24 + ref.abs() * 2.0 ** -8
