@@ -377,7 +377,8 @@ __global__ __launch_bounds__(C::kThreads) void dx_tile(
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   tile_product<F16ByE4M3, C>(
       A, B, M, N, K, m0, n0, SPLIT ? sp * kc : 0, SPLIT ? sp * kc + kc : INT32_MAX,
-      Exponents{nullptr, nullptr, 0, rows}, [] { return 0; }, [&](const auto& acc, int, uint8_t* smem) {
+      Exponents{nullptr, nullptr, 0, rows}, [] { return 0; },
+      [&](const auto& acc, int, uint8_t* smem) {
         rows_through_lds<C, kTileLds<F16ByE4M3, C>>(
             smem, acc, m0, n0, M, N, [&](int row, int col, float(&v)[8]) {
               if constexpr (SPLIT)

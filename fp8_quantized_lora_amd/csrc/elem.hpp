@@ -169,7 +169,7 @@ struct RowElems {
 };
 template <int E, bool ODD>
 struct RowElems<kept_t, E, ODD> {
-  typedef typename std::conditional<E == 8, v2i, typename std::conditional<E == 4, int, uint8_t>::type>::type V;
+  typedef std::conditional_t<E == 8, v2i, std::conditional_t<E == 4, int, uint8_t>> V;
   typedef V V_any __attribute__((aligned(1)));
   V v;
   uint8_t s0, s1;                              // of the first element's block, of the last's
@@ -200,9 +200,9 @@ struct RowElems<kept_t, E, ODD> {
       w = (uint32_t)v[e / 4];
     else
       w = (uint32_t)v;
-    const float2 p = (e & 2) ? dec2(w, true) : dec2(w, false);
-    const float s = e8m0_value(ODD && E > 1 && e >= turn ? s1 : s0);
-    return ((e & 1) ? p.y : p.x) * s;
+    const uint32_t s = ODD && E > 1 && e >= turn ? s1 : s0;
+    const float2 p = (e & 2) ? dec2_e8m0(w, true, s) : dec2_e8m0(w, false, s);
+    return (e & 1) ? p.y : p.x;
   }
 };
 

@@ -390,8 +390,7 @@ template <class XT, class GT, int E, int C, bool ODD>
 __global__ __launch_bounds__(1024) void ln_bwd_short(
     const GT* dy, const XT* __restrict__ x, const uint8_t* __restrict__ xs,
     const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
-    GT* dx,
-    float* __restrict__ dw, float* __restrict__ db, int T, int d, int nt, int row_blocks) {
+    GT* dx, float* __restrict__ dw, float* __restrict__ db, int T, int d, int nt, int row_blocks) {
   if ((int)blockIdx.x < row_blocks) {
     __shared__ float red[16][2];
     const Group gr(nt);
@@ -466,8 +465,8 @@ constexpr int kColRows = 8, kColLanes = 32;
 template <class XT, class GT, int E>
 __global__ __launch_bounds__(256) void ln_bwd_cols(
     const GT* __restrict__ dy, const XT* __restrict__ x, const uint8_t* __restrict__ xs,
-    const float* __restrict__ mean, const float* __restrict__ rstd, float* __restrict__ part, int64_t T, int64_t d,
-    int64_t rows_per_strip) {
+    const float* __restrict__ mean, const float* __restrict__ rstd, float* __restrict__ part,
+    int64_t T, int64_t d, int64_t rows_per_strip) {
   __shared__ float sw[kColRows][kColLanes * E], sb[kColRows][kColLanes * E];
   const int cl = threadIdx.x % kColLanes, rl = threadIdx.x / kColLanes;
   const int64_t col = ((int64_t)blockIdx.x * kColLanes + cl) * E;
@@ -545,8 +544,9 @@ BwdPlan bwd_plan(int64_t T, int64_t d) {
 }
 
 template <class XT, class GT, int E, int C, bool STREAM, bool ODD>
-hipError_t bwd_rows(const BwdPlan& p, const GT* dy, const XT* x, const uint8_t* xs, const float* w, const float* mean,
-                    const float* rstd, int64_t T, int64_t d, GT* dx, float* part, hipStream_t s) {
+hipError_t bwd_rows(const BwdPlan& p, const GT* dy, const XT* x, const uint8_t* xs, const float* w,
+                    const float* mean, const float* rstd, int64_t T, int64_t d, GT* dx, float* part,
+                    hipStream_t s) {
   const size_t lds = (size_t)C * E * (p.G / 2) * p.nt * 4;
   // a workgroup of at most 512 threads may use twice the registers
   if (p.nt <= 512)
@@ -564,9 +564,9 @@ bool bwd_short_fits(int64_t T, int64_t d) {
 }
 
 template <class XT, class GT, int E, bool ODD>
-hipError_t bwd_short(const GT* dy, const XT* x, const uint8_t* xs, const float* w, const float* mean,
-                     const float* rstd, int64_t T, int64_t d, GT* dx, float* dw, float* db,
-                     hipStream_t s) {
+hipError_t bwd_short(const GT* dy, const XT* x, const uint8_t* xs, const float* w,
+                     const float* mean, const float* rstd, int64_t T, int64_t d, GT* dx, float* dw,
+                     float* db, hipStream_t s) {
   const int nt = row_threads(d, 8, 1024), G = 1024 / nt;
   const int rows = dx ? (int)((T + G - 1) / G) : 0;
   const int cols = dw || db ? (int)((d + kShortCols - 1) / kShortCols) : 0;
@@ -596,13 +596,15 @@ hipError_t bwd_long(const GT* dy, const XT* x, const uint8_t* xs, const float* w
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (dx) ln_bwd_dx_long<XT, GT, E><<<row_grid(T), 1024, 0, s>>>(dy, x, xs, w, mean, rstd, dx, T, d);
+  if (dx)
+    ln_bwd_dx_long<XT, GT, E><<<row_grid(T), 1024, 0, s>>>(dy, x, xs, w, mean, rstd, dx, T, d);
   return hipGetLastError();
 }
 
 template <class XT, class GT, int E, bool ODD>
-hipError_t bwd(const GT* dy, const XT* x, const uint8_t* xs, const float* w, const float* mean, const float* rstd,
-               int64_t T, int64_t d, GT* dx, float* dw, float* db, float* part, hipStream_t s) {
+hipError_t bwd(const GT* dy, const XT* x, const uint8_t* xs, const float* w, const float* mean,
+               const float* rstd, int64_t T, int64_t d, GT* dx, float* dw, float* db, float* part,
+               hipStream_t s) {
   if (bwd_short_fits(T, d))
     return bwd_short<XT, GT, E, ODD>(dy, x, xs, w, mean, rstd, T, d, dx, dw, db, s);
   if (!dw && !db) part = nullptr;
@@ -612,11 +614,13 @@ hipError_t bwd(const GT* dy, const XT* x, const uint8_t* xs, const float* w, con
   const bool stream = HINT && T * d * (int64_t)(2 * sizeof(GT) + sizeof(XT)) > kStreamBytes;
   hipError_t e;
   if (p.n == 16)
-    e = stream ? bwd_rows<XT, GT, E, 16 / E, HINT, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx, part, s)
-               : bwd_rows<XT, GT, E, 16 / E, false, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx, part,
-                                                         s);
+    e = stream ? bwd_rows<XT, GT, E, 16 / E, HINT, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx,
+                                                        part, s)
+               : bwd_rows<XT, GT, E, 16 / E, false, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx,
+                                                         part, s);
   else if (p.n)
-    e = stream ? bwd_rows<XT, GT, E, 8 / E, HINT, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx, part, s)
+    e = stream ? bwd_rows<XT, GT, E, 8 / E, HINT, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx, part,
+                                                       s)
                : bwd_rows<XT, GT, E, 8 / E, false, ODD>(p, dy, x, xs, w, mean, rstd, T, d, dx, part,
                                                         s);
   else
@@ -626,9 +630,9 @@ hipError_t bwd(const GT* dy, const XT* x, const uint8_t* xs, const float* w, con
 }
 
 template <class XT, class GT>
-hipError_t bwd_by_width(const void* dy, const void* x, const uint8_t* xs, const float* w, const float* mean,
-                        const float* rstd, int64_t T, int64_t d, void* dx, float* dw, float* db,
-                        float* part, hipStream_t s) {
+hipError_t bwd_by_width(const void* dy, const void* x, const uint8_t* xs, const float* w,
+                        const float* mean, const float* rstd, int64_t T, int64_t d, void* dx,
+                        float* dw, float* db, float* part, hipStream_t s) {
   const GT* g = (const GT*)dy;
   const XT* v = (const XT*)x;
   constexpr int E = sizeof(XT) + sizeof(GT) <= 4 ? 8 : 4;
@@ -743,8 +747,9 @@ hipError_t launch_layer_norm_fwd(const void* x, int xt, const float* w, const fl
 }
 
 hipError_t launch_layer_norm_bwd(const void* dy, int gt, const void* x, int xt, const uint8_t* xs,
-                                 const float* w, const float* mean, const float* rstd, int64_t T, int64_t d,
-                                 void* dx, float* dw, float* db, void* ws, hipStream_t s) {
+                                 const float* w, const float* mean, const float* rstd, int64_t T,
+                                 int64_t d, void* dx, float* dw, float* db, void* ws,
+                                 hipStream_t s) {
   if (T == 0) {
     hipError_t e = dw ? launch_fill_f32(dw, d, 0.0f, s) : hipSuccess;
     if (e != hipSuccess) return e;

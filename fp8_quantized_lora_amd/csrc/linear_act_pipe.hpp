@@ -242,7 +242,8 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
   auto load_exponents = [&](auto ha, auto hb, int kt, int slot) FALQ_INLINE {
     if constexpr (OP::kScaled)
       if (loads_e)
-        load16_to_lds_at(tE + kt * estep, w == 0 ? vE[decltype(ha)::value] : vE[decltype(hb)::value],
+        load16_to_lds_at(tE + kt * estep,
+                         w == 0 ? vE[decltype(ha)::value] : vE[decltype(hb)::value],
                          ldsE + slot * SLOT);
   };
   // all of them, for any step; chunks past K load the row's last chunk
@@ -258,8 +259,10 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
       if constexpr (TURNED && J < LA) {
         load(ha, hb, j, kt, slot);
       } else if constexpr (TURNED) {                         // rows past the last: the last
-        const int r = (w * LB + J - LA) * RPL + lane / CPR, back = max(0, nk * 64 + r + 1 - rows_b);
-        load16_to_lds_at(tB + kt * stepB, vB[decltype(hb)::value][J - LA] - (uint32_t)back * (uint32_t)N,
+        const int r = (w * LB + J - LA) * RPL + lane / CPR;
+        const int back = max(0, nk * 64 + r + 1 - rows_b);
+        load16_to_lds_at(tB + kt * stepB,
+                         vB[decltype(hb)::value][J - LA] - (uint32_t)back * (uint32_t)N,
                          ldsB + slot * SLOT + (J - LA) * 1024);
       } else if constexpr (J < LA) {
         const int co = (lslot ^ gemm::dma::swz((w * LA + J) * 8 + lrow)) * 16;
@@ -301,7 +304,8 @@ __device__ __forceinline__ void pipe_product(const uint8_t* __restrict__ A,
       e = (int)*reinterpret_cast<const typename OP::Scales*>(smem + exps);
     uint4 q[OP::kParts];
 #pragma unroll
-    for (int p = 0; p < OP::kParts; ++p) q[p] = *reinterpret_cast<const uint4*>(smem + codes + o[p]);
+    for (int p = 0; p < OP::kParts; ++p)
+      q[p] = *reinterpret_cast<const uint4*>(smem + codes + o[p]);
     return OP::make(q, e);
   };
   auto fragA = [&](auto i, int at) FALQ_INLINE {

@@ -12,7 +12,7 @@ namespace falq {
 // matrix core's products: a lane group of 16 x 16 x 128 takes blocks g and g + 4, two
 // bytes; one of 32 x 32 x 64 takes two of these pairs, four bytes.  Bytes of blocks
 // past the row and of rows past the last are 127.
-constexpr int kMxBlock = 32, kMxStep = 256;
+constexpr int kMxStep = 256;
 __host__ __device__ constexpr int64_t mx_rows16(int64_t rows) { return (rows + 15) / 16 * 16; }
 __host__ __device__ constexpr int64_t mx_steps(int64_t K) { return (K + kMxStep - 1) / kMxStep; }
 // the place of block b of a step, and the block at a place

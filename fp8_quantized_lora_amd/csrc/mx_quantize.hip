@@ -58,11 +58,8 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const XT* __restric
     for (int p = 0; p < 2; ++p) {
       const int64_t row = first + p * 8 + (threadIdx.x >> 5);
       const int ex = mx_exp_fp4(quad_max(mag8(v[p])));
-      const float s = exp2_int(-ex);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[p][i] *= s;
       if (row < rows && col < K)
-        *reinterpret_cast<uint32_t*>(q + (row * K + col) / 2) = enc8_fp4(v[p]);
+        *reinterpret_cast<uint32_t*>(q + (row * K + col) / 2) = enc8_fp4(v[p], ex);
       if ((l & 3) == 0) e[mx_scale_at(row, step * 8 + b, rows16)] = (uint8_t)(ex + 127);
     }
   }
@@ -81,10 +78,8 @@ __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __
   for (int64_t row = (int64_t)blockIdx.y * 16 + (threadIdx.x >> 5); row < rows;
        row = (row & 8) ? row - 8 + (int64_t)gridDim.y * 16 : row + 8) {
     float v[8];
-    dec8_fp4(*reinterpret_cast<const uint32_t*>(q + (row * K + col) / 2), v);
-    const float s = e8m0_value(e[mx_scale_at(row, step * 8 + b, rows16)]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= s;
+    dec8_fp4(*reinterpret_cast<const uint32_t*>(q + (row * K + col) / 2),
+             e[mx_scale_at(row, step * 8 + b, rows16)], v);
     store_elems<8>(y + row * K + col, v);
   }
 }
@@ -151,7 +146,7 @@ __global__ __launch_bounds__(256) void checkpoint_restore_kernel(const uint8_t* 
     const int64_t col = (int64_t)k.b * 32 + l * 8, at = k.row * d + col;
     const int n = (int)min((int64_t)8, d - col);
     if (n <= 0) continue;
-    const float s = e8m0_value(e[k.row * k.nb + k.b]);
+    const uint32_t s = e[k.row * k.nb + k.b];
     uint32_t w[2] = {0, 0};
     if (n >= 8) {
       const v2i c = *reinterpret_cast<const v2i_any*>(q + at);
@@ -165,9 +160,9 @@ __global__ __launch_bounds__(256) void checkpoint_restore_kernel(const uint8_t* 
     float v[8];
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-      const float2 p = dec2(w[h / 2], h & 1);
-      v[2 * h] = p.x * s;
-      v[2 * h + 1] = p.y * s;
+      const float2 p = dec2_e8m0(w[h / 2], h & 1, s);
+      v[2 * h] = p.x;
+      v[2 * h + 1] = p.y;
     }
     store_upto8(y + at, n, v);
   }

@@ -1,9 +1,9 @@
 // What the tiled products (linear_act_few.hpp, linear_act_tile.hpp,
 // linear_act_pipe.hpp) multiply: E4M3 codes, E4M3 codes as float16, float16 by E4M3
-// codes of the other orientation, or FP4 E2M1 codes with a power of two per block of 32.  All count K in bytes, a step of
-// 128 of them a row.  A fragment is a step of kBlock rows (16 or 32): a lane holds
-// kParts chunks of 16 bytes of row lane % kBlock, chunk(g, p), g = lane / kBlock;
-// which ones is free, as long as both operands' agree.
+// codes of the other orientation, or FP4 E2M1 codes with a power of two per block of 32.
+// All count K in bytes, a step of 128 of them a row.  A fragment is a step of kBlock rows
+// (16 or 32): a lane holds kParts chunks of 16 bytes of row lane % kBlock, chunk(g, p), g =
+// lane / kBlock; which ones is free, as long as both operands' agree.
 //
 // Blocks of 32 x 32 take half the LDS reads of an instruction of 16 x 16 and, where
 // an instruction of 16 x 16 has four passes (float16, FP4), are the only ones that one
@@ -76,14 +76,14 @@ __device__ __forceinline__ void mfma_f16_in_place(v16f& d, v4i b, v4i a) {
   asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(d) : "v"(b), "v"(a));
 }
 
-// eight codes as float16
+// two and eight codes as float16
+template <bool HI>
+__device__ __forceinline__ int f16_pair_of_e4m3(int w) {
+  return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)w, 1.0f, HI));
+}
 __device__ __forceinline__ v4i f16_of_e4m3(int lo, int hi) {
-  v4i r;
-  r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)lo, 1.0f, false));
-  r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)lo, 1.0f, true));
-  r[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)hi, 1.0f, false));
-  r[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)hi, 1.0f, true));
-  return r;
+  return v4i{f16_pair_of_e4m3<false>(lo), f16_pair_of_e4m3<true>(lo), f16_pair_of_e4m3<false>(hi),
+             f16_pair_of_e4m3<true>(hi)};
 }
 // half H of a chunk
 template <int H>
