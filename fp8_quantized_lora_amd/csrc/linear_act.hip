@@ -20,9 +20,9 @@
 // from the registers would be 8 or 16 bytes wide.  Each wave passes its
 // accumulators through its own part of the LDS (16-byte chunks XOR-swizzled
 // by the row: no bank conflicts either way) and reads them back as eight
-// columns of a row per lane; bias, residual and the outputs are then 16-byte
-// accesses on whole 128-byte lines, and the epilogue's code is a short loop
-// instead of one copy per accumulator.
+// columns of a row per lane (bfloat16) or four at a time (float32); bias, residual
+// and the outputs are then 16-byte accesses on whole 128-byte lines, and the
+// epilogue's code is a short loop instead of one copy per accumulator.
 #include "activation.hpp"
 #include "elem.hpp"
 #include "gemm_fp8_kernel.hpp"
@@ -40,13 +40,15 @@ namespace {
 // Below, the hint only moves the cost to the reader: with fp8_quantize of y
 // behind the product, 8192 x 11008 x 4096 gelu (172 MB) 417 us with it, 425
 // without (alone 306 and 335); 4096 x 8192 x 4096 (64 MB) 140 and 135.
+// Twice as wide, float32's from what the last-level cache holds on (kStreamBytes): 8192 x
+// 11008 x 4096 with gelu and z (721 MB) 351 and 454, 444 and 588 without; 4096 x 11008 x
+// 4096 (180 MB) 155 and 225, 151 and 220 without.
 constexpr int64_t kStreamOut = (int64_t)80 << 20;
 
-// whether the outputs take the streaming hint, which needs whole lines: 16-byte
-// stores, so bfloat16
 template <class OT>
 bool stream_outputs(int64_t M, int64_t N, const Epilogue& ep) {
-  return sizeof(OT) == 2 && M * N * 2 * (1 + (ep.z != nullptr)) > kStreamOut;
+  return M * N * (int64_t)sizeof(OT) * (1 + (ep.z != nullptr)) >
+         (sizeof(OT) == 2 ? kStreamOut : kStreamBytes);
 }
 
 // tiles of C: linear_act_tile, or PIPE workgroups of linear_act_pipe per CU.  MANY:
@@ -65,7 +67,7 @@ hipError_t launch_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N
           A, B, (int)M, (int)N, (int)K, tM, tN, ep, Exponents{});
   };
   if (MANY && stream_outputs<OT>(M, N, ep))
-    go(std::bool_constant<MANY && sizeof(OT) == 2>{});
+    go(std::bool_constant<MANY>{});
   else
     go(std::false_type{});
   return hipGetLastError();

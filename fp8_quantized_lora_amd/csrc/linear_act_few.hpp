@@ -27,22 +27,22 @@ __device__ __forceinline__ float scale_of(const Epilogue& e) {
     return 1.0f / (e.sa[0] * e.sb[0]);
 }
 
-// eight columns of one row
-template <int ACT, class OT, bool STREAM>
-__device__ __forceinline__ void finish8(float (&v)[8], float scale, const float (&bias)[8],
-                                        const Epilogue& e, int64_t at) {
+// E columns of one row
+template <int ACT, class OT, bool STREAM, int E>
+__device__ __forceinline__ void finish(float (&v)[E], float scale, const float (&bias)[E],
+                                       const Epilogue& e, int64_t at) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], scale, bias[i]);
-  if (e.z) store_elems<8, STREAM>((OT*)e.z + at, v);
+  for (int i = 0; i < E; ++i) v[i] = fmaf(v[i], scale, bias[i]);
+  if (e.z) store_elems<E, STREAM>((OT*)e.z + at, v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = act_value<ACT, OT>(v[i]);
+  for (int i = 0; i < E; ++i) v[i] = act_value<ACT, OT>(v[i]);
   if (e.residual) {
-    float r[8];
-    load_elems<8>((const OT*)e.residual + at, r);
+    float r[E];
+    load_elems<E>((const OT*)e.residual + at, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += r[i];
+    for (int i = 0; i < E; ++i) v[i] += r[i];
   }
-  store_elems<8, STREAM>((OT*)e.y + at, v);
+  store_elems<E, STREAM>((OT*)e.y + at, v);
 }
 
 // one column of one row

@@ -112,23 +112,39 @@ __device__ __forceinline__ void tile_out(uint8_t* smem, const ACC (&acc)[MB][NB]
   auto slot = [](int r, int c) { return r * CH + (c ^ (r & SWZ)); };
   v4f* mine = reinterpret_cast<v4f*>(smem + w * (LDS / C::NW / 16 * 16));
   const int cl = lane % LPR, rl = lane / LPR;
-  const int col = n0 + wn * C::WTN + cl * 8;
-  const bool col_ok = rl < RPI && col < N;                   // N is a multiple of 16
-  float bias[8];
+  // a lane stores 16 bytes at a time, a row's lanes one run of them: eight columns of
+  // bfloat16, or twice four of float32
+  constexpr int E = !SPLIT && sizeof(OT) == 2 ? 8 : 4, H = 8 / E;
+  const auto chunk = [&](int h) { return E == 8 ? 2 * cl : cl + h * LPR; };
+  const int col0 = n0 + wn * C::WTN;
+  bool ok[H];                                                // N is a multiple of 16
+  float bias[H][E];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
-  if (!SPLIT && ep.bias && col_ok) load_elems<8>(ep.bias + col, bias);
+  for (int h = 0; h < H; ++h) {
+    ok[h] = rl < RPI && col0 + 4 * chunk(h) < N;
+#pragma unroll
+    for (int i = 0; i < E; ++i) bias[h][i] = 0.0f;
+    if (!SPLIT && ep.bias && ok[h]) load_elems<E>(ep.bias + col0 + 4 * chunk(h), bias[h]);
+  }
   auto rows = [&](auto act, int first) {
     for (int r = rl; r < PASS; r += RPI) {                // lanes past RPI rows: idle
       const int row = m0 + wm * C::WTM + first + r;
-      const v4f a = mine[slot(r, 2 * cl)];
-      const v4f b = mine[slot(r, 2 * cl + 1)];
-      if (!col_ok || row >= M) continue;
-      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      if constexpr (SPLIT)
-        store_elems<8>(part + ((int64_t)sp * M + row) * N + col, v);
-      else
-        finish8<decltype(act)::value, OT, STREAM>(v, scale, bias, ep, (int64_t)row * N + col);
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+          const v4f a = mine[slot(r, chunk(h) + i)];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * i + e] = a[e];
+        }
+        if (!ok[h] || row >= M) continue;
+        const int64_t at = (int64_t)row * N + col0 + 4 * chunk(h);
+        if constexpr (SPLIT)
+          store_elems<E>(part + (int64_t)sp * M * N + at, v);
+        else
+          finish<decltype(act)::value, OT, STREAM>(v, scale, bias[h], ep, at);
+      }
     }
   };
 #pragma unroll
@@ -391,7 +407,7 @@ __device__ __forceinline__ void join8(const float* __restrict__ part, int S, int
 #pragma unroll
   for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
   if (ep.bias) load_elems<8>(ep.bias + col, bias);
-  finish8<ACT, OT, false>(v, scale, bias, ep, at);
+  finish<ACT, OT, false>(v, scale, bias, ep, at);
 }
 template <class OP, class OT>
 __global__ __launch_bounds__(256) void linear_act_join(const float* __restrict__ part, int S,

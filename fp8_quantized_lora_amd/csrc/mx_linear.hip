@@ -15,15 +15,13 @@
 namespace falq {
 namespace {
 
-// Outputs from this on, the Infinity Cache's size, go past the caches (bfloat16's 16-byte
-// stores, whole lines): they do not fit, and each line written back for another waits.
-// Alone, and with mxfp4_quantize of y behind: 8192 x 11008 x 4096 with gelu and z
-// (344 MB) 227 and 271 us, 269 and 301 without the hint; 8192 x 8192 x 4096 with gelu and
-// z (256 MB) 160 and 200, 169 and 222; 65536 x 4096 x 256 (512 MB) 123 and 258, 131 and
-// 286.  Smaller ones do fit: 8192 x 11008 x 4096 with gelu (172 MB) 219 and 267, 208 and
+// Outputs from what the last-level cache holds on (kStreamBytes) go past the caches: they
+// do not fit, and each line written back for another waits.  Alone, and with
+// mxfp4_quantize of y behind: 8192 x 11008 x 4096 with gelu and z (361 MB of bfloat16) 227
+// and 271 us, 269 and 301 without the hint, 8192 x 8192 x 4096 with gelu and z (256 MiB) 160
+// and 200, 169 and 222; 8192 x 11008 x 4096 with gelu and z of float32 280 and 420, 355 and
+// 434.  Smaller ones do fit: 8192 x 11008 x 4096 with gelu (180 MB) 219 and 267, 208 and
 // 263 without.
-constexpr int64_t kStreamOut = (int64_t)256 << 20;
-
 template <class C, int PIPE, class OT, bool LEAN = false>
 hipError_t mx_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
                     const Epilogue& ep, const Exponents& ex, hipStream_t s) {
@@ -33,8 +31,8 @@ hipError_t mx_tiles(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, in
       linear_act_pipe<Fp4Wide, C, PIPE, OT, decltype(stream)::value, LEAN>
           <<<tM * tN, C::kThreads, 0, s>>>(A, B, (int)M, (int)N, (int)K, tM, tN, ep, ex);
     };
-    if (sizeof(OT) == 2 && M * N * 2 * (1 + (ep.z != nullptr)) >= kStreamOut)
-      go(std::bool_constant<sizeof(OT) == 2>{});
+    if (M * N * (int64_t)sizeof(OT) * (1 + (ep.z != nullptr)) >= kStreamBytes)
+      go(std::true_type{});
     else
       go(std::false_type{});
   } else {

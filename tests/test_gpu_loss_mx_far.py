@@ -10,6 +10,7 @@ from tests.loss_mx_plan import mx as plan
 
 pytestmark = pytest.mark.gpu
 
+U = 2.0 ** -24
 F32, BF16, U8 = torch.float32, torch.bfloat16, torch.uint8
 D, T = 32768 + 32, 140000                                   # 4.6e9 elements
 
@@ -27,7 +28,8 @@ def new(*s, t=U8):
 
 def filled(rows, d, t=BF16):
     """Rows that differ: a random one, shifted by the row's number and scaled by it."""
-    base = torch.empty(2 * d, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(5))
+    base = torch.empty(2 * d, device="cuda")
+    base.normal_(generator=torch.Generator("cuda").manual_seed(5))
     x = new(rows, d, t=t)
     for a in range(0, rows, 4096):
         n = min(4096, rows - a)
@@ -199,3 +201,42 @@ def test_cross_entropy_of_far_tokens(gpu_lib):
         rel = torch.expm1(S * 2.0 ** -13 + e[:, None]) + 2.0 ** -11
         tol = (G.abs() * rel) @ aw + (G.abs() @ aw) * (V * 2.0 ** -24) + want.abs() * 2.0 ** -8
         assert bool(((dx[s] - want).abs() <= tol + 2.0 ** -40 * aw.sum(0)).all())
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("tokens,d_out", [(8192, 8208), (8200, 16400)])
+def test_float32_outputs_past_the_caches(gpu_lib, fp4, tokens, d_out):
+    """269 MB of float32 and 1.1 GB of it, y and z, of the FP8 and the FP4 product with a
+    bias; 64 products each, off by 64 half steps of their absolute sum at most, the bias's
+    by one of the result."""
+    d_in = 64
+    x, w = filled(tokens, d_in, F32), filled(d_out, d_in, F32)
+    bias = new(d_out, t=F32).normal_()
+    y = new(tokens, d_out, t=F32)
+    z = new(tokens, d_out, t=F32) if d_out > 10000 else None
+    one = torch.ones(1, device="cuda")
+    if fp4:
+        ops, vals = [], []
+        for t in (x, w):
+            q, e = new(len(t), d_in // 2), new(*gpu_lib.mxfp4_scales_shape(len(t), d_in))
+            gpu_lib.mxfp4_quantize(t, q, e)
+            vals.append(new(len(t), d_in, t=F32))
+            gpu_lib.mxfp4_dequantize(q, e, vals[-1])
+            ops += [q, e]
+        gpu_lib.melded_linear_fwd_mxfp4(*ops, y, bias=bias, act="relu", z=z)
+    else:
+        q = [t.to(torch.float8_e4m3fn) for t in (x, w)]
+        vals = [t.float() for t in q]
+        gpu_lib.melded_linear_fwd_act(q[0].view(U8), one, q[1].view(U8), one, y, bias=bias,
+                                      act="relu", z=z)
+    for at in (0, tokens // 2 - 20, tokens - 40):
+        s = slice(at, at + 40)
+        ref = vals[0][s].double() @ vals[1].double().T
+        S = vals[0][s].abs().double() @ vals[1].abs().double().T
+        # (of E4M3's products the matrix core cuts what lies 2^-13 below the largest of eight)
+        tol = S * 64 * U + (S * 2.0 ** -13 if not fp4 else 0)
+        ref = ref + bias.double()
+        tol = tol + ref.abs() * U
+        if z is not None:
+            assert bool(((z[s] - ref).abs() <= tol).all())
+        assert bool(((y[s] - ref.clamp(min=0)).abs() <= tol).all())
