@@ -410,6 +410,7 @@ __global__ __launch_bounds__(256) void dx_join(const float* __restrict__ part, i
 // ---- host -----------------------------------------------------------------
 using P256 = Tile<256, 256, 2, 2>;
 using P256x128 = Tile<256, 128, 2, 2>;
+using P192x128 = Tile<192, 128, 2, 2>;
 using P128 = Tile<128, 128, 2, 2>;
 using T64 = Tile<64, 64, 2, 2, 4>;
 using T32 = Tile<32, 64, 1, 4, 4>;
@@ -563,7 +564,9 @@ hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const u
       const uint8_t* w = wq + v0 * d;
       const Grads gr{lse + r0, at_target, (_Float16*)g, ld, (int)v0};
       switch (grad_kind(n, ld, d)) {
+        case kGrad256: launch_logits_bwd<P256, 1>(x, w, n, d, cols, lg, gr, s); break;
         case kGrad256x128: launch_logits_bwd<P256x128, 2>(x, w, n, d, cols, lg, gr, s); break;
+        case kGrad192x128: launch_logits_bwd<P192x128, 2>(x, w, n, d, cols, lg, gr, s); break;
         case kGrad128: launch_logits_bwd<P128, 2>(x, w, n, d, cols, lg, gr, s); break;
         case kGrad64: launch_logits_bwd<T64, 0>(x, w, n, d, cols, lg, gr, s); break;
         default: launch_logits_bwd<T32, 0>(x, w, n, d, cols, lg, gr, s); break;

@@ -37,10 +37,15 @@ LossKind loss_kind(int64_t T, int64_t V, int64_t d) {
 }
 
 // G's tiles, by linear_act_plan.hpp's costs, those kinds that are cheapest somewhere:
-// 16000 columns of 4096 205 us in 256 x 128 at 4096 tokens (128 x 128: 246), 35 and 37 at
-// 512, 17 in 64 x 64 at 128 (128 x 128: 20), 12.1 in 32 x 64 at 17 (12.8).
-enum GradKind { kGrad256x128, kGrad128, kGrad64, kGrad32x64, kGradKinds };
-constexpr TileKind kGradTile[kGradKinds] = {k256x128, k128, k64, k32x64};
+//   4096 x 32000 x 4096: 453 us in 256 x 256, 469 in 192 x 128, 473 in 256 x 128, 562 in
+//     128 x 128; 512 tokens 59, 61, 57 and 61
+//   4096 x 50000 x 1024: 280 in 192 x 128, 318 in 256 x 128, 379 in 256 x 256; 333 x 131071
+//     x 1040 84, 106 and 132 (128 x 128: 101)
+//   128 x 16000 x 4096: 17 in 64 x 64, 20 in 128 x 128; 17 tokens 12.1 in 32 x 64, 12.8
+enum GradKind {
+  kGrad256, kGrad256x128, kGrad192x128, kGrad128, kGrad64, kGrad32x64, kGradKinds
+};
+constexpr TileKind kGradTile[kGradKinds] = {k256, k256x128, k192x128, k128, k64, k32x64};
 GradKind grad_kind(int64_t T, int64_t n, int64_t d) {
   GradKind best = kGrad64;
   float cost = HUGE_VALF;

@@ -37,7 +37,7 @@ extern "C" void loss(int64_t T, int64_t d, int64_t V, int64_t* out) {
 
 MX_KINDS = ("256x128", "128", "64", "32x64")
 LOSS_KINDS = ("256", "128", "64", "32x64")
-GRAD_KINDS = ("256x128", "128", "64", "32x64")
+GRAD_KINDS = ("256", "256x128", "192x128", "128", "64", "32x64")
 DX_KINDS = ("256", "256x128", "128", "64", "32x64")
 
 

@@ -43,14 +43,17 @@ SHAPES = {
     ("128", "128", "128*", 1): [(2100, 512, 9001)],
     ("128", "256x128", "64", 1): [(5000, 272, 3001)],
     ("128", "256x128", "128*", 1): [(600, 528, 20000)],
-    ("128", "256x128", "128", 1): [(2048, 1040, 12000), (3000, 3088, 3001)],
+    ("128", "256x128", "128", 1): [(2048, 1040, 12000)],
+    ("128", "192x128", "128", 1): [(3000, 3088, 3001)],
     ("128", "256x128", "256x128", 1): [(2048, 2064, 3001)],
-    ("256", "256x128", "256", 1): [(4096, 4096, 8000)],
-    ("128", "128", "64*", 1): [(2100, 48, 40000)],
-    ("256", "256x128", "128*", 1): [(513, 1040, 20000), (4096, 1040, 20001)],
+    ("256", "256", "256", 1): [(4096, 4096, 8000)],
+    ("128", "192x128", "64*", 1): [(2100, 48, 40000)],
+    ("256", "192x128", "128*", 1): [(513, 1040, 20000)],
+    ("256", "256x128", "128*", 1): [(4096, 1040, 20001)],
     ("128", "128", "64*", 2): [(9000, 48, 40000)],
-    ("128", "128", "256x128*", 2): [(9000, 272, 33000)],
-    ("256", "256x128", "256x128", 2): [(10000, 2064, 28000)],
+    ("128", "192x128", "256x128*", 2): [(9000, 272, 33000)],
+    ("256", "256", "256x128", 2): [(10000, 2064, 28000)],
+    ("256", "256", "128*", 1): [(4100, 2064, 14001)],
 }
 
 
