@@ -1,8 +1,14 @@
 // The product of FP4 operands with a power of two per block of 32 (mx.hpp):
 //   z = dec(Xq) dec(Wq)^T + bias,   y = act(z) + residual,
 // with the epilogue, the kernels and the rule of linear_act.hip; the matrix core
-// applies the blocks' scales itself (v_mfma_scale_f32_16x16x128_f8f6f4), whose bytes
-// ride along with the codes of a K step, eight for a row.
+// applies the blocks' scales itself (v_mfma_scale_f32_16x16x128_f8f6f4 and its form of 32
+// x 32 x 64), whose bytes ride along with the codes of a K step, eight for a row.
+//
+// Bound by the power of the card where it is long: 8192 x 8192 x 8192 250 us (4.4
+// PFLOP/s), 219 without its loads, 220 without its LDS reads, 179 without either, and 180
+// as it stands with zeros for operands.  8192 x 11008 x 4096 with gelu and z 227 us, of
+// which the outputs are 67 at a copy's rate; 1 x 4096 x 4096 4.3 us, 2 TB/s and a
+// launch's latency.
 #include "activation.hpp"
 #include "elem.hpp"
 #include "kernels.hpp"

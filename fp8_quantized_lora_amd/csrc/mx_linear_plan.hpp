@@ -9,8 +9,8 @@ namespace {
 
 // Tiles of 256 x 128, two on a CU: one workgroup's epilogue runs under the other's
 // products, which with FP4 take half the time for the same outputs: 8192 x 11008 x 4096
-// with gelu and z 256 us, 271 in 256 x 256 alone on a CU; 189 and 207 without; 8192^3 255
-// and 250.  128 x 128, which load more for a product, where 256 x 128 leave CUs empty:
+// with gelu and z 213 us, 257 in 256 x 256 alone on a CU; 189 and 207 without; 8192^3 250
+// and 240.  128 x 128, which load more for a product, where 256 x 128 leave CUs empty:
 // 4096 x 5120 x 13824 141 and 149, 1024 x 11008 x 4096 with gelu and z 36 and 40, 1024
 // x 4096 x 4096 13.7 and 20.9.  64 x 64 and 32 x 64 where those do: 512 x 4096 x 4096
 // 11.5 (128 x 128: 12.0), 256 x 11008 x 4096 17.7 (12.9), 128 x 4096 x 4096 8.5 and 7.1
