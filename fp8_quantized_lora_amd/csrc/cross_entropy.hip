@@ -205,75 +205,89 @@ __global__ __launch_bounds__(256) void loss_join(const float2* __restrict__ part
 }
 
 // ---- backward -------------------------------------------------------------
-// at_target[row] = 2^15 (p - 1) of the row's target: a wave a row
-__global__ __launch_bounds__(256) void target_grads(const uint8_t* __restrict__ x,
-                                                    const uint8_t* __restrict__ w, int M, int d,
-                                                    int64_t V, const float* __restrict__ sx,
-                                                    const float* __restrict__ sw,
-                                                    const int64_t* __restrict__ target,
-                                                    const float* __restrict__ lse,
-                                                    float* __restrict__ at_target) {
+// What G's epilogue takes of a row: the logarithm of its terms' factor, 15 - lse in base
+// 2 (-inf: the row is not counted, its terms are 0), G at its target and the target (-1:
+// none).
+struct __attribute__((aligned(16))) GradRow {
+  float shift, at_target;
+  int target, unused;
+};
+
+// a wave a row; G at the target is 2^15 (p - 1)
+__global__ __launch_bounds__(256) void grad_rows(const uint8_t* __restrict__ x,
+                                                 const uint8_t* __restrict__ w, int M, int d,
+                                                 int64_t V, const float* __restrict__ sx,
+                                                 const float* __restrict__ sw,
+                                                 const int64_t* __restrict__ target,
+                                                 const float* __restrict__ lse,
+                                                 GradRow* __restrict__ rows) {
   const int row = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (row >= M) return;
   const int64_t t = target[row];
-  if (t < 0 || t >= V) return;                               // not read
-  const uint8_t* a = x + (int64_t)row * d;
-  const uint8_t* b = w + t * d;
+  const bool has = t >= 0 && t < V;
   float sum = 0.0f;
-  for (int i = lane * 16; i < d; i += 1024) {
-    const uint4 p = *reinterpret_cast<const uint4*>(a + i);
-    const uint4 q = *reinterpret_cast<const uint4*>(b + i);
-    const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
+  if (has) {
+    const uint8_t* a = x + (int64_t)row * d;
+    const uint8_t* b = w + t * d;
+    for (int i = lane * 16; i < d; i += 1024) {
+      const uint4 p = *reinterpret_cast<const uint4*>(a + i);
+      const uint4 q = *reinterpret_cast<const uint4*>(b + i);
+      const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 u0 = dec2(u[j], false), u1 = dec2(u[j], true);
-      const float2 v0 = dec2(v[j], false), v1 = dec2(v[j], true);
-      sum = fmaf(u0.x, v0.x, fmaf(u0.y, v0.y, fmaf(u1.x, v1.x, fmaf(u1.y, v1.y, sum))));
+      for (int j = 0; j < 4; ++j) {
+        const float2 u0 = dec2(u[j], false), u1 = dec2(u[j], true);
+        const float2 v0 = dec2(v[j], false), v1 = dec2(v[j], true);
+        sum = fmaf(u0.x, v0.x, fmaf(u0.y, v0.y, fmaf(u1.x, v1.x, fmaf(u1.y, v1.y, sum))));
+      }
     }
+    sum = wave_sum_f32(sum);
   }
-  sum = wave_sum_f32(sum);
-  if (lane == 0) at_target[row] = expm1f(sum / (sx[0] * sw[0]) - lse[row]) * kGradScale;
+  if (lane != 0) return;
+  GradRow r;
+  r.shift = t < 0 ? -INFINITY : fmaf(lse[row], -kLog2e, 15.0f);
+  r.at_target = expm1f(sum / (sx[0] * sw[0]) - lse[row]) * kGradScale;
+  r.target = has ? (int)t : -1;
+  r.unused = 0;
+  rows[row] = r;
 }
 
 // G of a piece, [M x ldg] float16, columns past the vocabulary 0
 struct Grads {
-  const float* lse;
-  const float* at_target;
+  const GradRow* rows;
   _Float16* G;
   int64_t ldg;
   int v0;              // the piece's first column
 };
 
-// the row's -lse in base 2, and its target's column in the piece; columns of a row
-// that is not counted are 0
-struct GradRow {
-  float neg, at_target;
-  int64_t t;
-  bool counts;
-  __device__ __forceinline__ GradRow(const Logits& lg, const Grads& gr, int row) {
-    t = lg.target[row];
-    counts = t >= 0;
-    t -= gr.v0;
-    neg = -gr.lse[row] * kLog2e;
-    at_target = gr.at_target[row];
-  }
-  __device__ __forceinline__ float of(float acc, float k, int col, int V) const {
-    const float p = __builtin_amdgcn_exp2f(fmaf(acc, k, neg)) * kGradScale;
-    return !counts || col >= V ? 0.0f : col == t ? at_target : p;
-  }
-};
-
 // through the wave's part of the LDS, as tile_out: eight columns of a row per lane
 template <class C, int LDS, int MB, int NB, class ACC>
 __device__ __forceinline__ void grads_out(uint8_t* smem, const ACC (&acc)[MB][NB], int m0, int n0,
-                                          int M, int V, float k, const Logits& lg,
-                                          const Grads& gr) {
+                                          int M, int V, float k, const Grads& gr) {
   rows_through_lds<C, LDS>(smem, acc, m0, n0, M, (int)gr.ldg, [&](int row, int col, float(&v)[8]) {
-    const GradRow r(lg, gr, row);
+    const GradRow r = gr.rows[row];
     typedef _Float16 H8 __attribute__((ext_vector_type(8)));
     H8 h;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = (_Float16)r.of(v[i], k, col + i, V);
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], k, r.shift);
+    // logits so large that FP8's may pass lse by half a unit: p is 1 at most, and 2^16 is
+    // float16's end (by comparison, which leaves a NaN)
+    if (fabsf(r.shift) > 8192.0f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] > 15.0f ? 15.0f : v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (_Float16)__builtin_amdgcn_exp2f(v[i]);
+    const int at = r.target - gr.v0 - col;
+    if ((unsigned)at < 8u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i == at) h[i] = (_Float16)r.at_target;
+    }
+    if (col + 8 > V) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (col + i >= V) h[i] = (_Float16)0.0f;
+    }
     *reinterpret_cast<H8*>(gr.G + (int64_t)row * gr.ldg + col) = h;
   });
 }
@@ -289,7 +303,7 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void grads_pipe(
   pipe_product<E4M3, C, PER_CU>(
       A, B, M, N, K, m0, n0, 0, INT32_MAX, Exponents{}, [&] { return lg.k(); },
       [&](const auto& acc, float k, uint8_t* smem) {
-        grads_out<C, Ring<E4M3, C, PER_CU>::kLds>(smem, acc, m0, n0, M, N, k, lg, gr);
+        grads_out<C, Ring<E4M3, C, PER_CU>::kLds>(smem, acc, m0, n0, M, N, k, gr);
       });
 }
 template <class C>
@@ -302,7 +316,7 @@ __global__ __launch_bounds__(C::kThreads) void grads_tile(
   tile_product<E4M3, C>(
       A, B, M, N, K, m0, n0, 0, INT32_MAX, Exponents{}, [&] { return lg.k(); },
       [&](const auto& acc, float k, uint8_t* smem) {
-        grads_out<C, kTileLds<E4M3, C>>(smem, acc, m0, n0, M, N, k, lg, gr);
+        grads_out<C, kTileLds<E4M3, C>>(smem, acc, m0, n0, M, N, k, gr);
       });
 }
 // dx of all pieces up to this one: sums in `sums` between pieces, dx itself at the last
@@ -559,15 +573,15 @@ hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const u
     void* const to = (uint8_t*)dx + r0 * d * (dx_type == 0 ? 4 : 2);
     float* const sums = dx_type == 0 ? (float*)to : (float*)(g + p.g);
     float* const part = (float*)(g + p.g + p.sums);
-    float* const at_target = (float*)(g + p.g + p.sums + p.part);
-    target_grads<<<(unsigned)ceil_div64(n, 4), 256, 0, s>>>(x, wq, (int)n, (int)d, V, s_x, s_w,
-                                                            lg.target, lse + r0, at_target);
+    GradRow* const rows = (GradRow*)(g + p.g + p.sums + p.part);
+    grad_rows<<<(unsigned)ceil_div64(n, 4), 256, 0, s>>>(x, wq, (int)n, (int)d, V, s_x, s_w,
+                                                         lg.target, lse + r0, rows);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     for (int64_t v0 = 0; v0 < V; v0 += p.width) {
       const int64_t cols = std::min(p.width, V - v0), ld = up(cols, 64);
       const uint8_t* w = wq + v0 * d;
-      const Grads gr{lse + r0, at_target, (_Float16*)g, ld, (int)v0};
+      const Grads gr{rows, (_Float16*)g, ld, (int)v0};
       switch (grad_kind(n, ld, d)) {
         case kGrad256: launch_logits_bwd<P256, 1>(x, w, n, d, cols, lg, gr, s); break;
         case kGrad256x128: launch_logits_bwd<P256x128, 2>(x, w, n, d, cols, lg, gr, s); break;

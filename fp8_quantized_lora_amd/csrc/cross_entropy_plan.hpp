@@ -102,8 +102,8 @@ struct BwdPlan {
   int64_t width;
   DxKind kind;
   int splits, kc;                                            // kc K steps each
-  size_t g, sums, part, at_target;                           // bytes, multiples of 256
-  size_t bytes() const { return g + sums + part + at_target; }
+  size_t g, sums, part, rows;                           // bytes, multiples of 256
+  size_t bytes() const { return g + sums + part + rows; }
 };
 BwdPlan bwd_plan(int64_t T, int64_t d, int64_t V, int dx_type) {
   BwdPlan p;
@@ -134,7 +134,7 @@ BwdPlan bwd_plan(int64_t T, int64_t d, int64_t V, int dx_type) {
   // float32 gradients collect in place
   p.sums = dx_type != 0 && p.width < V ? (size_t)up(T * d * 4, 256) : 0;
   p.part = p.splits > 1 ? (size_t)up(p.splits * T * d * 4, 256) : 0;
-  p.at_target = (size_t)up(T * 4, 256);
+  p.rows = (size_t)up(T * 16, 256);                          // a GradRow each
   return p;
 }
 

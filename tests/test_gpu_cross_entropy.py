@@ -189,6 +189,30 @@ def test_sure_and_flat_tokens(gpu_lib):
     check(gpu_lib, c)
 
 
+@pytest.mark.parametrize("T,d,V", [(5, 64, 500), (70, 528, 2000), (700, 1040, 3001)])
+def test_logits_of_tens_of_thousands(gpu_lib, T, d, V):
+    """The FP8 product's logits are then off by more than one, and pass lse: what they give
+    is bounded, a sure token's gradient 0 up to the others' terms."""
+    c = Case(T, d, V, ignored=0.0)
+    c.s_x.copy_(c.s_x / 2e4)
+    z = c.xv @ c.wv.T * 2e4
+    c.target.copy_(z.argmax(1))
+    loss, lse = c.forward(gpu_lib)
+    assert bool(((lse - z.amax(1)).abs() <= z.amax(1) * 1e-4 + 1).all())
+    for dt in (F32, BF16):
+        dx = c.backward(gpu_lib, lse, dt)
+        # each of V terms at most |dloss| |w|, half a step of dx's type aside
+        most = c.dloss.abs()[:, None].double() * c.wv.abs().sum(0)
+        assert bool((dx.abs() <= most * (1 + 2.0 ** -7) + 1e-30).all())
+
+
+@pytest.mark.parametrize("T,d,V", [(16, 272, 9282), (40, 528, 41389), (100, 528, 8620),
+                                   (333, 16, 20536), (700, 48, 26825)])
+def test_splits_left_without_columns(gpu_lib, T, d, V):
+    """Of dx's splits the last ones begin past the vocabulary."""
+    check(gpu_lib, Case(T, d, V))
+
+
 @pytest.mark.parametrize("T", [3, 50, 700])
 def test_targets_out_of_range_and_nan(gpu_lib, T):
     """All tokens without a class; a class of V or more and a NaN in a row give NaN in
