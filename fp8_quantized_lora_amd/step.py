@@ -407,7 +407,8 @@ class LinearCrossEntropy:
 
     def forward(self, X: torch.Tensor, target: torch.Tensor, stream=None):
         """The loss of each row of X [tokens x d] (float32 or bfloat16) for the class
-        target [tokens] (int64; negative: it does not count, its loss is 0)."""
+        target [tokens] (int64; negative: it does not count, its loss is 0), which the
+        backward reads again."""
         fp8_quantize(X, self.xq, self.s_x, ws=self.ws_q, stream=stream)
         self.target = target
         linear_cross_entropy_fwd(self.xq, self.s_x, self.wq, self.s_w, target, self.loss, self.lse,
