@@ -263,8 +263,8 @@ struct Grads {
 template <class C, int LDS, int MB, int NB, class ACC>
 __device__ __forceinline__ void grads_out(uint8_t* smem, const ACC (&acc)[MB][NB], int m0, int n0,
                                           int M, int V, float k, const Grads& gr) {
-  rows_through_lds<C, LDS>(smem, acc, m0, n0, M, (int)gr.ldg, [&](int row, int col, float(&v)[8]) {
-    const GradRow r = gr.rows[row];
+  const auto row_of = [&](int row) { return gr.rows[row]; };
+  const auto out = [&](int row, int col, float(&v)[8], const GradRow& r) {
     typedef _Float16 H8 __attribute__((ext_vector_type(8)));
     H8 h;
 #pragma unroll
@@ -289,7 +289,8 @@ __device__ __forceinline__ void grads_out(uint8_t* smem, const ACC (&acc)[MB][NB
         if (col + i >= V) h[i] = (_Float16)0.0f;
     }
     *reinterpret_cast<H8*>(gr.G + (int64_t)row * gr.ldg + col) = h;
-  });
+  };
+  rows_through_lds<C, LDS>(smem, acc, m0, n0, M, (int)gr.ldg, row_of, out);
 }
 
 template <class C, int PER_CU>
@@ -330,8 +331,19 @@ struct DxOut {
   bool first;
 };
 
+// the row's factor, and whether it counts
+struct DxRow {
+  float factor;
+  bool counts;
+};
+__device__ __forceinline__ DxRow dx_row(const DxOut& o, int row) {
+  if (!o.dx) return {1.0f, true};
+  const int64_t t = o.target[row];
+  return {t >= o.V ? NAN : o.dloss[row] / (o.sw[0] * kGradScale), t >= 0};
+}
 template <class OT>
-__device__ __forceinline__ void dx_out8(float (&v)[8], int row, int64_t at, const DxOut& o) {
+__device__ __forceinline__ void dx_out8(float (&v)[8], const DxRow& r, int64_t at,
+                                        const DxOut& o) {
   if (!o.first) {
     float t[8];
     load_elems<8>(o.sums + at, t);
@@ -342,10 +354,8 @@ __device__ __forceinline__ void dx_out8(float (&v)[8], int row, int64_t at, cons
     store_elems<8>(o.sums + at, v);
     return;
   }
-  const int64_t t = o.target[row];
-  const float f = t >= o.V ? NAN : o.dloss[row] / (o.sw[0] * kGradScale);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = t < 0 ? 0.0f : v[i] * f;
+  for (int i = 0; i < 8; ++i) v[i] = r.counts ? v[i] * r.factor : 0.0f;
   store_elems<8>((OT*)o.dx + at, v);
 }
 
@@ -376,11 +386,13 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void dx_pipe(
       Exponents{nullptr, nullptr, 0, rows}, [] { return 0; },
       [&](const auto& acc, int, uint8_t* smem) {
         rows_through_lds<C, Ring<F16ByE4M3Wide, C, PER_CU>::kLds>(
-            smem, acc, m0, n0, M, N, [&](int row, int col, float(&v)[8]) {
+            smem, acc, m0, n0, M, N,
+            [&](int row) { return SPLIT ? DxRow{} : dx_row(o, row); },
+            [&](int row, int col, float(&v)[8], const DxRow& r) {
               if constexpr (SPLIT)
                 store_elems<8>(part + ((int64_t)sp * M + row) * N + col, v);
               else
-                dx_out8<OT>(v, row, (int64_t)row * N + col, o);
+                dx_out8<OT>(v, r, (int64_t)row * N + col, o);
             });
       });
 }
@@ -399,11 +411,13 @@ __global__ __launch_bounds__(C::kThreads) void dx_tile(
       Exponents{nullptr, nullptr, 0, rows}, [] { return 0; },
       [&](const auto& acc, int, uint8_t* smem) {
         rows_through_lds<C, kTileLds<F16ByE4M3, C>>(
-            smem, acc, m0, n0, M, N, [&](int row, int col, float(&v)[8]) {
+            smem, acc, m0, n0, M, N,
+            [&](int row) { return SPLIT ? DxRow{} : dx_row(o, row); },
+            [&](int row, int col, float(&v)[8], const DxRow& r) {
               if constexpr (SPLIT)
                 store_elems<8>(part + ((int64_t)sp * M + row) * N + col, v);
               else
-                dx_out8<OT>(v, row, (int64_t)row * N + col, o);
+                dx_out8<OT>(v, r, (int64_t)row * N + col, o);
             });
       });
 }
@@ -422,7 +436,7 @@ __global__ __launch_bounds__(256) void dx_join(const float* __restrict__ part, i
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += t[e];
     }
-    dx_out8<OT>(v, (int)(at / N), at, o);
+    dx_out8<OT>(v, dx_row(o, (int)(at / N)), at, o);
   }
 }
 

@@ -66,33 +66,41 @@ __device__ __forceinline__ void put_rows(v4f* mine, const ACC (&acc)[MB][NB], in
 }
 
 // A wave's accumulators through its part of the LDS: each(row, column, eight columns'
-// values) for eight columns of a row at a time, the columns below N.
-template <class C, int LDS, int MB, int NB, class ACC, class EACH>
+// values, of(row)) for eight columns of a row at a time, the columns below N.  of() is what
+// is read for a row: for all of a pass's rows at once, ahead of its stores, behind which
+// the compiler would wait for each one.
+template <class C, int LDS, int MB, int NB, class ACC, class OF, class EACH>
 __device__ __forceinline__ void rows_through_lds(uint8_t* smem, const ACC (&acc)[MB][NB], int m0,
-                                                 int n0, int M, int N, EACH&& each) {
+                                                 int n0, int M, int N, OF&& of, EACH&& each) {
   constexpr int PASS = C::pass_of(C::WTM, LDS);
   static_assert(PASS % (C::WTM / MB) == 0 && C::WTM % PASS == 0, "whole blocks per pass");
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wm = w / C::WGN, wn = w % C::WGN;
-  constexpr int CH = C::WTN / 4, LPR = C::WTN / 8, RPI = 64 / LPR;
+  constexpr int CH = C::WTN / 4, LPR = C::WTN / 8, RPI = 64 / LPR, TURNS = PASS / RPI;
+  static_assert(RPI * LPR == 64 && TURNS * RPI == PASS, "whole turns");
   constexpr int SWZ = (CH & (CH - 1)) == 0 ? CH - 1 : 0;     // as tile_out
   auto slot = [](int r, int c) { return r * CH + (c ^ (r & SWZ)); };
   v4f* mine = reinterpret_cast<v4f*>(smem + w * (LDS / C::NW / 16 * 16));
   const int cl = lane % LPR, rl = lane / LPR;
   const int col = n0 + wn * C::WTN + cl * 8;
-  const bool col_ok = rl < RPI && col < N;                   // N is a multiple of 8
+  const bool col_ok = col < N;                               // N is a multiple of 8
 #pragma unroll
   for (int p = 0; p < C::WTM / PASS; ++p) {
+    const int first = m0 + wm * C::WTM + p * PASS + rl;
+    decltype(of(0)) info[TURNS];
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) info[i] = of(min(first + i * RPI, M - 1));
     // the wave's own LDS: its accesses are executed in order
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     put_rows<PASS>(mine, acc, p, slot);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    for (int r = rl; r < PASS; r += RPI) {
-      const int row = m0 + wm * C::WTM + p * PASS + r;
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+      const int r = i * RPI + rl;
       const v4f a = mine[slot(r, 2 * cl)];
       const v4f b = mine[slot(r, 2 * cl + 1)];
-      if (!col_ok || row >= M) continue;
+      if (!col_ok || first + i * RPI >= M) continue;
       float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      each(row, col, v);
+      each(first + i * RPI, col, v, info[i]);
     }
   }
 }
