@@ -21,7 +21,7 @@
 // and 2^15 because p may be as small as 1 / V: under it float16 has its full precision
 // down to 2^-29 and absolute steps of 2^-39 below, while 1 still fits; E4M3 codes are
 // exact in it.  The row's factor dloss / s_w is applied at the end, in float32.  4096 x
-// 4096 x 32000: 1250 to 1290 us, of them G 450 and dx 760 to 820 (1.3 to 1.4 PFLOP/s; the
+// 4096 x 32000: 1200 to 1250 us, of them G 430 and dx 760 to 820 (1.3 to 1.4 PFLOP/s; the
 // matrix cores busy 77 % of the cycles at 1.6 GHz, the power's limit).
 #include "cross_entropy_plan.hpp"
 #include "elem.hpp"

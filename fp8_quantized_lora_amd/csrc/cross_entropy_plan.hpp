@@ -37,10 +37,10 @@ LossKind loss_kind(int64_t T, int64_t V, int64_t d) {
 }
 
 // G's tiles, by linear_act_plan.hpp's costs, those kinds that are cheapest somewhere:
-//   4096 x 32000 x 4096: 453 us in 256 x 256, 469 in 192 x 128, 473 in 256 x 128, 562 in
-//     128 x 128; 512 tokens 59, 61, 57 and 61
-//   4096 x 50000 x 1024: 280 in 192 x 128, 318 in 256 x 128, 379 in 256 x 256; 333 x 131071
-//     x 1040 84, 106 and 132 (128 x 128: 101)
+//   4096 x 32000 x 4096: 431 us in 256 x 256, 469 in 192 x 128, 466 in 256 x 128, 559 in
+//     128 x 128; 512 tokens 60, 61, 57 and 62
+//   4096 x 50000 x 1024: 258 in 192 x 128, 294 in 256 x 128, 321 in 256 x 256; 333 x 131071
+//     x 1040 76, 94 and 113 (128 x 128: 97)
 //   128 x 16000 x 4096: 17 in 64 x 64, 20 in 128 x 128; 17 tokens 12.1 in 32 x 64, 12.8
 enum GradKind {
   kGrad256, kGrad256x128, kGrad192x128, kGrad128, kGrad64, kGrad32x64, kGradKinds
