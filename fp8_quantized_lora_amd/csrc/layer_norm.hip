@@ -10,7 +10,7 @@
 // Both are bound by memory: x read and y written once (4096 x 5120, fp32 to
 // bf16: 25.3 us, 5.0 TB/s); dy and x read and dx written once (8192 x 4096, fp32
 // dy, bf16 x: 65.7 us, 5.1 TB/s; a copy on this card reaches 5.1 to 5.4; x as an 8-bit
-// checkpoint 64 to 66 us, 4.7 TB/s: each element is decoded for the sums and for dx).  A row
+// checkpoint 57 to 60 us on the GPU, 5.2 TB/s).  A row
 // lies in the registers of a group of 64 to 1024 threads from its one read on;
 // rows too long for that (32768 elements forward, 16384 backward) are read again
 // for each pass.
@@ -536,11 +536,15 @@ constexpr int kBwdBlocks = 256;
 struct BwdPlan {
   int n, nt, G, blocks;                        // n elements a thread; 0: rows too long or short
 };
-BwdPlan bwd_plan(int64_t T, int64_t d) {
+// threads: of a workgroup of several rows.  512, or for an 8-bit checkpoint 1024, whose
+// rows are fewer bytes under way, where there are rows for all: 8192 x 4096 with fp32 dy 62
+// us (512: 67), with bf16 dy 41.8 (44.7), 2048 x 4096 20.4 (21.3).
+BwdPlan bwd_plan(int64_t T, int64_t d, int threads = 512) {
   int n = 8, nt = row_threads(d, n, 1024);
   if (!nt) nt = row_threads(d, n = 16, 1024);
   if (!nt || d < 4) return {0, 0, 0, 0};
-  const int G = std::max(1, 512 / nt);
+  if (T < (int64_t)kBwdBlocks * (threads / nt)) threads = 512;
+  const int G = std::max(1, threads / nt);
   return {n, nt, G, (int)std::min<int64_t>((T + G - 1) / G, kBwdBlocks)};
 }
 
@@ -550,11 +554,11 @@ hipError_t bwd_rows(const BwdPlan& p, const GT* dy, const XT* x, const uint8_t* 
                     hipStream_t s) {
   const size_t lds = (size_t)C * E * (p.G / 2) * p.nt * 4;
   // a workgroup of at most 512 threads may use twice the registers
-  if (p.nt <= 512)
+  if (p.nt * p.G <= 512)
     ln_bwd_rows<XT, GT, E, C, 512, STREAM, ODD><<<p.blocks, p.nt * p.G, lds, s>>>(
         dy, x, xs, w, mean, rstd, dx, part, T, (int)d, p.nt);
   else
-    ln_bwd_rows<XT, GT, E, C, 1024, STREAM, ODD><<<p.blocks, p.nt, lds, s>>>(
+    ln_bwd_rows<XT, GT, E, C, 1024, STREAM, ODD><<<p.blocks, p.nt * p.G, lds, s>>>(
         dy, x, xs, w, mean, rstd, dx, part, T, (int)d, p.nt);
   return hipGetLastError();
 }
@@ -609,7 +613,7 @@ hipError_t bwd(const GT* dy, const XT* x, const uint8_t* xs, const float* w, con
   if (bwd_short_fits(T, d))
     return bwd_short<XT, GT, E, ODD>(dy, x, xs, w, mean, rstd, T, d, dx, dw, db, s);
   if (!dw && !db) part = nullptr;
-  const BwdPlan p = bwd_plan(T, d);
+  const BwdPlan p = bwd_plan(T, d, std::is_same_v<XT, kept_t> ? 1024 : 512);
   // the streaming hint needs whole lines
   constexpr bool HINT = !ODD;
   const bool stream = HINT && T * d * (int64_t)(2 * sizeof(GT) + sizeof(XT)) > kStreamBytes;

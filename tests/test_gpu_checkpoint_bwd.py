@@ -95,7 +95,8 @@ def test_act(gpu_lib, T, d, gt):
 
 
 @pytest.mark.parametrize("gt", [F32, BF16])
-@pytest.mark.parametrize("T, d", SIZES + [(40, 20000), (1030, 18000), (1030, 8200)])
+@pytest.mark.parametrize("T, d", SIZES + [(40, 20000), (1030, 18000), (1030, 8200),
+                                         (1031, 4096), (1500, 1540), (2500, 513), (4099, 100)])
 def test_norm(gpu_lib, T, d, gt):
     announce(f"layer_norm_bwd_ckpt T={T} d={d} {gt}")
     x, dy = draw(T, d, T * 3 + d)
