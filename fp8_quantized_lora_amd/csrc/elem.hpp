@@ -154,15 +154,21 @@ struct Piece {
 };
 
 // A lane's elements of a row: of float32 or bfloat16, or of an 8-bit checkpoint
-// (T = kept_t: E4M3 codes, and a power of two per block of 32 in `scales`).
+// (T = kept_t: E4M3 codes, and a power of two per block of 32 in `scales`).  at(): the row,
+// found once for all of a lane's pieces; with an address formed for each piece instead
+// layer norm's backward holds more of them, and spills (2048 x 11008 of float32 74.8 us, 69.2
+// so).
 typedef uint8_t kept_t;
 template <class T, int E, bool ODD>
 struct RowElems {
+  typedef const T* At;
   Raw<T, E> v;
+  static __device__ __forceinline__ At at(const T* x, const uint8_t*, int64_t row, int64_t d) {
+    return x + row * d;
+  }
   template <bool STREAM = false>
-  __device__ __forceinline__ void load(const T* x, const uint8_t*, int64_t row, int64_t d,
-                                       uint32_t base) {
-    v.template load<STREAM>(x + row * d + base);
+  __device__ __forceinline__ void load(At row, uint32_t base) {
+    v.template load<STREAM>(row + base);
   }
   __device__ __forceinline__ void clear() { v.clear(); }
   __device__ __forceinline__ float operator[](int e) const { return v[e]; }
@@ -174,18 +180,24 @@ struct RowElems<kept_t, E, ODD> {
   V v;
   uint8_t s0, s1;                              // of the first element's block, of the last's
   int turn;                                    // elements of the first
+  struct At {
+    const kept_t* x;
+    const uint8_t* s;
+  };
+  static __device__ __forceinline__ At at(const kept_t* x, const uint8_t* scales, int64_t row,
+                                          int64_t d) {
+    return {x + row * d, scales + row * ((d + 31) / 32)};
+  }
   template <bool STREAM = false>
-  __device__ __forceinline__ void load(const kept_t* x, const uint8_t* scales, int64_t row,
-                                       int64_t d, uint32_t base) {
-    const V_any* p = reinterpret_cast<const V_any*>(x + row * d + base);
+  __device__ __forceinline__ void load(const At& row, uint32_t base) {
+    const V_any* p = reinterpret_cast<const V_any*>(row.x + base);
     if constexpr (STREAM && E > 1)
       v = __builtin_nontemporal_load(p);
     else
       v = *p;
-    const uint8_t* s = scales + row * ((d + 31) / 32);
-    s0 = s[base / 32];
+    s0 = row.s[base / 32];
     if constexpr (ODD && E > 1) {              // the row's last piece may lie in two
-      s1 = s[(base + E - 1) / 32];
+      s1 = row.s[(base + E - 1) / 32];
       turn = 32 - (int)(base & 31);
     }
   }
@@ -212,7 +224,7 @@ __device__ __forceinline__ void load_row_elems(const T* x, const uint8_t* scales
                                                int64_t d, int64_t base, float (&v)[E]) {
   if constexpr (std::is_same_v<T, kept_t>) {
     RowElems<kept_t, E, false> r;
-    r.load(x, scales, row, d, (uint32_t)base);
+    r.load(r.at(x, scales, row, d), (uint32_t)base);
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = r[e];
   } else {

@@ -278,6 +278,7 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
   auto load = [&](Row& o, int64_t r) {
     const int64_t row = __builtin_amdgcn_readfirstlane((int)(r < T ? r : T - 1));
     const GT* dyr = dy + row * d;
+    const auto xr = RowElems<XT, E, ODD>::at(x, xs, row, d);
     o.mu = mean[row];
     o.rs = rstd[row];
 #pragma unroll
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(MOST) void ln_bwd_rows(const GT* dy, const XT* __re
       const Piece<E, ODD> p(gr.at<E>(c), d);
       if (p.any) {
         o.g[c].template load<STREAM>(dyr + p.base);
-        o.v[c].template load<STREAM>(x, xs, row, d, p.base);
+        o.v[c].template load<STREAM>(xr, p.base);
       } else {
         o.g[c].clear();
         o.v[c].clear();
@@ -408,7 +409,7 @@ __global__ __launch_bounds__(1024) void ln_bwd_short(
       float f[E];
       load_elems<E>(dy + from + p.base, gw[c]);
       RowElems<XT, E, ODD> v;
-      v.load(x, xs, live ? row : T - 1, d, p.base);
+      v.load(v.at(x, xs, live ? row : T - 1, d), p.base);
       if (w) load_elems<E>(w + p.base, f);
 #pragma unroll
       for (int e = 0; e < E; ++e) {

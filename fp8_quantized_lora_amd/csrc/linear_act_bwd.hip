@@ -36,7 +36,7 @@ __global__ __launch_bounds__(kRows * kLanes) void act_bwd_kernel(
       Raw<GT, E> gr;
       RowElems<ZT, E, ODD> v;
       gr.template load<STREAM>(dy + r * d + p.base);
-      if constexpr (ACT != kNone) v.template load<STREAM>(z, zs, r, d, p.base);
+      if constexpr (ACT != kNone) v.template load<STREAM>(v.at(z, zs, r, d), p.base);
       float g[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
