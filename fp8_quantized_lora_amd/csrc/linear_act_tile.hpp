@@ -120,40 +120,55 @@ __device__ __forceinline__ void tile_out(uint8_t* smem, const ACC (&acc)[MB][NB]
   auto slot = [](int r, int c) { return r * CH + (c ^ (r & SWZ)); };
   v4f* mine = reinterpret_cast<v4f*>(smem + w * (LDS / C::NW / 16 * 16));
   const int cl = lane % LPR, rl = lane / LPR;
-  // a lane stores 16 bytes at a time, a row's lanes one run of them: eight columns of
-  // bfloat16, or twice four of float32
-  constexpr int E = !SPLIT && sizeof(OT) == 2 ? 8 : 4, H = 8 / E;
-  const auto chunk = [&](int h) { return E == 8 ? 2 * cl : cl + h * LPR; };
+  // A lane stores 16 bytes at a time, a row's lanes one run of them: eight columns of
+  // bfloat16, or (RUNS) twice four of float32.  With a residual float32 is eight columns
+  // side by side as well, and in the caches: a load waits for the stores ahead of it, and
+  // the two runs have twice as many such waits, or lose more than those if both are read
+  // ahead: 4096 x 4096 x 4096 63 us, 72 and 79 in runs; 4096 x 8192 x 4096 154, 182 and 210.
+  constexpr bool F32 = SPLIT || sizeof(OT) == 4;
+  const bool runs = F32 && (SPLIT || !ep.residual);
+  const int c0 = runs ? cl : 2 * cl, c1 = runs ? cl + LPR : 2 * cl + 1;
   const int col0 = n0 + wn * C::WTN;
-  bool ok[H];                                                // N is a multiple of 16
-  float bias[H][E];
+  const bool ok0 = rl < RPI && col0 + 4 * c0 < N;            // N is a multiple of 16
+  const bool ok1 = rl < RPI && col0 + 4 * c1 < N;
+  float b0[4], b1[4];
 #pragma unroll
-  for (int h = 0; h < H; ++h) {
-    ok[h] = rl < RPI && col0 + 4 * chunk(h) < N;
-#pragma unroll
-    for (int i = 0; i < E; ++i) bias[h][i] = 0.0f;
-    if (!SPLIT && ep.bias && ok[h]) load_elems<E>(ep.bias + col0 + 4 * chunk(h), bias[h]);
+  for (int i = 0; i < 4; ++i) b0[i] = b1[i] = 0.0f;
+  if (!SPLIT && ep.bias) {
+    if (ok0) load_elems<4>(ep.bias + col0 + 4 * c0, b0);
+    if (ok1) load_elems<4>(ep.bias + col0 + 4 * c1, b1);
   }
   auto rows = [&](auto act, int first) {
-    for (int r = rl; r < PASS; r += RPI) {                // lanes past RPI rows: idle
-      const int row = m0 + wm * C::WTM + first + r;
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        float v[E];
-#pragma unroll
-        for (int i = 0; i < E / 4; ++i) {
-          const v4f a = mine[slot(r, chunk(h) + i)];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * i + e] = a[e];
+    constexpr int ACT = decltype(act)::value;
+    const auto run = [&](const v4f& a, const float (&bias)[4], int64_t at) {
+      float v[4] = {a[0], a[1], a[2], a[3]};
+      if constexpr (SPLIT)
+        store_elems<4>(part + (int64_t)sp * M * N + at, v);
+      else
+        finish<ACT, OT, STREAM>(v, scale, bias, ep, at);
+    };
+    const auto side_by_side = [&](const v4f& a, const v4f& b, int64_t at) {
+      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      const float bias[8] = {b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
+      finish<ACT, OT, STREAM && !F32>(v, scale, bias, ep, at);
+    };
+    const auto each_row = [&](auto in_runs) {
+      for (int r = rl; r < PASS; r += RPI) {              // lanes past RPI rows: idle
+        const int row = m0 + wm * C::WTM + first + r;
+        const v4f a = mine[slot(r, c0)], b = mine[slot(r, c1)];
+        const int64_t at = (int64_t)row * N + col0;
+        if constexpr (decltype(in_runs)::value) {
+          if (ok0 && row < M) run(a, b0, at + 4 * c0);
+          if (ok1 && row < M) run(b, b1, at + 4 * c1);
+        } else if constexpr (!SPLIT) {
+          if (ok0 && row < M) side_by_side(a, b, at + 4 * c0);
         }
-        if (!ok[h] || row >= M) continue;
-        const int64_t at = (int64_t)row * N + col0 + 4 * chunk(h);
-        if constexpr (SPLIT)
-          store_elems<E>(part + (int64_t)sp * M * N + at, v);
-        else
-          finish<decltype(act)::value, OT, STREAM>(v, scale, bias[h], ep, at);
       }
-    }
+    };
+    if (runs)
+      each_row(std::bool_constant<F32>{});
+    else
+      each_row(std::false_type{});
   };
 #pragma unroll
   for (int p = 0; p < C::WTM / PASS; ++p) {
