@@ -269,12 +269,10 @@ __device__ __forceinline__ void grads_out(uint8_t* smem, const ACC (&acc)[MB][NB
     H8 h;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], k, r.shift);
-    // logits so large that FP8's may pass lse by half a unit: p is 1 at most, and 2^16 is
-    // float16's end (by comparison, which leaves a NaN)
-    if (fabsf(r.shift) > 8192.0f) {
+    // p is 1 at most, but a logit's error, which goes with its terms and not with lse, may
+    // take it past lse, and 2^16 is float16's end.  (minimum: a NaN stays)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] > 15.0f ? 15.0f : v[i];
-    }
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_elementwise_minimum(v[i], 15.0f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = (_Float16)__builtin_amdgcn_exp2f(v[i]);
     const int at = r.target - gr.v0 - col;

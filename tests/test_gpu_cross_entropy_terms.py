@@ -1,0 +1,69 @@
+"""linear_cross_entropy_fwd and linear_cross_entropy_bwd where a logit is a small sum of large
+terms: two codes of each eight cancel, and what is left of the other six is a ten
+thousandth of them."""
+import pytest
+import torch
+
+from tests.gpu_util import announce
+from tests.loss_mx_plan import loss as plan
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, U8 = torch.float32, torch.bfloat16, torch.uint8
+
+# every kernel of G
+SHAPES = {
+    "32x64": [(1, 16, 2), (64, 16, 3), (50, 48, 70)],
+    "64": [(5000, 272, 77)],
+    "128": [(2100, 512, 9001)],
+    "192x128": [(3000, 3088, 3001)],
+    "256x128": [(2048, 2064, 3001)],
+    "256": [(4096, 4096, 8000)],
+}
+CASES = [(k, s) for k, v in SHAPES.items() for s in v]
+
+
+class Case:
+    """Logits of a standard deviation of `spread`."""
+
+    def __init__(self, T, d, V, spread=4.0, big=448.0, seed=0):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed + T + d + V)
+
+        def rows(n, second):
+            v = torch.empty((n, d // 8, 8), device="cuda").normal_(generator=g) * 4
+            v[:, :, 0] = big
+            v[:, :, 1] = second * big
+            return v.view(n, d).to(torch.float8_e4m3fn)
+        x, w = rows(T, 1.0), rows(V, -1.0)
+        self.T, self.d, self.V = T, d, V
+        self.s_x = torch.full((1,), 16 * (d * 6 / 8) ** 0.5 / spread, device="cuda")
+        self.s_w = torch.ones(1, device="cuda")
+        self.xv, self.wv = x.double() / self.s_x.double(), w.double()
+        self.target = torch.randint(0, V, (T,), generator=g, device="cuda")
+        self.dloss = torch.empty(T, device="cuda").normal_(generator=g) * 1e-2
+        self.args = (x.view(U8), self.s_x, w.view(U8), self.s_w, self.target)
+
+    def forward(self, fq):
+        loss, lse = torch.full((2, self.T), float("nan"), device="cuda")
+        fq.linear_cross_entropy_fwd(*self.args, loss, lse)
+        return loss, lse
+
+    def backward(self, fq, lse, dtype):
+        dx = torch.full((self.T, self.d), float("nan"), dtype=dtype, device="cuda")
+        fq.linear_cross_entropy_bwd(*self.args, lse, self.dloss, dx)
+        return dx
+
+
+@pytest.mark.parametrize("kind, shape", CASES)
+def test_probabilities_are_one_at_most(gpu_lib, kind, shape):
+    """Whatever a logit's error, dx is a sum of V terms of at most |dloss| |w| each."""
+    announce(f"cancelling terms, T, d, V = {shape}")
+    assert plan(*shape)[1] == kind
+    c = Case(*shape)
+    loss, lse = c.forward(gpu_lib)
+    assert float(lse.abs().max()) < 100
+    # (the terms' half steps, and that of the sum in dx's type)
+    most = c.dloss.abs().double()[:, None] * c.wv.abs().sum(0) * (1 + 2.0 ** -7)
+    for dt in (F32, BF16):
+        assert bool((c.backward(gpu_lib, lse, dt).abs() <= most).all())
