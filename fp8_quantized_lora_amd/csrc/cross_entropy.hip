@@ -245,7 +245,9 @@ __global__ __launch_bounds__(256) void grad_rows(const uint8_t* __restrict__ x,
   if (lane != 0) return;
   GradRow r;
   r.shift = t < 0 ? -INFINITY : fmaf(lse[row], -kLog2e, 15.0f);
-  r.at_target = expm1f(sum / (sx[0] * sw[0]) - lse[row]) * kGradScale;
+  // (p is 1 at most: half a step of an lse of 10^8 is four.  A NaN stays)
+  r.at_target = expm1f(__builtin_elementwise_minimum(sum / (sx[0] * sw[0]) - lse[row], 0.0f)) *
+                kGradScale;
   r.target = has ? (int)t : -1;
   r.unused = 0;
   rows[row] = r;

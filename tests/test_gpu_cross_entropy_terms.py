@@ -67,3 +67,26 @@ def test_probabilities_are_one_at_most(gpu_lib, kind, shape):
     most = c.dloss.abs().double()[:, None] * c.wv.abs().sum(0) * (1 + 2.0 ** -7)
     for dt in (F32, BF16):
         assert bool((c.backward(gpu_lib, lse, dt).abs() <= most).all())
+
+
+@pytest.mark.parametrize("size", [1e5, 1e7, 1e8])
+@pytest.mark.parametrize("T, d, V", [(64, 16, 3), (300, 272, 999)])
+def test_a_target_does_not_pass_lse(gpu_lib, T, d, V, size):
+    """Logits whose half steps are units: the target's own logit, summed apart, may lie above
+    lse, and its probability is 1 at most all the same."""
+    announce(f"logits of {size}, T, d, V = {(T, d, V)}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    x = torch.empty((T, d), device="cuda").normal_(generator=g).to(torch.float8_e4m3fn)
+    w = torch.empty((V, d), device="cuda").normal_(generator=g).to(torch.float8_e4m3fn)
+    s_x, s_w = torch.full((2, 1), (d ** 0.5 / size) ** 0.5, device="cuda")
+    target = (x.double() @ w.double().T).argmax(1)
+    args = (x.view(U8), s_x, w.view(U8), s_w, target)
+    loss, lse = torch.empty((2, T), device="cuda")
+    gpu_lib.linear_cross_entropy_fwd(*args, loss, lse)
+    assert bool(torch.isfinite(lse).all())
+    most = w.double().abs().sum(0) / s_w.double() * (1 + 2.0 ** -7)
+    for dt in (F32, BF16):
+        dx = torch.empty((T, d), dtype=dt, device="cuda")
+        gpu_lib.linear_cross_entropy_bwd(*args, lse, torch.ones(T, device="cuda"), dx)
+        assert bool((dx.abs() <= most).all())
