@@ -59,19 +59,21 @@ __device__ __forceinline__ float sum_over_g(float v) {
 }
 
 // ---- forward --------------------------------------------------------------
-// part[i][row] = (maximum, sum of 2^(z - maximum)) of the row's columns in the i-th
-// run; at_target[row] = the target's base-2 logit.
+// part[i][row] = (maximum, sum of 2^(k (a - maximum))) of the accumulators a of the row's
+// columns in the i-th run; at_target[row] = the target's.  Differences of accumulators are
+// nearly exact, those of their products with k are off by half a step of a logit: a sure
+// token's loss of 0 came out as that, of either sign, and 2^31 and more as infinity.
 struct Stats {
   float2* part;
   float* at_target;
 };
 
 // (m, s) of two runs
-__device__ __forceinline__ void join_runs(float& m, float& s, float m2, float s2) {
+__device__ __forceinline__ void join_runs(float& m, float& s, float m2, float s2, float k) {
   const float top = fmaxf(m, m2);
   // a run without a column is (-inf, 0); one of NaN alone is (-inf, NaN) and stays
-  const float a = s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f(m - top);
-  const float b = s2 == 0.0f ? 0.0f : s2 * __builtin_amdgcn_exp2f(m2 - top);
+  const float a = s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f((m - top) * k);
+  const float b = s2 == 0.0f ? 0.0f : s2 * __builtin_amdgcn_exp2f((m2 - top) * k);
   m = top;
   s = a + b;
 }
@@ -104,18 +106,18 @@ __device__ __forceinline__ void stats_out(uint8_t* smem, const ACC (&acc)[MB][NB
         for (int e = 0; e < E; ++e)
           if (col0 + column(j, e) < V) m = fmaxf(m, acc[i][j][e]);
     }
-    m = max_over_g<BLK>(m) * k;
+    m = max_over_g<BLK>(m);
     if (whole) {
 #pragma unroll
       for (int j = 0; j < NB; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], k, -m));
+        for (int e = 0; e < E; ++e) s += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * k);
     } else {
 #pragma unroll
       for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if (col0 + column(j, e) < V) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], k, -m));
+          if (col0 + column(j, e) < V) s += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * k);
     }
     s = sum_over_g<BLK>(s);
     if (g == 0) runs[wn * C::BM + wm * C::WTM + i * BLK + r] = make_float2(m, s);
@@ -127,7 +129,7 @@ __device__ __forceinline__ void stats_out(uint8_t* smem, const ACC (&acc)[MB][NB
       for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if (at == column(j, e)) st.at_target[row] = acc[i][j][e] * k;
+          if (at == column(j, e)) st.at_target[row] = acc[i][j][e];
     }
   }
   __syncthreads();
@@ -136,7 +138,7 @@ __device__ __forceinline__ void stats_out(uint8_t* smem, const ACC (&acc)[MB][NB
 #pragma unroll
     for (int n = 1; n < C::WGN; ++n) {
       const float2 b = runs[n * C::BM + i];
-      join_runs(a.x, a.y, b.x, b.y);
+      join_runs(a.x, a.y, b.x, b.y, k);
     }
     st.part[(int64_t)tn * M + m0 + i] = a;
   }
@@ -172,7 +174,7 @@ __global__ __launch_bounds__(C::kThreads) void loss_tile(
 // R rows of P runs each per workgroup, the runs dealt to 256 / R lanes in order
 template <int R>
 __global__ __launch_bounds__(256) void loss_join(const float2* __restrict__ part, int P, int M,
-                                                 int64_t V, const int64_t* __restrict__ target,
+                                                 int64_t V, Logits lg,
                                                  const float* __restrict__ at_target,
                                                  float* __restrict__ loss,
                                                  float* __restrict__ lse) {
@@ -180,28 +182,29 @@ __global__ __launch_bounds__(256) void loss_join(const float2* __restrict__ part
   __shared__ float2 red[L][R];
   const int r = threadIdx.x % R, l = threadIdx.x / R;
   const int row = blockIdx.x * R + r;
+  const float k = lg.k();
   float m = -INFINITY, s = 0.0f;
   if (row < M)
 #pragma unroll 4
     for (int i = l; i < P; i += L) {
       const float2 p = part[(int64_t)i * M + row];
-      join_runs(m, s, p.x, p.y);
+      join_runs(m, s, p.x, p.y, k);
     }
   red[l][r] = make_float2(m, s);
   __syncthreads();
   for (int n = L / 2; n > 0; n /= 2) {
     if (l < n) {
       const float2 p = red[l + n][r];
-      join_runs(m, s, p.x, p.y);
+      join_runs(m, s, p.x, p.y, k);
       red[l][r] = make_float2(m, s);
     }
     __syncthreads();
   }
   if (l != 0 || row >= M) return;
   const float bits = __builtin_amdgcn_logf(s);               // log2
-  const int64_t t = target[row];
-  if (lse) lse[row] = (m + bits) * kLn2;
-  loss[row] = t < 0 ? 0.0f : t >= V ? NAN : ((m - at_target[row]) + bits) * kLn2;
+  const int64_t t = lg.target[row];
+  if (lse) lse[row] = fmaf(m, k, bits) * kLn2;
+  loss[row] = t < 0 ? 0.0f : t >= V ? NAN : fmaf(m - at_target[row], k, bits) * kLn2;
 }
 
 // ---- backward -------------------------------------------------------------
@@ -552,8 +555,8 @@ hipError_t launch_cross_entropy_fwd(const uint8_t* xq, const float* s_x, const u
     // are: 8-byte partials of adjacent rows are one line
     const auto join = [&](auto rows) {
       constexpr int R = decltype(rows)::value;
-      loss_join<R><<<(int)ceil_div64(n, R), 256, 0, s>>>(st.part, P, (int)n, V, lg.target,
-                                                         st.at_target, loss + r0, out);
+      loss_join<R><<<(int)ceil_div64(n, R), 256, 0, s>>>(st.part, P, (int)n, V, lg, st.at_target,
+                                                         loss + r0, out);
     };
     if (n < 4 * kCUs)
       join(std::integral_constant<int, 1>{});

@@ -90,3 +90,35 @@ def test_a_target_does_not_pass_lse(gpu_lib, T, d, V, size):
         dx = torch.empty((T, d), dtype=dt, device="cuda")
         gpu_lib.linear_cross_entropy_bwd(*args, lse, torch.ones(T, device="cuda"), dx)
         assert bool((dx.abs() <= most).all())
+
+
+@pytest.mark.parametrize("size", [1.0, 100.0, 1e4, 1e6, 1e9, 1e11])
+@pytest.mark.parametrize("T, d, V", [(64, 16, 3), (300, 272, 999), (700, 1040, 5001)])
+def test_a_sure_token_has_no_loss(gpu_lib, T, d, V, size):
+    """The target's logit is the largest, in exact sums of whole numbers: loss = log of the
+    sum of exp(differences), each difference off by four half steps (k's two roundings, the
+    difference's product with it, the exponential's own), 2^-21 of it with a factor of two to
+    spare; the sum and its logarithm by 2^-20 of one and of the loss.  Never below 0.  And
+    lse is finite at any size of a logit, and off by as much of itself besides."""
+    announce(f"sure tokens at logits of {size}, T, d, V = {(T, d, V)}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    # whole numbers up to 8: every sum of d products is exact
+    x = torch.randint(-8, 9, (T, d), generator=g, device="cuda").float()
+    w = torch.randint(-8, 9, (V, d), generator=g, device="cuda").float()
+    s_x, s_w = torch.full((2, 1), (25 * d ** 0.5 / size) ** 0.5, device="cuda")
+    f8 = lambda t: t.to(torch.float8_e4m3fn).view(U8)  # noqa: E731
+    sums = x.double() @ w.double().T
+    target = sums.argmax(1)
+    loss, lse = torch.empty((2, T), device="cuda")
+    gpu_lib.linear_cross_entropy_fwd(f8(x), s_x, f8(w), s_w, target, loss, lse)
+    # k is rounded a few times, as are the differences' products with it
+    z = sums / (s_x.double() * s_w.double())
+    diff = z - z.gather(1, target[:, None])
+    want = torch.log(torch.exp(diff).sum(1))
+    grown = torch.exp(diff) * diff.abs() * 2.0 ** -21            # an exponential's error
+    tol = grown.sum(1) / torch.exp(want) + (want + 1) * 2.0 ** -20
+    assert bool(((loss - want).abs() <= tol).all())
+    assert bool((loss >= 0).all())
+    ref = torch.logsumexp(z, 1)
+    assert bool(((lse - ref).abs() <= tol + ref.abs() * 2.0 ** -21).all())
