@@ -1160,7 +1160,9 @@ def linear_cross_entropy_bwd(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tens
                              ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """dx [T x d] (float32 or bfloat16), the gradient in x of sum_t dloss[t] loss[t]:
     dloss[t] sum_v (exp(z[t][v] - lse[t]) - [v = target[t]]) dec(wq[v]) / s_w, the
-    logits z formed again a piece of the vocabulary at a time."""
+    logits z formed again a piece of the vocabulary at a time.  In float32 to its
+    precision; in bfloat16 from FP8's logits and in half the time (falqon.h says how far
+    either is off)."""
     T, d = _matrix(xq, "xq")
     V, dev = _matrix(wq, "wq")[0], _device(xq, "xq")
     u8, f32, lib, st = torch.uint8, torch.float32, load(), _stream_of(dev, stream)

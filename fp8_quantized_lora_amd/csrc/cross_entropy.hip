@@ -12,17 +12,26 @@
 // product 753), bound by the power of the card; 1 token 32 us from a cold cache, W's 131
 // MB at 4.1 TB/s with the launch.
 //
-// Backward, a piece of the vocabulary after the other: the product again, as FP8's
-// (p is then off by some 2^-13 of itself), whose epilogue now leaves G = 2^15 (p - [v =
-// target]) of the piece as float16, the target's from its own logit, summed in float32,
-// as 2^15 expm1(z - lse): a sure token's gradient is a small difference; then G times
-// the piece's rows of W, which are read as they lie (F16ByE4M3), added onto dx.  G is
-// float16 because its 11 bits keep the gradient to 2^-11 of its terms (bfloat16: 2^-8),
-// and 2^15 because p may be as small as 1 / V: under it float16 has its full precision
+// Backward, a piece of the vocabulary after the other: the product again, whose epilogue
+// now leaves G = 2^15 (p - [v = target]) of the piece as float16, the target's from its own
+// logit, summed in float32, as 2^15 expm1(z - lse): a sure token's gradient is a small
+// difference, right down to half a step of lse, a float32 number (2^-21 for an lse of 8 to
+// 16); then G times the piece's rows of W, which are read as they lie (F16ByE4M3), added
+// onto dx.  2^15 because p may be as small as 1 / V: under it float16 has its full precision
 // down to 2^-29 and absolute steps of 2^-39 below, while 1 still fits; E4M3 codes are
-// exact in it.  The row's factor dloss / s_w is applied at the end, in float32.  4096 x
-// 4096 x 32000: 1200 to 1250 us, of them G 430 and dx 760 to 820 (1.3 to 1.4 PFLOP/s; the
-// matrix cores busy 77 % of the cycles at 1.6 GHz, the power's limit).
+// exact in it.  The row's factor dloss / s_w is applied at the end, in float32.
+//
+// dx in bfloat16, whose half step is 2^-8: the product is FP8's, which of each eight
+// products drops what lies 2^-13 below the largest one, so that p is off by expm1 of the sum
+// of those (4.5e-5 of the logits' spread with outlier channels: 2^-8 from a spread of a
+// hundred on), and G's 11 bits keep the gradient to 2^-11 of its terms.  4096 x 4096 x
+// 32000: 1200 to 1250 us, of them G 430 and dx 760 to 820 (1.3 to 1.4 PFLOP/s; the matrix
+// cores busy 77 % of the cycles at 1.6 GHz, the power's limit).
+//
+// dx in float32: the product is the forward's, and G two float16 numbers, itself and what
+// that rounding leaves, 2^-22 of the terms; dx's product takes one after the other.  4096 x
+// 4096 x 32000: 2480 us where bfloat16 takes 1270.  The gradient as a whole is off by 4e-7
+// to 9e-7 (rel-L2; with FP8's logits and one number 1.3e-4 to 1.6e-4).
 #include "cross_entropy_plan.hpp"
 #include "elem.hpp"
 #include "kernels.hpp"
@@ -256,16 +265,18 @@ __global__ __launch_bounds__(256) void grad_rows(const uint8_t* __restrict__ x,
   rows[row] = r;
 }
 
-// G of a piece, [M x ldg] float16, columns past the vocabulary 0
+// G of a piece, [M x ldg] float16, columns past the vocabulary 0; rest: what that rounding
+// leaves of it (null: not wanted)
 struct Grads {
   const GradRow* rows;
   _Float16* G;
+  _Float16* rest;
   int64_t ldg;
   int v0;              // the piece's first column
 };
 
 // through the wave's part of the LDS, as tile_out: eight columns of a row per lane
-template <class C, int LDS, int MB, int NB, class ACC>
+template <bool REST, class C, int LDS, int MB, int NB, class ACC>
 __device__ __forceinline__ void grads_out(uint8_t* smem, const ACC (&acc)[MB][NB], int m0, int n0,
                                           int M, int V, float k, const Grads& gr) {
   const auto row_of = [&](int row) { return gr.rows[row]; };
@@ -279,24 +290,32 @@ __device__ __forceinline__ void grads_out(uint8_t* smem, const ACC (&acc)[MB][NB
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __builtin_elementwise_minimum(v[i], 15.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = (_Float16)__builtin_amdgcn_exp2f(v[i]);
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_exp2f(v[i]);
     const int at = r.target - gr.v0 - col;
     if ((unsigned)at < 8u) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i == at) h[i] = (_Float16)r.at_target;
+        if (i == at) v[i] = r.at_target;
     }
     if (col + 8 > V) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (col + i >= V) h[i] = (_Float16)0.0f;
+        if (col + i >= V) v[i] = 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (_Float16)v[i];
     *reinterpret_cast<H8*>(gr.G + (int64_t)row * gr.ldg + col) = h;
+    if constexpr (REST) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = (_Float16)(v[i] - (float)h[i]);
+      *reinterpret_cast<H8*>(gr.rest + (int64_t)row * gr.ldg + col) = h;
+    }
   };
   rows_through_lds<C, LDS>(smem, acc, m0, n0, M, (int)gr.ldg, row_of, out);
 }
 
-template <class C, int PER_CU>
+// EXACT: the forward's products, and what G's rounding leaves; otherwise FP8's
+template <class C, int PER_CU, bool EXACT>
 __global__ __launch_bounds__(C::kThreads, PER_CU) void grads_pipe(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
     int tilesN, Logits lg, Grads gr) {
@@ -304,23 +323,25 @@ __global__ __launch_bounds__(C::kThreads, PER_CU) void grads_pipe(
   gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
   const int m0 = __builtin_amdgcn_readfirstlane(tm * C::BM);
   const int n0 = __builtin_amdgcn_readfirstlane(tn * C::BN);
-  pipe_product<E4M3, C, PER_CU>(
+  using OP = std::conditional_t<EXACT, E4M3AsF16Wide, E4M3>;
+  pipe_product<OP, C, PER_CU>(
       A, B, M, N, K, m0, n0, 0, INT32_MAX, Exponents{}, [&] { return lg.k(); },
       [&](const auto& acc, float k, uint8_t* smem) {
-        grads_out<C, Ring<E4M3, C, PER_CU>::kLds>(smem, acc, m0, n0, M, N, k, gr);
+        grads_out<EXACT, C, Ring<OP, C, PER_CU>::kLds>(smem, acc, m0, n0, M, N, k, gr);
       });
 }
-template <class C>
+template <class C, bool EXACT>
 __global__ __launch_bounds__(C::kThreads) void grads_tile(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tilesM,
     int tilesN, Logits lg, Grads gr) {
   int tm, tn;
   gemm::tile_of(gemm::xcd_remap((int)blockIdx.x, tilesM * tilesN), tilesM, tilesN, tm, tn);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
-  tile_product<E4M3, C>(
+  using OP = std::conditional_t<EXACT, E4M3AsF16, E4M3>;
+  tile_product<OP, C>(
       A, B, M, N, K, m0, n0, 0, INT32_MAX, Exponents{}, [&] { return lg.k(); },
       [&](const auto& acc, float k, uint8_t* smem) {
-        grads_out<C, kTileLds<E4M3, C>>(smem, acc, m0, n0, M, N, k, gr);
+        grads_out<EXACT, C, kTileLds<OP, C>>(smem, acc, m0, n0, M, N, k, gr);
       });
 }
 // dx of all pieces up to this one: sums in `sums` between pieces, dx itself at the last
@@ -462,15 +483,36 @@ void launch_logits_fwd(const uint8_t* x, const uint8_t* w, int64_t T, int64_t d,
     loss_tile<C><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM, tN, lg, st);
 }
 // V: rows of w from the piece's first on, and columns counted
-template <class C, int PIPE>
+template <class C, int PIPE, bool EXACT>
 void launch_logits_bwd(const uint8_t* x, const uint8_t* w, int64_t T, int64_t d, int64_t V,
                        const Logits& lg, const Grads& gr, hipStream_t s) {
   const int tM = (int)ceil_div64(T, C::BM), tN = (int)ceil_div64(gr.ldg, C::BN);
   if constexpr (PIPE > 0)
-    grads_pipe<C, PIPE><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM, tN, lg,
-                                                        gr);
+    grads_pipe<C, PIPE, EXACT><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM,
+                                                               tN, lg, gr);
   else
-    grads_tile<C><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM, tN, lg, gr);
+    grads_tile<C, EXACT><<<tM * tN, C::kThreads, 0, s>>>(x, w, (int)T, (int)V, (int)d, tM, tN, lg,
+                                                         gr);
+}
+void launch_grads(const uint8_t* x, const uint8_t* w, int64_t T, int64_t d, int64_t V,
+                  const Logits& lg, const Grads& gr, hipStream_t s) {
+  if (gr.rest) {
+    switch (loss_kind(T, gr.ldg, d)) {
+      case kLoss256: launch_logits_bwd<P256, 1, true>(x, w, T, d, V, lg, gr, s); break;
+      case kLoss128: launch_logits_bwd<P128, 2, true>(x, w, T, d, V, lg, gr, s); break;
+      case kLoss64: launch_logits_bwd<T64, 0, true>(x, w, T, d, V, lg, gr, s); break;
+      default: launch_logits_bwd<T32, 0, true>(x, w, T, d, V, lg, gr, s); break;
+    }
+    return;
+  }
+  switch (grad_kind(T, gr.ldg, d)) {
+    case kGrad256: launch_logits_bwd<P256, 1, false>(x, w, T, d, V, lg, gr, s); break;
+    case kGrad256x128: launch_logits_bwd<P256x128, 2, false>(x, w, T, d, V, lg, gr, s); break;
+    case kGrad192x128: launch_logits_bwd<P192x128, 2, false>(x, w, T, d, V, lg, gr, s); break;
+    case kGrad128: launch_logits_bwd<P128, 2, false>(x, w, T, d, V, lg, gr, s); break;
+    case kGrad64: launch_logits_bwd<T64, 0, false>(x, w, T, d, V, lg, gr, s); break;
+    default: launch_logits_bwd<T32, 0, false>(x, w, T, d, V, lg, gr, s); break;
+  }
 }
 
 template <class C, int PIPE, class OT, bool SPLIT>
@@ -598,21 +640,22 @@ hipError_t launch_cross_entropy_bwd(const uint8_t* xq, const float* s_x, const u
     for (int64_t v0 = 0; v0 < V; v0 += p.width) {
       const int64_t cols = std::min(p.width, V - v0), ld = up(cols, 64);
       const uint8_t* w = wq + v0 * d;
-      const Grads gr{rows, (_Float16*)g, ld, (int)v0};
-      switch (grad_kind(n, ld, d)) {
-        case kGrad256: launch_logits_bwd<P256, 1>(x, w, n, d, cols, lg, gr, s); break;
-        case kGrad256x128: launch_logits_bwd<P256x128, 2>(x, w, n, d, cols, lg, gr, s); break;
-        case kGrad192x128: launch_logits_bwd<P192x128, 2>(x, w, n, d, cols, lg, gr, s); break;
-        case kGrad128: launch_logits_bwd<P128, 2>(x, w, n, d, cols, lg, gr, s); break;
-        case kGrad64: launch_logits_bwd<T64, 0>(x, w, n, d, cols, lg, gr, s); break;
-        default: launch_logits_bwd<T32, 0>(x, w, n, d, cols, lg, gr, s); break;
-      }
+      _Float16* const rest = dx_type == 0 ? (_Float16*)g + n * ld : nullptr;
+      launch_grads(x, w, n, d, cols, lg, Grads{rows, (_Float16*)g, rest, ld, (int)v0}, s);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
       const bool last = v0 + p.width >= V;
-      const DxOut o{lg.target, dloss + r0, s_w, sums, last ? to : nullptr, V, v0 == 0};
-      e = dx_type == 0 ? run_dx_product<float>(p, g, w, n, d, ld * 2, cols, o, part, s)
-                       : run_dx_product<__bf16>(p, g, w, n, d, ld * 2, cols, o, part, s);
+      DxOut o{lg.target, dloss + r0, s_w, sums, last ? to : nullptr, V, v0 == 0};
+      if (rest) {                              // G's rounding, and then G, added onto it
+        o.dx = nullptr;
+        e = run_dx_product<float>(p, (const uint8_t*)rest, w, n, d, ld * 2, cols, o, part, s);
+        if (e != hipSuccess) return e;
+        o.first = false;
+        o.dx = last ? to : nullptr;
+        e = run_dx_product<float>(p, g, w, n, d, ld * 2, cols, o, part, s);
+      } else {
+        e = run_dx_product<__bf16>(p, g, w, n, d, ld * 2, cols, o, part, s);
+      }
       if (e != hipSuccess) return e;
     }
   }

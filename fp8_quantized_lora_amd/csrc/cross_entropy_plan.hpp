@@ -36,7 +36,8 @@ LossKind loss_kind(int64_t T, int64_t V, int64_t d) {
   return best;
 }
 
-// G's tiles, by linear_act_plan.hpp's costs, those kinds that are cheapest somewhere:
+// G's tiles for gradients in bfloat16 (in float32 they are the forward's), by
+// linear_act_plan.hpp's costs, those kinds that are cheapest somewhere:
 //   4096 x 32000 x 4096: 431 us in 256 x 256, 469 in 192 x 128, 466 in 256 x 128, 559 in
 //     128 x 128; 512 tokens 60, 61, 57 and 62
 //   4096 x 50000 x 1024: 258 in 192 x 128, 294 in 256 x 128, 321 in 256 x 256; 333 x 131071
@@ -70,14 +71,15 @@ int64_t runs_of(int64_t T, int64_t d, int64_t V) {
   return ceil_div64(V, kLossTile[loss_kind(T, V, d)].bn);
 }
 
-// pieces of the vocabulary: as many as keep G within kPiece bytes, of one width, a
-// multiple of 64.  Larger ones than the last-level cache holds cost G's way to memory and
+// pieces of the vocabulary: as many as keep G (and, for float32 gradients, what its rounding
+// leaves) within kPiece bytes, of one width, a multiple of 64.  Larger ones than the last-level cache holds cost G's way to memory and
 // back, smaller ones more launches' ends and dx's sums read and written again: 4096 x 4096
 // x 32000 1276 us with 512 MB, 1279 with 256, 1323 with 128, 1374 with 64; 8192 tokens
 // 2522, 2593, 2756 and 2948; 4096 x 1024 x 50000 716, 743, 766 and 800.
 constexpr int64_t kPiece = (int64_t)512 << 20;
-int64_t piece_width(int64_t T, int64_t V) {
-  const int64_t most = std::clamp<int64_t>(kPiece / (2 * T), 2048, 1 << 21);
+// bytes: of an element of G
+int64_t piece_width(int64_t T, int64_t V, int bytes) {
+  const int64_t most = std::clamp<int64_t>(kPiece / (bytes * T), 2048, 1 << 21);
   return up(ceil_div64(V, ceil_div64(V, most)), 64);
 }
 
@@ -107,7 +109,9 @@ struct BwdPlan {
 };
 BwdPlan bwd_plan(int64_t T, int64_t d, int64_t V, int dx_type) {
   BwdPlan p;
-  p.width = piece_width(T, V);
+  // (float32 gradients: of G and of what its rounding leaves)
+  const int bytes = dx_type == 0 ? 4 : 2;
+  p.width = piece_width(T, V, bytes);
   p.kind = kDx64;
   p.splits = 1;
   p.kc = 0;
@@ -130,7 +134,7 @@ BwdPlan bwd_plan(int64_t T, int64_t d, int64_t V, int dx_type) {
       p.kc = (int)kc;
     }
   }
-  p.g = (size_t)up(T * p.width * 2, 256);
+  p.g = (size_t)up(T * p.width * bytes, 256);
   // float32 gradients collect in place
   p.sums = dx_type != 0 && p.width < V ? (size_t)up(T * d * 4, 256) : 0;
   p.part = p.splits > 1 ? (size_t)up(p.splits * T * d * 4, 256) : 0;

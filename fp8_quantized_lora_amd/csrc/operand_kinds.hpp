@@ -13,7 +13,8 @@
 // E4M3 in v_mfma_..._f8f6f4 is not exact: of eight products at a time, bits 2^-13
 // below the largest are lost (4.5e-5 of a logit's spread where some channels are
 // twenty times the others).  As float16, which holds every code, sums are float32's,
-// at half the rate: the softmax's logits are formed so (E4M3AsF16).
+// at half the rate: the softmax's logits are formed so (E4M3AsF16), but for gradients in
+// bfloat16.
 #pragma once
 
 #include "gemm_fp8_kernel.hpp"

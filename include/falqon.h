@@ -822,10 +822,16 @@ falq_status layer_norm_bwd_ckpt(const void *dy, int dy_dtype, const uint8_t *x_q
  * linear_cross_entropy_bwd — the gradient in x of sum_t dloss[t] loss[t], the logits
  * formed again a piece of the vocabulary at a time:
  *     dx[t] = dloss[t] sum_v (exp(z[t][v] - lse[t]) - [v = target[t]]) dec(wq[v]) / s_w
- * (0 for a token that does not count, NaN for a target of V or more).  The factors of
- * dec(wq[v]) are rounded to float16, 2^-11 of each at most, before the sum over v, which
- * is float32's; but for the target's, they come from logits of the FP8 product, which
- * is off as melded_linear_fwd is.
+ * (0 for a token that does not count, NaN for a target of V or more), summed over v in
+ * float32.  dx's type says how exactly the factors of dec(wq[v]) are formed:
+ *     float32   from the forward's logits, each to 2^-22 of itself;
+ *     bfloat16  rounded to float16, 2^-11 of each at most, and, but for the target's, from
+ *               logits of the FP8 product, which of each eight products drops what lies
+ *               2^-13 below the largest: an exponential is off by expm1 of the sum of
+ *               those, and bounded by 1.  Half the time of float32.
+ * In both an exponential is off by what lse is, half a step of a float32 number: where a
+ * token's loss is smaller than that (2^-21 for an lse of 8 to 16), so is the factor of its
+ * target only in size, not in its digits.
  *
  *   xq, s_x   [T x d] E4M3 codes and their scale (fp8_quantize's, positive)
  *   wq, s_w   [V x d] likewise: the output layer; d a multiple of 16, 16 to 2^22;
