@@ -10,6 +10,7 @@ the library is missing, load() raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from array import array
@@ -809,13 +810,17 @@ def _scratch(ws: Optional[torch.Tensor], need: int, dev: int, stream, st: int):
         return ws
     if not need:
         return None
-    where = torch.device("cuda", dev)
+    with _on_stream(dev, stream, st):
+        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+
+
+def _on_stream(dev: int, stream, st: int):
+    """A context in which torch's own work is on the call's stream."""
     if stream is None or st == _raw_stream(dev):
-        return torch.empty(need, dtype=torch.uint8, device=where)
-    own = (torch.cuda.ExternalStream(st, device=where) if st
-           else torch.cuda.default_stream(where))
-    with torch.cuda.stream(own):
-        return torch.empty(need, dtype=torch.uint8, device=where)
+        return contextlib.nullcontext()
+    where = torch.device("cuda", dev)
+    return torch.cuda.stream(torch.cuda.ExternalStream(st, device=where) if st
+                             else torch.cuda.default_stream(where))
 
 
 def _run(fn, what: str, dev: int, *args) -> None:

@@ -71,7 +71,7 @@ from . import (fp8_quantize, fp8_quantize_workspace_bytes, fp8_dequantize, melde
                linear_act_bwd_workspace_bytes, grad_clip, ACTIVATIONS, checkpoint_save,
                checkpoint_scales_shape, linear_act_bwd_ckpt, linear_cross_entropy_fwd,
                linear_cross_entropy_fwd_workspace_bytes, linear_cross_entropy_bwd,
-               linear_cross_entropy_bwd_workspace_bytes)
+               linear_cross_entropy_bwd_workspace_bytes, _arg, _device, _on_stream, _stream_of)
 
 
 def clip_gradients(layers, max_norm: float, norm: torch.Tensor, extra=(), eps: float = 1e-6,
@@ -391,6 +391,7 @@ class LinearCrossEntropy:
         self.s_w = torch.empty(1, dtype=f32, device=dev)
         self.xq = torch.empty((tokens, d), dtype=u8, device=dev)
         self.s_x = torch.empty(1, dtype=f32, device=dev)
+        self.target = torch.empty(tokens, dtype=torch.int64, device=dev)
         self.loss = torch.empty(tokens, dtype=f32, device=dev)
         self.lse = torch.empty(tokens, dtype=f32, device=dev)
         self.dx = torch.empty((tokens, d), dtype=dx_dtype, device=dev)
@@ -407,12 +408,15 @@ class LinearCrossEntropy:
 
     def forward(self, X: torch.Tensor, target: torch.Tensor, stream=None):
         """The loss of each row of X [tokens x d] (float32 or bfloat16) for the class
-        target [tokens] (int64; negative: it does not count, its loss is 0), which the
-        backward reads again."""
+        target [tokens] (int64; negative: it does not count, its loss is 0).  The layer
+        keeps what its backward needs of both: they may be overwritten once this has run."""
+        dev = _device(self.loss, "loss")
+        _arg(target, torch.int64, (self.T,), dev, "target")
         fp8_quantize(X, self.xq, self.s_x, ws=self.ws_q, stream=stream)
-        self.target = target
-        linear_cross_entropy_fwd(self.xq, self.s_x, self.wq, self.s_w, target, self.loss, self.lse,
-                                 ws=self.ws_fwd, stream=stream)
+        with _on_stream(dev, stream, _stream_of(dev, stream)):
+            self.target.copy_(target)
+        linear_cross_entropy_fwd(self.xq, self.s_x, self.wq, self.s_w, self.target, self.loss,
+                                 self.lse, ws=self.ws_fwd, stream=stream)
         return self.loss
 
     def backward(self, dloss: torch.Tensor, stream=None):
