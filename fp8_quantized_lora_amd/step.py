@@ -48,10 +48,11 @@ global norm, between their backward calls and their adapter updates.
 
 Every buffer and workspace is allocated once up front, so a step makes no
 allocation and no host synchronisation.  This module only sequences calls
-into the HIP library; it computes nothing itself.
+into the HIP library (and keeps a copy of a loss's targets); it computes nothing itself.
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
@@ -376,6 +377,18 @@ class MeldedLinear:
         self.update(lr, tau, k_max, stream, merge=self.n_steps % merge_every == 0)
 
 
+def _on_own_device(method):
+    """The method with the layer's device current, which is where fp8_quantize runs."""
+    @functools.wraps(method)
+    def run(self, *args, **kwargs):
+        dev = self.loss.device
+        if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+            return method(self, *args, **kwargs)
+        with torch.cuda.device(dev):
+            return method(self, *args, **kwargs)
+    return run
+
+
 class LinearCrossEntropy:
     """Softmax cross entropy over the `vocab` rows of an output layer that is frozen in
     FP8, for `tokens` rows of d features, every buffer allocated once: forward gives the
@@ -402,10 +415,12 @@ class LinearCrossEntropy:
         nb = linear_cross_entropy_bwd_workspace_bytes(tokens, d, vocab, dx_dtype)
         self.ws_bwd = torch.empty(max(1, nb), dtype=u8, device=dev)
 
+    @_on_own_device
     def init_state(self, W: torch.Tensor, stream=None):
         """W~ = E4M3(W * s_w), s_w = 448 / max|W|, of the output layer [vocab x d]."""
         fp8_quantize(W, self.wq, self.s_w, ws=self.ws_q, stream=stream)
 
+    @_on_own_device
     def forward(self, X: torch.Tensor, target: torch.Tensor, stream=None):
         """The loss of each row of X [tokens x d] (float32 or bfloat16) for the class
         target [tokens] (int64; negative: it does not count, its loss is 0).  The layer
@@ -419,6 +434,7 @@ class LinearCrossEntropy:
                                  self.lse, ws=self.ws_fwd, stream=stream)
         return self.loss
 
+    @_on_own_device
     def backward(self, dloss: torch.Tensor, stream=None):
         """dX of sum_t dloss[t] loss[t] (1 / tokens that count for their mean), through
         the quantisation as melded_linear_bwd's."""
