@@ -1156,6 +1156,8 @@ def linear_cross_entropy_fwd(xq: torch.Tensor, s_x: torch.Tensor, wq: torch.Tens
 
 def linear_cross_entropy_bwd_workspace_bytes(T: int, d: int, V: int,
                                              dx_dtype=torch.float32) -> int:
+    if dx_dtype not in _ELEM:
+        raise FalqError(f"dx_dtype: expected float32 or bfloat16, got {dx_dtype}")
     return int(load().linear_cross_entropy_bwd_workspace_bytes(T, d, V, _ELEM[dx_dtype]))
 
 

@@ -397,6 +397,10 @@ class LinearCrossEntropy:
     def __init__(self, vocab: int, d: int, tokens: int, device="cuda", dx_dtype=torch.float32):
         if dx_dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("dx_dtype must be float32 or bfloat16")
+        if d < 16 or d % 16 or d > 1 << 22 or not 1 <= vocab <= 1 << 22:
+            raise ValueError("d must be a multiple of 16, 16 to 2^22, and vocab 1 to 2^22")
+        if not 0 <= tokens <= 1 << 30:
+            raise ValueError("tokens must be 0 to 2^30")
         dev = torch.device(device)
         u8, f32 = torch.uint8, torch.float32
         self.vocab, self.d, self.T = vocab, d, tokens
