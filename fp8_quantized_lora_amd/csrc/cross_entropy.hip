@@ -1,6 +1,6 @@
 // Softmax cross entropy over the vocabulary of an FP8 output layer, the logits
 //   z[t][v] = dec(xq[t]) . dec(wq[v]) / (s_x s_w)
-// never kept:
+// never kept (of a piece of the vocabulary, the backward's probabilities are):
 //   lse[t] = log sum_v exp z[t][v],   loss[t] = lse[t] - z[t][target[t]],
 //   dx[t] = dloss[t] sum_v (exp(z[t][v] - lse[t]) - [v = target[t]]) dec(wq[v]) / s_w.
 //
@@ -8,9 +8,10 @@
 // epilogue leaves of each row the maximum and the sum of exponentials under it over the
 // tile's columns, straight from the accumulators, 8 bytes for 64 to 256 logits; a second
 // launch joins them.  All of it in float32 and base 2.  The codes are multiplied as
-// float16, exactly.  4096 x 32000 x 4096: 740 us, 1.45 PFLOP/s (a library's float16
-// product 753), bound by the power of the card; 1 token 32 us from a cold cache, W's 131
-// MB at 4.1 TB/s with the launch.
+// float16, exactly.  4096 x 32000 x 4096: 747 us, 1.44 PFLOP/s (a library's float16
+// product 753), the matrix cores busy 67 % of the cycles at the 1.6 to 1.9 GHz that the
+// card's power leaves; 1 token 32 us from a cold cache, W's 131 MB at 4.1 TB/s with the
+// launch.  (256 x 256 spills 42 registers, in the loop of the last K steps alone.)
 //
 // Backward, a piece of the vocabulary after the other: the product again, whose epilogue
 // now leaves G = 2^15 (p - [v = target]) of the piece as float16, the target's from its own

@@ -20,9 +20,9 @@
 // from the registers would be 8 or 16 bytes wide.  Each wave passes its
 // accumulators through its own part of the LDS (16-byte chunks XOR-swizzled
 // by the row: no bank conflicts either way) and reads them back as eight
-// columns of a row per lane (bfloat16) or four at a time (float32); bias, residual
-// and the outputs are then 16-byte accesses on whole 128-byte lines, and the
-// epilogue's code is a short loop instead of one copy per accumulator.
+// columns of a row per lane (bfloat16, and float32 with a residual) or four at a time
+// (float32); bias, residual and the outputs are then 16-byte accesses on whole 128-byte
+// lines, and the epilogue's code is a short loop instead of one copy per accumulator.
 #include "activation.hpp"
 #include "elem.hpp"
 #include "gemm_fp8_kernel.hpp"
@@ -42,7 +42,8 @@ namespace {
 // without (alone 306 and 335); 4096 x 8192 x 4096 (64 MB) 140 and 135.
 // Twice as wide, float32's from what the last-level cache holds on (kStreamBytes): 8192 x
 // 11008 x 4096 with gelu and z (721 MB) 351 and 454, 444 and 588 without; 4096 x 11008 x
-// 4096 (180 MB) 155 and 225, 151 and 220 without.
+// 4096 (180 MB) 155 and 225, 151 and 220 without.  With a residual float32's are not whole
+// lines (tile_out), and stay in the caches: 8192 x 11008 x 4096 425, 559 past them.
 constexpr int64_t kStreamOut = (int64_t)80 << 20;
 
 template <class OT>

@@ -7,7 +7,9 @@
 // 8-bit checkpoints (E4M3 codes): the smallest exponent with amax <= 448 2^e: no
 // element saturates, at the price of half a binade for those blocks whose largest
 // element lies in (448, 512).
-// A block without a finite non-zero element has exponent 0 (byte 127).
+// A block without a finite non-zero element has exponent 0 (byte 127).  Infinities and NaN
+// have no part in the exponent: an infinity becomes the largest code under its block's
+// finite neighbours' exponent, however small those are, and E2M1 has no NaN.
 #pragma once
 
 #include "common.hpp"

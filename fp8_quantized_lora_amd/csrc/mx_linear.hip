@@ -4,11 +4,13 @@
 // applies the blocks' scales itself (v_mfma_scale_f32_16x16x128_f8f6f4 and its form of 32
 // x 32 x 64), whose bytes ride along with the codes of a K step, eight for a row.
 //
-// Bound by the power of the card where it is long: 8192 x 8192 x 8192 250 us (4.4
-// PFLOP/s), 219 without its loads, 220 without its LDS reads, 179 without either, and 180
-// as it stands with zeros for operands.  8192 x 11008 x 4096 with gelu and z 227 us, of
-// which the outputs are 67 at a copy's rate; 1 x 4096 x 4096 4.3 us, 2 TB/s and a
-// launch's latency.
+// Bound where it is long by two things: the matrix cores wait for loads and LDS reads, and
+// the card's power lowers the clock.  8192 x 8192 x 8192: 250 us (4.4 PFLOP/s; 129 at the
+// rate of the instructions alone), the matrix cores busy 58 % of the cycles at 1.7 GHz;
+// with zeros for operands busy as much, at 2.2 GHz; 219 without its loads, 220 without its
+// LDS reads, 179 without either.  8192 x 11008 x 4096 with gelu and z 227 us, busy 42 % at
+// 1.9 GHz: the outputs are 67 at a copy's rate; 1 x 4096 x 4096 4.3 us, 2 TB/s and a launch's
+// latency.
 #include "activation.hpp"
 #include "elem.hpp"
 #include "kernels.hpp"

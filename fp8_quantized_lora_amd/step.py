@@ -38,10 +38,14 @@ decay, which is meant for matrices).
 With keep_z="fp8" a layer with an activation keeps its z in 8 bits between forward
 and backward (checkpoint_save, linear_act_bwd_ckpt): half of bfloat16's memory.  The
 product writes z itself into `z_scratch`, which layers that run one after the other
-may share.
+may share.  An infinity in z comes back as the largest of its block's finite neighbours,
+not as one: where z may overflow, keep it "exact".
 
 LinearCrossEntropy is the loss behind the last layer: an output layer frozen in FP8,
-whose logits are never kept, and the gradient that the last layer's backward takes.
+whose logits are never kept, and the gradient that the last layer's backward takes.  Its
+workspaces hold up to 512 MB: of a piece of the vocabulary the backward keeps the
+probabilities, in 16 bits for a gradient in bfloat16 and in twice 16 for one in float32,
+which has float32's precision and takes twice the time.
 
 clip_gradients clips the adapter (and bias) gradients of many layers by their
 global norm, between their backward calls and their adapter updates.

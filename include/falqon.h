@@ -743,7 +743,8 @@ falq_status grad_clip(int64_t count, void *const *g, const int64_t *n, const int
  *         (0 for a block without a non-zero one; at least -127),
  *     q[i] = E2M1(x[i] 2^-e), nearest, ties to the even code, saturating at 6:
  * the block's largest elements may saturate (those of 6 2^e to 8 2^e).  An infinity
- * saturates, a NaN gives a zero.  mxfp4_dequantize — x[i] = dec(q[i]) 2^e, rounded
+ * saturates, to 6 2^e of the e of its finite neighbours; a NaN gives a zero, of which the
+ * product knows nothing (fp8_quantize counts such elements, and keeps a NaN).  mxfp4_dequantize — x[i] = dec(q[i]) 2^e, rounded
  * once to x's type.
  *
  *   x   [rows x K] float32 or bfloat16; K a multiple of 32
@@ -784,7 +785,8 @@ falq_status melded_linear_fwd_mxfp4(const uint8_t *xq, const uint8_t *x_e, const
  *     e = the smallest with amax <= 448 2^e, amax the block's largest finite
  *         magnitude (0 for a block without a non-zero one; at least -127),
  *     q[i] = E4M3(x[i] 2^-e)
- * (nearest, ties to even; infinities saturate at 448, a NaN stays one).
+ * (nearest, ties to even; infinities saturate at 448, under the e of their finite
+ * neighbours: beside elements of 0.1 an infinity comes back as about 0.1; a NaN stays one).
  * checkpoint_restore — x[i] = dec(q[i]) 2^e, rounded once to x's type.
  *
  *   x   [T x d] float32 or bfloat16; 1 <= d <= 2^24
