@@ -26,7 +26,7 @@
 // products drops what lies 2^-13 below the largest one, so that p is off by expm1 of the sum
 // of those (4.5e-5 of the logits' spread with outlier channels: 2^-8 from a spread of a
 // hundred on), and G's 11 bits keep the gradient to 2^-11 of its terms.  4096 x 4096 x
-// 32000: 1200 to 1250 us, of them G 430 and dx 760 to 820 (1.3 to 1.4 PFLOP/s; the matrix
+// 32000: 1200 to 1280 us, of them G 430 and dx 760 to 820 (1.3 to 1.4 PFLOP/s; the matrix
 // cores busy 77 % of the cycles at 1.6 GHz, the power's limit).
 //
 // dx in float32: the product is the forward's, and G two float16 numbers, itself and what

@@ -122,3 +122,76 @@ def test_a_sure_token_has_no_loss(gpu_lib, T, d, V, size):
     assert bool((loss >= 0).all())
     ref = torch.logsumexp(z, 1)
     assert bool(((lse - ref).abs() <= tol + ref.abs() * 2.0 ** -21).all())
+
+
+def powers(v):
+    """The largest power of two in each eight of a row of codes."""
+    e = torch.where(v == 0, -6.0, v.abs().clamp(min=2.0 ** -6).log2().floor())
+    return torch.exp2(e.view(v.shape[0], -1, 8).amax(2))
+
+
+def bf16_reference(c, lse):
+    """dx and its tolerance (u = 2^-24) where FP8's logits are off by e, 7 2^-13 of the largest
+    product's power of two of each eight, (d / 8 + 2) u of the absolute sum and 8 u |z|: p lies
+    between p exp(-e) and the smaller of p exp(e) and 1, whatever e is; the rest as in
+    tests/test_gpu_cross_entropy.py."""
+    u = 2.0 ** -24
+    w = c.wv
+    z, S = c.xv @ w.T, c.xv.abs() @ w.abs().T
+    s = c.s_x.double()
+    e = (powers(c.xv * s) / s) @ powers(w).T * (7 * 2.0 ** -13) + S * ((c.d / 8 + 2) * u)
+    given = lse.double()[:, None]
+    e += 8 * u * z.abs() + 2 * u * given.abs() + 2.0 ** -20
+    p = torch.exp((z - given).clamp(max=0))      # (lse itself is off by what its sums are)
+    onehot = torch.zeros_like(p).scatter_(1, c.target[:, None], 1.0)
+    G = p - onehot
+    et = S * ((16 * -(-c.d // 1024) + 6) * u + (c.d / 4 + 8) * u) + 4 * u * (z.abs() + given.abs())
+    EG = torch.maximum(p * -torch.expm1(-e), torch.exp((z - given + e).clamp(max=0)) - p)
+    EGt = torch.maximum(p * -torch.expm1(-et), torch.exp((z - given + et).clamp(max=0)) - p)
+    EG = torch.where(onehot > 0, EGt + 2.0 ** -20 * G.abs(), EG)
+    EG += (G.abs() + EG) * 2.0 ** -11 + 2.0 ** -40
+    f = c.dloss.double()[:, None]
+    dx = f * (G @ w)
+    tol = f.abs() * (EG @ w.abs() + (G.abs() @ w.abs()) * ((c.V / 4 + 8) * u)) + 4 * u * dx.abs()
+    return dx, tol + (dx.abs() + tol) * 2.0 ** -8 + 1e-37
+
+
+@pytest.mark.parametrize("spread", [0.5, 4.0, 100.0])
+@pytest.mark.parametrize("big", [8.0, 64.0, 448.0])
+@pytest.mark.parametrize("shape", [(64, 16, 3), (50, 48, 70), (5000, 272, 77), (2100, 512, 9001)])
+def test_bfloat16_is_off_by_its_logits_error(gpu_lib, shape, big, spread):
+    announce(f"bfloat16 gradient of cancelling terms, T, d, V = {shape}, {big}, {spread}")
+    c = Case(*shape, spread=spread, big=big)
+    loss, lse = c.forward(gpu_lib)
+    dx = c.backward(gpu_lib, lse, BF16)
+    ref, tol = bf16_reference(c, lse)
+    assert bool(((dx.double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [2, 3, 64, 1000])
+def test_classes_alike_and_lse_near_zero(gpu_lib, V, dtype):
+    """All rows of the weight the same, with terms that cancel: every p is 1 / V to what half a
+    step of lse makes of it (lse is 0 up to its rounding, as the logits are -log V), though
+    FP8's logits are alike as well; so dx = dloss w (V / V - 1) = 0, up to the terms' errors,
+    2^-11 of each in bfloat16, and their sums'."""
+    d, T = 32, 40
+    w = torch.zeros(d, device="cuda")
+    w[0], w[1], w[2:8] = 448, -448, 1
+    x = torch.zeros(d, device="cuda")
+    x[0], x[1], x[2:8] = 448, 448, -1
+    f8 = lambda t, n: t.to(torch.float8_e4m3fn).view(U8).repeat(n, 1)  # noqa: E731
+    s = torch.full((1,), 6 / float(torch.log(torch.tensor(float(V)))), device="cuda")
+    one = torch.ones(1, device="cuda")
+    target = torch.arange(T, device="cuda") % V
+    args = (f8(x, T), s, f8(w, V), one, target)
+    loss, lse = torch.empty((2, T), device="cuda")
+    gpu_lib.linear_cross_entropy_fwd(*args, loss, lse)
+    assert float(lse.abs().max()) <= 1e-5
+    assert float((loss - 6 / float(s)).abs().max()) <= 1e-5
+    dx = torch.empty((T, d), dtype=dtype, device="cuda")
+    gpu_lib.linear_cross_entropy_bwd(*args, lse, torch.ones(T, device="cuda"), dx)
+    # of the logit -6 / s = -log V, FP8 may drop all six ones (each 2^-17 of 448^2)
+    off = 1e-5 if dtype == F32 else float(torch.expm1(6 / s))
+    tol = (off + 2.0 ** -10 + (V / 4 + 8) * 2.0 ** -24) * w.abs() * 2
+    assert bool((dx.abs() <= tol * (1 + 2.0 ** -7) + 1e-30).all())
