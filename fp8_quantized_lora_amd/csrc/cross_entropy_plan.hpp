@@ -73,10 +73,11 @@ int64_t runs_of(int64_t T, int64_t d, int64_t V) {
 }
 
 // pieces of the vocabulary: as many as keep G (and, for float32 gradients, what its rounding
-// leaves) within kPiece bytes, of one width, a multiple of 64.  Larger ones than the last-level cache holds cost G's way to memory and
-// back, smaller ones more launches' ends and dx's sums read and written again: 4096 x 4096
-// x 32000 1276 us with 512 MB, 1279 with 256, 1323 with 128, 1374 with 64; 8192 tokens
-// 2522, 2593, 2756 and 2948; 4096 x 1024 x 50000 716, 743, 766 and 800.
+// leaves) within kPiece bytes, of one width, a multiple of 64.  Larger ones than the
+// last-level cache holds cost G's way to memory and back, smaller ones more launches' ends
+// and dx's sums read and written again: 4096 x 4096 x 32000 1276 us with 512 MB, 1279 with
+// 256, 1323 with 128, 1374 with 64; 8192 tokens 2522, 2593, 2756 and 2948; 4096 x 1024 x
+// 50000 716, 743, 766 and 800.
 constexpr int64_t kPiece = (int64_t)512 << 20;
 // bytes: of an element of G
 int64_t piece_width(int64_t T, int64_t V, int bytes) {

@@ -832,8 +832,8 @@ falq_status layer_norm_bwd_ckpt(const void *dy, int dy_dtype, const uint8_t *x_q
  *               2^-13 below the largest: an exponential is off by expm1 of the sum of
  *               those, and bounded by 1.  Half the time of float32.
  * In both an exponential is off by what lse is, half a step of a float32 number: where a
- * token's loss is smaller than that (2^-21 for an lse of 8 to 16), so is the factor of its
- * target only in size, not in its digits.
+ * token's loss is smaller than that (2^-21 for an lse of 8 to 16), the factor of its target
+ * is right in size only.
  *
  *   xq, s_x   [T x d] E4M3 codes and their scale (fp8_quantize's, positive)
  *   wq, s_w   [V x d] likewise: the output layer; d a multiple of 16, 16 to 2^22;
