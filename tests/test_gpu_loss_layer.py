@@ -81,3 +81,27 @@ def test_targets_are_checked_before_anything_runs(gpu_lib):
         with pytest.raises(gpu_lib.FalqError):
             head.forward(x + 1, bad)
     assert torch.equal(head.xq, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab, d, tokens", [(50, 32, 0), (1, 16, 1), (1, 16, 40), (300, 16, 1)])
+def test_smallest_layers(gpu_lib, vocab, d, tokens, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    head = gpu_lib.LinearCrossEntropy(vocab, d, tokens, dx_dtype=dtype)
+    head.init_state(torch.empty((vocab, d), device="cuda").normal_(generator=g))
+    x = torch.empty((tokens, d), device="cuda").normal_(generator=g)
+    target = torch.zeros(tokens, dtype=torch.int64, device="cuda")
+    loss = head.forward(x, target)
+    dx = head.backward(torch.ones(tokens, device="cuda"))
+    assert loss.shape == (tokens,) and dx.shape == (tokens, d)
+    if vocab == 1:
+        # dx = w expm1(z - lse) with lse = z: z is summed twice, once in float32 with 16 + 6
+        # roundings of its absolute sum and its scale's 4 half steps, lse has k's three, the
+        # two products' with k and ln 2 and ln 2's own, 2^-24 of z each
+        dec = lambda q, s: q.view(torch.float8_e4m3fn).double() / s.double()  # noqa: E731
+        terms = dec(head.xq, head.s_x) * dec(head.wq, head.s_w)
+        off = (22 * terms.abs().sum(1) + 10 * terms.sum(1).abs()) * 2.0 ** -24
+        most = off[:, None] * dec(head.wq, head.s_w).abs()
+        assert not bool(loss.any()) and bool((dx.abs() <= most * (1 + 2.0 ** -7) + 1e-30).all())
+    assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(dx).all())
